@@ -57,7 +57,15 @@ typedef enum {
   KD_ERR_IO = 7             /* cache file: open/read/write failed, truncated or corrupt */
 } kd_status;
 
+/* Element type of a logits matrix. */
+typedef enum {
+  KD_BF16 = 0,
+  KD_F16 = 1,
+  KD_F32 = 2
+} kd_dtype;
+
 #define KD_MAX_K 1024
+#define KD_MAX_TOP 128        /* alternatives per position of kd_token_logprobs_fwd */
 
 /* Human-readable name of a kd_status value (static string, never NULL). */
 KD_API const char* kd_status_string(int status);
@@ -261,6 +269,111 @@ KD_API int kd_fused_kl_fwd_static(const void* H_bf16, const void* W_bf16,
  * detail (0x7xxx: top-K), after skipping the access.
  */
 KD_API int kd_get_device_error(void* ws, void* stream, int64_t* detail_out);
+
+/* ------------------------------------------------------------------------ *
+ * Scoring and distillation on dense logits.  No page has a counterpart: they are the
+ * calls that a training loop or a server needs next to the cache and the fused loss
+ * once a model hands out its logits.
+ *
+ * Conventions shared by these calls
+ *   logits : [N, ld] of type `dtype`, row r at logits + r * ld elements, columns [0, V)
+ *            read, V <= ld, V <= 2^30.  Any row stride and any alignment of the element
+ *            type; rows that start on 16 bytes are read fastest.
+ *   mask   : [N] uint8, 1 = valid, 0 = padding (its logits, tokens and cached entries
+ *            are not looked at; its outputs are 0 and its gradients 0); NULL = all valid.
+ *   tau    : temperature > 0; x = logits / tau.
+ *   Logits of -inf take no part.  A row whose logits are all -inf has logsumexp -inf,
+ *   log probabilities -inf, entropy 0 and zero gradients.  A NaN or +inf logit makes
+ *   its row's results NaN.  Sums and statistics are fp32.
+ * ------------------------------------------------------------------------ */
+
+/* Workspace bytes of kd_token_logprobs_fwd / _bwd (control block only). */
+KD_API size_t kd_token_logprobs_workspace(int64_t N, int64_t V);
+
+/*
+ * Log probabilities of M given tokens per position, with the entropy and the top
+ * alternatives of the position's distribution:
+ *   tokens      : [N, M] int32 in [0, V), 1 <= M <= KD_MAX_K (one outside is recorded
+ *                 in the error word with its row; its output is NaN).
+ *   logp_out    : [N, M] fp32, x[token] - logsumexp(x).    lse_out : [N] fp32, logsumexp(x).
+ *   entropy_out : [N] fp32 or NULL, -sum_v p_v ln p_v.
+ *   top         : alternatives per position, 0 <= top <= min(V, KD_MAX_TOP).
+ *   top_ids_out : [N, top] int32 and top_logp_out: [N, top] fp32: the largest logits of
+ *                 the row, largest first, equal ones by ascending id (-0 equals +0), as
+ *                 log probabilities; both NULL when top == 0.  In a row with a NaN or
+ *                 +inf logit the ids are 0, 1, ... and carry no meaning.
+ */
+KD_API int kd_token_logprobs_fwd(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* tokens, int M, const uint8_t* mask, float tau, int top,
+                    float* logp_out, float* lse_out, float* entropy_out, int32_t* top_ids_out, float* top_logp_out,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the logits from the gradients of the log probabilities and entropies:
+ *   dz_v = (1 / tau) (sum_m g_m [v = token_m] - p_v (sum_m g_m + h (ln p_v + H)))
+ *   lse, entropy : [N] fp32 from the forward pass with the same inputs (entropy may be
+ *                  NULL when grad_entropy is).
+ *   grad_logp    : [N, M] fp32.   grad_entropy: [N] fp32 or NULL.  A token that occurs
+ *                  more than once in a row receives the sum of its gradients.
+ *   grad_logits  : [N, ld_grad] of type `dtype`, columns [0, V) written (rounded once from
+ *                  fp32); may be `logits` itself with ld_grad == ld, otherwise the two
+ *                  must not overlap.
+ */
+KD_API int kd_token_logprobs_bwd(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* tokens, int M, const uint8_t* mask, float tau,
+                    const float* lse, const float* entropy, const float* grad_logp, const float* grad_entropy,
+                    void* grad_logits, int64_t ld_grad, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of kd_logits_kl_fwd / _bwd / _step. */
+KD_API size_t kd_logits_kl_workspace(int64_t N, int64_t V, int K);
+
+/*
+ * KL(teacher || student) of dense student logits against cached top-K teacher logits,
+ * with q = softmax(x) over the V logits and S the row's cached ids:
+ *   t_lse == NULL : p = softmax(t / tau) over S, as kd_fused_kl_fwd;
+ *                   KL_t = sum_k p_k (ln p_k - ln q_k).
+ *   t_lse given   : the teacher's mass outside its cache is kept as one more class:
+ *                   p_k = exp(t_k / tau - t_lse), p_R = max(0, 1 - sum_k p_k), q_R = the
+ *                   student's mass outside S;  KL_t gains p_R (ln p_R - ln q_R).  Where S
+ *                   is the whole vocabulary there is no such class.
+ *                   t_lse: [N] fp32, logsumexp of the teacher's full row of logits / tau
+ *                   (for tau = 1 the lse_out of kd_topk_cache and kd_teacher_topk).
+ *   loss          = sum over valid t of KL_t / N_valid   (0 when N_valid == 0).
+ *   t_ids    : [N, K] int32, 1 <= K <= min(V, KD_MAX_K).  An id that repeats within a row
+ *              adds up its entries' probabilities.  One outside [0, V) is recorded in the
+ *              error word with its row and its entry left out.
+ *   t_logits : [N, K] fp32, any order; an entry of -inf is absent (its id is not looked
+ *              at).  Without t_lse, a row with no entry has KL 0 and zero gradient.
+ *   loss_out : device fp32 scalar.     kl_per_token_out: [N] fp32 or NULL.
+ *   stats_out: [N, 4] fp32, the row statistics that the backward pass takes: the largest
+ *              logit and sum exp((logit - largest) / tau) over the row, then over the ids
+ *              outside S (with t_lse; -inf and 0 without).
+ * KD_ERR_UNSUPPORTED when a row's bitmap of S and its K entries exceed the shared memory
+ * of an SM (V over about 1.4 million, 0.7 million for fp32).
+ */
+KD_API int kd_logits_kl_fwd(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* t_ids, const float* t_logits, int K, const float* t_lse, const uint8_t* mask,
+                    float tau, float* loss_out, float* stats_out, float* kl_per_token_out,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Its gradient, with c = grad_loss / (N_valid tau):
+ *   dz_v = c (q_v - p_v) on S, c q_v outside; with t_lse, outside S
+ *   c (q_v - p_R q_v / q_R).
+ *   stats     : from the forward pass with the same inputs.   grad_loss: device fp32 scalar.
+ *   grad_logits as for kd_token_logprobs_bwd (may be `logits` itself).
+ */
+KD_API int kd_logits_kl_bwd(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* t_ids, const float* t_logits, int K, const float* t_lse, const uint8_t* mask,
+                    float tau, const float* stats, const float* grad_loss, void* grad_logits, int64_t ld_grad,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* Loss and gradient in one call, for callers that know grad_loss beforehand: the logits
+ * come from memory once.  Arguments as above. */
+KD_API int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* t_ids, const float* t_logits, int K, const float* t_lse, const uint8_t* mask,
+                    float tau, const float* grad_loss, float* loss_out, float* kl_per_token_out,
+                    void* grad_logits, int64_t ld_grad, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * On-disk teacher cache ([ART] paragraph on the first fix: run the teacher once,

@@ -26,6 +26,7 @@ from .kl import (
     fused_chunked_kl,
     OracleResult,
 )
+from .scores import DenseKL, Scores, logits_kl, token_logprobs, token_logprobs_grad
 from .topk import topk_cache, teacher_logsumexp, dropped_mass, teacher_logits_bf16
 
 __all__ = [
@@ -35,6 +36,11 @@ __all__ = [
     "forward_chunked_kl",
     "fused_chunked_kl",
     "OracleResult",
+    "Scores",
+    "token_logprobs",
+    "token_logprobs_grad",
+    "DenseKL",
+    "logits_kl",
     "topk_cache",
     "teacher_logsumexp",
     "dropped_mass",

@@ -11,12 +11,12 @@ runs in the CUDA kernels of ``libkdkl.so`` (see ``include/kdkl.h``).
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
 from . import _abi
-from ._abi import KDError, KD_MAX_K
+from ._abi import KDError, KD_MAX_K, KD_MAX_TOP
 
 __all__ = [
     "topk_cache",
@@ -26,6 +26,14 @@ __all__ = [
     "fused_kl_backward",
     "chunked_kl_forward",
     "chunked_kl_backward",
+    "TokenLogprobs",
+    "token_logprobs",
+    "token_logprobs_forward",
+    "token_logprobs_backward",
+    "logits_kl",
+    "logits_kl_forward",
+    "logits_kl_backward",
+    "logits_kl_step",
     "gemm_bf16",
     "cache_write",
     "cache_info",
@@ -35,6 +43,7 @@ __all__ = [
     "Profile",
     "KDError",
     "KD_MAX_K",
+    "KD_MAX_TOP",
     "workspace",
 ]
 
@@ -201,6 +210,209 @@ class _FusedKL(torch.autograd.Function):
 def fused_kl(H, W, ids, tlog, mask=None, chunk=4096, tau=1.0):
     """Differentiable fused chunked KL(p_teacher || q_student) token mean (scalar tensor)."""
     return _FusedKL.apply(H, W, ids, tlog, mask, int(chunk), float(tau))
+
+
+# ------------------------------------------------------------- dense logits
+
+_DTYPES = {torch.bfloat16: _abi.KD_BF16, torch.float16: _abi.KD_F16, torch.float32: _abi.KD_F32}
+
+
+def _check(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    """A contiguous tensor of this type and shape on this device (or None)."""
+    if t is None:
+        return
+    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _check_logits(z: torch.Tensor, name: str = "logits"):
+    """(type code, N, V, row stride) of a 2-D CUDA matrix whose rows are contiguous."""
+    if not z.is_cuda or z.dim() != 2 or z.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be a 2-D bf16, fp16 or fp32 CUDA tensor")
+    N, V = z.shape
+    if N < 1 or V < 1:
+        raise ValueError(f"{name} must not be empty")
+    ld = z.stride(0) if N > 1 else V
+    if (z.stride(1) != 1 and V > 1) or ld < V:
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    return _DTYPES[z.dtype], N, V, ld
+
+
+def _grad_like(z: torch.Tensor, grad: Optional[torch.Tensor]):
+    """(gradient matrix, its row stride): a new one, or the caller's (the logits themselves included)."""
+    if grad is None:
+        grad = torch.empty(z.shape, dtype=z.dtype, device=z.device)
+        return grad, z.shape[1]
+    if grad.shape != z.shape or grad.dtype != z.dtype or grad.device != z.device:
+        raise ValueError("grad_logits must have the logits' shape, type and device")
+    return grad, _check_logits(grad, "grad_logits")[3]
+
+
+def _ws(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    return workspace(nbytes, device) if ws is None else ws
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs_forward returns (None for what was not asked for)."""
+    logp: torch.Tensor                      # [N, M] (or [N]) log probabilities of the given tokens
+    lse: torch.Tensor                       # [N] logsumexp of logits / tau
+    entropy: Optional[torch.Tensor]         # [N]
+    top_ids: Optional[torch.Tensor]         # [N, top] int32, most probable first
+    top_logp: Optional[torch.Tensor]        # [N, top]
+
+
+def token_logprobs_forward(logits, tokens, mask=None, tau=1.0, top=0, entropy=False, ws=None) -> TokenLogprobs:
+    """kd_token_logprobs_fwd: log probabilities of ``tokens`` (int32 [N] or [N, M]) under softmax(logits / tau),
+    with the ``top`` most probable alternatives and the entropy when asked.  ``logits``: [N, V] bf16, fp16 or
+    fp32 with contiguous rows (any row stride)."""
+    dt, N, V, ld = _check_logits(logits)
+    dev = logits.device
+    M = tokens.shape[1] if tokens.dim() == 2 else 1
+    _check(tokens, "tokens", torch.int32, (N, M) if tokens.dim() == 2 else (N,), dev)
+    _check(mask, "mask", torch.uint8, (N,), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    logp = torch.empty(tokens.shape, **f32)
+    lse = torch.empty((N,), **f32)
+    ent = torch.empty((N,), **f32) if entropy else None
+    top_ids = torch.empty((N, top), dtype=torch.int32, device=dev) if top else None
+    top_logp = torch.empty((N, top), **f32) if top else None
+    ws = _ws(ws, _abi.kd_token_logprobs_workspace(N, V), dev)
+    st = _abi.kd_token_logprobs_fwd(_ptr(logits), dt, N, V, ld, _ptr(tokens), M, _ptr(mask), float(tau), int(top),
+                                    _ptr(logp), _ptr(lse), _ptr(ent), _ptr(top_ids), _ptr(top_logp), _ptr(ws),
+                                    ws.numel(), _stream(dev))
+    _abi.check(st, "kd_token_logprobs_fwd")
+    return TokenLogprobs(logp, lse, ent, top_ids, top_logp)
+
+
+def token_logprobs_backward(logits, tokens, lse, grad_logp, mask=None, tau=1.0, entropy=None, grad_entropy=None,
+                            ws=None, grad_logits=None):
+    """kd_token_logprobs_bwd: the gradient of the logits, in their type.  ``grad_logits`` may be the logits
+    themselves (their memory is then reused)."""
+    dt, N, V, ld = _check_logits(logits)
+    dev = logits.device
+    M = tokens.shape[1] if tokens.dim() == 2 else 1
+    _check(tokens, "tokens", torch.int32, (N, M) if tokens.dim() == 2 else (N,), dev)
+    _check(grad_logp, "grad_logp", torch.float32, tokens.shape, dev)
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_entropy, "grad_entropy")):
+        _check(t, name, torch.float32, (N,), dev)
+    _check(mask, "mask", torch.uint8, (N,), dev)
+    grad_logits, ldg = _grad_like(logits, grad_logits)
+    ws = _ws(ws, _abi.kd_token_logprobs_workspace(N, V), dev)
+    st = _abi.kd_token_logprobs_bwd(_ptr(logits), dt, N, V, ld, _ptr(tokens), M, _ptr(mask), float(tau), _ptr(lse),
+                                    _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_logits), ldg,
+                                    _ptr(ws), ws.numel(), _stream(dev))
+    _abi.check(st, "kd_token_logprobs_bwd")
+    return grad_logits
+
+
+def _f32c(g):
+    return None if g is None else g.to(torch.float32).contiguous()
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, mask, tau):
+        r = token_logprobs_forward(logits, tokens, mask, tau, entropy=True)
+        ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
+        ctx.mask, ctx.tau = mask, tau
+        ctx.set_materialize_grads(False)
+        return r.logp, r.entropy
+
+    @staticmethod
+    def backward(ctx, g_logp, g_entropy):
+        logits, tokens, lse, ent = ctx.saved_tensors
+        if g_logp is None and g_entropy is None:
+            return None, None, None, None
+        if g_logp is None:
+            g_logp = torch.zeros(tokens.shape, dtype=torch.float32, device=logits.device)
+        g = token_logprobs_backward(logits, tokens, lse, _f32c(g_logp), ctx.mask, ctx.tau, ent, _f32c(g_entropy))
+        return g, None, None, None
+
+
+def token_logprobs(logits, tokens, mask=None, tau=1.0):
+    """Differentiable (log probabilities of ``tokens``, entropy [N]) of softmax(logits / tau)."""
+    return _TokenLogprobs.apply(logits, tokens, mask, float(tau))
+
+
+def _check_kl(logits, ids, tlog, mask, t_lse, kl_out=None):
+    dt, N, V, ld = _check_logits(logits)
+    dev = logits.device
+    if ids.dim() != 2:
+        raise ValueError("ids must be an int32 [N, K] tensor")
+    K = ids.shape[1]
+    _check(ids, "ids", torch.int32, (N, K), dev)
+    _check(tlog, "tlog", torch.float32, (N, K), dev)
+    _check(t_lse, "t_lse", torch.float32, (N,), dev)
+    _check(mask, "mask", torch.uint8, (N,), dev)
+    _check(kl_out, "kl_out", torch.float32, (N,), dev)
+    return dt, N, V, ld, K, dev
+
+
+def logits_kl_forward(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, ws=None, kl_out=None):
+    """kd_logits_kl_fwd: KL of the cached teacher (``ids`` int32, ``tlog`` fp32 [N, K]; with ``t_lse`` its mass
+    outside the cache as one more class) against softmax(logits / tau): (loss [1], stats [N, 4], ws)."""
+    dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse, kl_out)
+    ws = _ws(ws, _abi.kd_logits_kl_workspace(N, V, K), dev)
+    loss = torch.empty((1,), dtype=torch.float32, device=dev)
+    stats = torch.empty((N, 4), dtype=torch.float32, device=dev)
+    st = _abi.kd_logits_kl_fwd(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
+                               float(tau), _ptr(loss), _ptr(stats), _ptr(kl_out), _ptr(ws), ws.numel(), _stream(dev))
+    _abi.check(st, "kd_logits_kl_fwd")
+    return loss, stats, ws
+
+
+def logits_kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau=1.0, t_lse=None, ws=None, grad_logits=None):
+    """kd_logits_kl_bwd: the gradient of the logits, in their type (``grad_logits`` may be the logits themselves)."""
+    dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse)
+    _check(stats, "stats", torch.float32, (N, 4), dev)
+    _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
+    grad_logits, ldg = _grad_like(logits, grad_logits)
+    ws = _ws(ws, _abi.kd_logits_kl_workspace(N, V, K), dev)
+    st = _abi.kd_logits_kl_bwd(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
+                               float(tau), _ptr(stats), _ptr(grad_loss), _ptr(grad_logits), ldg, _ptr(ws), ws.numel(),
+                               _stream(dev))
+    _abi.check(st, "kd_logits_kl_bwd")
+    return grad_logits
+
+
+def logits_kl_step(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=None, ws=None, kl_out=None,
+                   grad_logits=None):
+    """kd_logits_kl_step: loss and gradient in one pass over the logits, for a ``grad_loss`` ([1] fp32, default 1)
+    known beforehand: (loss [1], grad_logits).  ``grad_logits`` may be the logits themselves."""
+    dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse, kl_out)
+    if grad_loss is None:
+        grad_loss = torch.ones((1,), dtype=torch.float32, device=dev)
+    _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
+    grad_logits, ldg = _grad_like(logits, grad_logits)
+    ws = _ws(ws, _abi.kd_logits_kl_workspace(N, V, K), dev)
+    loss = torch.empty((1,), dtype=torch.float32, device=dev)
+    st = _abi.kd_logits_kl_step(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
+                                float(tau), _ptr(grad_loss), _ptr(loss), _ptr(kl_out), _ptr(grad_logits), ldg,
+                                _ptr(ws), ws.numel(), _stream(dev))
+    _abi.check(st, "kd_logits_kl_step")
+    return loss, grad_logits
+
+
+class _LogitsKL(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, tlog, mask, tau, t_lse):
+        loss, stats, ws = logits_kl_forward(logits, ids, tlog, mask, tau, t_lse)
+        ctx.save_for_backward(logits, ids, tlog, stats)
+        ctx.mask, ctx.tau, ctx.t_lse, ctx.ws = mask, tau, t_lse, ws
+        return loss[0]
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        logits, ids, tlog, stats = ctx.saved_tensors
+        g = logits_kl_backward(logits, ids, tlog, ctx.mask, stats, _f32c(grad_out.reshape(1)), ctx.tau, ctx.t_lse,
+                               ws=ctx.ws)
+        return g, None, None, None, None, None
+
+
+def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None):
+    """Differentiable KL(p_teacher || q_student) token mean on dense student logits (scalar tensor)."""
+    return _LogitsKL.apply(logits, ids, tlog, mask, float(tau), t_lse)
 
 
 def gemm_bf16(A, B, M, N, K, a_mn_major=False, b_mn_major=False, C=None):

@@ -23,7 +23,11 @@ KD_ERR_CUDA = 4
 KD_ERR_TIMEOUT = 5
 KD_ERR_DEVICE = 6
 KD_ERR_IO = 7
+KD_BF16 = 0
+KD_F16 = 1
+KD_F32 = 2
 KD_MAX_K = 1024
+KD_MAX_TOP = 128
 KD_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 _c_i64 = ctypes.c_int64
@@ -54,6 +58,18 @@ _SIGNATURES = {
                                    _c_ptr]),
     "kd_fused_kl_fwd_static": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_int,
                                         _c_i64, _c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "kd_token_logprobs_workspace": (_c_size, [_c_i64, _c_i64]),
+    "kd_token_logprobs_fwd": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_int, _c_ptr, _c_float, _c_int,
+                                       _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "kd_token_logprobs_bwd": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_int, _c_ptr, _c_float, _c_ptr,
+                                       _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_size, _c_ptr]),
+    "kd_logits_kl_workspace": (_c_size, [_c_i64, _c_i64, _c_int]),
+    "kd_logits_kl_fwd": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr,
+                                  _c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "kd_logits_kl_bwd": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr,
+                                  _c_float, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_size, _c_ptr]),
+    "kd_logits_kl_step": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr,
+                                   _c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_size, _c_ptr]),
     "kd_get_device_error": (_c_int, [_c_ptr, _c_ptr, ctypes.POINTER(_c_i64)]),
     "kd_gemm_bf16": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_ptr, _c_size,
                               _c_ptr]),
@@ -135,6 +151,13 @@ kd_fused_kl_fwd_static = _wrap("kd_fused_kl_fwd_static")
 kd_chunked_kl_logits_bytes = _wrap("kd_chunked_kl_logits_bytes")
 kd_chunked_kl_fwd = _wrap("kd_chunked_kl_fwd")
 kd_chunked_kl_bwd = _wrap("kd_chunked_kl_bwd")
+kd_token_logprobs_workspace = _wrap("kd_token_logprobs_workspace")
+kd_token_logprobs_fwd = _wrap("kd_token_logprobs_fwd")
+kd_token_logprobs_bwd = _wrap("kd_token_logprobs_bwd")
+kd_logits_kl_workspace = _wrap("kd_logits_kl_workspace")
+kd_logits_kl_fwd = _wrap("kd_logits_kl_fwd")
+kd_logits_kl_bwd = _wrap("kd_logits_kl_bwd")
+kd_logits_kl_step = _wrap("kd_logits_kl_step")
 kd_get_device_error = _wrap("kd_get_device_error")
 kd_gemm_bf16 = _wrap("kd_gemm_bf16")
 kd_gemm_workspace = _wrap("kd_gemm_workspace")

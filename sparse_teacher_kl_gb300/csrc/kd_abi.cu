@@ -110,7 +110,7 @@ bool make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64
 static PerDevice<int> g_dev_ok;  // per device: 1 = sm_103, 0 = another architecture
 
 // The current device is an sm_103 GPU (the kernels are built for sm_103a only).
-static kd_status check_device() {
+kd_status check_device() {
   int dev = 0, ok = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KD_ERR_CUDA;
   const int rc = g_dev_ok.get(dev, &ok, [](int d, int* v) {
@@ -127,8 +127,6 @@ static kd_status check_device() {
 }
 
 // -------------------------------------------------------------- layout ---
-
-static inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 struct KlLayout {
   size_t ids_sorted, p_sorted, negent, kl, partials, dz, gh_part, total;
@@ -194,8 +192,6 @@ static int choose_splits(int64_t tiles, int k_blocks, int grid) {
   return best;
 }
 
-static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 static kd_status check_kl_args(const void* H, const void* W, const int32_t* ids, const float* tlog, int64_t N,
                                int64_t d, int64_t V, int K, int64_t chunk, float tau, const void* ws,
                                size_t ws_bytes) {
@@ -210,8 +206,6 @@ static kd_status check_kl_args(const void* H, const void* W, const int32_t* ids,
   if (ws_bytes < kl_layout(N, d, V, K, chunk).total) return KD_ERR_WORKSPACE;
   return KD_OK;
 }
-
-static kd_status map_cuda(cudaError_t e) { return e == cudaSuccess ? KD_OK : KD_ERR_CUDA; }
 
 }  // namespace kd
 

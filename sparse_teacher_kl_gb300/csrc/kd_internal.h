@@ -129,7 +129,14 @@ struct GemmProblem {
   uint32_t* err;
 };
 
-// Host helpers (kd_tma.cpp part of kd_abi.cu).
+// Host helpers of the C ABI.
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline kd_status map_cuda(cudaError_t e) { return e == cudaSuccess ? KD_OK : KD_ERR_CUDA; }
+// KD_OK if the current device is an sm_103 GPU.
+kd_status check_device();
+
+// Tensor maps (kd_abi.cu).
 bool make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                        uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 // dZ chunk in blocked layout: [nvb = ceil(V/64)][rows_pad][64] bf16; dims {64, rows, nvb},
@@ -202,6 +209,21 @@ cudaError_t launch_dz_from_z(const uint16_t* z, int64_t N, int64_t c0, int rows,
                              int K, uint16_t* dz, cudaStream_t s);
 cudaError_t launch_split_reduce(const float* parts, int splits, int64_t split_stride, int64_t count, void* out,
                                 int out_bf16, cudaStream_t s);
+
+// Dense logits [N, ld] of element type `dtype` (kd_dtype), see kdkl.h.
+cudaError_t launch_logprobs_fwd(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* tokens,
+                                int M, const uint8_t* mask, float tau, int top, float* logp, float* lse,
+                                float* entropy, int32_t* top_ids, float* top_logp, uint32_t* err, cudaStream_t s);
+cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* tokens,
+                                int M, const uint8_t* mask, float tau, const float* lse, const float* entropy,
+                                const float* g_logp, const float* g_ent, void* dz, int64_t ld_dz, uint32_t* err,
+                                cudaStream_t s);
+// mode: 1 = forward (stats, kl), 2 = backward (stats -> dz), 3 = both in one pass (kl, dz).
+bool logits_kl_fits(int64_t V, int K, int dtype);
+cudaError_t launch_logits_kl(int mode, const void* z, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* ids,
+                             const float* tlog, int K, const float* t_lse, const uint8_t* mask, float tau,
+                             float* stats, float* kl, const float* grad_loss, const int32_t* n_valid, void* dz,
+                             int64_t ld_dz, uint32_t* err, cudaStream_t s);
 
 constexpr int KD_MAX_SPLITS = 8;
 
