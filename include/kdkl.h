@@ -376,6 +376,35 @@ KD_API int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V
                     void* grad_logits, int64_t ld_grad, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * The same scores straight from hidden states: log probability of one given token per
+ * position and the entropy under softmax(H W^T / tau), formed `chunk` positions at a
+ * time by the fused loss's projection, so that the [N, V] logits never exist (no page
+ * has a counterpart: the hard-label term next to the KL, and scoring without logits).
+ *   H_bf16, W_bf16, mask, chunk, tau : as for kd_fused_kl_fwd.
+ *   tokens : [N] int32 in [0, V) (one outside is recorded in the error word with its
+ *            row; its log probability is NaN, its one-hot gradient is left out).
+ *   logp_out, lse_out : [N] fp32.   entropy_out: [N] fp32 or NULL.  Padding rows give 0;
+ *            their tokens are not looked at.
+ * The backward pass recomputes each chunk's logits and takes, per valid position,
+ *   dZ_v = (1 / tau) (g [v = token] - p_v (g + h (ln p_v + H)))
+ * with g = grad_logp, h = grad_entropy ([N] fp32; grad_entropy and entropy may be NULL
+ * together); grad_H, grad_W and the rounding of dZ to bf16 as for kd_fused_kl_bwd.
+ * Workspace: `backward` != 0 asks for what the backward pass needs (both calls may use
+ * it; it grows with chunk * V), 0 for the forward pass alone (chunk * V / 16 bytes).
+ * ------------------------------------------------------------------------ */
+
+KD_API size_t kd_fused_logprobs_workspace(int64_t N, int64_t d, int64_t V, int64_t chunk, int backward);
+
+KD_API int kd_fused_logprobs_fwd(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
+                    int64_t N, int64_t d, int64_t V, int64_t chunk, float tau,
+                    float* logp_out, float* lse_out, float* entropy_out, void* ws, size_t ws_bytes, void* stream);
+
+KD_API int kd_fused_logprobs_bwd(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
+                    int64_t N, int64_t d, int64_t V, int64_t chunk, float tau,
+                    const float* lse, const float* entropy, const float* grad_logp, const float* grad_entropy,
+                    void* grad_H, int grad_H_is_fp32, float* grad_W, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * On-disk teacher cache ([ART] paragraph on the first fix: run the teacher once,
  * keep its top-K logits per position on disk, reuse them across experiments).
  * HOST memory and host files only; no CUDA call.  One file per contiguous range

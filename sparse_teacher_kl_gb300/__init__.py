@@ -34,6 +34,9 @@ __all__ = [
     "logits_kl_forward",
     "logits_kl_backward",
     "logits_kl_step",
+    "fused_logprobs",
+    "fused_logprobs_forward",
+    "fused_logprobs_backward",
     "gemm_bf16",
     "cache_write",
     "cache_info",
@@ -249,8 +252,15 @@ def _grad_like(z: torch.Tensor, grad: Optional[torch.Tensor]):
     return grad, _check_logits(grad, "grad_logits")[3]
 
 
+def _fresh_ws(nbytes: int, device) -> torch.Tensor:
+    """A workspace with its control block zeroed and the rest left as it is (the allocator's blocks are aligned)."""
+    ws = torch.empty((int(nbytes),), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
 def _ws(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
-    return workspace(nbytes, device) if ws is None else ws
+    return _fresh_ws(nbytes, device) if ws is None else ws
 
 
 class TokenLogprobs(NamedTuple):
@@ -413,6 +423,81 @@ class _LogitsKL(torch.autograd.Function):
 def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None):
     """Differentiable KL(p_teacher || q_student) token mean on dense student logits (scalar tensor)."""
     return _LogitsKL.apply(logits, ids, tlog, mask, float(tau), t_lse)
+
+
+def _check_projection(H, W, tokens, mask):
+    for t, name in ((H, "H"), (W, "W")):
+        if not t.is_cuda or t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 2-D bf16 CUDA tensor")
+    N, d = H.shape
+    if W.shape[1] != d or W.device != H.device:
+        raise ValueError("W must be [V, d] on the device of H [N, d]")
+    _check(tokens, "tokens", torch.int32, (N,), H.device)
+    _check(mask, "mask", torch.uint8, (N,), H.device)
+    return N, d, W.shape[0], H.device
+
+
+def fused_logprobs_forward(H, W, tokens, mask=None, chunk=4096, tau=1.0, entropy=False, ws=None):
+    """kd_fused_logprobs_fwd: (logp [N], lse [N], entropy [N] or None, ws) of ``tokens`` (int32 [N]) under
+    softmax(H W^T / tau), the logits never stored."""
+    N, d, V, dev = _check_projection(H, W, tokens, mask)
+    if ws is None:
+        ws = _fresh_ws(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 0), dev)
+    logp = torch.empty((N,), dtype=torch.float32, device=dev)
+    lse = torch.empty((N,), dtype=torch.float32, device=dev)
+    ent = torch.empty((N,), dtype=torch.float32, device=dev) if entropy else None
+    st = _abi.kd_fused_logprobs_fwd(_ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), N, d, V, chunk, float(tau), _ptr(logp),
+                                    _ptr(lse), _ptr(ent), _ptr(ws), ws.numel(), _stream(dev))
+    _abi.check(st, "kd_fused_logprobs_fwd")
+    return logp, lse, ent, ws
+
+
+def fused_logprobs_backward(H, W, tokens, lse, grad_logp, mask=None, chunk=4096, tau=1.0, entropy=None,
+                            grad_entropy=None, ws=None, grad_H=None, grad_W=None, grad_H_fp32=False):
+    """kd_fused_logprobs_bwd: (grad_H [N, d] bf16 or fp32, grad_W [V, d] fp32 accumulated)."""
+    N, d, V, dev = _check_projection(H, W, tokens, mask)
+    for t, name in ((lse, "lse"), (grad_logp, "grad_logp"), (entropy, "entropy"), (grad_entropy, "grad_entropy")):
+        _check(t, name, torch.float32, (N,), dev)
+    if ws is None:
+        ws = _fresh_ws(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 1), dev)
+    if grad_H is None:
+        grad_H = torch.empty((N, d), dtype=torch.float32 if grad_H_fp32 else torch.bfloat16, device=dev)
+    if grad_W is None:
+        grad_W = torch.zeros((V, d), dtype=torch.float32, device=dev)
+    _check(grad_H, "grad_H", torch.float32 if grad_H.dtype == torch.float32 else torch.bfloat16, (N, d), dev)
+    _check(grad_W, "grad_W", torch.float32, (V, d), dev)
+    st = _abi.kd_fused_logprobs_bwd(_ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), N, d, V, chunk, float(tau), _ptr(lse),
+                                    _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_H),
+                                    1 if grad_H.dtype == torch.float32 else 0, _ptr(grad_W), _ptr(ws), ws.numel(),
+                                    _stream(dev))
+    _abi.check(st, "kd_fused_logprobs_bwd")
+    return grad_H, grad_W
+
+
+class _FusedLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, W, tokens, mask, chunk, tau):
+        logp, lse, ent, _ = fused_logprobs_forward(H, W, tokens, mask, chunk, tau, entropy=True)
+        ctx.save_for_backward(H, W, tokens, lse, ent)
+        ctx.mask, ctx.chunk, ctx.tau = mask, chunk, tau
+        ctx.set_materialize_grads(False)
+        return logp, ent
+
+    @staticmethod
+    def backward(ctx, g_logp, g_entropy):
+        H, W, tokens, lse, ent = ctx.saved_tensors
+        if g_logp is None and g_entropy is None:
+            return None, None, None, None, None, None
+        if g_logp is None:
+            g_logp = torch.zeros_like(lse)
+        grad_H, grad_W = fused_logprobs_backward(H, W, tokens, lse, _f32c(g_logp), ctx.mask, ctx.chunk, ctx.tau, ent,
+                                                 _f32c(g_entropy))
+        return grad_H, grad_W.to(W.dtype), None, None, None, None
+
+
+def fused_logprobs(H, W, tokens, mask=None, chunk=4096, tau=1.0):
+    """Differentiable (log probability of ``tokens`` [N], entropy [N]) of softmax(H W^T / tau)."""
+    return _FusedLogprobs.apply(H, W, tokens, mask, int(chunk), float(tau))
 
 
 def gemm_bf16(A, B, M, N, K, a_mn_major=False, b_mn_major=False, C=None):

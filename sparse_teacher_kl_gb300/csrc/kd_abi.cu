@@ -192,16 +192,23 @@ static int choose_splits(int64_t tiles, int k_blocks, int grid) {
   return best;
 }
 
+static kd_status check_proj_args(const void* H, const void* W, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                                 float tau) {
+  if (N < 1 || d < 8 || V < 1 || chunk < BM) return KD_ERR_INVALID_ARG;
+  if (d % 8 != 0 || chunk % BM != 0) return KD_ERR_INVALID_ARG;
+  if (V > 0x7fffffffLL || N > 0x7fffffffLL || d > 0x7fffffffLL) return KD_ERR_INVALID_ARG;
+  if (!(tau > 0.f) || !isfinite(tau)) return KD_ERR_INVALID_ARG;
+  if (!H || !W || !aligned(H, 16) || !aligned(W, 16)) return KD_ERR_INVALID_ARG;
+  return KD_OK;
+}
+
 static kd_status check_kl_args(const void* H, const void* W, const int32_t* ids, const float* tlog, int64_t N,
                                int64_t d, int64_t V, int K, int64_t chunk, float tau, const void* ws,
                                size_t ws_bytes) {
-  if (N < 1 || d < 8 || V < 1 || K < 1 || chunk < BM) return KD_ERR_INVALID_ARG;
-  if (d % 8 != 0 || chunk % BM != 0) return KD_ERR_INVALID_ARG;
-  if (K > KD_MAX_K || int64_t(K) > V) return KD_ERR_INVALID_ARG;
-  if (V > 0x7fffffffLL || N > 0x7fffffffLL || d > 0x7fffffffLL) return KD_ERR_INVALID_ARG;
-  if (!(tau > 0.f) || !isfinite(tau)) return KD_ERR_INVALID_ARG;
-  if (!H || !W || !ids || !tlog) return KD_ERR_INVALID_ARG;
-  if (!aligned(H, 16) || !aligned(W, 16) || !aligned(ids, 4) || !aligned(tlog, 4)) return KD_ERR_INVALID_ARG;
+  const kd_status st = check_proj_args(H, W, N, d, V, chunk, tau);
+  if (st != KD_OK) return st;
+  if (K < 1 || K > KD_MAX_K || int64_t(K) > V) return KD_ERR_INVALID_ARG;
+  if (!ids || !tlog || !aligned(ids, 4) || !aligned(tlog, 4)) return KD_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return KD_ERR_WORKSPACE;
   if (ws_bytes < kl_layout(N, d, V, K, chunk).total) return KD_ERR_WORKSPACE;
   return KD_OK;
@@ -366,16 +373,45 @@ size_t kd_chunked_kl_logits_bytes(int64_t N, int64_t V) {
 
 }  // extern "C"
 
+// What fused_logprobs puts in the place of the teacher: the given tokens, and the outputs of
+// the forward or the gradients of the backward pass.
+struct LogprobTerm {
+  const int32_t* tokens;
+  float *logp, *entropy;                       // forward outputs (entropy may be NULL)
+  const float *g_logp, *g_entropy, *entropy_in;  // backward
+};
+
+// Workspace of the forward pass of fused_logprobs: control block and partials alone.
+static size_t logprob_fwd_ws(int64_t N, int64_t V, int64_t chunk) {
+  const int64_t c = chunk < N ? chunk : N;
+  return sizeof(Ctrl) + size_t((V + BN - 1) / BN) * size_t((c + BM - 1) / BM * BM) * 16;
+}
+
+static kd_status check_logprob_args(const void* H, const void* W, const int32_t* tokens, int64_t N, int64_t d,
+                                    int64_t V, int64_t chunk, float tau, const void* ws, size_t ws_bytes,
+                                    bool backward) {
+  const kd_status st = check_proj_args(H, W, N, d, V, chunk, tau);
+  if (st != KD_OK) return st;
+  if (!tokens || !aligned(tokens, 4)) return KD_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256)) return KD_ERR_WORKSPACE;
+  return ws_bytes < (backward ? kl_layout(N, d, V, 1, chunk).total : logprob_fwd_ws(N, V, chunk)) ? KD_ERR_WORKSPACE
+                                                                                                 : KD_OK;
+}
+
 // Forward pass of both modes: z_store == NULL is the fused chunked loss; otherwise
 // each chunk's raw logits are also written (bf16, blocked) for a backward pass that
-// reads them instead of recomputing them.
+// reads them instead of recomputing them.  lp (else NULL): log probabilities of given
+// tokens and entropies in place of the loss against a teacher.
 static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids, const float* t_logits,
                     const uint8_t* mask, int64_t N, int64_t d, int64_t V, int K, int64_t chunk, float tau,
                     float* loss_out, float* lse_out, float* kl_per_token_out, void* z_store, size_t z_bytes,
-                    void* ws, size_t ws_bytes, void* stream) {
-  kd_status st = check_kl_args(H_bf16, W_bf16, t_ids, t_logits, N, d, V, K, chunk, tau, ws, ws_bytes);
+                    void* ws, size_t ws_bytes, void* stream, const LogprobTerm* lp = nullptr) {
+  kd_status st = lp ? check_logprob_args(H_bf16, W_bf16, lp->tokens, N, d, V, chunk, tau, ws, ws_bytes, false)
+                    : check_kl_args(H_bf16, W_bf16, t_ids, t_logits, N, d, V, K, chunk, tau, ws, ws_bytes);
   if (st != KD_OK) return st;
-  if (!loss_out || !lse_out || !aligned(loss_out, 4) || !aligned(lse_out, 4)) return KD_ERR_INVALID_ARG;
+  if (!lse_out || !aligned(lse_out, 4)) return KD_ERR_INVALID_ARG;
+  if (!lp && (!loss_out || !aligned(loss_out, 4))) return KD_ERR_INVALID_ARG;
+  if (lp && (!lp->logp || !aligned(lp->logp, 4) || !aligned(lp->entropy, 4))) return KD_ERR_INVALID_ARG;
   if (kl_per_token_out && !aligned(kl_per_token_out, 4)) return KD_ERR_INVALID_ARG;
   st = check_device();
   if (st != KD_OK) return st;
@@ -388,7 +424,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   float* p_sorted = reinterpret_cast<float*>(w8 + L.p_sorted);
   float* negent = reinterpret_cast<float*>(w8 + L.negent);
   float* kl = kl_per_token_out ? kl_per_token_out : reinterpret_cast<float*>(w8 + L.kl);
-  float4* partials = reinterpret_cast<float4*>(w8 + L.partials);
+  float4* partials = reinterpret_cast<float4*>(w8 + (lp ? sizeof(Ctrl) : L.partials));
   const float inv_tau = 1.0f / tau;
   const uint16_t* H = static_cast<const uint16_t*>(H_bf16);
 
@@ -405,20 +441,21 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
       return KD_ERR_CUDA;
   }
 
-  cudaError_t e = launch_count_valid(mask, N, &ctrl->n_valid, s);
+  cudaError_t e = lp ? cudaSuccess : launch_count_valid(mask, N, &ctrl->n_valid, s);
   if (e != cudaSuccess) return KD_ERR_CUDA;
   const int grid_max = gemm_max_grid();
   for (int64_t c0 = 0; c0 < N; c0 += chunk) {
     const int n = int((N - c0) < chunk ? (N - c0) : chunk);
-    e = launch_teacher_prologue(t_ids + c0 * K, t_logits + c0 * K, n, K, V, inv_tau, ids_sorted, p_sorted, negent,
-                                &ctrl->err, c0, s);
+    if (!lp)
+      e = launch_teacher_prologue(t_ids + c0 * K, t_logits + c0 * K, n, K, V, inv_tau, ids_sorted, p_sorted, negent,
+                                  &ctrl->err, c0, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
     if (!make_tmap_2d_bf16(&th, H + c0 * d, uint64_t(d), uint64_t(n), uint64_t(d) * 2, BK, BM)) return KD_ERR_CUDA;
     if (d64 && !make_tmap_mn2_bf16(&th2, H + c0 * d, uint64_t(d), uint64_t(n), uint64_t(d) * 2, BM))
       return KD_ERR_CUDA;
     GemmProblem p{};
     p.M = n; p.N = int(V); p.K = int(d);
-    p.a_mn = 0; p.b_mn = 0; p.epi = z_store ? EPI_LSE_Z : EPI_LSE;
+    p.a_mn = 0; p.b_mn = 0; p.epi = lp ? EPI_LSE_H : z_store ? EPI_LSE_Z : EPI_LSE;
     p.z_row0 = int(c0);
     p.m_tiles = (n + BM - 1) / BM;
     p.n_tiles = int((V + BN - 1) / BN);
@@ -428,28 +465,43 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     p.k_splits = 1;
     p.ids_sorted = ids_sorted; p.p_sorted = p_sorted; p.Kt = K; p.inv_tau = inv_tau;
     p.partials = partials; p.rows = n; p.err = &ctrl->err;
+    if (lp) {
+      p.tokens = lp->tokens + c0;
+      p.mask = mask ? mask + c0 : nullptr;
+    }
     p.a_k3d = p.b_k3d = p.cta_pair && d64;
     e = launch_gemm(p, p.a_k3d ? th2 : th,
                     p.b_k3d ? tw2 : (p.cta_pair ? tw_half : tw), z_store ? tz : tw,
                     grid_max, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
-    e = launch_lse_combine(partials, L.n_groups, n, negent, inv_tau, lse_out + c0, kl + c0, s);
+    if (lp)
+      e = launch_logprob_combine(partials, L.n_groups, n, V, lp->tokens + c0, mask ? mask + c0 : nullptr,
+                                 lp->logp + c0, lse_out + c0, lp->entropy ? lp->entropy + c0 : nullptr, &ctrl->err,
+                                 c0, s);
+    else
+      e = launch_lse_combine(partials, L.n_groups, n, negent, inv_tau, lse_out + c0, kl + c0, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
   }
+  if (lp) return KD_OK;
   e = launch_loss_reduce(kl, mask, N, &ctrl->n_valid, loss_out, s);
   return map_cuda(e);
 }
 
 // Backward pass of both modes: z_store == NULL recomputes each chunk's logits on
-// the tensor cores (fused); otherwise dZ is formed from the stored logits.
+// the tensor cores (fused); otherwise dZ is formed from the stored logits.  lp as in
+// fwd_impl.
 static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids, const float* t_logits,
                     const uint8_t* mask, int64_t N, int64_t d, int64_t V, int K, int64_t chunk, float tau,
                     const float* lse, const float* grad_loss, const void* z_store, void* grad_H, int grad_H_is_fp32,
-                    float* grad_W, void* ws, size_t ws_bytes, void* stream) {
-  kd_status st = check_kl_args(H_bf16, W_bf16, t_ids, t_logits, N, d, V, K, chunk, tau, ws, ws_bytes);
+                    float* grad_W, void* ws, size_t ws_bytes, void* stream, const LogprobTerm* lp = nullptr) {
+  kd_status st = lp ? check_logprob_args(H_bf16, W_bf16, lp->tokens, N, d, V, chunk, tau, ws, ws_bytes, true)
+                    : check_kl_args(H_bf16, W_bf16, t_ids, t_logits, N, d, V, K, chunk, tau, ws, ws_bytes);
   if (st != KD_OK) return st;
-  if (!lse || !grad_loss || !grad_H || !grad_W) return KD_ERR_INVALID_ARG;
-  if (!aligned(lse, 4) || !aligned(grad_loss, 4) || !aligned(grad_H, 16) || !aligned(grad_W, 16))
+  if (!lse || !grad_H || !grad_W) return KD_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(grad_H, 16) || !aligned(grad_W, 16)) return KD_ERR_INVALID_ARG;
+  if (!lp && (!grad_loss || !aligned(grad_loss, 4))) return KD_ERR_INVALID_ARG;
+  if (lp && (!lp->g_logp || !aligned(lp->g_logp, 4) || !aligned(lp->g_entropy, 4) || !aligned(lp->entropy_in, 4) ||
+             (lp->g_entropy && !lp->entropy_in)))
     return KD_ERR_INVALID_ARG;
   st = check_device();
   if (st != KD_OK) return st;
@@ -484,13 +536,14 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   if (d64 && !make_tmap_mn2_bf16(&tw_k2, W_bf16, uint64_t(d), uint64_t(V), uint64_t(d) * 2, BN / 2))
     return KD_ERR_CUDA;
 
-  cudaError_t e = launch_count_valid(mask, N, &ctrl->n_valid, s);
+  cudaError_t e = lp ? cudaSuccess : launch_count_valid(mask, N, &ctrl->n_valid, s);
   if (e != cudaSuccess) return KD_ERR_CUDA;
   const int grid_max = gemm_max_grid();
   for (int64_t c0 = 0; c0 < N; c0 += chunk) {
     const int n = int((N - c0) < chunk ? (N - c0) : chunk);
-    e = launch_teacher_prologue(t_ids + c0 * K, t_logits + c0 * K, n, K, V, inv_tau, ids_sorted, p_sorted, negent,
-                                &ctrl->err, c0, s);
+    if (!lp)
+      e = launch_teacher_prologue(t_ids + c0 * K, t_logits + c0 * K, n, K, V, inv_tau, ids_sorted, p_sorted, negent,
+                                  &ctrl->err, c0, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
     const uint16_t* Hc = H + c0 * d;
     if (!make_tmap_2d_bf16(&th_k, Hc, uint64_t(d), uint64_t(n), uint64_t(d) * 2, BK, BM)) return KD_ERR_CUDA;
@@ -518,7 +571,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     // B1: recompute the chunk's logits, dZ -> bf16 workspace
     GemmProblem p{};
     p.M = n; p.N = int(V); p.K = int(d);
-    p.a_mn = 0; p.b_mn = 0; p.epi = EPI_DZ;
+    p.a_mn = 0; p.b_mn = 0; p.epi = lp ? EPI_DZ_LP : EPI_DZ;
     p.m_tiles = (n + BM - 1) / BM;
     p.n_tiles = int((V + BN - 1) / BN);
     p.n_group = 1;
@@ -528,6 +581,12 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     p.ids_sorted = ids_sorted; p.p_sorted = p_sorted; p.Kt = K; p.inv_tau = inv_tau;
     p.lse = lse + c0; p.mask = mask ? mask + c0 : nullptr; p.grad_loss = grad_loss; p.n_valid = &ctrl->n_valid;
     p.dz = dz; p.ldz = L.ldz; p.rows = n; p.err = &ctrl->err;
+    if (lp) {
+      p.tokens = lp->tokens + c0;
+      p.g_logp = lp->g_logp + c0;
+      p.g_entropy = lp->g_entropy ? lp->g_entropy + c0 : nullptr;
+      p.entropy = lp->entropy_in ? lp->entropy_in + c0 : nullptr;
+    }
     p.a_k3d = p.b_k3d = p.cta_pair && d64;
     e = launch_gemm(p, p.a_k3d ? th_k2 : th_k,
                     p.b_k3d ? tw_k2 : (p.cta_pair ? tw_k_half : tw_k), tdz_st,
@@ -602,6 +661,35 @@ int kd_fused_kl_bwd(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
                     void* ws, size_t ws_bytes, void* stream) {
   return bwd_impl(H_bf16, W_bf16, t_ids, t_logits, mask, N, d, V, K, chunk, tau, lse, grad_loss, nullptr, grad_H,
                   grad_H_is_fp32, grad_W, ws, ws_bytes, stream);
+}
+
+size_t kd_fused_logprobs_workspace(int64_t N, int64_t d, int64_t V, int64_t chunk, int backward) {
+  if (N < 1 || d < 1 || V < 1 || chunk < 1) return 0;
+  return backward ? kl_layout(N, d, V, 1, chunk).total : logprob_fwd_ws(N, V, chunk);
+}
+
+int kd_fused_logprobs_fwd(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
+                          int64_t N, int64_t d, int64_t V, int64_t chunk, float tau, float* logp_out, float* lse_out,
+                          float* entropy_out, void* ws, size_t ws_bytes, void* stream) {
+  LogprobTerm lp{};
+  lp.tokens = tokens;
+  lp.logp = logp_out;
+  lp.entropy = entropy_out;
+  return fwd_impl(H_bf16, W_bf16, nullptr, nullptr, mask, N, d, V, 1, chunk, tau, nullptr, lse_out, nullptr, nullptr,
+                  0, ws, ws_bytes, stream, &lp);
+}
+
+int kd_fused_logprobs_bwd(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
+                          int64_t N, int64_t d, int64_t V, int64_t chunk, float tau, const float* lse,
+                          const float* entropy, const float* grad_logp, const float* grad_entropy, void* grad_H,
+                          int grad_H_is_fp32, float* grad_W, void* ws, size_t ws_bytes, void* stream) {
+  LogprobTerm lp{};
+  lp.tokens = tokens;
+  lp.g_logp = grad_logp;
+  lp.g_entropy = grad_entropy;
+  lp.entropy_in = entropy;
+  return bwd_impl(H_bf16, W_bf16, nullptr, nullptr, mask, N, d, V, 1, chunk, tau, lse, nullptr, nullptr, grad_H,
+                  grad_H_is_fp32, grad_W, ws, ws_bytes, stream, &lp);
 }
 
 int kd_chunked_kl_fwd(const void* H_bf16, const void* W_bf16, const int32_t* t_ids, const float* t_logits,

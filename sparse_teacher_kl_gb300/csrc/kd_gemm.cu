@@ -20,6 +20,9 @@
 //             - p on the cached ids), rounded to bf16 into a [rows, ldz] buffer.
 //   EPI_LSE_Z as EPI_LSE, and also writes the raw logits (bf16) out for a
 //             backward pass that does not recompute them (forward-chunked mode).
+//   EPI_LSE_H / EPI_DZ_LP  log probabilities of given tokens with the entropy, and their
+//             gradient: as EPI_LSE / EPI_DZ with one token per row in the teacher's place;
+//             the entropy takes one more sum, u = sum 2^t t, t the term's exponent.
 //   EPI_STORE / EPI_ACCUM  plain C = acc / C += acc for the gradient products.
 #include <math.h>
 #include <stdio.h>
@@ -75,7 +78,7 @@ __device__ __forceinline__ void unit_coords(const GemmProblem& p, int u, uint32_
                                             int& n_first, int& n_count, int& kb_lo, int& kb_hi, int& split) {
   const int k_blocks = ((p.K + BK - 1) / BK + kkb - 1) / kkb;
   const int m_groups = (p.m_tiles + p.cluster - 1) / p.cluster;
-  if (p.epi == EPI_LSE || p.epi == EPI_DZ || p.epi == EPI_LSE_Z) {
+  if (p.epi == EPI_LSE || p.epi == EPI_DZ || p.epi == EPI_LSE_Z || p.epi == EPI_LSE_H || p.epi == EPI_DZ_LP) {
     const int g = u / m_groups;
     m_blk = (u - g * m_groups) * p.cluster + int(crank);
     n_first = g * p.n_group;
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tmap_a);
     tma_prefetch_map(&tmap_b);
-    if (EPI == EPI_DZ || EPI == EPI_LSE_Z) tma_prefetch_map(&tmap_c);
+    if (EPI == EPI_DZ || EPI == EPI_LSE_Z || EPI == EPI_DZ_LP) tma_prefetch_map(&tmap_c);
   }
   if (warp == 1) {
     if (CG == 2) tmem_alloc_pair(&tail->tmem_base, TMEM_COLS); else tmem_alloc(&tail->tmem_base, TMEM_COLS);
@@ -331,7 +334,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       const int row = m_blk * BM + r_local;
 
       // Per-row state for the loss epilogues.
-      float run_m = -INFINITY, run_s = 0.f, run_g = 0.f;
+      float run_m = -INFINITY, run_s = 0.f, run_g = 0.f, run_u = 0.f;
+      float c0 = 0.f, c1 = 0.f;  // EPI_DZ_LP: dZ = p (c0 + c1 log2 p)
       int cur = 0;
       int nid = 0x7fffffff;
       float np_ = 0.f;
@@ -361,6 +365,24 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           const int nv = *p.n_valid;
           const bool valid = (p.mask == nullptr) || (p.mask[row] != 0);
           rowscale = (valid && nv > 0) ? (*p.grad_loss) * p.inv_tau / float(nv) : 0.f;
+        }
+      }
+
+      if (EPI == EPI_LSE_H || EPI == EPI_DZ_LP) {
+        // a padding row (its token is not looked at): no token, no gradient
+        const bool valid = row < p.rows && (p.mask == nullptr || p.mask[row] != 0);
+        if (valid) nid = __ldg(p.tokens + row);
+        if (nid < 0 || nid >= p.N) nid = 0x7fffffff;  // out of range: reported by the combine
+        if (EPI == EPI_DZ_LP) {
+          lse2 = 1e30f;  // p = 0
+          if (valid) {
+            lse2 = p.lse[row] * 1.4426950408889634f;
+            const float g = nid == 0x7fffffff ? 0.f : p.g_logp[row] * p.inv_tau;
+            const float h = p.g_entropy ? p.g_entropy[row] * p.inv_tau : 0.f;
+            np_ = g;
+            c0 = -g - (h != 0.f ? h * p.entropy[row] : 0.f);
+            c1 = -h * 0.69314718055994531f;
+          }
         }
       }
 
@@ -451,11 +473,54 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 }
               }
             }
-          } else if (EPI == EPI_DZ) {
+          } else if (EPI == EPI_LSE_H) {
+            if (row < p.rows && col0 < p.N) {
+              if (col0 + 32 > p.N) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (col0 + i >= p.N) x[i] = -1e30f;  // past the vocabulary: weight 0, exponent finite
+              }
+              float cm = x[0];
+#pragma unroll
+              for (int i = 1; i < 32; ++i) cm = fmaxf(cm, x[i]);
+              if (cm > run_m) {
+                const float t = fmaxf((run_m - cm) * scale2, -200.f);  // 2^-200 is 0
+                const float f = ex2_approx(t);
+                run_u = fmaf(t, run_s, run_u) * f;
+                run_s *= f;
+                run_m = cm;
+              }
+              const float off = -run_m * scale2;
+              float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float t0 = fmaf(x[i], scale2, off), t1 = fmaf(x[i + 1], scale2, off);
+                const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+                s0 += e0;
+                s1 += e1;
+                u0 = fmaf(e0, t0, u0);
+                u1 = fmaf(e1, t1, u1);
+              }
+              run_s += s0 + s1;
+              run_u += u0 + u1;
+              if (uint32_t(nid - col0) < 32u) run_g = select32(x, uint32_t(nid - col0));
+            }
+          } else if (EPI == EPI_DZ || EPI == EPI_DZ_LP) {
             float q[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) q[i] = 0.f;
-            if (row < p.rows) {
+            if (EPI == EPI_DZ_LP) {
+              if (row < p.rows) {
+                const int off = nid - col0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float t = fmaf(x[i], scale2, -lse2);
+                  q[i] = ex2_approx(t) * fmaf(c1, t, c0);
+                  q[i] = (i == off) ? q[i] + np_ : q[i];
+                  if (col0 + i >= p.N) q[i] = 0.f;
+                }
+              }
+            } else if (row < p.rows) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) q[i] = ex2_approx(fmaf(x[i], scale2, -lse2));
               while (nid < col0 + 32) {
@@ -476,6 +541,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                   if (col0 + i >= p.N) q[i] = 0.f;
               }
             }
+            const float qs = EPI == EPI_DZ_LP ? 1.f : rowscale;
             // Stage bf16 dZ for this warp's 32 rows: two 32-column chunks fill one 32 x 64
             // box (128-byte rows, 128-byte swizzle), written out by one TMA store that clips
             // rows past the chunk and columns past the vocabulary.
@@ -487,10 +553,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
             for (int g8 = 0; g8 < 4; ++g8) {
               uint4 v;
-              v.x = pack_bf16x2(q[g8 * 8 + 0] * rowscale, q[g8 * 8 + 1] * rowscale);
-              v.y = pack_bf16x2(q[g8 * 8 + 2] * rowscale, q[g8 * 8 + 3] * rowscale);
-              v.z = pack_bf16x2(q[g8 * 8 + 4] * rowscale, q[g8 * 8 + 5] * rowscale);
-              v.w = pack_bf16x2(q[g8 * 8 + 6] * rowscale, q[g8 * 8 + 7] * rowscale);
+              v.x = pack_bf16x2(q[g8 * 8 + 0] * qs, q[g8 * 8 + 1] * qs);
+              v.y = pack_bf16x2(q[g8 * 8 + 2] * qs, q[g8 * 8 + 3] * qs);
+              v.z = pack_bf16x2(q[g8 * 8 + 4] * qs, q[g8 * 8 + 5] * qs);
+              v.w = pack_bf16x2(q[g8 * 8 + 6] * qs, q[g8 * 8 + 7] * qs);
               const uint32_t j = uint32_t((c & 1) * 4 + g8);
               *reinterpret_cast<uint4*>(box + lane * 128u + ((j ^ (lane & 7u)) * 16u)) = v;
             }
@@ -644,8 +710,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         p.partials[size_t(g) * (p.m_tiles * BM) + row] =
             make_float4(run_m * scale2, run_s, run_g * p.inv_tau, 0.f);
       }
+      if (EPI == EPI_LSE_H && ok && row < p.rows)
+        p.partials[size_t(n_first / p.n_group) * (p.m_tiles * BM) + row] =
+            make_float4(run_m * scale2, run_s, run_g * p.inv_tau, run_u);
     }
-    if ((EPI == EPI_DZ || EPI == EPI_LSE_Z || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
+    if ((EPI == EPI_DZ || EPI == EPI_DZ_LP || EPI == EPI_LSE_Z || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
       bulk_wait_all();  // output boxes done before exit
   }
 
@@ -739,6 +808,8 @@ static const char* gemm_name(int epi, int a_mn, int b_mn) {
     case EPI_LSE: return "kd_proj_lse_fwd";
     case EPI_LSE_Z: return "kd_proj_lse_z_fwd";
     case EPI_DZ: return "kd_proj_dz_bwd";
+    case EPI_LSE_H: return "kd_proj_logprob_fwd";
+    case EPI_DZ_LP: return "kd_proj_logprob_bwd";
     case EPI_STORE: return (a_mn == 0 && b_mn == 1) ? "kd_gemm_dz_w" : "kd_gemm_store";
     default: return (a_mn == 1 && b_mn == 1) ? "kd_gemm_dzT_h" : "kd_gemm_accum";
   }
@@ -758,6 +829,8 @@ cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUten
       case EPI_LSE: e = two ? launch_one<EPI_LSE, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_LSE_Z: e = two ? launch_one<EPI_LSE_Z, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_DZ: e = two ? launch_one<EPI_DZ, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
+      case EPI_LSE_H: e = two ? launch_one<EPI_LSE_H, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
+      case EPI_DZ_LP: e = two ? launch_one<EPI_DZ_LP, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_STORE:
         e = two ? launch_one<EPI_STORE, 2, 2>(p, ta, tb, tc, grid, s) : launch_one<EPI_STORE, 2, 1>(p, ta, tb, tc, grid, s);
         break;
@@ -770,6 +843,8 @@ cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUten
       case EPI_LSE: e = launch_one<EPI_LSE, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_LSE_Z: e = launch_one<EPI_LSE_Z, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_DZ: e = launch_one<EPI_DZ, 1>(p, ta, tb, tc, grid, s); break;
+      case EPI_LSE_H: e = launch_one<EPI_LSE_H, 1>(p, ta, tb, tc, grid, s); break;
+      case EPI_DZ_LP: e = launch_one<EPI_DZ_LP, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_STORE: e = launch_one<EPI_STORE, 1>(p, ta, tb, tc, grid, s); break;
       default: e = launch_one<EPI_ACCUM, 1>(p, ta, tb, tc, grid, s); break;
     }

@@ -53,6 +53,8 @@ enum EpiKind : int {
   EPI_STORE = 2,  // C = acc -> fp32 or bf16
   EPI_ACCUM = 3,  // C += acc (fp32)
   EPI_LSE_Z = 4,  // forward-chunked: EPI_LSE plus the raw logits z -> bf16, blocked [V/64][N][64]
+  EPI_LSE_H = 5,  // log probabilities: online logsumexp and entropy sum, the token's logit -> partials
+  EPI_DZ_LP = 6,  // their gradient: dZ = p (c0 + c1 log2 p) + [v = token] g / tau -> bf16, blocked
 };
 
 // 64-deep k-blocks per ring stage of a CTA-pair launch: two when both operands are
@@ -118,7 +120,13 @@ struct GemmProblem {
   const float* p_sorted;      // [rows, K] teacher probabilities matching ids_sorted
   int Kt;                     // teacher K
   float inv_tau;
-  float4* partials;           // EPI_LSE: [n_units_per_row, rows] (m2, s, G, 0)
+  float4* partials;           // EPI_LSE: [n_units_per_row, rows] (m2, s, G, 0); EPI_LSE_H: (m2, s, z_token, u)
+  // EPI_LSE_H / EPI_DZ_LP (chunk-relative): the given token of each row; the gradients that
+  // reach its log probability and (NULL: none) the entropy
+  const int32_t* tokens;
+  const float* g_logp;
+  const float* g_entropy;
+  const float* entropy;
   const float* lse;           // EPI_DZ: [rows] natural-log lse (chunk-relative pointer)
   const uint8_t* mask;        // EPI_DZ: [rows] or null (chunk-relative pointer)
   const float* grad_loss;     // EPI_DZ: device scalar
@@ -199,6 +207,10 @@ cudaError_t launch_teacher_prologue(const int32_t* ids, const float* tlog, int r
                                     uint32_t* err, int64_t row0, cudaStream_t s);
 cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int rows, const float* negent,
                                float inv_tau, float* lse_out, float* kl_out, cudaStream_t s);
+// Log probability, logsumexp and entropy (NULL: not wanted) of each row from EPI_LSE_H's partials.
+cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, int rows, int64_t V,
+                                   const int32_t* tokens, const uint8_t* mask, float* logp, float* lse,
+                                   float* entropy, uint32_t* err, int64_t row0, cudaStream_t s);
 cudaError_t launch_loss_reduce(const float* kl, const uint8_t* mask, int64_t N, const int32_t* n_valid,
                                float* loss_out, cudaStream_t s);
 

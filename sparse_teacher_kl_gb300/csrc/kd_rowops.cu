@@ -228,6 +228,70 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
   return cudaGetLastError();
 }
 
+// --------------------------------------------------- logprob combine ---
+// Merge the per-unit (max, s, z_token, u) partials of a position, s = sum 2^t and u = sum 2^t t
+// with t = (z / tau) log2 e - max:
+//   lse = ln 2 (M + log2 s),  logp = z_token / tau - lse,  entropy = ln 2 (log2 s - u / s)
+// Block shape as in the lse combine.
+
+__global__ void __launch_bounds__(LC_ROWS * LC_PHASES)
+    kd_logprob_combine_kernel(const float4* __restrict__ partials, int n_units, int rows, int rows_pad, int64_t V,
+                              const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask,
+                              float* __restrict__ logp, float* __restrict__ lse_out, float* __restrict__ entropy,
+                              uint32_t* __restrict__ err, int64_t row0) {
+  __shared__ float4 sm[LC_PHASES][LC_ROWS];
+  const int x = threadIdx.x, y = threadIdx.y;
+  const int r = blockIdx.x * LC_ROWS + x;
+  float M = -INFINITY, S = 0.f, G = 0.f, U = 0.f;
+  auto fold = [&](const float4& q) {
+    G += q.z;
+    if (q.x > M) {
+      const float t = fmaxf(M - q.x, -200.f), f = exp2f(t);  // 2^-200 is 0 in fp32
+      U = fmaf(t, S, U) * f + q.w;
+      S = S * f + q.y;
+      M = q.x;
+    } else {
+      const float t = fmaxf(q.x - M, -200.f), f = exp2f(t);
+      U += fmaf(t, q.y, q.w) * f;
+      S += q.y * f;
+    }
+  };
+  if (r < rows) {
+#pragma unroll 4
+    for (int u = y; u < n_units; u += LC_PHASES) fold(partials[size_t(u) * rows_pad + r]);
+  }
+  sm[y][x] = make_float4(M, S, G, U);
+  __syncthreads();
+  if (y == 0 && r < rows) {
+    const int units = n_units < LC_PHASES ? n_units : LC_PHASES;
+    for (int k = 1; k < units; ++k) fold(sm[k][x]);
+    if (mask && mask[r] == 0) {
+      logp[r] = 0.f;
+      lse_out[r] = 0.f;
+      if (entropy) entropy[r] = 0.f;
+      return;
+    }
+    const float l2s = log2f(S), lse = (M + l2s) * 0.69314718055994531f;
+    const int32_t id = tokens[r];
+    const bool bad = id < 0 || int64_t(id) >= V;
+    if (bad) raise_error(err, KD_DEVERR_BAD_ID, uint32_t(row0 + r));
+    logp[r] = bad ? __int_as_float(0x7FC00000) : G - lse;
+    lse_out[r] = lse;
+    if (entropy) entropy[r] = (l2s - U / S) * 0.69314718055994531f;
+  }
+}
+
+cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, int rows, int64_t V,
+                                   const int32_t* tokens, const uint8_t* mask, float* logp, float* lse,
+                                   float* entropy, uint32_t* err, int64_t row0, cudaStream_t s) {
+  const int rows_pad = ((rows + BM - 1) / BM) * BM;
+  prof_before("kd_logprob_combine", s);
+  kd_logprob_combine_kernel<<<(rows + LC_ROWS - 1) / LC_ROWS, dim3(LC_ROWS, LC_PHASES), 0, s>>>(
+      partials, n_units_per_row, rows, rows_pad, V, tokens, mask, logp, lse, entropy, err, row0);
+  prof_after(s);
+  return cudaGetLastError();
+}
+
 // ------------------------------------------------------- loss reduce ---
 // loss = sum over valid positions of KL_t / N_valid, 0 if none ([ART] drop-in
 // KL term; the token mean with a padding mask).  One block, fixed summation

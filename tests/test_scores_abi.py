@@ -99,3 +99,33 @@ def test_wrappers_refuse_wrong_tensors():
         kd.logits_kl_forward(z, tok[:, None], z[:, :1])
     with pytest.raises(ValueError):
         kd.logits_kl_step(z.double(), tok[:, None], z[:, :1])
+
+
+def _fused(lib, backward, **kw):
+    a = dict(H=P, W=P, tok=P, mask=None, N=256, d=64, V=1000, chunk=128, tau=1.0, logp=P, lse=P, ent=P, gl=P, ge=P,
+             gH=P, f32=0, gW=P, ws=P, wsb=1 << 30)
+    a.update(kw)
+    head = (a["H"], a["W"], a["tok"], a["mask"], a["N"], a["d"], a["V"], a["chunk"], a["tau"])
+    if backward:
+        return lib.kd_fused_logprobs_bwd(*head, a["lse"], a["ent"], a["gl"], a["ge"], a["gH"], a["f32"], a["gW"],
+                                         a["ws"], a["wsb"], None)
+    return lib.kd_fused_logprobs_fwd(*head, a["logp"], a["lse"], a["ent"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("backward,kw", [(b, k) for b in (False, True) for k in (
+    dict(N=0), dict(d=0), dict(d=60), dict(V=0), dict(chunk=100), dict(chunk=0), dict(tau=0.0), dict(tau=float("nan")),
+    dict(H=None), dict(W=None), dict(H=P + 8), dict(tok=None), dict(tok=P + 1), dict(lse=None), dict(lse=P + 2))]
+    + [(False, k) for k in (dict(logp=None), dict(logp=P + 1), dict(ent=P + 2))]
+    + [(True, k) for k in (dict(gl=None), dict(ent=None), dict(gH=None), dict(gW=None), dict(gH=P + 4), dict(gW=P + 8),
+                           dict(ge=P + 2))])
+def test_fused_logprobs_refuse(lib, backward, kw):
+    assert _fused(lib, backward, **kw) == _abi.KD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_fused_logprobs_refuse_a_bad_workspace(lib, backward):
+    need = lib.kd_fused_logprobs_workspace(256, 64, 1000, 128, int(backward))
+    assert _fused(lib, backward, wsb=need - 1) == _abi.KD_ERR_WORKSPACE
+    assert _fused(lib, backward, ws=None) == _abi.KD_ERR_WORKSPACE
+    assert _fused(lib, backward, ws=P + 64) == _abi.KD_ERR_WORKSPACE
+    assert lib.kd_fused_logprobs_workspace(0, 64, 1000, 128, 1) == 0
