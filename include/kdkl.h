@@ -258,6 +258,10 @@ KD_API int kd_fused_kl_fwd_static(const void* H_bf16, const void* W_bf16,
                     int64_t N, int64_t d, int64_t V, int K, int64_t chunk, float tau,
                     float* loss_out, float* lse_out, float* kl_per_token_out, void* stream);
 
+/* Clears the control block (error word included) of a new workspace: one asynchronous
+ * memset of its first 256 bytes.  A workspace of zeroed memory needs no call. */
+KD_API int kd_workspace_clear(void* ws, size_t ws_bytes, void* stream);
+
 /*
  * Reads (synchronising `stream`) and clears the device error word of a
  * workspace used by the calls above; ws == NULL names the scratch array of
@@ -348,8 +352,8 @@ KD_API size_t kd_logits_kl_workspace(int64_t N, int64_t V, int K);
  *   stats_out: [N, 4] fp32, the row statistics that the backward pass takes: the largest
  *              logit and sum exp((logit - largest) / tau) over the row, then over the ids
  *              outside S (with t_lse; -inf and 0 without).
- * KD_ERR_UNSUPPORTED when a row's bitmap of S and its K entries exceed the shared memory
- * of an SM (V over about 1.4 million, 0.7 million for fp32).
+ * KD_ERR_UNSUPPORTED when the bitmap of S and the K entries of two rows do not fit into the
+ * shared memory of an SM (V over about 0.7 million, 0.35 million for fp32).
  */
 KD_API int kd_logits_kl_fwd(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
                     const int32_t* t_ids, const float* t_logits, int K, const float* t_lse, const uint8_t* mask,

@@ -48,6 +48,7 @@ __all__ = [
     "KD_MAX_K",
     "KD_MAX_TOP",
     "workspace",
+    "control_block",
 ]
 
 
@@ -56,7 +57,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle of the current stream, without a Stream object around it (2 us less per call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -255,12 +257,23 @@ def _grad_like(z: torch.Tensor, grad: Optional[torch.Tensor]):
 def _fresh_ws(nbytes: int, device) -> torch.Tensor:
     """A workspace with its control block zeroed and the rest left as it is (the allocator's blocks are aligned)."""
     ws = torch.empty((int(nbytes),), dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+    _abi.check(_abi.kd_workspace_clear(ws.data_ptr(), ws.numel(), _stream(device)), "kd_workspace_clear")
     return ws
 
 
-def _ws(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
-    return _fresh_ws(nbytes, device) if ws is None else ws
+_control = {}  # device index -> control block
+
+
+def control_block(device) -> torch.Tensor:
+    """The control block that token_logprobs calls without a workspace share on a device: its only content is the
+    error word, which ``device_error(control_block(device))`` reads."""
+    ws = _control.get(device.index)
+    if ws is None:
+        ws = _fresh_ws(256, device)
+        if not torch.cuda.is_current_stream_capturing():  # memory of a capture belongs to its graph
+            torch.cuda.current_stream(device).synchronize()  # cleared before another stream uses it
+            _control[device.index] = ws
+    return ws
 
 
 class TokenLogprobs(NamedTuple):
@@ -287,7 +300,8 @@ def token_logprobs_forward(logits, tokens, mask=None, tau=1.0, top=0, entropy=Fa
     ent = torch.empty((N,), **f32) if entropy else None
     top_ids = torch.empty((N, top), dtype=torch.int32, device=dev) if top else None
     top_logp = torch.empty((N, top), **f32) if top else None
-    ws = _ws(ws, _abi.kd_token_logprobs_workspace(N, V), dev)
+    if ws is None:
+        ws = control_block(dev)
     st = _abi.kd_token_logprobs_fwd(_ptr(logits), dt, N, V, ld, _ptr(tokens), M, _ptr(mask), float(tau), int(top),
                                     _ptr(logp), _ptr(lse), _ptr(ent), _ptr(top_ids), _ptr(top_logp), _ptr(ws),
                                     ws.numel(), _stream(dev))
@@ -308,7 +322,8 @@ def token_logprobs_backward(logits, tokens, lse, grad_logp, mask=None, tau=1.0, 
         _check(t, name, torch.float32, (N,), dev)
     _check(mask, "mask", torch.uint8, (N,), dev)
     grad_logits, ldg = _grad_like(logits, grad_logits)
-    ws = _ws(ws, _abi.kd_token_logprobs_workspace(N, V), dev)
+    if ws is None:
+        ws = control_block(dev)
     st = _abi.kd_token_logprobs_bwd(_ptr(logits), dt, N, V, ld, _ptr(tokens), M, _ptr(mask), float(tau), _ptr(lse),
                                     _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_logits), ldg,
                                     _ptr(ws), ws.numel(), _stream(dev))
@@ -363,7 +378,8 @@ def logits_kl_forward(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, ws=None
     """kd_logits_kl_fwd: KL of the cached teacher (``ids`` int32, ``tlog`` fp32 [N, K]; with ``t_lse`` its mass
     outside the cache as one more class) against softmax(logits / tau): (loss [1], stats [N, 4], ws)."""
     dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse, kl_out)
-    ws = _ws(ws, _abi.kd_logits_kl_workspace(N, V, K), dev)
+    if ws is None:
+        ws = _fresh_ws(_abi.kd_logits_kl_workspace(N, V, K), dev)
     loss = torch.empty((1,), dtype=torch.float32, device=dev)
     stats = torch.empty((N, 4), dtype=torch.float32, device=dev)
     st = _abi.kd_logits_kl_fwd(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
@@ -378,7 +394,8 @@ def logits_kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau=1.0, t_lse
     _check(stats, "stats", torch.float32, (N, 4), dev)
     _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
     grad_logits, ldg = _grad_like(logits, grad_logits)
-    ws = _ws(ws, _abi.kd_logits_kl_workspace(N, V, K), dev)
+    if ws is None:  # not returned: nobody reads its error word
+        ws = torch.empty((_abi.kd_logits_kl_workspace(N, V, K),), dtype=torch.uint8, device=dev)
     st = _abi.kd_logits_kl_bwd(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
                                float(tau), _ptr(stats), _ptr(grad_loss), _ptr(grad_logits), ldg, _ptr(ws), ws.numel(),
                                _stream(dev))
@@ -395,7 +412,8 @@ def logits_kl_step(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=
         grad_loss = torch.ones((1,), dtype=torch.float32, device=dev)
     _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
     grad_logits, ldg = _grad_like(logits, grad_logits)
-    ws = _ws(ws, _abi.kd_logits_kl_workspace(N, V, K), dev)
+    if ws is None:  # not returned: nobody reads its error word
+        ws = torch.empty((_abi.kd_logits_kl_workspace(N, V, K),), dtype=torch.uint8, device=dev)
     loss = torch.empty((1,), dtype=torch.float32, device=dev)
     st = _abi.kd_logits_kl_step(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
                                 float(tau), _ptr(grad_loss), _ptr(loss), _ptr(kl_out), _ptr(grad_logits), ldg,

@@ -76,6 +76,7 @@ _SIGNATURES = {
     "kd_fused_logprobs_bwd": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_float,
                                        _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_size,
                                        _c_ptr]),
+    "kd_workspace_clear": (_c_int, [_c_ptr, _c_size, _c_ptr]),
     "kd_get_device_error": (_c_int, [_c_ptr, _c_ptr, ctypes.POINTER(_c_i64)]),
     "kd_gemm_bf16": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_ptr, _c_size,
                               _c_ptr]),
@@ -167,6 +168,7 @@ kd_logits_kl_step = _wrap("kd_logits_kl_step")
 kd_fused_logprobs_workspace = _wrap("kd_fused_logprobs_workspace")
 kd_fused_logprobs_fwd = _wrap("kd_fused_logprobs_fwd")
 kd_fused_logprobs_bwd = _wrap("kd_fused_logprobs_bwd")
+kd_workspace_clear = _wrap("kd_workspace_clear")
 kd_get_device_error = _wrap("kd_get_device_error")
 kd_gemm_bf16 = _wrap("kd_gemm_bf16")
 kd_gemm_workspace = _wrap("kd_gemm_workspace")

@@ -13,16 +13,22 @@
 
 namespace kd {
 
-constexpr int LP_THREADS = 512;
-constexpr int LP_SLOTS = 16;      // group maxima kept per thread
-constexpr int LP_CAND = 1024;     // candidates for the top alternatives
+constexpr int LP_THREADS = 256;      // forward
+constexpr int LP_WARPS = LP_THREADS / 32;
+constexpr int LP_SLOTS = 32;         // group maxima kept per thread
+constexpr int LP_CAND = 1024;        // candidates for the top alternatives
+constexpr int LP_LIST = 512;         // groups that may hold one
+constexpr int LP_MAX_CLUSTER = 16;
+constexpr int LB_THREADS = 512;      // backward
 
 // ------------------------------------------------------------ alternatives ---
 // The n largest elements of a row, exactly, without selecting while it streams by.  While the
 // row is read each thread keeps the largest element of every group of vectors it reads (it
-// needs those maxima for the softmax anyway) and its largest of all.  At least n elements
-// reach the n-th largest of the threads' maxima, T, so the n largest elements all reach T, and
-// they lie in the few groups whose maximum reaches T: those groups alone are read again.
+// needs those maxima for the softmax anyway) and its largest of all, m.  In each of w warps
+// the ceil(n / w)-th largest m is reached by that many elements, so the smallest of the w,
+// the floor, is reached by at least n: the n largest elements all reach it, and they lie in
+// the few groups whose maximum does.  Those groups alone are read again, each vector by a
+// thread of its own, so that their latency is paid once.
 // Each element's rank key is unique, (value, ~id), so the order is the id's on ties, and a
 // candidate's place is the number of candidates above it.  When ties or a crowded row bring
 // more candidates than the buffer holds, the row is counted and collected directly.
@@ -30,44 +36,23 @@ constexpr int LP_CAND = 1024;     // candidates for the top alternatives
 struct TopState {
   unsigned long long cand[LP_CAND];
   int count;
-  uint32_t floor;   // key that at least n elements reach
+  int groups;              // of this CTA
+  uint32_t list[LP_LIST];  // slot * LP_THREADS + thread
 };
 
 __device__ __forceinline__ unsigned long long rank_key(float x, int64_t col) {
   return (static_cast<unsigned long long>(order_key(x)) << 32) | uint32_t(~uint32_t(col));
 }
 
-// Warp 0: a key that at least n of the THREADS values reach (n <= THREADS), and few more.
-template <int THREADS>
-__device__ __forceinline__ uint32_t warp_floor(const float* vals, int n) {
-  constexpr int E = THREADS / 32;
-  const int lane = threadIdx.x & 31;
-  uint32_t key[E], lo = 0xFFFFFFFFu, hi = 0;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    key[i] = order_key(vals[i * 32 + lane]);
-    lo = min(lo, key[i]);
-    hi = max(hi, key[i]);
+// Key of the n-th largest (n <= 32) of the lanes' values.
+__device__ __forceinline__ uint32_t warp_nth_key(float x, int n) {
+  uint32_t key = order_key(x), top = 0;
+  for (int i = 0; i < n; ++i) {
+    top = __reduce_max_sync(0xffffffffu, key);
+    const uint32_t who = __ballot_sync(0xffffffffu, key == top);
+    if ((threadIdx.x & 31) == uint32_t(__ffs(who) - 1)) key = 0;  // one of them is taken out
   }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lo == hi) return lo;
-  ++hi;  // no value reaches hi; all reach lo
-  const int enough = n + (n >> 2) + 4;
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + ((hi - lo) >> 1);
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < E; ++i) c += key[i] >= mid;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (c >= n) {
-      lo = mid;
-      if (c <= enough) break;
-    } else {
-      hi = mid;
-    }
-  }
-  return lo;
+  return top;
 }
 
 // All threads: visit(column, value) for every element of vectors [lo, hi) of the row.
@@ -96,11 +81,12 @@ __device__ int count_reaching(const Row<DT>& row, int lo, int hi, uint32_t key, 
   return *sh;
 }
 
-// The n largest of vectors [lo, hi) when more than LP_CAND elements reach the floor: elements
-// above a key T that fewer than n elements exceed, then the first ones equal to T by column.
+// The n largest of vectors [lo, hi) when more than LP_CAND elements reach the floor (a key that
+// at least n elements reach): the elements above a key T that fewer than n elements exceed, then
+// the first ones equal to T by column.
 template <int DT>
-__device__ void collect_crowded(const Row<DT>& row, int lo, int hi, int n, TopState& ts, int* sh) {
-  uint32_t T = ts.floor;
+__device__ void collect_crowded(const Row<DT>& row, int lo, int hi, int n, uint32_t floor, TopState& ts, int* sh) {
+  uint32_t T = floor;  // the same in every thread, and so are the counts: all take the same branches
   if (count_reaching<DT>(row, lo, hi, T + 1, sh) >= n) {
     uint32_t a = T, b = 0xFFFFFFFFu;  // count(a) >= n; nothing reaches b
     while (b - a > 1) {
@@ -152,7 +138,7 @@ __device__ void collect_crowded(const Row<DT>& row, int lo, int hi, int n, TopSt
 struct LogprobArgs {
   const void* z;
   int64_t N, ld;
-  int V, M, top, dtype;
+  int V, M, top;
   const int32_t* tokens;
   const uint8_t* mask;
   float tau, k;  // k = log2(e) / tau
@@ -162,16 +148,28 @@ struct LogprobArgs {
   uint32_t* err;
 };
 
-// One block per row.
+struct LpShared {
+  RowStats warp[LP_WARPS];
+  uint32_t nth[LP_WARPS];
+  // written by the CTAs of the row's cluster (each its own entry)
+  RowStats part[LP_MAX_CLUSTER];
+  uint32_t floor[LP_MAX_CLUSTER];
+  int scratch[32];
+};
+
+// One cluster per row (a single CTA where there are rows enough to fill the GPU): each CTA
+// streams its share of the row's vectors; the first one puts the results together.
 template <int DT, bool ENT, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS) kd_logprobs_fwd_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(LP_THREADS, 4) kd_logprobs_fwd_kernel(const LogprobArgs a) {
   extern __shared__ __align__(16) uint8_t lp_smem[];
-  __shared__ RowStats sh_stats[32];
-  __shared__ float sh_max[LP_THREADS];
-  __shared__ int sh_int[32];
-  const int64_t r = blockIdx.x;
+  __shared__ LpShared sh;
+  __shared__ TopState ts;
+  constexpr int VE = Elt<DT>::kVec;
+  const uint32_t ctas = cluster_size(), rank = cluster_ctarank();
+  const int64_t r = blockIdx.x / ctas;
   const int tid = int(threadIdx.x);
-  if (a.mask && a.mask[r] == 0) {
+  if (a.mask && a.mask[r] == 0) {  // the whole cluster leaves
+    if (rank != 0) return;
     for (int j = tid; j < a.M; j += LP_THREADS) a.logp[r * a.M + j] = 0.f;
     if (TOP)
       for (int j = tid; j < a.top; j += LP_THREADS) {
@@ -185,127 +183,224 @@ __global__ void __launch_bounds__(LP_THREADS) kd_logprobs_fwd_kernel(const Logpr
     return;
   }
   const Row<DT> row(static_cast<const typename Elt<DT>::raw*>(a.z) + r * a.ld, a.V);
+  const int share = (row.nv + int(ctas) - 1) / int(ctas);
+  const int lo = min(int(rank) * share, row.nv), hi = min(lo + share, row.nv);
+  if (TOP && tid == 0) ts.count = ts.groups = 0;
+  __syncwarp();
+  if (ctas > 1) cluster_arrive();  // waited for before the first access to another CTA
 
-  float* gmax_sh = reinterpret_cast<float*>(lp_smem);  // [slots][LP_THREADS]
-  const int per_round = ROW_GROUP * LP_THREADS;
-  const int rounds = (row.nv + per_round - 1) / per_round;
-  const int merge = (rounds + LP_SLOTS - 1) / LP_SLOTS;  // rounds that share a slot
-  RowStats st;
-  float slot_max = -INFINITY;
-  for (int it = 0; it < rounds; ++it) {
-    uint4 v[ROW_GROUP];
-    row.load_group(v, it * per_round + tid, LP_THREADS, row.nv);
-    const float g = group_max<DT>(v);
-    if (TOP) {
-      slot_max = fmaxf(slot_max, g);
-      if ((it + 1) % merge == 0 || it + 1 == rounds) {
-        gmax_sh[(it / merge) * LP_THREADS + tid] = slot_max;
-        slot_max = -INFINITY;
+  // the first CTA's given tokens: their logits are on their way while the row streams by
+  int32_t id = 0;
+  float z_id = 0.f;
+  auto token = [&](int j) {
+    id = a.tokens[r * a.M + j];
+    if (id >= 0 && id < a.V) z_id = row.at(id);
+  };
+  if (rank == 0 && tid < a.M) token(tid);
+
+  float* slot_max = reinterpret_cast<float*>(lp_smem);  // [slots][LP_THREADS]
+  const int body_lo = max(lo, row.full_lo), body_hi = max(body_lo, min(hi, row.full_hi));
+  constexpr int STEP = ROW_GROUP * LP_THREADS;
+  const int rounds = (body_hi - body_lo + STEP - 1) / STEP;
+  int shift = 0;  // 2^shift rounds share a slot
+  while (((rounds - 1) >> shift) >= LP_SLOTS) ++shift;
+  RowStats st = stats_empty();
+  float running = -INFINITY;
+  stream_stats<DT, ENT, LP_THREADS>(
+      row, lo, hi, a.k, st, LoadOnce(), [](uint4&, int) {},
+      [&](int round, float g) {
+        if (!TOP) return;
+        running = fmaxf(running, g);  // a NaN leaves it: such a row has no order
+        slot_max[(round >> shift) * LP_THREADS + tid] = running;
+        if (((round + 1) & ((1 << shift) - 1)) == 0) running = -INFINITY;
+      });
+  const float own_max = st.m;
+
+  // ---- the block's statistics and floor
+  stats_block_put<ENT>(st, a.k, sh.warp);
+  const int full_warps = min(LP_WARPS, (body_hi - body_lo) / 32);  // every lane has a vector
+  const int nth = full_warps ? (a.top + full_warps - 1) / full_warps : 33;
+  if (TOP && nth <= 32 && tid / 32 < full_warps) {
+    const uint32_t key = warp_nth_key(own_max, nth);
+    if ((tid & 31) == 0) sh.nth[tid / 32] = key;
+  }
+  __syncthreads();
+  st = stats_block_get<LP_THREADS, ENT>(a.k, sh.warp);
+  uint32_t floor = 0;  // reached by everything
+  if (TOP && nth <= 32) {
+    floor = 0xFFFFFFFFu;
+    for (int w = 0; w < full_warps; ++w) floor = min(floor, sh.nth[w]);
+  }
+
+  // ---- the row's
+  if (ctas > 1) {
+    cluster_wait();
+    if (tid < int(ctas)) {
+      LpShared* other = cluster_map(&sh, uint32_t(tid));
+      if (TOP || tid == 0) {
+        other->part[rank] = st;
+        other->floor[rank] = floor;
       }
     }
-    stats_add<DT, ENT>(st, v, g, a.k);
-  }
-  if (TOP) sh_max[tid] = st.m;
-  st = stats_block<LP_THREADS>(st, a.k, sh_stats);
-  const float ln_s = st.s > 0.f ? logf(st.s) : st.s;  // s = 0: every logit is -inf; NaN stays
-  const bool empty = st.s == 0.f;
-
-  for (int j = tid; j < a.M; j += LP_THREADS) {
-    const int32_t id = a.tokens[r * a.M + j];
-    float lp;
-    if (id < 0 || id >= a.V) {
-      raise_error(a.err, KD_DEVERR_BAD_ID, uint32_t(r));
-      lp = __int_as_float(0x7FC00000);
+    cluster_sync();
+    if (!TOP && rank != 0) return;
+    st = stats_empty();
+    const int lane = tid & (LP_MAX_CLUSTER - 1);
+    if (lane < int(ctas)) {
+      st = sh.part[lane];
+      floor = sh.floor[lane];
     } else {
-      lp = empty ? -INFINITY : (row.at(id) - st.m) / a.tau - ln_s;
+      floor = 0;
     }
-    a.logp[r * a.M + j] = lp;
+    stats_warp<ENT>(st, a.k, LP_MAX_CLUSTER);
+    if (TOP) floor = __reduce_max_sync(0xffffffffu, floor);  // each CTA's holds for the whole row
   }
-  if (tid == 0) {
-    a.lse[r] = empty ? -INFINITY : st.m / a.tau + ln_s;
-    if (ENT) a.entropy[r] = empty ? 0.f : ln_s - kLn2 * (st.u / st.s);
+  const bool empty = st.s == 0.f;  // every logit is -inf
+  const bool odd = st.s != st.s;   // a NaN or +inf logit
+  const float log2_s = odd ? st.s : log2f(st.s);
+  auto logp_of = [&](float x) { return empty ? -INFINITY : stats_logp(x, st.m, log2_s, a.k, a.tau); };
+  if (rank == 0) {
+    for (int j = tid; j < a.M; j += LP_THREADS) {
+      if (j != tid) token(j);
+      float lp;
+      if (id < 0 || id >= a.V) {
+        raise_error(a.err, KD_DEVERR_BAD_ID, uint32_t(r));
+        lp = __int_as_float(0x7FC00000);
+      } else {
+        lp = logp_of(z_id);
+      }
+      a.logp[r * a.M + j] = lp;
+    }
+    if (tid == 0) {
+      const float big = fabsf(st.m) <= kPlainMax ? kLn2 * (__fmul_rn(st.m, a.k) + log2_s) : st.m / a.tau + kLn2 * log2_s;
+      a.lse[r] = empty ? -INFINITY : big;
+      if (ENT) a.entropy[r] = empty ? 0.f : kLn2 * (log2_s - st.u / st.s);
+    }
   }
   if (!TOP) return;
 
-  if (st.s != st.s) {  // a NaN or +inf logit: no order to report
-    for (int j = tid; j < a.top; j += LP_THREADS) {
-      a.top_ids[r * a.top + j] = j;
-      a.top_logp[r * a.top + j] = st.s;
-    }
-    return;
-  }
-  __shared__ TopState ts;
-  if (tid < 32) {
-    const uint32_t f = warp_floor<LP_THREADS>(sh_max, a.top);
-    if (tid == 0) {
-      ts.floor = f;
-      ts.count = 0;
-    }
-  }
-  __syncthreads();
-  const float floor_v = order_value(ts.floor);
-  const int slots = (rounds + merge - 1) / merge;
-  for (int q = 0; q < slots; ++q) {
-    if (!(gmax_sh[q * LP_THREADS + tid] >= floor_v)) continue;
-    const int it_hi = min(rounds, (q + 1) * merge);
-    for (int it = q * merge; it < it_hi; ++it) {
-      for (int j = 0; j < ROW_GROUP; ++j) {
-        const int i = it * per_round + j * LP_THREADS + tid;
-        if (i >= row.nv) break;
-        float x[Elt<DT>::kVec];
-        unpack_vec<DT>(row.load(i), x);
-        const int64_t c0 = row.col(i);
-#pragma unroll
-        for (int e = 0; e < Elt<DT>::kVec; ++e)
-          if (x[e] >= floor_v && c0 + e >= 0 && c0 + e < row.V) {
-            const int at = atomicAdd(&ts.count, 1);
-            if (at < LP_CAND) ts.cand[at] = rank_key(x[e], c0 + e);
-          }
+  // ---- the alternatives
+  if (odd) {
+    if (rank == 0)
+      for (int j = tid; j < a.top; j += LP_THREADS) {
+        a.top_ids[r * a.top + j] = j;
+        a.top_logp[r * a.top + j] = st.s;
       }
-    }
+    return;  // the whole cluster: nothing below is waited for
+  }
+  TopState* first = ctas > 1 ? cluster_map(&ts, 0) : &ts;
+  const float floor_v = floor ? order_value(floor) : -INFINITY;
+  auto test = [&](int i) {
+    float x[VE];
+    unpack_vec<DT>(row.load(i), x);
+    const int64_t c0 = row.col(i);
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (x[e] >= floor_v && c0 + e >= 0 && c0 + e < row.V) {
+        const int at = atomicAdd(&first->count, 1);
+        if (at < LP_CAND) first->cand[at] = rank_key(x[e], c0 + e);
+      }
+  };
+  if (own_max >= floor_v) {
+    const int slots = rounds > 0 ? ((rounds - 1) >> shift) + 1 : 0;
+    for (int q = 0; q < slots; ++q)
+      if (slot_max[q * LP_THREADS + tid] >= floor_v) {
+        const int at = atomicAdd(&ts.groups, 1);
+        if (at < LP_LIST) ts.list[at] = uint32_t(q * LP_THREADS + tid);
+      }
+    const int edge = tid == 0 ? 0 : row.nv - 1;
+    if (tid < 2 && edge >= lo && edge < hi && !row.whole(edge) && (tid == 0 || edge != 0)) test(edge);
   }
   __syncthreads();
-  if (ts.count > LP_CAND) collect_crowded<DT>(row, 0, row.nv, a.top, ts, sh_int);
+  const int groups = ts.groups;
+  if (groups > LP_LIST) {
+    if (tid == 0) atomicAdd(&first->count, LP_CAND + 1);
+  } else {
+    const int vec_bits = 2 + shift;  // vectors of a group
+    static_assert(ROW_GROUP == 4, "a group's vectors as bits");
+    for (int w = tid; w < groups << vec_bits; w += LP_THREADS) {
+      const uint32_t g = ts.list[w >> vec_bits];
+      const int in_group = w & ((1 << vec_bits) - 1);
+      const int round = (int(g / LP_THREADS) << shift) + in_group / ROW_GROUP;
+      const int i = body_lo + round * STEP + (in_group % ROW_GROUP) * LP_THREADS + int(g % LP_THREADS);
+      if (i < body_hi) test(i);
+    }
+  }
+  if (ctas > 1) {
+    cluster_sync();
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
+  if (ts.count > LP_CAND) {
+    collect_crowded<DT>(row, 0, row.nv, a.top, floor, ts, sh.scratch);  // starts with a barrier
+  }
   const int c = ts.count;
   for (int i = tid; i < c; i += LP_THREADS) {
     const unsigned long long mine = ts.cand[i];
     int place = 0;
     for (int j = 0; j < c; ++j) place += ts.cand[j] > mine;
     if (place < a.top) {
-      const float x = order_value(uint32_t(mine >> 32));
       a.top_ids[r * a.top + place] = int32_t(~uint32_t(mine));
-      a.top_logp[r * a.top + place] = empty ? -INFINITY : (x - st.m) / a.tau - ln_s;
+      a.top_logp[r * a.top + place] = logp_of(order_value(uint32_t(mine >> 32)));
     }
   }
 }
 
-size_t logprobs_smem(int V, int dtype) {
-  const int64_t vec = dtype == KD_F32 ? 4 : 8;
-  const int64_t nv = (int64_t(V) + vec - 1) / vec + 1;
-  int64_t rounds = (nv + ROW_GROUP * LP_THREADS - 1) / (ROW_GROUP * LP_THREADS);
-  return size_t(rounds < LP_SLOTS ? rounds : LP_SLOTS) * LP_THREADS * sizeof(float);
+// CTAs per row: one where the rows alone give every SM its four CTAs; otherwise as many as
+// would, up to the largest cluster, while each thread still has a whole group of vectors.
+static int logprobs_cluster(int64_t N, int64_t nv) {
+  const int64_t want = int64_t(gemm_max_grid()) * 4;
+  int c = 1;
+  while (c < LP_MAX_CLUSTER && N * c < want && nv >= int64_t(2 * c) * ROW_GROUP * LP_THREADS) c *= 2;
+  return c;
+}
+
+template <int DT, bool ENT, bool TOP>
+static cudaError_t logprobs_fwd_one(const LogprobArgs& a, cudaStream_t s) {
+  static PerDevice<int> wide;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int v = 0;
+  const auto kernel = kd_logprobs_fwd_kernel<DT, ENT, TOP>;
+  const int rc = wide.get(dev, &v, [&](int, int* out) {  // clusters of more than 8 CTAs are opted into
+    *out = 1;
+    return int(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  });
+  if (rc != 0) return rc > 0 ? cudaError_t(rc) : cudaErrorInvalidDevice;
+  const int64_t nv = (int64_t(a.V) + Elt<DT>::kVec - 1) / Elt<DT>::kVec;
+  const int ctas = logprobs_cluster(a.N, nv);
+  const int64_t rounds = ((nv + 1 + ctas - 1) / ctas + ROW_GROUP * LP_THREADS - 1) / (ROW_GROUP * LP_THREADS);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(a.N * ctas), 1, 1);
+  cfg.blockDim = dim3(LP_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = TOP ? size_t(rounds < LP_SLOTS ? rounds : LP_SLOTS) * LP_THREADS * sizeof(float) : 0;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_logprobs_fwd(const void* z, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* tokens,
                                 int M, const uint8_t* mask, float tau, int top, float* logp, float* lse,
                                 float* entropy, int32_t* top_ids, float* top_logp, uint32_t* err, cudaStream_t s) {
   LogprobArgs a{};
-  a.z = z; a.N = N; a.ld = ld; a.V = int(V); a.M = M; a.top = top; a.dtype = dtype;
+  a.z = z; a.N = N; a.ld = ld; a.V = int(V); a.M = M; a.top = top;
   a.tokens = tokens; a.mask = mask; a.tau = tau; a.k = float(1.4426950408889634 / double(tau));
   a.logp = logp; a.lse = lse; a.entropy = entropy; a.top_ids = top_ids; a.top_logp = top_logp; a.err = err;
-  const size_t smem = top ? logprobs_smem(a.V, dtype) : 0;
+  cudaError_t e;
   prof_before("kd_logprobs_fwd", s);
   KD_DISPATCH_TYPE(dtype, {
-    if (top) {
-      if (entropy) kd_logprobs_fwd_kernel<DT, true, true><<<unsigned(N), LP_THREADS, smem, s>>>(a);
-      else kd_logprobs_fwd_kernel<DT, false, true><<<unsigned(N), LP_THREADS, smem, s>>>(a);
-    } else {
-      if (entropy) kd_logprobs_fwd_kernel<DT, true, false><<<unsigned(N), LP_THREADS, 0, s>>>(a);
-      else kd_logprobs_fwd_kernel<DT, false, false><<<unsigned(N), LP_THREADS, 0, s>>>(a);
-    }
+    if (top) e = entropy ? logprobs_fwd_one<DT, true, true>(a, s) : logprobs_fwd_one<DT, false, true>(a, s);
+    else e = entropy ? logprobs_fwd_one<DT, true, false>(a, s) : logprobs_fwd_one<DT, false, false>(a, s);
   });
   prof_after(s);
-  return cudaGetLastError();
+  return e;
 }
 
 // ----------------------------------------------------------------- backward ---
@@ -326,7 +421,7 @@ struct LogprobGradArgs {
 // tokens first and rewrites their gradients last, and every vector is read and written by one
 // thread.
 template <int DT>
-__global__ void __launch_bounds__(LP_THREADS) kd_logprobs_bwd_kernel(const LogprobGradArgs a) {
+__global__ void __launch_bounds__(LB_THREADS) kd_logprobs_bwd_kernel(const LogprobGradArgs a) {
   extern __shared__ __align__(16) uint8_t lp_smem[];
   __shared__ float sh_sum[32];
   int32_t* ids = reinterpret_cast<int32_t*>(lp_smem);     // [M]
@@ -343,11 +438,11 @@ __global__ void __launch_bounds__(LP_THREADS) kd_logprobs_bwd_kernel(const Logpr
   const bool live = (a.mask == nullptr || a.mask[r] != 0) && a.lse[r] != -INFINITY;
   if (!live) {  // padding, or every logit -inf: no gradient
     const float zero[Elt<DT>::kVec] = {};
-    for (int i = lo + tid; i < hi; i += LP_THREADS) out.store(i, in.lead, zero);
+    for (int i = lo + tid; i < hi; i += LB_THREADS) out.store(i, in.lead, zero);
     return;
   }
   float gsum = 0.f;
-  for (int j = tid; j < a.M; j += LP_THREADS) {
+  for (int j = tid; j < a.M; j += LB_THREADS) {
     int32_t id = a.tokens[r * a.M + j];
     const float g = a.g_logp[r * a.M + j];
     if (id < 0 || id >= a.V) {
@@ -361,46 +456,49 @@ __global__ void __launch_bounds__(LP_THREADS) kd_logprobs_bwd_kernel(const Logpr
     ids[j] = id;
     gs[j] = g;
   }
-  const float G = sum_block<LP_THREADS>(gsum, sh_sum);  // its barrier: ids, gs, zs written, logits read
+  const float G = sum_block<LB_THREADS>(gsum, sh_sum);  // its barrier: ids, gs, zs written, logits read
   const float h = a.g_ent ? a.g_ent[r] : 0.f;
-  // log2 p = (x - base) k - off
-  float base = 0.f, off = a.lse[r] * kLog2e;
+  // log2 p = (x - base) k - off - log2_s
+  float base = 0.f, off = a.lse[r] * kLog2e, log2_s = 0.f;
   if (fabsf(a.lse[r]) > 1024.f) {
     // fp32 holds a logsumexp this large to 1e-4 or worse (a row of a type's lowest value: not at
     // all): take the row's maximum and sum again
-    RowStats st;
-    for (int i0 = 0; i0 < in.nv; i0 += ROW_GROUP * LP_THREADS) {
-      uint4 v[ROW_GROUP];
-      in.load_group(v, i0 + tid, LP_THREADS, in.nv);
-      stats_add<DT, false>(st, v, group_max<DT>(v), a.k);
-    }
-    __shared__ RowStats sh_stats[32];
-    st = stats_block<LP_THREADS>(st, a.k, sh_stats);  // its barrier: the row is read before any of it is written
-    base = st.m;
-    off = log2f(st.s);
+    RowStats st = stats_empty();
+    stream_stats<DT, false, LB_THREADS>(in, 0, in.nv, a.k, st, LoadOnce(), [](uint4&, int) {}, [](int, float) {});
+    __shared__ RowStats sh_stats[LB_THREADS / 32];
+    // its barrier: the row is read before any of it is written
+    st = stats_block<LB_THREADS, false>(st, a.k, sh_stats);
+    const bool plain = fabsf(st.m) <= kPlainMax;
+    base = plain ? 0.f : st.m;
+    off = plain ? __fmul_rn(st.m, a.k) : 0.f;
+    log2_s = log2f(st.s);
   }
   const float c0 = -(G + (h != 0.f ? h * a.entropy[r] : 0.f)) * a.inv_tau, c1 = -h * kLn2 * a.inv_tau;
   // p (c0 + c1 log2 p); where p is 0 the second factor is kept finite
   auto grad = [&](float x) {
-    const float t = fmaf(x - base, a.k, -off);
+    const float t = fmaf(x - base, a.k, -off) - log2_s;
     return ex2_approx(t) * fmaf(c1, fmaxf(t, -200.f), c0);
   };
-  for (int i0 = lo; i0 < hi; i0 += ROW_GROUP * LP_THREADS) {
-    uint4 v[ROW_GROUP];
-    in.load_group(v, i0 + tid, LP_THREADS, hi);
+  constexpr int VE = Elt<DT>::kVec;
+  if (base == 0.f && log2_s == 0.f) {
+    const uint64_t k2 = pack2(a.k, a.k), off2 = pack2(-off, -off), c02 = pack2(c0, c0), c12 = pack2(c1, c1);
+    stream_map<DT, LB_THREADS>(in, out, lo, hi, [&](float (&x)[VE]) {
 #pragma unroll
-    for (int j = 0; j < ROW_GROUP; ++j) {
-      const int64_t i = int64_t(i0) + tid + j * LP_THREADS;
-      if (i >= hi) break;
-      float x[Elt<DT>::kVec];
-      unpack_vec<DT>(v[j], x);
+      for (int e = 0; e < VE; e += 2) {
+        float t0, t1;
+        unpack2(fma2(pack2(x[e], x[e + 1]), k2, off2), t0, t1);
+        const uint64_t p2 = pack2(ex2_approx(t0), ex2_approx(t1));
+        unpack2(mul2(p2, fma2(c12, pack2(fmaxf(t0, -200.f), fmaxf(t1, -200.f)), c02)), x[e], x[e + 1]);
+      }
+    });
+  } else {
+    stream_map<DT, LB_THREADS>(in, out, lo, hi, [&](float (&x)[VE]) {
 #pragma unroll
-      for (int e = 0; e < Elt<DT>::kVec; ++e) x[e] = grad(x[e]);
-      out.store(int(i), in.lead, x);
-    }
+      for (int e = 0; e < VE; ++e) x[e] = grad(x[e]);
+    });
   }
   __syncthreads();
-  for (int j = tid; j < a.M; j += LP_THREADS) {
+  for (int j = tid; j < a.M; j += LB_THREADS) {
     const int id = ids[j];
     if (id < 0) continue;
     const int i = (in.lead + id) / Elt<DT>::kVec;
@@ -426,7 +524,7 @@ cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, 
   a.lse = lse; a.entropy = entropy; a.g_logp = g_logp; a.g_ent = g_ent; a.err = err;
   a.slices = 1;  // more only where dz is not z: a block may read the whole row
   prof_before("kd_logprobs_bwd", s);
-  KD_DISPATCH_TYPE(dtype, kd_logprobs_bwd_kernel<DT><<<unsigned(N), LP_THREADS, size_t(M) * 12, s>>>(a));
+  KD_DISPATCH_TYPE(dtype, kd_logprobs_bwd_kernel<DT><<<unsigned(N), LB_THREADS, size_t(M) * 12, s>>>(a));
   prof_after(s);
   return cudaGetLastError();
 }

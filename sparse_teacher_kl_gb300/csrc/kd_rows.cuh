@@ -104,12 +104,12 @@ __device__ __forceinline__ uint4 pack_vec(const float (&x)[Elt<DT>::kVec]) {
 }
 
 // Largest element of a thread's vectors; NaN if one of them is NaN.
-template <int DT>
-__device__ __forceinline__ float group_max(const uint4 (&v)[ROW_GROUP]) {
+template <int DT, int N>
+__device__ __forceinline__ float group_max(const uint4 (&v)[N]) {
   if constexpr (DT == KD_F32) {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < ROW_GROUP; ++j) {
+    for (int j = 0; j < N; ++j) {
       const float a = max_nan(__uint_as_float(v[j].x), __uint_as_float(v[j].y));
       const float b = max_nan(__uint_as_float(v[j].z), __uint_as_float(v[j].w));
       m = max_nan(m, max_nan(a, b));
@@ -118,7 +118,7 @@ __device__ __forceinline__ float group_max(const uint4 (&v)[ROW_GROUP]) {
   } else {
     uint32_t m = Elt<DT>::kNegInf;
 #pragma unroll
-    for (int j = 0; j < ROW_GROUP; ++j)
+    for (int j = 0; j < N; ++j)
       m = Elt<DT>::max2(m, Elt<DT>::max2(Elt<DT>::max2(v[j].x, v[j].y), Elt<DT>::max2(v[j].z, v[j].w)));
     float a, b;
     Elt<DT>::unpack(m, a, b);
@@ -169,20 +169,6 @@ struct Row {
     if (whole(i)) return __ldcs(reinterpret_cast<const uint4*>(base) + i);
     return load_edge(i);
   }
-  // The vectors first, first + step, ... (ROW_GROUP of them) below `end`; -inf from there on.
-  __device__ __forceinline__ void load_group(uint4 (&v)[ROW_GROUP], int first, int step, int end) const {
-    if (first >= full_lo && int64_t(first) + int64_t(ROW_GROUP - 1) * step < (end < full_hi ? end : full_hi)) {
-#pragma unroll
-      for (int j = 0; j < ROW_GROUP; ++j) v[j] = __ldcs(reinterpret_cast<const uint4*>(base) + first + j * step);
-    } else {
-#pragma unroll
-      for (int j = 0; j < ROW_GROUP; ++j) {
-        const int64_t i = int64_t(first) + int64_t(j) * step;
-        v[j] = i < end ? load(int(i))
-                       : make_uint4(Elt<DT>::kNegInf, Elt<DT>::kNegInf, Elt<DT>::kNegInf, Elt<DT>::kNegInf);
-      }
-    }
-  }
   // Elements of vector i of a row that starts `lead_` elements into its grid, written to this row.
   __device__ __forceinline__ void store(int i, int lead_, const float (&x)[kVec]) const {
     if (lead_ == lead && whole(i)) {
@@ -197,93 +183,257 @@ struct Row {
 };
 
 // ----------------------------------------------------- softmax statistics ---
-// Over the elements x seen so far, with k = log2(e) / tau:
-//   m = max x,  s = sum 2^((x - m) k),  u = sum 2^((x - m) k) (x - m) k
-// so that logsumexp(x / tau) = m / tau + ln s and the entropy of softmax(x / tau) is
-// ln s - ln2 u / s: a sum of two terms that are never negative.  x - m is formed first
-// (exact for neighbours, and finite or -inf even for masks of a type's lowest value), then
-// scaled.  An empty set has m = -inf, s = 0; a NaN makes s NaN (m skips it).
+// Over the elements x seen so far, with k = log2(e) / tau and t(x) = x k - fl(m k):
+//   m = max x,  s = sum 2^t,  u = sum 2^t t
+// so that log2 of p(x) is t(x) - log2 s, logsumexp(x / tau) is ln2 (fl(m k) + log2 s) and the
+// entropy of softmax(x / tau) is ln2 (log2 s - u / s), two terms that (but for the rounding of
+// m k) are never negative.  t is one fused multiply-add against the same rounded offset
+// everywhere, so the offset's rounding cancels.  Where |m| is above 1e29 (a row of a type's
+// lowest value) the offset would overflow and t(x) = (x - m) k is taken instead.  An empty set
+// has m = -inf, s = 0; a NaN or +inf element makes s NaN (m skips a NaN).
 
 struct RowStats {
-  float m = -INFINITY, s = 0.f, u = 0.f;
+  float m, s, u;
 };
+__device__ __forceinline__ RowStats stats_empty() { return {-INFINITY, 0.f, 0.f}; }
 
-// 2^t of a difference of maxima; t = -inf (one side empty or far below) gives 0.
-__device__ __forceinline__ float stats_shift(float from, float to, float k, float& t) {
-  t = fmaxf((from - to) * k, -200.f);  // 2^-200 is 0 in fp32; keeps t * 0 finite
-  return ex2_approx(t);
+constexpr float kPlainMax = 1e29f;
+
+__device__ __forceinline__ float stats_t(float x, float m, float k) {
+  return fabsf(m) <= kPlainMax ? fmaf(x, k, -__fmul_rn(m, k)) : (x - m) * k;
 }
 
-__device__ __forceinline__ void stats_merge(RowStats& a, const RowStats& b, float k) {
-  const float M = fmaxf(a.m, b.m);
-  if (M == -INFINITY) {
-    a.s += b.s;  // 0, or NaN where a side held one
+// ln p of an element from its row's statistics, log2_s = log2 of s.
+__device__ __forceinline__ float stats_logp(float x, float m, float log2_s, float k, float tau) {
+  if (fmaxf(fabsf(x), fabsf(m)) <= kPlainMax) return kLn2 * (stats_t(x, m, k) - log2_s);
+  return (x - m) / tau - kLn2 * log2_s;
+}
+
+// log2 of the factor that takes a sum relative to `from` to one relative to `to` >= from; -200
+// stands for anything that far below (2^-200 is 0 in fp32, and -200 times 0 is 0).
+__device__ __forceinline__ float stats_shift(float from, float to, float k) {
+  const float t = fmaxf(fabsf(from), fabsf(to)) <= kPlainMax ? __fmul_rn(from, k) - __fmul_rn(to, k) : (from - to) * k;
+  return fmaxf(t, -200.f);
+}
+
+__device__ __forceinline__ void stats_rescale(RowStats& a, float to, float k) {
+  if (a.m == to || a.m == -INFINITY) {  // nothing summed yet: s is 0, or NaN
+    a.m = to;
     return;
   }
-  float ta = 0.f, tb = 0.f;
-  const float fa = a.m == M ? 1.f : (a.m == -INFINITY ? 0.f : stats_shift(a.m, M, k, ta));
-  const float fb = b.m == M ? 1.f : (b.m == -INFINITY ? 0.f : stats_shift(b.m, M, k, tb));
-  const float u = fmaf(ta, a.s, a.u) * fa + fmaf(tb, b.s, b.u) * fb;
-  a.s = a.s * fa + b.s * fb;
-  a.u = u;
-  a.m = M;
+  const float t = stats_shift(a.m, to, k), f = ex2_approx(t);
+  a.u = fmaf(t, a.s, a.u) * f;
+  a.s *= f;
+  a.m = to;
 }
 
-// Add the elements of a thread's vectors, whose largest is gmax.
-template <int DT, bool ENT>
-__device__ __forceinline__ void stats_add(RowStats& st, const uint4 (&v)[ROW_GROUP], float gmax, float k) {
+__device__ __forceinline__ void stats_merge(RowStats& a, RowStats b, float k) {
+  const float M = fmaxf(a.m, b.m);
+  if (M != -INFINITY) {
+    stats_rescale(a, M, k);
+    stats_rescale(b, M, k);
+  }
+  a.s += b.s;
+  a.u += b.u;
+}
+
+// Two floats in one 64-bit register, for the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Add the elements of N vectors whose largest element is gmax.
+template <int DT, bool ENT, int N>
+__device__ __forceinline__ void stats_add(RowStats& st, const uint4 (&v)[N], float gmax, float k) {
+  constexpr int VE = Elt<DT>::kVec;
   if (gmax == -INFINITY) return;
   if (!(gmax <= st.m)) {
     if (gmax != gmax) {
       st.s = gmax;
       return;
     }
-    if (st.m != -INFINITY) {
-      float t;
-      const float f = stats_shift(st.m, gmax, k, t);
-      if (ENT) st.u = fmaf(t, st.s, st.u) * f;
-      st.s *= f;
+    stats_rescale(st, gmax, k);
+  }
+  // An element of -inf has weight 0, but its exponent must stay finite for u: elements are
+  // raised to a floor, which changes nothing while the floor's own weight is 0.
+  constexpr float kFloor = DT == KD_F16 ? -65504.f : -1e30f;
+  if (fabsf(st.m) <= kPlainMax && (!ENT || (st.m - kFloor) * k > 150.f)) {
+    const float off = -__fmul_rn(st.m, k);
+    const uint64_t k2 = pack2(k, k), off2 = pack2(off, off);
+    uint64_t s2[2] = {0, 0}, u2[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int h = 0; h < VE / 2; ++h) {
+        float x0, x1;
+        if constexpr (DT == KD_F32) {
+          x0 = __uint_as_float(w[2 * h]);
+          x1 = __uint_as_float(w[2 * h + 1]);
+          if (ENT) {
+            x0 = max_nan(x0, kFloor);
+            x1 = max_nan(x1, kFloor);
+          }
+        } else {
+          constexpr uint32_t low = DT == KD_F16 ? 0xFBFFFBFFu : 0xF14AF14Au;  // -65504; -1e30 in bf16
+          Elt<DT>::unpack(ENT ? Elt<DT>::max2(w[h], low) : w[h], x0, x1);
+        }
+        const uint64_t t2 = fma2(pack2(x0, x1), k2, off2);
+        float t0, t1;
+        unpack2(t2, t0, t1);
+        const uint64_t p2 = pack2(ex2_approx(t0), ex2_approx(t1));
+        s2[h & 1] = add2(s2[h & 1], p2);
+        if (ENT) u2[h & 1] = fma2(p2, t2, u2[h & 1]);
+      }
     }
-    st.m = gmax;
+    float a, b;
+    unpack2(add2(s2[0], s2[1]), a, b);
+    st.s += a + b;
+    if (ENT) {
+      unpack2(add2(u2[0], u2[1]), a, b);
+      st.u += a + b;
+    }
+    return;
   }
 #pragma unroll
-  for (int j = 0; j < ROW_GROUP; ++j) {
-    float x[Elt<DT>::kVec];
+  for (int j = 0; j < N; ++j) {
+    float x[VE];
     unpack_vec<DT>(v[j], x);
 #pragma unroll
-    for (int e = 0; e < Elt<DT>::kVec; ++e) {
-      const float t = (x[e] - st.m) * k;
-      const float p = ex2_approx(t);
+    for (int e = 0; e < VE; ++e) {
+      const float t = stats_t(x[e], st.m, k), p = ex2_approx(t);
       st.s += p;
       if (ENT) st.u = fmaf(p, fmaxf(t, -200.f), st.u);
     }
   }
 }
 
-__device__ __forceinline__ RowStats stats_shfl_xor(const RowStats& a, int o) {
-  RowStats b;
-  b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-  b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-  b.u = __shfl_xor_sync(0xffffffffu, a.u, o);
-  return b;
+__device__ __forceinline__ float warp_max(float x, int width = 32) {
+  for (int o = width / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x, int width = 32) {
+  for (int o = width / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
-// The block's statistics in every thread; `sh`: one entry per warp.
-template <int THREADS>
-__device__ __forceinline__ RowStats stats_block(RowStats st, float k, RowStats* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) stats_merge(st, stats_shfl_xor(st, o), k);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) sh[warp] = st;
-  __syncthreads();
-  st = lane < THREADS / 32 ? sh[lane] : RowStats{};
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) stats_merge(st, stats_shfl_xor(st, o), k);
-  // a merge rounds differently from its mirror image: every thread takes lane 0's result
-  st.m = __shfl_sync(0xffffffffu, st.m, 0);
-  st.s = __shfl_sync(0xffffffffu, st.s, 0);
-  st.u = __shfl_sync(0xffffffffu, st.u, 0);
+// The statistics of `width` consecutive lanes (a power of two), in each of them.
+template <bool ENT>
+__device__ __forceinline__ void stats_warp(RowStats& st, float k, int width = 32) {
+  const float M = warp_max(st.m, width);
+  if (M != -INFINITY) stats_rescale(st, M, k);
+  st.s = warp_sum(st.s, width);
+  if (ENT) st.u = warp_sum(st.u, width);
+}
+
+// The block's statistics in every thread, in two halves with a barrier of the caller's between
+// them.  `sh`: one entry per warp.
+template <bool ENT>
+__device__ __forceinline__ void stats_block_put(RowStats st, float k, RowStats* sh) {
+  stats_warp<ENT>(st, k);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = st;
+}
+template <int THREADS, bool ENT>
+__device__ __forceinline__ RowStats stats_block_get(float k, const RowStats* sh) {
+  constexpr int W = THREADS / 32;
+  RowStats st = sh[threadIdx.x & (W - 1)];
+  stats_warp<ENT>(st, k, W);
   return st;
+}
+template <int THREADS, bool ENT>
+__device__ __forceinline__ RowStats stats_block(const RowStats& st, float k, RowStats* sh) {
+  stats_block_put<ENT>(st, k, sh);
+  __syncthreads();
+  return stats_block_get<THREADS, ENT>(k, sh);
+}
+
+// Loads of a row that is read once, and of one that is read again soon: the second asks L2 to keep
+// the lines.
+struct LoadOnce {
+  __device__ __forceinline__ uint4 operator()(const uint4* p) const { return __ldcs(p); }
+};
+struct LoadKeep {
+  uint64_t policy;
+  __device__ __forceinline__ LoadKeep() {
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+  }
+  __device__ __forceinline__ uint4 operator()(const uint4* p) const {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
+    return v;
+  }
+};
+
+// Stream vectors [lo, hi) of a row through the block's first THREADS threads, ROW_GROUP vectors of a
+// thread in flight while the previous ones are added:
+//   load(address)        reads a vector
+//   fix(vector, i)       may change vector i before it is added
+//   on_group(round, max) sees the largest element of each group of a thread
+// The vectors that the row only partly covers are added last, one thread each.
+template <int DT, bool ENT, int THREADS, class Load, class Fix, class OnGroup>
+__device__ __forceinline__ void stream_stats(const Row<DT>& row, int lo, int hi, float k, RowStats& st, Load&& get,
+                                             Fix&& fix, OnGroup&& on_group) {
+  constexpr uint32_t NI = Elt<DT>::kNegInf;
+  const int first = max(lo, row.full_lo) + int(threadIdx.x), end = min(hi, row.full_hi);
+  const uint4* p = reinterpret_cast<const uint4*>(row.base);
+  constexpr int STEP = ROW_GROUP * THREADS;
+  auto load = [&](uint4 (&v)[ROW_GROUP], int i0) {
+    if (i0 + (ROW_GROUP - 1) * THREADS < end) {
+#pragma unroll
+      for (int j = 0; j < ROW_GROUP; ++j) v[j] = get(p + i0 + j * THREADS);
+    } else {
+#pragma unroll
+      for (int j = 0; j < ROW_GROUP; ++j)
+        v[j] = i0 + j * THREADS < end ? get(p + i0 + j * THREADS) : make_uint4(NI, NI, NI, NI);
+    }
+  };
+  int round = 0, i0 = first;
+  auto add = [&](uint4 (&v)[ROW_GROUP]) {
+#pragma unroll
+    for (int j = 0; j < ROW_GROUP; ++j) fix(v[j], i0 + j * THREADS);
+    const float g = group_max<DT>(v);
+    on_group(round, g);
+    stats_add<DT, ENT>(st, v, g, k);
+    i0 += STEP;
+    ++round;
+  };
+  uint4 even[ROW_GROUP], uneven[ROW_GROUP];
+  load(even, i0);
+  while (i0 < end) {
+    if (i0 + STEP < end) load(uneven, i0 + STEP);
+    add(even);
+    if (i0 >= end) break;
+    if (i0 + STEP < end) load(even, i0 + STEP);
+    add(uneven);
+  }
+  const int edge = threadIdx.x == 0 ? 0 : row.nv - 1;
+  if (threadIdx.x < 2 && edge >= lo && edge < hi && !row.whole(edge) && (threadIdx.x == 0 || edge != 0)) {
+    uint4 v[1] = {row.load_edge(edge)};
+    fix(v[0], edge);
+    stats_add<DT, ENT>(st, v, group_max<DT>(v), k);
+  }
 }
 
 template <int THREADS>
@@ -306,6 +456,53 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 __device__ __forceinline__ float order_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
+// Map vectors [lo, hi) of a row through the block's first THREADS threads: x = f(x) for every
+// element, from `in` to `out` (in place where they are the same row).  Whole vectors of rows that
+// are aligned alike go as such, ROW_GROUP of a thread at a time; the others by elements.
+template <int DT, int THREADS, class F>
+__device__ __forceinline__ void stream_map(const Row<DT>& in, const Row<DT>& out, int lo, int hi, F&& f) {
+  constexpr int VE = Elt<DT>::kVec, STEP = ROW_GROUP * THREADS;
+  const bool alike = in.lead == out.lead;
+  const int body_lo = max(lo, in.full_lo), body_hi = max(body_lo, min(hi, in.full_hi));
+  if (alike) {
+    const uint4* p = reinterpret_cast<const uint4*>(in.base) + body_lo + threadIdx.x;
+    uint4* o = reinterpret_cast<uint4*>(out.base) + body_lo + threadIdx.x;
+    int left = body_hi - body_lo - int(threadIdx.x);  // vectors from this one on
+    for (; left > (ROW_GROUP - 1) * THREADS; left -= STEP, p += STEP, o += STEP) {
+      uint4 v[ROW_GROUP];
+#pragma unroll
+      for (int j = 0; j < ROW_GROUP; ++j) v[j] = __ldcs(p + j * THREADS);
+#pragma unroll
+      for (int j = 0; j < ROW_GROUP; ++j) {
+        float x[VE];
+        unpack_vec<DT>(v[j], x);
+        f(x);
+        __stcs(o + j * THREADS, pack_vec<DT>(x));
+      }
+    }
+    for (; left > 0; left -= THREADS, p += THREADS, o += THREADS) {
+      float x[VE];
+      unpack_vec<DT>(__ldcs(p), x);
+      f(x);
+      __stcs(o, pack_vec<DT>(x));
+    }
+  } else {
+    for (int i = body_lo + int(threadIdx.x); i < body_hi; i += THREADS) {
+      float x[VE];
+      unpack_vec<DT>(in.load(i), x);
+      f(x);
+      out.store(i, in.lead, x);
+    }
+  }
+  const int edge = threadIdx.x == 0 ? 0 : in.nv - 1;
+  if (threadIdx.x < 2 && edge >= lo && edge < hi && !in.whole(edge) && (threadIdx.x == 0 || edge != 0)) {
+    float x[VE];
+    unpack_vec<DT>(in.load_edge(edge), x);
+    f(x);
+    out.store(edge, in.lead, x);
+  }
 }
 
 // Call f.template operator()<DT>() for a run-time element type.

@@ -56,6 +56,12 @@ kd_status count_valid(const uint8_t* mask, int64_t N, Ctrl* ctrl, const int32_t*
 
 extern "C" {
 
+int kd_workspace_clear(void* ws, size_t ws_bytes, void* stream) {
+  kd_status st = check_ws(ws, ws_bytes, sizeof(Ctrl));
+  if (st != KD_OK) return st;
+  return map_cuda(cudaMemsetAsync(ws, 0, sizeof(Ctrl), static_cast<cudaStream_t>(stream)));
+}
+
 size_t kd_token_logprobs_workspace(int64_t N, int64_t V) {
   (void)N;
   (void)V;

@@ -161,6 +161,23 @@ def test_masked_vocabularies(kd, cuda_device, dtype, tail, fill):
     check(kd, z, ids, t, t_lse)
 
 
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("where", ["cached", "other"])
+def test_nan_and_infinity_stay_in_their_rows(kd, cuda_device, tail, where):
+    z, ids, t, t_lse = case(5, 2500, 9, torch.bfloat16, tail=tail)
+    other = [c for c in range(20) if c not in ids[1].tolist() and c not in ids[3].tolist()][0]
+    z[1, int(ids[1, 2]) if where == "cached" else other] = math.nan
+    z[3, int(ids[3, 0]) if where == "cached" else other] = math.inf
+    kl = torch.empty((5,), device="cuda")
+    loss, dz = kd.logits_kl_step(z, ids, t, None, 1.0, t_lse, kl_out=kl)
+    assert math.isnan(float(loss)) and torch.isnan(kl[[1, 3]]).all() and torch.isnan(dz[[1, 3]]).any(1).all()
+    rows = [0, 2, 4]
+    ref = oracle.logits_kl(host(z)[rows], host(ids)[rows], host(t)[rows],
+                           t_lse=None if t_lse is None else host(t_lse)[rows], grad_loss=3 / 5)
+    near(kl.cpu()[rows], ref.kl, 6e-5)
+    check_grad(dz[rows], ref.grad, torch.bfloat16)
+
+
 @pytest.mark.parametrize("q_rest", [1e-3, 1e-6, 1e-12, 1e-30])
 def test_rest_class_keeps_its_digits(kd, cuda_device, q_rest):
     """The student's mass outside the cache is tiny: it is summed alone, not as 1 minus the cached mass."""

@@ -275,6 +275,16 @@ def test_bad_token_is_reported(kd, cuda_device):
     check_grad(dz, oracle.token_logprobs_grad(z.double().cpu().numpy(), tok.cpu().numpy(), g), torch.float32)
 
 
+def test_control_block_without_a_workspace(kd, cuda_device):
+    z, tok = draw(3, 90, torch.float32, 1), tokens_for(3, 90, 1, 1)
+    tok[2] = -1
+    block = kd.control_block(z.device)
+    assert block is kd.control_block(z.device) and kd.device_error(block)[0] == 0
+    kd.token_logprobs_forward(z, tok)
+    assert kd.device_error(block) == (kd._abi.KD_ERR_DEVICE, 2)
+    assert kd.device_error(block)[0] == 0
+
+
 def test_gradient_matches_differences(kd, cuda_device):
     """Central differences of the fp32 forward: step 1/16, truncation error (step^2 / 6) |f'''| < 7e-4."""
     z, tok = draw(2, 50, torch.float32, 9), tokens_for(2, 50, 1, 3)
