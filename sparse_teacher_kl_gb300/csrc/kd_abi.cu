@@ -428,6 +428,16 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   const float inv_tau = 1.0f / tau;
   const uint16_t* H = static_cast<const uint16_t*>(H_bf16);
 
+  if (lp && N <= FEW_ROWS && FEW_ROWS * d * 4 <= FEW_MAX_SMEM) {
+    // a few positions: bound by reading W, which CUDA cores do faster than 128-row tiles
+    int units = 0;
+    cudaError_t e = launch_logprob_few(H, static_cast<const uint16_t*>(W_bf16), int(N), int(d), V, lp->tokens, mask,
+                                       tau, partials, L.n_groups, &units, s);
+    if (e != cudaSuccess) return KD_ERR_CUDA;
+    return map_cuda(launch_logprob_combine(partials, units, int(N), V, lp->tokens, mask, lp->logp, lse_out,
+                                           lp->entropy, &ctrl->err, 0, s));
+  }
+
   alignas(64) CUtensorMap tw, tw_half, th, tz;
   if (!make_tmap_2d_bf16(&tw, W_bf16, uint64_t(d), uint64_t(V), uint64_t(d) * 2, BK, BN)) return KD_ERR_CUDA;
   if (!make_tmap_2d_bf16(&tw_half, W_bf16, uint64_t(d), uint64_t(V), uint64_t(d) * 2, BK, BN / 2))

@@ -211,6 +211,13 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
 cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, int rows, int64_t V,
                                    const int32_t* tokens, const uint8_t* mask, float* logp, float* lse,
                                    float* entropy, uint32_t* err, int64_t row0, cudaStream_t s);
+// EPI_LSE_H's partials for up to FEW_ROWS rows without the tensor cores; *units: how many per row
+// were written (at most max_units).
+constexpr int FEW_ROWS = 4;
+constexpr int FEW_MAX_SMEM = 200 * 1024;  // the hidden states in fp32: a limit on rows * d
+cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, int d, int64_t V, const int32_t* tokens,
+                               const uint8_t* mask, float tau, float4* partials, int max_units, int* units,
+                               cudaStream_t s);
 cudaError_t launch_loss_reduce(const float* kl, const uint8_t* mask, int64_t N, const int32_t* n_valid,
                                float* loss_out, cudaStream_t s);
 
@@ -236,6 +243,9 @@ cudaError_t launch_logits_kl(int mode, const void* z, int dtype, int64_t N, int6
                              const float* tlog, int K, const float* t_lse, const uint8_t* mask, float tau,
                              float* stats, float* kl, const float* grad_loss, const int32_t* n_valid, void* dz,
                              int64_t ld_dz, uint32_t* err, cudaStream_t s);
+
+// loss = mean of kl over the valid rows, 0 if there are none.
+cudaError_t launch_masked_mean(const float* kl, const uint8_t* mask, int64_t N, float* loss, cudaStream_t s);
 
 constexpr int KD_MAX_SPLITS = 8;
 

@@ -607,7 +607,7 @@ static cudaError_t lk_launch(LogitsKlArgs a, int ctas, cudaStream_t s) {
 }
 
 // How a row is shared out, by its bytes:
-//   up to 96 KB   four blocks of 256 threads on an SM, a row each
+//   up to 96 KB   four blocks of 288 threads on an SM, a row each
 //   up to 192 KB  two of 512
 //   longer        one of 1024; over 416 KB a cluster of two or more, so that the rows in flight
 //                 (at most 152 x 4 x 96 KB = 58 MB, 152 x 416 KB = 62 MB) stay in half of L2
@@ -616,7 +616,7 @@ template <int DT, bool REST, bool STEP>
 static cudaError_t lk_one(const LogitsKlArgs& a, cudaStream_t s) {
   const int64_t nv = a.V / Elt<DT>::kVec + 2, kb = nv * 16 / 1024;
   const int sms = gemm_max_grid();
-  if (a.N > sms && kb <= 96) return lk_launch<DT, REST, STEP, 6, 2, 4>(a, 1, s);
+  if (a.N > sms && kb <= 96) return lk_launch<DT, REST, STEP, 8, 1, 4>(a, 1, s);
   if (a.N > sms && kb <= 192) return lk_launch<DT, REST, STEP, 13, 3, 2>(a, 1, s);
   int c = 1;
   while (c < LK_MAX_CLUSTER && kb > int64_t(416) * c) c *= 2;
@@ -705,6 +705,47 @@ cudaError_t launch_logits_kl(int mode, const void* z, int dtype, int64_t N, int6
   });
   prof_after(s);
   return e;
+}
+
+// --------------------------------------------------------------- the loss ---
+// Mean of kl over the valid rows (0 if there are none) and their number, by one block in a fixed
+// order, in fp64.
+__global__ void __launch_bounds__(1024) kd_masked_mean_kernel(const float* __restrict__ kl,
+                                                              const uint8_t* __restrict__ mask, int64_t N,
+                                                              float* __restrict__ loss) {
+  __shared__ double sums[32];
+  __shared__ int counts[32];
+  double sum = 0.0;
+  int n = 0;
+  for (int64_t i = threadIdx.x; i < N; i += 1024)
+    if (mask == nullptr || mask[i] != 0) {
+      sum += double(kl[i]);
+      ++n;
+    }
+  const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
+  auto reduce = [&] {
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
+    n = __reduce_add_sync(0xffffffffu, n);
+  };
+  reduce();
+  if (lane == 0) {
+    sums[warp] = sum;
+    counts[warp] = n;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    sum = sums[lane];
+    n = counts[lane];
+    reduce();
+    if (lane == 0) *loss = n > 0 ? float(sum / double(n)) : 0.f;
+  }
+}
+
+cudaError_t launch_masked_mean(const float* kl, const uint8_t* mask, int64_t N, float* loss, cudaStream_t s) {
+  prof_before("kd_masked_mean", s);
+  kd_masked_mean_kernel<<<1, 1024, 0, s>>>(kl, mask, N, loss);
+  prof_after(s);
+  return cudaGetLastError();
 }
 
 }  // namespace kd

@@ -15,6 +15,7 @@ namespace kd {
 
 constexpr int LP_THREADS = 256;      // forward
 constexpr int LP_WARPS = LP_THREADS / 32;
+constexpr int LP_PER_SM = 5;         // blocks on an SM
 constexpr int LP_SLOTS = 32;         // group maxima kept per thread
 constexpr int LP_CAND = 1024;        // candidates for the top alternatives
 constexpr int LP_LIST = 512;         // groups that may hold one
@@ -160,7 +161,7 @@ struct LpShared {
 // One cluster per row (a single CTA where there are rows enough to fill the GPU): each CTA
 // streams its share of the row's vectors; the first one puts the results together.
 template <int DT, bool ENT, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS, 4) kd_logprobs_fwd_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(const LogprobArgs a) {
   extern __shared__ __align__(16) uint8_t lp_smem[];
   __shared__ LpShared sh;
   __shared__ TopState ts;
@@ -347,12 +348,12 @@ __global__ void __launch_bounds__(LP_THREADS, 4) kd_logprobs_fwd_kernel(const Lo
   }
 }
 
-// CTAs per row: one where the rows alone give every SM its four CTAs; otherwise as many as
-// would, up to the largest cluster, while each thread still has a whole group of vectors.
+// CTAs per row: one where the rows alone give every SM its blocks; otherwise as many as
+// would, up to the largest cluster, while each thread still has two groups of vectors.
 static int logprobs_cluster(int64_t N, int64_t nv) {
-  const int64_t want = int64_t(gemm_max_grid()) * 4;
+  const int64_t want = int64_t(gemm_max_grid()) * LP_PER_SM;
   int c = 1;
-  while (c < LP_MAX_CLUSTER && N * c < want && nv >= int64_t(2 * c) * ROW_GROUP * LP_THREADS) c *= 2;
+  while (c < LP_MAX_CLUSTER && 2 * N * c <= want && nv >= int64_t(2 * c) * ROW_GROUP * LP_THREADS) c *= 2;
   return c;
 }
 
@@ -527,6 +528,123 @@ cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, 
   KD_DISPATCH_TYPE(dtype, kd_logprobs_bwd_kernel<DT><<<unsigned(N), LB_THREADS, size_t(M) * 12, s>>>(a));
   prof_after(s);
   return cudaGetLastError();
+}
+
+// ---------------------------------------------------- few hidden states ---
+// The same scores straight from a few hidden states (fused_logprobs with up to FEW_ROWS rows, a
+// generated token or so): z_v = H W_v^T is then bound by reading W once, V d elements.  A warp
+// takes FEW_VOCAB rows of W at a time, a lane 16 bytes of each in turn, sums the products over the
+// lanes and keeps running statistics of the logits; a block leaves one partial per hidden state,
+// as the projection engine's epilogue does per tile.
+
+constexpr int FEW_THREADS = 256;
+constexpr int FEW_VOCAB = 4;
+constexpr int few_per_sm(int rows) { return rows == 1 ? 3 : 2; }  // blocks on an SM, by their registers
+
+template <int R>
+__global__ void __launch_bounds__(FEW_THREADS, few_per_sm(R))
+    kd_logprob_few_kernel(const uint16_t* __restrict__ H, const uint16_t* __restrict__ W, int rows, int d, int64_t V,
+                          const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, float k, float inv_tau,
+                          float4* __restrict__ partials, int rows_pad) {
+  extern __shared__ __align__(16) float few_h[];  // [R][d] hidden states
+  __shared__ RowStats sh[R][FEW_THREADS / 32];
+  __shared__ float z_token[R];
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < R * d; i += FEW_THREADS)
+    few_h[i] = i < rows * d ? __uint_as_float(uint32_t(H[i]) << 16) : 0.f;
+  if (tid < R) z_token[tid] = 0.f;
+  int64_t want[R];  // the given tokens (a padding row's is not looked at)
+#pragma unroll
+  for (int r = 0; r < R; ++r) want[r] = r < rows && (mask == nullptr || mask[r] != 0) ? tokens[r] : -1;
+  __syncthreads();
+  RowStats st[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) st[r] = stats_empty();
+  const int nv = d / 8;  // 16-byte vectors of a row (d is a multiple of 8)
+  const int64_t warps = int64_t(gridDim.x) * (FEW_THREADS / 32);
+  for (int64_t v0 = (int64_t(blockIdx.x) * (FEW_THREADS / 32) + warp) * FEW_VOCAB; v0 < V; v0 += warps * FEW_VOCAB) {
+    float acc[FEW_VOCAB][R] = {};
+    const uint4* w[FEW_VOCAB];
+#pragma unroll
+    for (int q = 0; q < FEW_VOCAB; ++q)  // past the vocabulary: its last row again, not added below
+      w[q] = reinterpret_cast<const uint4*>(W + (v0 + q < V ? v0 + q : V - 1) * d);
+#pragma unroll 2
+    for (int i = lane; i < nv; i += 32) {
+      uint4 x[FEW_VOCAB];
+#pragma unroll
+      for (int q = 0; q < FEW_VOCAB; ++q) x[q] = __ldcs(w[q] + i);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 a = reinterpret_cast<const float4*>(few_h + r * d)[2 * i];
+        const float4 b = reinterpret_cast<const float4*>(few_h + r * d)[2 * i + 1];
+#pragma unroll
+        for (int q = 0; q < FEW_VOCAB; ++q) {
+          float y[8];
+          unpack_vec<KD_BF16>(x[q], y);
+          float s = acc[q][r];
+          s = fmaf(y[0], a.x, s); s = fmaf(y[1], a.y, s); s = fmaf(y[2], a.z, s); s = fmaf(y[3], a.w, s);
+          s = fmaf(y[4], b.x, s); s = fmaf(y[5], b.y, s); s = fmaf(y[6], b.z, s); s = fmaf(y[7], b.w, s);
+          acc[q][r] = s;
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < FEW_VOCAB; ++q)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float z = warp_sum(acc[q][r]);
+        if (lane == 0 && v0 + q < V) {
+          if (v0 + q == want[r]) z_token[r] = z;
+          if (!(z <= st[r].m)) {
+            if (z != z) st[r].s = z;
+            else stats_rescale(st[r], z, k);
+          }
+          const float t = fmaf(z, k, -__fmul_rn(st[r].m, k)), p = ex2_approx(t);
+          st[r].s += p;
+          st[r].u = fmaf(p, fmaxf(t, -200.f), st[r].u);
+        }
+      }
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) sh[r][warp] = st[r];
+  }
+  __syncthreads();
+  if (warp < R && warp < rows) {
+    RowStats s = lane < FEW_THREADS / 32 ? sh[warp][lane] : stats_empty();
+    stats_warp<true>(s, k);
+    if (lane == 0)
+      partials[size_t(blockIdx.x) * rows_pad + warp] =
+          make_float4(__fmul_rn(s.m, k), s.s, z_token[warp] * inv_tau, s.u);
+  }
+}
+
+cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, int d, int64_t V, const int32_t* tokens,
+                               const uint8_t* mask, float tau, float4* partials, int max_units, int* units,
+                               cudaStream_t s) {
+  const int64_t per_block = FEW_VOCAB * (FEW_THREADS / 32);
+  int64_t grid = (V + per_block - 1) / per_block;
+  const int most = gemm_max_grid() * few_per_sm(rows);
+  if (grid > most) grid = most;
+  if (grid > max_units) grid = max_units;
+  *units = int(grid);
+  const float k = float(1.4426950408889634 / double(tau));
+  prof_before("kd_logprob_few", s);
+  cudaError_t e = cudaSuccess;
+#define KD_FEW(R_)                                                                                                   \
+  do {                                                                                                               \
+    static PerDevice<int> done;                                                                                      \
+    e = smem_attr_once(done, reinterpret_cast<const void*>(kd_logprob_few_kernel<R_>), FEW_MAX_SMEM);                \
+    if (e == cudaSuccess)                                                                                            \
+      kd_logprob_few_kernel<R_><<<unsigned(grid), FEW_THREADS, size_t(R_) * d * 4, s>>>(                             \
+          H, W, rows, d, V, tokens, mask, k, 1.0f / tau, partials, BM);                                              \
+  } while (0)
+  if (rows == 1) KD_FEW(1);
+  else if (rows == 2) KD_FEW(2);
+  else KD_FEW(4);
+#undef KD_FEW
+  prof_after(s);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace kd

@@ -387,7 +387,7 @@ struct LoadKeep {
 };
 
 // Stream vectors [lo, hi) of a row through the block's first THREADS threads, ROW_GROUP vectors of a
-// thread in flight while the previous ones are added:
+// thread at a time:
 //   load(address)        reads a vector
 //   fix(vector, i)       may change vector i before it is added
 //   on_group(round, max) sees the largest element of each group of a thread
@@ -419,14 +419,12 @@ __device__ __forceinline__ void stream_stats(const Row<DT>& row, int lo, int hi,
     i0 += STEP;
     ++round;
   };
-  uint4 even[ROW_GROUP], uneven[ROW_GROUP];
-  load(even, i0);
+  // one set of registers: a second one, loaded while the first is added, measured slower, since it
+  // halves the warps that an SM holds
   while (i0 < end) {
-    if (i0 + STEP < end) load(uneven, i0 + STEP);
-    add(even);
-    if (i0 >= end) break;
-    if (i0 + STEP < end) load(even, i0 + STEP);
-    add(uneven);
+    uint4 v[ROW_GROUP];
+    load(v, i0);
+    add(v);
   }
   const int edge = threadIdx.x == 0 ? 0 : row.nv - 1;
   if (threadIdx.x < 2 && edge >= lo && edge < hi && !row.whole(edge) && (threadIdx.x == 0 || edge != 0)) {

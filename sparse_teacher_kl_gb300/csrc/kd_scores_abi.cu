@@ -125,8 +125,7 @@ int kd_logits_kl_fwd(const void* logits, int dtype, int64_t N, int64_t V, int64_
   if (launch_logits_kl(1, logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, stats_out, kl, nullptr,
                        nullptr, nullptr, 0, &ctrl->err, s) != cudaSuccess)
     return KD_ERR_CUDA;
-  if (launch_count_valid(mask, N, &ctrl->n_valid, s) != cudaSuccess) return KD_ERR_CUDA;
-  return map_cuda(launch_loss_reduce(kl, mask, N, &ctrl->n_valid, loss_out, s));
+  return map_cuda(launch_masked_mean(kl, mask, N, loss_out, s));
 }
 
 int kd_logits_kl_bwd(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* t_ids,
@@ -163,11 +162,12 @@ int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V, int64
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Ctrl* ctrl = static_cast<Ctrl*>(ws);
   float* kl = kl_per_token_out ? kl_per_token_out : reinterpret_cast<float*>(ctrl + 1);
-  if (launch_count_valid(mask, N, &ctrl->n_valid, s) != cudaSuccess) return KD_ERR_CUDA;
+  const int32_t* n_valid;
+  if ((st = count_valid(mask, N, ctrl, &n_valid, s)) != KD_OK) return st;
   if (launch_logits_kl(3, logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, nullptr, kl, grad_loss,
-                       &ctrl->n_valid, grad_logits, ld_grad, &ctrl->err, s) != cudaSuccess)
+                       n_valid, grad_logits, ld_grad, &ctrl->err, s) != cudaSuccess)
     return KD_ERR_CUDA;
-  return map_cuda(launch_loss_reduce(kl, mask, N, &ctrl->n_valid, loss_out, s));
+  return map_cuda(launch_masked_mean(kl, mask, N, loss_out, s));
 }
 
 }  // extern "C"
