@@ -19,7 +19,8 @@ namespace kd {
 
 constexpr int LK_MAX_CLUSTER = 16;
 constexpr int LK_MAX_SMEM = 200 * 1024;
-constexpr int LKB_THREADS = 512;       // backward
+constexpr int LKB_THREADS = 256;       // backward
+constexpr int LKB_PER_SM = 4;
 
 struct LogitsKlArgs {
   const void* z;
@@ -607,17 +608,17 @@ static cudaError_t lk_launch(LogitsKlArgs a, int ctas, cudaStream_t s) {
 }
 
 // How a row is shared out, by its bytes:
-//   up to 96 KB   four blocks of 288 threads on an SM, a row each
-//   up to 192 KB  two of 512
+//   up to 96 KB   four blocks of 288 threads on an SM, a row each (up to 32 KB: also few rows)
+//   up to 208 KB  two of 512
 //   longer        one of 1024; over 416 KB a cluster of two or more, so that the rows in flight
-//                 (at most 152 x 4 x 96 KB = 58 MB, 152 x 416 KB = 62 MB) stay in half of L2
+//                 (at most 152 x 4 x 96 KB = 58 MB, 152 x 416 KB = 63 MB) stay in half of L2
 // With few rows a cluster takes each, while a thread keeps more than a group of vectors.
 template <int DT, bool REST, bool STEP>
 static cudaError_t lk_one(const LogitsKlArgs& a, cudaStream_t s) {
   const int64_t nv = a.V / Elt<DT>::kVec + 2, kb = nv * 16 / 1024;
   const int sms = gemm_max_grid();
-  if (a.N > sms && kb <= 96) return lk_launch<DT, REST, STEP, 8, 1, 4>(a, 1, s);
-  if (a.N > sms && kb <= 192) return lk_launch<DT, REST, STEP, 13, 3, 2>(a, 1, s);
+  if ((a.N > sms && kb <= 96) || kb <= 32) return lk_launch<DT, REST, STEP, 8, 1, 4>(a, 1, s);
+  if (a.N > sms && kb <= 208) return lk_launch<DT, REST, STEP, 13, 3, 2>(a, 1, s);
   int c = 1;
   while (c < LK_MAX_CLUSTER && kb > int64_t(416) * c) c *= 2;
   while (2 * c <= LK_MAX_CLUSTER && a.N * c * 2 <= sms && nv >= 2 * c * 1024) c *= 2;
@@ -629,7 +630,7 @@ static cudaError_t lk_one(const LogitsKlArgs& a, cudaStream_t s) {
 // entries first and rewrites their gradients last, and every vector is read and written by one
 // thread.  One pass over the row: bound by HBM (2 N V elements).
 template <int DT, bool REST>
-__global__ void __launch_bounds__(LKB_THREADS) kd_logits_kl_bwd_kernel(const LogitsKlArgs a) {
+__global__ void __launch_bounds__(LKB_THREADS, LKB_PER_SM) kd_logits_kl_bwd_kernel(const LogitsKlArgs a) {
   extern __shared__ __align__(16) uint8_t lkb_raw[];
   __shared__ LkEntryScratch scratch;
   __shared__ LkRow sh_row;
@@ -677,13 +678,16 @@ static cudaError_t lk_bwd_one(LogitsKlArgs a, cudaStream_t s) {
   static PerDevice<int> done;
   const auto kernel = kd_logits_kl_bwd_kernel<DT, REST>;
   const int64_t nv = a.V / Elt<DT>::kVec + 2;
-  // blocks per row: more than one where the rows alone leave SMs idle, each of a group a thread
+  // blocks per row: more than one where the rows alone leave SMs idle, while each thread keeps two
+  // groups of vectors, or where a row's bitmap is more than a block's share of shared memory
   a.slices = 1;
-  while (a.N * a.slices < 2 * gemm_max_grid() && nv >= 2 * a.slices * ROW_GROUP * LKB_THREADS) a.slices *= 2;
+  while ((a.N * a.slices < int64_t(LKB_PER_SM) * gemm_max_grid() &&
+          nv >= int64_t(4) * a.slices * ROW_GROUP * LKB_THREADS) ||
+         lk_entry_bytes((nv + a.slices - 1) / a.slices, a.K) > LK_MAX_SMEM)
+    a.slices *= 2;
   const int64_t smem = lk_entry_bytes((nv + a.slices - 1) / a.slices, a.K);
   const cudaError_t e = smem_attr_once(done, reinterpret_cast<const void*>(kernel), LK_MAX_SMEM);
   if (e != cudaSuccess) return e;
-  if (smem > LK_MAX_SMEM) return cudaErrorInvalidValue;  // logits_kl_fits leaves room
   kernel<<<unsigned(a.N * a.slices), LKB_THREADS, size_t(smem), s>>>(a);
   return cudaGetLastError();
 }

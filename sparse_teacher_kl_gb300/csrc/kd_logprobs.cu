@@ -15,12 +15,13 @@ namespace kd {
 
 constexpr int LP_THREADS = 256;      // forward
 constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_PER_SM = 5;         // blocks on an SM
+constexpr int LP_PER_SM = 6;         // blocks on an SM
 constexpr int LP_SLOTS = 32;         // group maxima kept per thread
 constexpr int LP_CAND = 1024;        // candidates for the top alternatives
 constexpr int LP_LIST = 512;         // groups that may hold one
 constexpr int LP_MAX_CLUSTER = 16;
-constexpr int LB_THREADS = 512;      // backward
+constexpr int LB_THREADS = 256;      // backward
+constexpr int LB_PER_SM = 4;
 
 // ------------------------------------------------------------ alternatives ---
 // The n largest elements of a row, exactly, without selecting while it streams by.  While the
@@ -33,11 +34,16 @@ constexpr int LB_THREADS = 512;      // backward
 // Each element's rank key is unique, (value, ~id), so the order is the id's on ties, and a
 // candidate's place is the number of candidates above it.  When ties or a crowded row bring
 // more candidates than the buffer holds, the row is counted and collected directly.
+// In a cluster of c each CTA does this for its share, and sends the first one the keys of its list
+// from a bound on: the row's n-th key is at least every share's n-th, and at least the smallest
+// of the shares' ceil(n / c)-th.
 
 struct TopState {
   unsigned long long cand[LP_CAND];
   int count;
-  int groups;              // of this CTA
+  int groups;
+  int merged;              // in the first CTA: keys that the cluster sent
+  unsigned long long sorted[KD_MAX_TOP];
   uint32_t list[LP_LIST];  // slot * LP_THREADS + thread
 };
 
@@ -101,7 +107,10 @@ __device__ void collect_crowded(const Row<DT>& row, int lo, int hi, int n, uint3
   if (threadIdx.x == 0) ts.count = 0;
   __syncthreads();
   for_each<DT>(row, lo, hi, [&](int64_t c, float x) {
-    if (order_key(x) > T) ts.cand[atomicAdd(&ts.count, 1)] = rank_key(x, c);  // fewer than n of them
+    if (order_key(x) > T) {
+      const int at = atomicAdd(&ts.count, 1);  // fewer than n of them, but in a row of NaNs
+      if (at < LP_CAND) ts.cand[at] = rank_key(x, c);
+    }
   });
   __syncthreads();
   // columns in ascending order, a block's width at a time, until n are found
@@ -154,7 +163,7 @@ struct LpShared {
   uint32_t nth[LP_WARPS];
   // written by the CTAs of the row's cluster (each its own entry)
   RowStats part[LP_MAX_CLUSTER];
-  uint32_t floor[LP_MAX_CLUSTER];
+  unsigned long long nth_key[LP_MAX_CLUSTER], part_key[LP_MAX_CLUSTER];  // the share's n-th, ceil(n / c)-th
   int scratch[32];
 };
 
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
   const Row<DT> row(static_cast<const typename Elt<DT>::raw*>(a.z) + r * a.ld, a.V);
   const int share = (row.nv + int(ctas) - 1) / int(ctas);
   const int lo = min(int(rank) * share, row.nv), hi = min(lo + share, row.nv);
-  if (TOP && tid == 0) ts.count = ts.groups = 0;
+  if (TOP && tid == 0) ts.count = ts.groups = ts.merged = 0;
   __syncwarp();
   if (ctas > 1) cluster_arrive();  // waited for before the first access to another CTA
 
@@ -233,28 +242,86 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
     for (int w = 0; w < full_warps; ++w) floor = min(floor, sh.nth[w]);
   }
 
+  // ---- the share's candidates, and in a cluster its n largest
+  if (TOP) {
+    const float floor_v = floor ? order_value(floor) : -INFINITY;
+    auto test = [&](int i) {
+      float x[VE];
+      unpack_vec<DT>(row.load(i), x);
+      const int64_t c0 = row.col(i);
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (x[e] >= floor_v && c0 + e >= 0 && c0 + e < row.V) {
+          const int at = atomicAdd(&ts.count, 1);
+          if (at < LP_CAND) ts.cand[at] = rank_key(x[e], c0 + e);
+        }
+    };
+    if (own_max >= floor_v) {
+      const int slots = rounds > 0 ? ((rounds - 1) >> shift) + 1 : 0;
+      for (int q = 0; q < slots; ++q)
+        if (slot_max[q * LP_THREADS + tid] >= floor_v) {
+          const int at = atomicAdd(&ts.groups, 1);
+          if (at < LP_LIST) ts.list[at] = uint32_t(q * LP_THREADS + tid);
+        }
+      const int edge = tid == 0 ? 0 : row.nv - 1;
+      if (tid < 2 && edge >= lo && edge < hi && !row.whole(edge) && (tid == 0 || edge != 0)) test(edge);
+    }
+    __syncthreads();
+    const int groups = ts.groups;
+    if (groups <= LP_LIST) {
+      const int vec_bits = 2 + shift;  // vectors of a group
+      static_assert(ROW_GROUP == 4, "a group's vectors as bits");
+      for (int w = tid; w < groups << vec_bits; w += LP_THREADS) {
+        const uint32_t g = ts.list[w >> vec_bits];
+        const int in_group = w & ((1 << vec_bits) - 1);
+        const int round = (int(g / LP_THREADS) << shift) + in_group / ROW_GROUP;
+        const int i = body_lo + round * STEP + (in_group % ROW_GROUP) * LP_THREADS + int(g % LP_THREADS);
+        if (i < body_hi) test(i);
+      }
+    }
+    __syncthreads();
+    if (groups > LP_LIST || ts.count > LP_CAND)  // starts with a barrier
+      collect_crowded<DT>(row, lo, hi, a.top, floor, ts, sh.scratch);
+    if (ctas > 1) {
+      for (int j = tid; j < a.top; j += LP_THREADS) ts.sorted[j] = 0;
+      __syncthreads();
+      const int c = min(ts.count, LP_CAND);
+      for (int i = tid; i < c; i += LP_THREADS) {
+        const unsigned long long mine = ts.cand[i];
+        int place = 0;
+        for (int j = 0; j < c; ++j) place += ts.cand[j] > mine;
+        if (place < a.top) ts.sorted[place] = mine;
+      }
+      __syncthreads();
+    }
+  }
+
   // ---- the row's
+  unsigned long long bound = 0;
   if (ctas > 1) {
     cluster_wait();
-    if (tid < int(ctas)) {
+    if (tid < int(ctas) && (TOP || tid == 0)) {
       LpShared* other = cluster_map(&sh, uint32_t(tid));
-      if (TOP || tid == 0) {
-        other->part[rank] = st;
-        other->floor[rank] = floor;
+      other->part[rank] = st;
+      if (TOP) {
+        other->nth_key[rank] = ts.sorted[a.top - 1];
+        other->part_key[rank] = ts.sorted[(a.top - 1) / int(ctas)];
       }
     }
     cluster_sync();
     if (!TOP && rank != 0) return;
     st = stats_empty();
     const int lane = tid & (LP_MAX_CLUSTER - 1);
-    if (lane < int(ctas)) {
-      st = sh.part[lane];
-      floor = sh.floor[lane];
-    } else {
-      floor = 0;
-    }
+    if (lane < int(ctas)) st = sh.part[lane];
     stats_warp<ENT>(st, a.k, LP_MAX_CLUSTER);
-    if (TOP) floor = __reduce_max_sync(0xffffffffu, floor);  // each CTA's holds for the whole row
+    if (TOP) {
+      unsigned long long least = ~0ull;
+      for (uint32_t q = 0; q < ctas; ++q) {
+        bound = max(bound, sh.nth_key[q]);
+        least = min(least, sh.part_key[q]);
+      }
+      bound = max(bound, least);
+    }
   }
   const bool empty = st.s == 0.f;  // every logit is -inf
   const bool odd = st.s != st.s;   // a NaN or +inf logit
@@ -273,74 +340,39 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
       a.logp[r * a.M + j] = lp;
     }
     if (tid == 0) {
-      const float big = fabsf(st.m) <= kPlainMax ? kLn2 * (__fmul_rn(st.m, a.k) + log2_s) : st.m / a.tau + kLn2 * log2_s;
-      a.lse[r] = empty ? -INFINITY : big;
+      const float lse = fabsf(st.m) <= kPlainMax ? kLn2 * (__fmul_rn(st.m, a.k) + log2_s) : st.m / a.tau + kLn2 * log2_s;
+      a.lse[r] = empty ? -INFINITY : lse;
       if (ENT) a.entropy[r] = empty ? 0.f : kLn2 * (log2_s - st.u / st.s);
     }
   }
   if (!TOP) return;
 
   // ---- the alternatives
-  if (odd) {
-    if (rank == 0)
-      for (int j = tid; j < a.top; j += LP_THREADS) {
-        a.top_ids[r * a.top + j] = j;
-        a.top_logp[r * a.top + j] = st.s;
-      }
-    return;  // the whole cluster: nothing below is waited for
-  }
-  TopState* first = ctas > 1 ? cluster_map(&ts, 0) : &ts;
-  const float floor_v = floor ? order_value(floor) : -INFINITY;
-  auto test = [&](int i) {
-    float x[VE];
-    unpack_vec<DT>(row.load(i), x);
-    const int64_t c0 = row.col(i);
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (x[e] >= floor_v && c0 + e >= 0 && c0 + e < row.V) {
-        const int at = atomicAdd(&first->count, 1);
-        if (at < LP_CAND) first->cand[at] = rank_key(x[e], c0 + e);
-      }
-  };
-  if (own_max >= floor_v) {
-    const int slots = rounds > 0 ? ((rounds - 1) >> shift) + 1 : 0;
-    for (int q = 0; q < slots; ++q)
-      if (slot_max[q * LP_THREADS + tid] >= floor_v) {
-        const int at = atomicAdd(&ts.groups, 1);
-        if (at < LP_LIST) ts.list[at] = uint32_t(q * LP_THREADS + tid);
-      }
-    const int edge = tid == 0 ? 0 : row.nv - 1;
-    if (tid < 2 && edge >= lo && edge < hi && !row.whole(edge) && (tid == 0 || edge != 0)) test(edge);
-  }
-  __syncthreads();
-  const int groups = ts.groups;
-  if (groups > LP_LIST) {
-    if (tid == 0) atomicAdd(&first->count, LP_CAND + 1);
-  } else {
-    const int vec_bits = 2 + shift;  // vectors of a group
-    static_assert(ROW_GROUP == 4, "a group's vectors as bits");
-    for (int w = tid; w < groups << vec_bits; w += LP_THREADS) {
-      const uint32_t g = ts.list[w >> vec_bits];
-      const int in_group = w & ((1 << vec_bits) - 1);
-      const int round = (int(g / LP_THREADS) << shift) + in_group / ROW_GROUP;
-      const int i = body_lo + round * STEP + (in_group % ROW_GROUP) * LP_THREADS + int(g % LP_THREADS);
-      if (i < body_hi) test(i);
-    }
-  }
+  const unsigned long long* keys = ts.cand;
+  int c = min(ts.count, LP_CAND);
   if (ctas > 1) {
+    unsigned long long* merged = reinterpret_cast<unsigned long long*>(lp_smem);  // the maxima have served
+    for (int j = tid; j < a.top; j += LP_THREADS) {
+      const unsigned long long key = ts.sorted[j];
+      if (key != 0 && key >= bound)
+        cluster_map(merged, 0)[atomicAdd(cluster_map(&ts.merged, 0), 1)] = key;
+    }
     cluster_sync();
     if (rank != 0) return;
-  } else {
-    __syncthreads();
+    keys = merged;
+    c = ts.merged;
   }
-  if (ts.count > LP_CAND) {
-    collect_crowded<DT>(row, 0, row.nv, a.top, floor, ts, sh.scratch);  // starts with a barrier
+  if (odd) {
+    for (int j = tid; j < a.top; j += LP_THREADS) {
+      a.top_ids[r * a.top + j] = j;
+      a.top_logp[r * a.top + j] = st.s;
+    }
+    return;
   }
-  const int c = ts.count;
   for (int i = tid; i < c; i += LP_THREADS) {
-    const unsigned long long mine = ts.cand[i];
+    const unsigned long long mine = keys[i];
     int place = 0;
-    for (int j = 0; j < c; ++j) place += ts.cand[j] > mine;
+    for (int j = 0; j < c; ++j) place += keys[j] > mine;
     if (place < a.top) {
       a.top_ids[r * a.top + place] = int32_t(~uint32_t(mine));
       a.top_logp[r * a.top + place] = logp_of(order_value(uint32_t(mine >> 32)));
@@ -380,7 +412,9 @@ static cudaError_t logprobs_fwd_one(const LogprobArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(unsigned(a.N * ctas), 1, 1);
   cfg.blockDim = dim3(LP_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = TOP ? size_t(rounds < LP_SLOTS ? rounds : LP_SLOTS) * LP_THREADS * sizeof(float) : 0;
+  const size_t maxima = size_t(rounds < LP_SLOTS ? rounds : LP_SLOTS) * LP_THREADS * sizeof(float);
+  const size_t merged = ctas > 1 ? size_t(ctas) * a.top * 8 : 0;  // fewer keys than this reach the first CTA
+  cfg.dynamicSmemBytes = TOP ? (maxima > merged ? maxima : merged) : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
@@ -422,7 +456,7 @@ struct LogprobGradArgs {
 // tokens first and rewrites their gradients last, and every vector is read and written by one
 // thread.
 template <int DT>
-__global__ void __launch_bounds__(LB_THREADS) kd_logprobs_bwd_kernel(const LogprobGradArgs a) {
+__global__ void __launch_bounds__(LB_THREADS, LB_PER_SM) kd_logprobs_bwd_kernel(const LogprobGradArgs a) {
   extern __shared__ __align__(16) uint8_t lp_smem[];
   __shared__ float sh_sum[32];
   int32_t* ids = reinterpret_cast<int32_t*>(lp_smem);     // [M]
@@ -523,9 +557,15 @@ cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, 
   a.z = z; a.dz = dz; a.N = N; a.ld = ld; a.ld_dz = ld_dz; a.V = int(V); a.M = M;
   a.tokens = tokens; a.mask = mask; a.inv_tau = 1.0f / tau; a.k = float(1.4426950408889634 / double(tau));
   a.lse = lse; a.entropy = entropy; a.g_logp = g_logp; a.g_ent = g_ent; a.err = err;
-  a.slices = 1;  // more only where dz is not z: a block may read the whole row
+  // blocks per row: more than one where the rows alone leave SMs idle, while each thread keeps two
+  // groups of vectors; one in place, since a block may have to read the whole row first
+  const int64_t nv = V / (dtype == KD_F32 ? 4 : 8);
+  a.slices = 1;
+  while (dz != z && N * a.slices < int64_t(LB_PER_SM) * gemm_max_grid() &&
+         nv >= int64_t(4) * a.slices * ROW_GROUP * LB_THREADS)
+    a.slices *= 2;
   prof_before("kd_logprobs_bwd", s);
-  KD_DISPATCH_TYPE(dtype, kd_logprobs_bwd_kernel<DT><<<unsigned(N), LB_THREADS, size_t(M) * 12, s>>>(a));
+  KD_DISPATCH_TYPE(dtype, kd_logprobs_bwd_kernel<DT><<<unsigned(N * a.slices), LB_THREADS, size_t(M) * 12, s>>>(a));
   prof_after(s);
   return cudaGetLastError();
 }
@@ -539,10 +579,10 @@ cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, 
 
 constexpr int FEW_THREADS = 256;
 constexpr int FEW_VOCAB = 4;
-constexpr int few_per_sm(int rows) { return rows == 1 ? 3 : 2; }  // blocks on an SM, by their registers
+constexpr int FEW_PER_SM = 2;  // blocks on an SM
 
 template <int R>
-__global__ void __launch_bounds__(FEW_THREADS, few_per_sm(R))
+__global__ void __launch_bounds__(FEW_THREADS, FEW_PER_SM)
     kd_logprob_few_kernel(const uint16_t* __restrict__ H, const uint16_t* __restrict__ W, int rows, int d, int64_t V,
                           const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, float k, float inv_tau,
                           float4* __restrict__ partials, int rows_pad) {
@@ -624,7 +664,7 @@ cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, i
                                cudaStream_t s) {
   const int64_t per_block = FEW_VOCAB * (FEW_THREADS / 32);
   int64_t grid = (V + per_block - 1) / per_block;
-  const int most = gemm_max_grid() * few_per_sm(rows);
+  const int most = gemm_max_grid() * FEW_PER_SM;
   if (grid > most) grid = most;
   if (grid > max_units) grid = max_units;
   *units = int(grid);

@@ -199,6 +199,22 @@ def test_ties_and_crowded_rows(kd, cuda_device, V, kind):
         check_both(kd, z, tokens_for(3, V, 1, 4), top=top)
 
 
+@pytest.mark.parametrize("N,V", [(1, 201088), (3, 60001)])
+@pytest.mark.parametrize("top", [20, 128])
+def test_alternatives_of_few_long_rows(kd, cuda_device, N, V, top):
+    """Rows that clusters share: the shares' lists are merged; a row whose largest values lie in one share, a
+    row of NaNs, a row of few distinct values."""
+    z = draw(N, V, torch.bfloat16, 77)
+    check_both(kd, z, tokens_for(N, V, 1, 4), top=top)
+    z[0, 1000:1300] = 40.0 + (torch.arange(300, device="cuda") % 50)
+    check_both(kd, z, tokens_for(N, V, 1, 4), top=top)
+    z[0] = (torch.arange(V, device="cuda") % 3).to(torch.bfloat16)
+    check_both(kd, z, tokens_for(N, V, 1, 4), top=top)
+    z[0] = math.nan
+    r = kd.token_logprobs_forward(z, tokens_for(N, V, 1, 4), top=top)
+    assert torch.isnan(r.top_logp[0]).all() and r.top_ids[0].tolist() == list(range(top))
+
+
 def test_signed_zeros_tie(kd, cuda_device):
     z = torch.tensor([[-0.0, 0.0, -1.0, -0.0, 0.0]], device="cuda")
     assert kd.token_logprobs_forward(z, tokens_for(1, 5, 1, 0), top=5).top_ids.tolist() == [[0, 1, 3, 4, 2]]
