@@ -270,7 +270,7 @@ KD_API int kd_workspace_clear(void* ws, size_t ws_bytes, void* stream);
  * (for a bad teacher id: the first offending row).  A library built with
  * KD_DEBUG (libkdkl_debug.so) also checks the indices its kernels compute and
  * reports one out of range as KD_ERR_DEVICE with the place of the check as the
- * detail (0x7xxx: top-K), after skipping the access.
+ * detail (0x7xxx: top-K and the calls on dense logits), after skipping the access.
  */
 KD_API int kd_get_device_error(void* ws, void* stream, int64_t* detail_out);
 

@@ -149,7 +149,7 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
         ts = fmaf(tj, a.inv_tau, -shift);
         e = expf(REST ? ts - ahead.t_lse : ts);
         const int at = row.lead + id - e_lo;
-        if (at >= 0 && at < e_hi - e_lo) {
+        if (at >= 0 && at < e_hi - e_lo && KD_DCHECK(at / VE / 16 < words, a.err, 0x7701)) {
           const uint32_t bit = 1u << (((at / VE) & 3) * 8 + at % VE);
           if (atomicOr(&t.bits[at / (4 * VE)], bit) & bit) {
             ++o.repeats;

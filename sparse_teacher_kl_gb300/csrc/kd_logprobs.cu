@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
       [&](int round, float g) {
         if (!TOP) return;
         running = fmaxf(running, g);  // a NaN leaves it: such a row has no order
-        slot_max[(round >> shift) * LP_THREADS + tid] = running;
+        if (KD_DCHECK((round >> shift) < LP_SLOTS, a.err, 0x7601)) slot_max[(round >> shift) * LP_THREADS + tid] = running;
         if (((round + 1) & ((1 << shift) - 1)) == 0) running = -INFINITY;
       });
   const float own_max = st.m;
@@ -354,8 +354,10 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
     unsigned long long* merged = reinterpret_cast<unsigned long long*>(lp_smem);  // the maxima have served
     for (int j = tid; j < a.top; j += LP_THREADS) {
       const unsigned long long key = ts.sorted[j];
-      if (key != 0 && key >= bound)
-        cluster_map(merged, 0)[atomicAdd(cluster_map(&ts.merged, 0), 1)] = key;
+      if (key != 0 && key >= bound) {
+        const int at = atomicAdd(cluster_map(&ts.merged, 0), 1);
+        if (KD_DCHECK(at < int(ctas) * a.top, a.err, 0x7602)) cluster_map(merged, 0)[at] = key;
+      }
     }
     cluster_sync();
     if (rank != 0) return;
