@@ -64,6 +64,13 @@ typedef enum {
   KD_F32 = 2
 } kd_dtype;
 
+/* What kd_fused_logprobs_bwd does with grad_W [V, d]. */
+typedef enum {
+  KD_GRAD_ADD_F32 = 0,    /* fp32, added into what the caller passes           */
+  KD_GRAD_STORE_F32 = 1,  /* fp32, overwritten                                 */
+  KD_GRAD_STORE_BF16 = 2  /* bf16, overwritten, rounded once: N <= chunk alone */
+} kd_grad_kind;
+
 #define KD_MAX_K 1024
 #define KD_MAX_TOP 128        /* alternatives per position of kd_token_logprobs_fwd */
 
@@ -392,7 +399,8 @@ KD_API int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V
  * The backward pass recomputes each chunk's logits and takes, per valid position,
  *   dZ_v = (1 / tau) (g [v = token] - p_v (g + h (ln p_v + H)))
  * with g = grad_logp, h = grad_entropy ([N] fp32; grad_entropy and entropy may be NULL
- * together); grad_H, grad_W and the rounding of dZ to bf16 as for kd_fused_kl_bwd.
+ * together); grad_H and the rounding of dZ to bf16 as for kd_fused_kl_bwd; grad_W as
+ * grad_W_kind (kd_grad_kind) says.
  * Workspace: `backward` != 0 asks for what the backward pass needs (both calls may use
  * it; it grows with chunk * V), 0 for the forward pass alone (chunk * V / 16 bytes).
  * ------------------------------------------------------------------------ */
@@ -406,7 +414,8 @@ KD_API int kd_fused_logprobs_fwd(const void* H_bf16, const void* W_bf16, const i
 KD_API int kd_fused_logprobs_bwd(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
                     int64_t N, int64_t d, int64_t V, int64_t chunk, float tau,
                     const float* lse, const float* entropy, const float* grad_logp, const float* grad_entropy,
-                    void* grad_H, int grad_H_is_fp32, float* grad_W, void* ws, size_t ws_bytes, void* stream);
+                    void* grad_H, int grad_H_is_fp32, void* grad_W, int grad_W_kind,
+                    void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * On-disk teacher cache ([ART] paragraph on the first fix: run the teacher once,

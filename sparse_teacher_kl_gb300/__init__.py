@@ -471,8 +471,9 @@ def fused_logprobs_forward(H, W, tokens, mask=None, chunk=4096, tau=1.0, entropy
 
 
 def fused_logprobs_backward(H, W, tokens, lse, grad_logp, mask=None, chunk=4096, tau=1.0, entropy=None,
-                            grad_entropy=None, ws=None, grad_H=None, grad_W=None, grad_H_fp32=False):
-    """kd_fused_logprobs_bwd: (grad_H [N, d] bf16 or fp32, grad_W [V, d] fp32 accumulated)."""
+                            grad_entropy=None, ws=None, grad_H=None, grad_W=None, grad_H_fp32=False, grad_W_bf16=False):
+    """kd_fused_logprobs_bwd: (grad_H [N, d] bf16 or fp32, grad_W [V, d]).  A ``grad_W`` of the caller's (fp32) is
+    added into; without one it is a new tensor, fp32 or with ``grad_W_bf16`` (one chunk only) bf16."""
     N, d, V, dev = _check_projection(H, W, tokens, mask)
     for t, name in ((lse, "lse"), (grad_logp, "grad_logp"), (entropy, "entropy"), (grad_entropy, "grad_entropy")):
         _check(t, name, torch.float32, (N,), dev)
@@ -480,14 +481,17 @@ def fused_logprobs_backward(H, W, tokens, lse, grad_logp, mask=None, chunk=4096,
         ws = _fresh_ws(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 1), dev)
     if grad_H is None:
         grad_H = torch.empty((N, d), dtype=torch.float32 if grad_H_fp32 else torch.bfloat16, device=dev)
+    kind = _abi.KD_GRAD_ADD_F32
     if grad_W is None:
-        grad_W = torch.zeros((V, d), dtype=torch.float32, device=dev)
+        kind = _abi.KD_GRAD_STORE_BF16 if grad_W_bf16 else _abi.KD_GRAD_STORE_F32
+        grad_W = torch.empty((V, d), dtype=torch.bfloat16 if grad_W_bf16 else torch.float32, device=dev)
+    else:
+        _check(grad_W, "grad_W", torch.float32, (V, d), dev)
     _check(grad_H, "grad_H", torch.float32 if grad_H.dtype == torch.float32 else torch.bfloat16, (N, d), dev)
-    _check(grad_W, "grad_W", torch.float32, (V, d), dev)
     st = _abi.kd_fused_logprobs_bwd(_ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), N, d, V, chunk, float(tau), _ptr(lse),
                                     _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_H),
-                                    1 if grad_H.dtype == torch.float32 else 0, _ptr(grad_W), _ptr(ws), ws.numel(),
-                                    _stream(dev))
+                                    1 if grad_H.dtype == torch.float32 else 0, _ptr(grad_W), kind, _ptr(ws),
+                                    ws.numel(), _stream(dev))
     _abi.check(st, "kd_fused_logprobs_bwd")
     return grad_H, grad_W
 
@@ -509,7 +513,7 @@ class _FusedLogprobs(torch.autograd.Function):
         if g_logp is None:
             g_logp = torch.zeros_like(lse)
         grad_H, grad_W = fused_logprobs_backward(H, W, tokens, lse, _f32c(g_logp), ctx.mask, ctx.chunk, ctx.tau, ent,
-                                                 _f32c(g_entropy))
+                                                 _f32c(g_entropy), grad_W_bf16=H.shape[0] <= ctx.chunk)
         return grad_H, grad_W.to(W.dtype), None, None, None, None
 
 

@@ -26,6 +26,9 @@ KD_ERR_IO = 7
 KD_BF16 = 0
 KD_F16 = 1
 KD_F32 = 2
+KD_GRAD_ADD_F32 = 0
+KD_GRAD_STORE_F32 = 1
+KD_GRAD_STORE_BF16 = 2
 KD_MAX_K = 1024
 KD_MAX_TOP = 128
 KD_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -74,7 +77,7 @@ _SIGNATURES = {
     "kd_fused_logprobs_fwd": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_float,
                                        _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "kd_fused_logprobs_bwd": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_float,
-                                       _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_size,
+                                       _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int, _c_ptr, _c_size,
                                        _c_ptr]),
     "kd_workspace_clear": (_c_int, [_c_ptr, _c_size, _c_ptr]),
     "kd_get_device_error": (_c_int, [_c_ptr, _c_ptr, ctypes.POINTER(_c_i64)]),

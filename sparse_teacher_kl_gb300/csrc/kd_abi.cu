@@ -503,7 +503,8 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
 static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids, const float* t_logits,
                     const uint8_t* mask, int64_t N, int64_t d, int64_t V, int K, int64_t chunk, float tau,
                     const float* lse, const float* grad_loss, const void* z_store, void* grad_H, int grad_H_is_fp32,
-                    float* grad_W, void* ws, size_t ws_bytes, void* stream, const LogprobTerm* lp = nullptr) {
+                    void* grad_W, void* ws, size_t ws_bytes, void* stream, const LogprobTerm* lp = nullptr,
+                    int w_kind = KD_GRAD_ADD_F32) {
   kd_status st = lp ? check_logprob_args(H_bf16, W_bf16, lp->tokens, N, d, V, chunk, tau, ws, ws_bytes, true)
                     : check_kl_args(H_bf16, W_bf16, t_ids, t_logits, N, d, V, K, chunk, tau, ws, ws_bytes);
   if (st != KD_OK) return st;
@@ -538,7 +539,11 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   if (!make_tmap_2d_bf16(&tw_k, W_bf16, uint64_t(d), uint64_t(V), uint64_t(d) * 2, BK, BN)) return KD_ERR_CUDA;
   if (!make_tmap_2d_bf16(&tw_k_half, W_bf16, uint64_t(d), uint64_t(V), uint64_t(d) * 2, BK, BN / 2))
     return KD_ERR_CUDA;
-  if (!make_tmap_2d_f32(&tgw, grad_W, uint64_t(d), uint64_t(V), uint64_t(d) * 4, 32, 32)) return KD_ERR_CUDA;
+  if (w_kind == KD_GRAD_STORE_BF16) {  // the boxes that the store epilogue writes; else the accumulate epilogue's
+    if (!make_tmap_2d_bf16(&tgw, grad_W, uint64_t(d), uint64_t(V), uint64_t(d) * 2, 64, 32)) return KD_ERR_CUDA;
+  } else if (!make_tmap_2d_f32(&tgw, grad_W, uint64_t(d), uint64_t(V), uint64_t(d) * 4, 32, 32)) {
+    return KD_ERR_CUDA;
+  }
   if (!make_tmap_2d_bf16(&tw_mn, W_bf16, uint64_t(d), uint64_t(V), uint64_t(d) * 2, 64, BK)) return KD_ERR_CUDA;
   if (d64 && !make_tmap_mn2_bf16(&tw_mn2, W_bf16, uint64_t(d), uint64_t(V), uint64_t(d) * 2, BK * kq))
     return KD_ERR_CUDA;
@@ -635,10 +640,11 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
       if (e != cudaSuccess) return KD_ERR_CUDA;
     }
 
-    // B3: grad_W += dZ^T H_c  (A = dZ with V contiguous, B = H_c with d contiguous)
+    // B3: grad_W += dZ^T H_c  (A = dZ with V contiguous, B = H_c with d contiguous); a first chunk that
+    // is stored needs no zeroed grad_W and reads none
     GemmProblem r{};
     r.M = int(V); r.N = int(d); r.K = n;
-    r.a_mn = 1; r.b_mn = 1; r.epi = EPI_ACCUM;
+    r.a_mn = 1; r.b_mn = 1; r.epi = (w_kind != KD_GRAD_ADD_F32 && c0 == 0) ? EPI_STORE : EPI_ACCUM;
     r.m_tiles = int((V + BM - 1) / BM);
     r.n_tiles = int((d + BN - 1) / BN);
     r.n_group = 1;
@@ -646,7 +652,8 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     r.k_splits = 1;
     set_cluster(r);
     r.n_units = ((r.m_tiles + r.cluster - 1) / r.cluster) * r.n_tiles;
-    r.C = grad_W; r.ldc = d; r.c_bf16 = 0; r.err = &ctrl->err;
+    r.C = grad_W; r.ldc = d; r.err = &ctrl->err;
+    r.c_bf16 = r.c_tma = w_kind == KD_GRAD_STORE_BF16;
     r.b_box2 = r.cta_pair && d64;
     e = launch_gemm(r, r.cta_pair ? tdz_mn_p : tdz_mn, r.b_box2 ? th_mn2 : (r.cta_pair ? th_mn_p : th_mn), tgw,
                     grid_max, s);
@@ -692,14 +699,17 @@ int kd_fused_logprobs_fwd(const void* H_bf16, const void* W_bf16, const int32_t*
 int kd_fused_logprobs_bwd(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
                           int64_t N, int64_t d, int64_t V, int64_t chunk, float tau, const float* lse,
                           const float* entropy, const float* grad_logp, const float* grad_entropy, void* grad_H,
-                          int grad_H_is_fp32, float* grad_W, void* ws, size_t ws_bytes, void* stream) {
+                          int grad_H_is_fp32, void* grad_W, int grad_W_kind, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (grad_W_kind < KD_GRAD_ADD_F32 || grad_W_kind > KD_GRAD_STORE_BF16) return KD_ERR_INVALID_ARG;
+  if (grad_W_kind == KD_GRAD_STORE_BF16 && N > chunk) return KD_ERR_INVALID_ARG;
   LogprobTerm lp{};
   lp.tokens = tokens;
   lp.g_logp = grad_logp;
   lp.g_entropy = grad_entropy;
   lp.entropy_in = entropy;
   return bwd_impl(H_bf16, W_bf16, nullptr, nullptr, mask, N, d, V, 1, chunk, tau, lse, nullptr, nullptr, grad_H,
-                  grad_H_is_fp32, grad_W, ws, ws_bytes, stream, &lp);
+                  grad_H_is_fp32, grad_W, ws, ws_bytes, stream, &lp, grad_W_kind);
 }
 
 int kd_chunked_kl_fwd(const void* H_bf16, const void* W_bf16, const int32_t* t_ids, const float* t_logits,

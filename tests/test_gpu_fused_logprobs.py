@@ -116,6 +116,28 @@ def test_grad_W_accumulates(kd, cuda_device):
     assert torch.allclose(twice, once + base, atol=1e-6, rtol=0)
 
 
+@pytest.mark.parametrize("N,d,V", [(1, 64, 1000), (130, 72, 257), (512, 192, 3000)])
+def test_grad_W_kinds(kd, cuda_device, N, d, V):
+    """Stored fp32 and bf16 gradients: nothing of what the memory held before is left in them."""
+    H, W, tokens, gl, ge = case(N, d, V)
+    _, lse, ent, _ = kd.fused_logprobs_forward(H, W, tokens, entropy=True)
+    _, _, rW = reference(H, W, tokens, None, 1.0, gl, ge)
+    zero = torch.zeros((V, d), device="cuda")
+    _, added = kd.fused_logprobs_backward(H, W, tokens, lse, gl, entropy=ent, grad_entropy=ge, grad_W=zero)
+    junk = torch.full((V, d), float("nan"), device="cuda")
+    del junk   # its memory is likely the next allocation's
+    _, stored = kd.fused_logprobs_backward(H, W, tokens, lse, gl, entropy=ent, grad_entropy=ge)
+    _, narrow = kd.fused_logprobs_backward(H, W, tokens, lse, gl, entropy=ent, grad_entropy=ge, grad_W_bf16=True)
+    assert torch.equal(stored, added) and narrow.dtype == torch.bfloat16
+    assert torch.equal(narrow, stored.to(torch.bfloat16))
+    assert off(stored, rW) <= 1e-2
+    _, chunked = kd.fused_logprobs_backward(H, W, tokens, lse, gl, chunk=128, entropy=ent, grad_entropy=ge)
+    assert off(chunked, rW) <= 1e-2
+    if N > 128:
+        with pytest.raises(kd.KDError):
+            kd.fused_logprobs_backward(H, W, tokens, lse, gl, chunk=128, entropy=ent, grad_entropy=ge, grad_W_bf16=True)
+
+
 def test_autograd(kd, cuda_device):
     H, W, tokens, gl, ge = case(140, 96, 800)
     s, rH, rW = reference(H, W, tokens, None, 1.0, gl, ge)

@@ -103,12 +103,12 @@ def test_wrappers_refuse_wrong_tensors():
 
 def _fused(lib, backward, **kw):
     a = dict(H=P, W=P, tok=P, mask=None, N=256, d=64, V=1000, chunk=128, tau=1.0, logp=P, lse=P, ent=P, gl=P, ge=P,
-             gH=P, f32=0, gW=P, ws=P, wsb=1 << 30)
+             gH=P, f32=0, gW=P, kind=0, ws=P, wsb=1 << 30)
     a.update(kw)
     head = (a["H"], a["W"], a["tok"], a["mask"], a["N"], a["d"], a["V"], a["chunk"], a["tau"])
     if backward:
         return lib.kd_fused_logprobs_bwd(*head, a["lse"], a["ent"], a["gl"], a["ge"], a["gH"], a["f32"], a["gW"],
-                                         a["ws"], a["wsb"], None)
+                                         a["kind"], a["ws"], a["wsb"], None)
     return lib.kd_fused_logprobs_fwd(*head, a["logp"], a["lse"], a["ent"], a["ws"], a["wsb"], None)
 
 
@@ -117,7 +117,7 @@ def _fused(lib, backward, **kw):
     dict(H=None), dict(W=None), dict(H=P + 8), dict(tok=None), dict(tok=P + 1), dict(lse=None), dict(lse=P + 2))]
     + [(False, k) for k in (dict(logp=None), dict(logp=P + 1), dict(ent=P + 2))]
     + [(True, k) for k in (dict(gl=None), dict(ent=None), dict(gH=None), dict(gW=None), dict(gH=P + 4), dict(gW=P + 8),
-                           dict(ge=P + 2))])
+                           dict(ge=P + 2), dict(kind=3), dict(kind=-1), dict(kind=2, N=129))])
 def test_fused_logprobs_refuse(lib, backward, kw):
     assert _fused(lib, backward, **kw) == _abi.KD_ERR_INVALID_ARG
 
