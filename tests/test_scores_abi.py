@@ -129,3 +129,9 @@ def test_fused_logprobs_refuse_a_bad_workspace(lib, backward):
     assert _fused(lib, backward, ws=None) == _abi.KD_ERR_WORKSPACE
     assert _fused(lib, backward, ws=P + 64) == _abi.KD_ERR_WORKSPACE
     assert lib.kd_fused_logprobs_workspace(0, 64, 1000, 128, 1) == 0
+
+
+def test_workspace_clear_refuses(lib):
+    assert lib.kd_workspace_clear(None, 4096, None) == _abi.KD_ERR_WORKSPACE
+    assert lib.kd_workspace_clear(P + 64, 4096, None) == _abi.KD_ERR_WORKSPACE
+    assert lib.kd_workspace_clear(P, 255, None) == _abi.KD_ERR_WORKSPACE
