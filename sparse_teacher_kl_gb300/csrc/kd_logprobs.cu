@@ -583,8 +583,9 @@ cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, 
 // takes FEW_VOCAB rows of W at a time, a lane 16 bytes of each in turn, sums the products over the
 // lanes and keeps running statistics of the logits; a block leaves one partial per hidden state,
 // as the projection engine's epilogue does per tile.
-// Measured, V = 201088, d = 2880 (1.16 GB): 1 / 2 / 4 rows 196 / 214 / 269 us; the engine's 128-row
-// tiles 263 / 269 / 286, and 265 for 5.  Two blocks on an SM: 196 us; 3 203, 4 226.
+// Measured, whole calls, V = 201088, d = 2880 (1.16 GB): one row 187 us (6.2 TB/s, 91 % of the copy
+// bandwidth).  With a slower combine kernel 1 / 2 / 4 rows 196 / 214 / 269 us; the engine's 128-row
+// tiles 263 / 269 / 286, and 265 for 5; two blocks on an SM 196, three 203, four 226.
 
 constexpr int FEW_THREADS = 256;
 constexpr int FEW_VOCAB = 4;
