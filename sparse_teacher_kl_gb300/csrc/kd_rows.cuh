@@ -388,7 +388,7 @@ struct LoadKeep {
 
 // Stream vectors [lo, hi) of a row through the block's first THREADS threads, ROW_GROUP vectors of a
 // thread at a time:
-//   load(address)        reads a vector
+//   get(address)         reads a vector
 //   fix(vector, i)       may change vector i before it is added
 //   on_group(round, max) sees the largest element of each group of a thread
 // The vectors that the row only partly covers are added last, one thread each.
