@@ -44,7 +44,7 @@ struct LogitsKlArgs {
   float4* stats;          // [N] (m, s) of the row and (m, s) outside S
   float* kl;              // [N]
   const float* grad_loss;
-  const int32_t* n_valid; // NULL: N
+  const int32_t* n_valid; // NULL: N, or in a step with a mask the block counts them
   uint32_t* err;
 };
 
@@ -356,6 +356,7 @@ struct LkShared {
   LkPart part[2][LK_MAX_CLUSTER];
   LkEntryScratch entry[2];
   LkRow row[2];
+  int valid[32];  // rows counted by each warp
   uint32_t abort_flag;
 };
 
@@ -452,7 +453,19 @@ __global__ void __launch_bounds__((CW + EW) * 32, PER_SM) kd_logits_kl_kernel(co
     const int warp = tid >> 5;
     float c = 0.f;
     if (STEP) {
-      const float n_valid = a.n_valid ? float(*a.n_valid) : float(a.N);
+      float n_valid = float(a.N);
+      if (a.n_valid) {
+        n_valid = float(*a.n_valid);
+      } else if (a.mask) {
+        int n = 0;
+        for (int64_t i = tid; i < a.N; i += CT) n += a.mask[i] != 0;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) sh.valid[warp] = n;
+        named_sync<CT>(2);
+        n = 0;
+        for (int q = 0; q < CW; ++q) n += sh.valid[q];
+        n_valid = float(n);
+      }
       c = *a.grad_loss * a.inv_tau / n_valid;
     }
     uint32_t exchanges = 0;

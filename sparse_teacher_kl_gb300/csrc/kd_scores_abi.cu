@@ -10,6 +10,10 @@ namespace {
 
 constexpr int64_t kMaxV = int64_t(1) << 30;
 
+// A step over up to this many rows lets each block count the valid ones, which costs less than a
+// launch does (128 x 4096: 14.5 against 16.6 us; 8192 x 4096: 67.3 against 69.7).
+constexpr int64_t kCountInBlock = 8192;
+
 size_t elt_size(int dtype) { return dtype == KD_F32 ? 4 : 2; }
 
 // What every call on dense logits checks: sizes, type, temperature, alignment to the element.
@@ -162,8 +166,8 @@ int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V, int64
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Ctrl* ctrl = static_cast<Ctrl*>(ws);
   float* kl = kl_per_token_out ? kl_per_token_out : reinterpret_cast<float*>(ctrl + 1);
-  const int32_t* n_valid;
-  if ((st = count_valid(mask, N, ctrl, &n_valid, s)) != KD_OK) return st;
+  const int32_t* n_valid = nullptr;
+  if (N > kCountInBlock && (st = count_valid(mask, N, ctrl, &n_valid, s)) != KD_OK) return st;
   if (launch_logits_kl(3, logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, nullptr, kl, grad_loss,
                        n_valid, grad_logits, ld_grad, &ctrl->err, s) != cudaSuccess)
     return KD_ERR_CUDA;
