@@ -511,8 +511,11 @@ __global__ void __launch_bounds__((CW + EW) * 32, PER_SM) kd_logits_kl_kernel(co
       else stream_stats<DT, false, CT>(in, lo, hi, a.k, st, LoadOnce(), without_s, [](int, float) {});
       __syncwarp();
       stats_warp<false>(st, a.k);
-      if (lane == 0) sh.warp[b][warp] = st;
+      // The wait stands before the write: the row's entries are posted after every consumer warp is done
+      // with row it - 2, and so warp 0 has read that row's statistics.  (A padding row between the two has
+      // no barrier of the consumers that would say so.)
       if (!REST) wait(&sh.ready[b], uint32_t(it >> 1) & 1u, 0x602u);
+      if (lane == 0) sh.warp[b][warp] = st;
       named_sync<CT>(2);
       if (warp == 0) {
         st = lane < CW ? sh.warp[b][lane] : stats_empty();
