@@ -275,9 +275,10 @@ __device__ __forceinline__ void stats_add(RowStats& st, const uint4 (&v)[N], flo
     stats_rescale(st, gmax, k);
   }
   // An element of -inf has weight 0, but its exponent must stay finite for u: elements are
-  // raised to a floor, which changes nothing while the floor's own weight is 0.
+  // raised to a floor, which changes nothing while the floor's own weight is 0 and its exponent
+  // finite (not at temperatures below 1e-8, nor fp16 ones above a few hundred: the loop below then).
   constexpr float kFloor = DT == KD_F16 ? -65504.f : -1e30f;
-  if (fabsf(st.m) <= kPlainMax && (!ENT || (st.m - kFloor) * k > 150.f)) {
+  if (fabsf(st.m) <= kPlainMax && (!ENT || ((st.m - kFloor) * k > 150.f && -kFloor * k < 1e38f))) {
     const float off = -__fmul_rn(st.m, k);
     const uint64_t k2 = pack2(k, k), off2 = pack2(off, off);
     uint64_t s2[2] = {0, 0}, u2[2] = {0, 0};
