@@ -119,11 +119,11 @@ def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=1.0) 
             outside = np.ones(V, bool)
             outside[at] = False
             p_rest = max(0.0, 1.0 - float(p.sum())) if outside.any() else 0.0
-            q_rest = float(q[outside].sum())
+            lq_out, lq_rest = _log_softmax(lq[outside]) if outside.any() else (None, -np.inf)
             if p_rest > 0:
-                kl[r] += p_rest * (np.log(p_rest) - np.log(q_rest)) if q_rest > 0 else np.inf
-            if q_rest > 0:
-                d[outside] = q[outside] * (1.0 - p_rest / q_rest)
+                kl[r] += p_rest * (np.log(p_rest) - lq_rest)
+            if lq_rest > -np.inf:
+                d[outside] = (np.exp(lq_rest) - p_rest) * np.exp(lq_out)
         np.add.at(d, at, -p)
         if lse != -np.inf:
             grad[r] = c * d
