@@ -261,9 +261,7 @@ __device__ __forceinline__ LkRow lk_row(const LogitsKlArgs& a, const RowStats& a
     const float p_rest = t.distinct == a.V ? 0.f : fmaxf(1.f - t.e_sum, 0.f);
     float log_q = -INFINITY;  // of the rest
     if (b.s > 0.f) {
-      const bool plain = fmaxf(fabsf(b.m), fabsf(all.m)) <= kPlainMax;
-      const float d = plain ? __fmul_rn(b.m, a.k) - __fmul_rn(all.m, a.k) : (b.m - all.m) * a.k;
-      log_q = kLn2 * (d + log2f(b.s) - w.log2_s);
+      log_q = kLn2 * (stats_shift(b.m, all.m, a.k) + log2f(b.s) - w.log2_s);
     }
     if (p_rest > 0.f) w.rest_kl = p_rest * (logf(p_rest) - log_q);
     w.scale = b.s == 0.f ? 0.f : c * (expf(log_q) - p_rest) / b.s;
@@ -273,7 +271,7 @@ __device__ __forceinline__ LkRow lk_row(const LogitsKlArgs& a, const RowStats& a
     w.inv_sum = 1.f / t.e_sum;
     w.scale = c / b.s;
   }
-  const bool plain = fabsf(b.m) <= kPlainMax;
+  const bool plain = stats_plain(b.m, a.k);
   w.sub = plain || b.m == -INFINITY ? 0.f : b.m;  // nothing outside S: every x there is -inf
   w.off = plain ? -__fmul_rn(b.m, a.k) : 0.f;
   return w;
@@ -303,7 +301,7 @@ __device__ __forceinline__ void lk_stream_grad(const Row<DT>& in, const Row<DT>&
   };
   if (sub == 0.f)
     stream_map<DT, THREADS>(in, out, lo, hi, grad);
-  else  // a row of a type's lowest value: see stats_t
+  else  // far from zero: see stats_t
     stream_map<DT, THREADS>(in, out, lo, hi, [&](float (&x)[VE]) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) x[e] -= sub;

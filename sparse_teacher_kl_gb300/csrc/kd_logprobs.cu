@@ -344,8 +344,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
       a.logp[r * a.M + j] = lp;
     }
     if (tid == 0) {
-      const float lse = fabsf(st.m) <= kPlainMax ? kLn2 * (__fmul_rn(st.m, a.k) + log2_s) : st.m / a.tau + kLn2 * log2_s;
-      a.lse[r] = empty ? -INFINITY : lse;
+      a.lse[r] = empty ? -INFINITY : stats_lse(st.m, log2_s, a.k, a.tau);
       if (ENT) a.entropy[r] = empty ? 0.f : kLn2 * (log2_s - st.u / st.s);
     }
   }
@@ -510,7 +509,7 @@ __global__ void __launch_bounds__(LB_THREADS, LB_PER_SM) kd_logprobs_bwd_kernel(
     __shared__ RowStats sh_stats[LB_THREADS / 32];
     // its barrier: the row is read before any of it is written
     st = stats_block<LB_THREADS, false>(st, a.k, sh_stats);
-    const bool plain = fabsf(st.m) <= kPlainMax;
+    const bool plain = stats_plain(st.m, a.k);
     base = plain ? 0.f : st.m;
     off = plain ? __fmul_rn(st.m, a.k) : 0.f;
     log2_s = log2f(st.s);

@@ -183,37 +183,57 @@ struct Row {
 };
 
 // ----------------------------------------------------- softmax statistics ---
-// Over the elements x seen so far, with k = log2(e) / tau and t(x) = x k - fl(m k):
+// Over the elements x seen so far, with k = log2(e) / tau and t(x) = x k - O(m):
 //   m = max x,  s = sum 2^t,  u = sum 2^t t
-// so that log2 of p(x) is t(x) - log2 s, logsumexp(x / tau) is ln2 (fl(m k) + log2 s) and the
-// entropy of softmax(x / tau) is ln2 (log2 s - u / s), two terms that (but for the rounding of
-// m k) are never negative.  t is one fused multiply-add against the same rounded offset
-// everywhere, so the offset's rounding cancels.  Where |m| is above 1e29 (a row of a type's
-// lowest value) the offset would overflow and t(x) = (x - m) k is taken instead.  An empty set
-// has m = -inf, s = 0; a NaN or +inf element makes s NaN (m skips a NaN).
+// so that log2 of p(x) is t(x) - log2 s, logsumexp(x / tau) is ln2 (O(m) + log2 s) and the
+// entropy of softmax(x / tau) is ln2 (log2 s - u / s).  The offset O(m) is
+//   fl(m k)  where |m k| is up to 2^20: t is one fused multiply-add against the same rounded
+//            offset everywhere, so its rounding (up to 2^-5) cancels;
+//   m k      elsewhere (small temperatures, masks of large finite values), unrounded: there the
+//            rounding would reach 2^7 and more and the sums overflow, so t is (x - m) k.
+// An empty set has m = -inf, s = 0; a NaN or +inf element makes s NaN (m skips a NaN).
 
 struct RowStats {
   float m, s, u;
 };
 __device__ __forceinline__ RowStats stats_empty() { return {-INFINITY, 0.f, 0.f}; }
 
-constexpr float kPlainMax = 1e29f;
+constexpr float kPlainMax = 1048576.f;  // of |m k|
 
-__device__ __forceinline__ float stats_t(float x, float m, float k) {
-  return fabsf(m) <= kPlainMax ? fmaf(x, k, -__fmul_rn(m, k)) : (x - m) * k;
+// Whether the offset of maximum m is rounded; its rounding, m k - O(m).
+__device__ __forceinline__ bool stats_plain(float m, float k) { return fabsf(__fmul_rn(m, k)) <= kPlainMax; }
+__device__ __forceinline__ float stats_rounding(float m, float k) {
+  const float o = __fmul_rn(m, k);
+  return fabsf(o) <= kPlainMax ? fmaf(m, k, -o) : 0.f;
 }
 
-// ln p of an element from its row's statistics, log2_s = log2 of s.
+__device__ __forceinline__ float stats_t(float x, float m, float k) {
+  const float o = __fmul_rn(m, k);
+  return fabsf(o) <= kPlainMax ? fmaf(x, k, -o) : (x - m) * k;
+}
+
+// ln p of an element from its row's statistics, log2_s = log2 of s.  Where x k would overflow
+// although the log probability need not, x / tau is formed instead (fl(m k)'s rounding is nothing
+// beside it).
 __device__ __forceinline__ float stats_logp(float x, float m, float log2_s, float k, float tau) {
-  if (fmaxf(fabsf(x), fabsf(m)) <= kPlainMax) return kLn2 * (stats_t(x, m, k) - log2_s);
+  if (stats_plain(m, k) && fabsf(__fmul_rn(x, k)) <= 1e30f) return kLn2 * (stats_t(x, m, k) - log2_s);
   return (x - m) / tau - kLn2 * log2_s;
 }
 
-// log2 of the factor that takes a sum relative to `from` to one relative to `to` >= from; -200
-// stands for anything that far below (2^-200 is 0 in fp32, and -200 times 0 is 0).
+// logsumexp(x / tau); infinite where fp32 does not hold it.
+__device__ __forceinline__ float stats_lse(float m, float log2_s, float k, float tau) {
+  return stats_plain(m, k) ? kLn2 * (__fmul_rn(m, k) + log2_s) : m / tau + kLn2 * log2_s;
+}
+
+// log2 of the factor that takes a sum relative to `from` to one relative to `to`: O(from) - O(to).
+// The unlikely half is a call, so that it takes no registers of the loops around it (scoring 4096 x
+// 151936: 217 us; in line 227).
+static __device__ __noinline__ float stats_shift_far(float from, float to, float k) {
+  return (from - to) * k + (stats_rounding(to, k) - stats_rounding(from, k));
+}
 __device__ __forceinline__ float stats_shift(float from, float to, float k) {
-  const float t = fmaxf(fabsf(from), fabsf(to)) <= kPlainMax ? __fmul_rn(from, k) - __fmul_rn(to, k) : (from - to) * k;
-  return fmaxf(t, -200.f);
+  const float a = __fmul_rn(from, k), b = __fmul_rn(to, k);
+  return fmaxf(fabsf(a), fabsf(b)) <= kPlainMax ? a - b : stats_shift_far(from, to, k);
 }
 
 __device__ __forceinline__ void stats_rescale(RowStats& a, float to, float k) {
@@ -221,7 +241,8 @@ __device__ __forceinline__ void stats_rescale(RowStats& a, float to, float k) {
     a.m = to;
     return;
   }
-  const float t = stats_shift(a.m, to, k), f = ex2_approx(t);
+  // -200 stands for anything that far below (2^-200 is 0 in fp32, and -200 times 0 is 0)
+  const float t = fmaxf(stats_shift(a.m, to, k), -200.f), f = ex2_approx(t);
   a.u = fmaf(t, a.s, a.u) * f;
   a.s *= f;
   a.m = to;
@@ -278,8 +299,8 @@ __device__ __forceinline__ void stats_add(RowStats& st, const uint4 (&v)[N], flo
   // raised to a floor, which changes nothing while the floor's own weight is 0 and its exponent
   // finite (not at temperatures below 1e-8, nor fp16 ones above a few hundred: the loop below then).
   constexpr float kFloor = DT == KD_F16 ? -65504.f : -1e30f;
-  if (fabsf(st.m) <= kPlainMax && (!ENT || ((st.m - kFloor) * k > 150.f && -kFloor * k < 1e38f))) {
-    const float off = -__fmul_rn(st.m, k);
+  const float off = -__fmul_rn(st.m, k), low = (st.m - kFloor) * k;
+  if (fabsf(off) <= kPlainMax && (!ENT || (low > 150.f && low < 1e38f))) {
     const uint64_t k2 = pack2(k, k), off2 = pack2(off, off);
     uint64_t s2[2] = {0, 0}, u2[2] = {0, 0};
 #pragma unroll

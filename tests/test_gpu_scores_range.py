@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_logprobs import check_forward
+from test_gpu_logprobs import EPS, check_both, check_forward, check_grad, draw, near, run_both, tokens_for
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,99 @@ def test_entropy_of_rows_of_zeros(kd, cuda_device, dtype, V, tau):
     r = kd.token_logprobs_forward(z, torch.zeros((3, 1), dtype=torch.int32, device="cuda"), tau=tau, top=3,
                                   entropy=True)
     check_forward(r, ref, 3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("N,V", [(3, 40), (5, 2051), (2, 201088)])
+@pytest.mark.parametrize("tau", [1e-30, 1e-10, 4e-9, 1e-7, 1e-5, 1e-3])
+def test_small_temperatures(kd, cuda_device, dtype, N, V, tau):
+    z = draw(N, V, dtype, 5)
+    z[1, ::2] = -math.inf
+    tok = tokens_for(N, V, 2, 3)
+    tok[:, 0] = z.argmax(1).to(torch.int32)
+    if dtype is torch.float16:       # its gradients would not fit the type
+        r = kd.token_logprobs_forward(z, tok, tau=tau, top=3, entropy=True)
+        check_forward(r, oracle.token_logprobs(z.double().cpu().numpy(), tok.cpu().numpy(), None, f32(tau), 3), 3)
+    else:
+        check_both(kd, z, tok, tau=f32(tau), top=3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tau", [1e-30, 1e-10, 4e-9, 1e-7, 1e-5, 1e-3])
+def test_small_temperatures_of_many_rows(kd, cuda_device, dtype, tau):
+    """Among many rows some have both tokens on the largest logit, where the gradient's terms cancel: 1e-5
+    of the terms' sizes in the place of the row's largest entry."""
+    z = draw(930, 1003, dtype, 5)
+    z[1, ::2] = -math.inf
+    tok = tokens_for(930, 1003, 2, 3)
+    tok[:, 0] = z.argmax(1).to(torch.int32)
+    r, dz, gl, ge = run_both(kd, z, tok, tau=f32(tau), top=3)
+    host, t = z.double().cpu().numpy(), tok.cpu().numpy()
+    check_forward(r, oracle.token_logprobs(host, t, None, f32(tau), 3), 3)
+    ref = oracle.token_logprobs_grad(host, t, gl.cpu().numpy(), ge.cpu().numpy(), None, f32(tau))
+    terms = (gl.abs().sum(1) + 40 * ge.abs()).double().cpu().numpy()[:, None] / f32(tau)
+    near(dz.double().cpu(), ref, (EPS[dtype] + 1e-4) * np.abs(ref) + 1e-5 * terms)
+
+
+def far_rows(dtype, V=6007):
+    """Rows whose largest logit is far from zero, as a finite mask leaves them, at every size that leaves
+    their differences representable; with a few logits just above the others; with two far values."""
+    low = [-1e4, -6e4] if dtype is torch.float16 else [-1e6, -1e9, -1e10, -1e15, -1e20, -9e28, -1e30, -1e38]
+    z = torch.stack([torch.full((V,), x, device="cuda") for x in low + [-x for x in low]]).to(dtype)
+    step = z.abs() * 2.0 ** -8                    # representable in every type
+    g = torch.Generator(device="cuda").manual_seed(3)
+    up = torch.rand(z.shape, generator=g, device="cuda") < 0.01
+    near_top = torch.where(up, (z.float() + step).to(dtype), z)
+    mixed = z.clone()
+    mixed[:, ::3] = (-z.float() * 0.5).to(dtype)[:, ::3]
+    masked = z.clone()
+    masked[:, 7::501] = 2.5
+    return torch.cat([z, near_top, mixed, masked])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("tau", [1.0, 1.7])
+def test_rows_far_from_zero(kd, cuda_device, dtype, tau):
+    z = far_rows(dtype)
+    check_both(kd, z, tokens_for(z.shape[0], z.shape[1], 2, 1), tau=f32(tau), top=5)
+
+
+# ------------------------------------------------------------- KL on dense logits
+
+def kl_rows(dtype, V=5003, K=12):
+    """Student rows as far_rows, the cached ids with logits of their own or masked like the rest."""
+    z = far_rows(dtype, V)
+    N = z.shape[0]
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ids = torch.argsort(torch.rand((N, V), generator=g, device="cuda"), dim=1)[:, :K]
+    own = torch.arange(N, device="cuda") % 2 == 0
+    z[own] = z[own].scatter(1, ids[own], torch.randn((int(own.sum()), K), generator=g, device="cuda").to(dtype))
+    t = torch.randn((N, K), generator=g, device="cuda") * 2
+    return z, ids.to(torch.int32).contiguous(), t.contiguous(), torch.logsumexp(t, 1) + 0.25
+
+
+def check_kl(kd, z, ids, t, t_lse, tau, grad=0.75):
+    """Forward, backward and step; each row's KL to 4e-7 of itself."""
+    def host(x):
+        return None if x is None else x.double().cpu().numpy() if x.is_floating_point() else x.cpu().numpy()
+
+    ref = oracle.logits_kl(host(z), host(ids), host(t), None, tau, host(t_lse), grad)
+    N, V = z.shape
+    g = torch.full((1,), grad, device="cuda")
+    tol = 6e-5 + 8e-7 * np.abs(np.nan_to_num(ref.kl, posinf=0))
+    ws = kd.workspace(kd._abi.kd_logits_kl_workspace(N, V, ids.shape[1]), "cuda")
+    kl = torch.empty((N,), device="cuda")
+    _, stats, _ = kd.logits_kl_forward(z, ids, t, None, tau, t_lse, ws=ws, kl_out=kl)
+    dz = kd.logits_kl_backward(z, ids, t, None, stats, g, tau, t_lse, ws=ws)
+    near(kl.cpu(), ref.kl, tol)
+    check_grad(dz, ref.grad, z.dtype)
+    _, dz = kd.logits_kl_step(z, ids, t, None, tau, t_lse, g, ws=ws, kl_out=kl)
+    near(kl.cpu(), ref.kl, tol)
+    check_grad(dz, ref.grad, z.dtype)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_kl_of_rows_far_from_zero(kd, cuda_device, dtype, tail):
+    z, ids, t, t_lse = kl_rows(dtype)
+    check_kl(kd, z, ids, t, t_lse if tail else None, 1.0)
