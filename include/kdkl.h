@@ -294,7 +294,8 @@ KD_API int kd_get_device_error(void* ws, void* stream, int64_t* detail_out);
  *            are not looked at; its outputs are 0 and its gradients 0); NULL = all valid.
  *   tau    : temperature > 0; x = logits / tau.
  *   Logits of -inf take no part.  A row whose logits are all -inf has logsumexp -inf,
- *   log probabilities -inf, entropy 0 and zero gradients.  A NaN or +inf logit makes
+ *   log probabilities -inf, entropy 0 and zero gradients; a logsumexp beyond fp32's range is
+ *   infinite as well, with log probabilities and gradients of the row as it is.  A NaN or +inf logit makes
  *   its row's results NaN.  Sums and statistics are fp32.
  * ------------------------------------------------------------------------ */
 

@@ -476,10 +476,12 @@ __global__ void __launch_bounds__(LB_THREADS, LB_PER_SM) kd_logprobs_bwd_kernel(
   const Row<DT> out(static_cast<raw*>(a.dz) + r * a.ld_dz, a.V);
   const int per = (in.nv + a.slices - 1) / a.slices;
   const int lo = min(slice * per, in.nv), hi = min(lo + per, in.nv);
-  const bool live = (a.mask == nullptr || a.mask[r] != 0) && a.lse[r] != -INFINITY;
-  if (!live) {  // padding, or every logit -inf: no gradient
+  auto no_gradient = [&] {  // padding, or every logit -inf
     const float zero[Elt<DT>::kVec] = {};
     for (int i = lo + tid; i < hi; i += LB_THREADS) out.store(i, in.lead, zero);
+  };
+  if (a.mask && a.mask[r] == 0) {
+    no_gradient();
     return;
   }
   float gsum = 0.f;
@@ -502,13 +504,17 @@ __global__ void __launch_bounds__(LB_THREADS, LB_PER_SM) kd_logprobs_bwd_kernel(
   // log2 p = (x - base) k - off - log2_s
   float base = 0.f, off = a.lse[r] * kLog2e, log2_s = 0.f;
   if (fabsf(a.lse[r]) > 1024.f) {
-    // fp32 holds a logsumexp this large to 1e-4 or worse (a row of a type's lowest value: not at
-    // all): take the row's maximum and sum again
+    // fp32 holds a logsumexp this large to 1e-4 or worse (or not at all: -inf may be an overflow, of a
+    // row of a type's lowest value at tau < 1): take the row's maximum and sum again
     RowStats st = stats_empty();
     stream_stats<DT, false, LB_THREADS>(in, 0, in.nv, a.k, st, LoadOnce(), [](uint4&, int) {}, [](int, float) {});
     __shared__ RowStats sh_stats[LB_THREADS / 32];
     // its barrier: the row is read before any of it is written
     st = stats_block<LB_THREADS, false>(st, a.k, sh_stats);
+    if (st.s == 0.f) {
+      no_gradient();
+      return;
+    }
     const bool plain = stats_plain(st.m, a.k);
     base = plain ? 0.f : st.m;
     off = plain ? __fmul_rn(st.m, a.k) : 0.f;

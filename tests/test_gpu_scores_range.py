@@ -138,3 +138,18 @@ def check_kl(kd, z, ids, t, t_lse, tau, grad=0.75):
 def test_kl_of_rows_far_from_zero(kd, cuda_device, dtype, tail):
     z, ids, t, t_lse = kl_rows(dtype)
     check_kl(kd, z, ids, t, t_lse if tail else None, 1.0)
+
+
+def test_gradient_where_the_logsumexp_overflows(kd, cuda_device):
+    """A row of fp32's lowest value at tau < 1: the logsumexp is -inf in fp32, and the row is still uniform;
+    rows of nothing but -inf have no gradient."""
+    z = torch.full((3, 1003), torch.finfo(torch.float32).min, device="cuda")
+    z[1] = -math.inf
+    z[2] = -torch.finfo(torch.float32).min
+    tok = tokens_for(3, 1003, 1, 2)
+    r, dz, gl, ge = run_both(kd, z, tok, tau=0.5)
+    ref = oracle.token_logprobs_grad(z.double().cpu().numpy(), tok.cpu().numpy(), gl.cpu().numpy(), ge.cpu().numpy(),
+                                     None, 0.5)
+    check_grad(dz, ref, torch.float32)
+    assert r.lse.tolist() == [-math.inf, -math.inf, math.inf]
+    near(r.logp.cpu()[[0, 2]], np.full((2, 1), -math.log(1003)), 5e-5)
