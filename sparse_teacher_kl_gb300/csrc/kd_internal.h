@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -141,6 +142,13 @@ struct GemmProblem {
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline kd_status map_cuda(cudaError_t e) { return e == cudaSuccess ? KD_OK : KD_ERR_CUDA; }
+// 1 / tau and log2(e) / tau of the calls on dense logits and of the scores from hidden states, finite
+// for every tau > 0: below 3e-39 (4e-39) they would be infinite, and 0 times them NaN.
+inline float inverse_tau(float tau) { return 1.0f / tau <= FLT_MAX ? 1.0f / tau : FLT_MAX; }
+inline float log2e_over_tau(float tau) {
+  const double k = 1.4426950408889634 / double(tau);
+  return k <= double(FLT_MAX) ? float(k) : FLT_MAX;
+}
 // KD_OK if the current device is an sm_103 GPU.
 kd_status check_device();
 

@@ -15,7 +15,7 @@ cudaError_t launch_logits_kl(int mode, const void* z, int dtype, int64_t N, int6
                              int64_t ld_dz, uint32_t* err, cudaStream_t s) {
   LogitsKlArgs a{};
   a.z = z; a.dz = dz; a.N = N; a.ld = ld; a.ld_dz = ld_dz; a.V = int(V); a.K = K; a.ids = ids; a.tlog = tlog;
-  a.t_lse = t_lse; a.mask = mask; a.tau = tau; a.inv_tau = 1.0f / tau; a.k = float(1.4426950408889634 / double(tau));
+  a.t_lse = t_lse; a.mask = mask; a.tau = tau; a.inv_tau = inverse_tau(tau); a.k = log2e_over_tau(tau);
   a.stats = reinterpret_cast<float4*>(stats); a.kl = kl; a.grad_loss = grad_loss; a.n_valid = n_valid; a.err = err;
   cudaError_t e;
   prof_before(mode == 1 ? "kd_logits_kl_fwd" : mode == 2 ? "kd_logits_kl_bwd" : "kd_logits_kl_step", s);

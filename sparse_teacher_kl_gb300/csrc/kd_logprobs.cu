@@ -432,7 +432,7 @@ cudaError_t launch_logprobs_fwd(const void* z, int dtype, int64_t N, int64_t V, 
                                 float* entropy, int32_t* top_ids, float* top_logp, uint32_t* err, cudaStream_t s) {
   LogprobArgs a{};
   a.z = z; a.N = N; a.ld = ld; a.V = int(V); a.M = M; a.top = top;
-  a.tokens = tokens; a.mask = mask; a.tau = tau; a.k = float(1.4426950408889634 / double(tau));
+  a.tokens = tokens; a.mask = mask; a.tau = tau; a.k = log2e_over_tau(tau);
   a.logp = logp; a.lse = lse; a.entropy = entropy; a.top_ids = top_ids; a.top_logp = top_logp; a.err = err;
   cudaError_t e;
   prof_before("kd_logprobs_fwd", s);
@@ -567,7 +567,7 @@ cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, 
                                 cudaStream_t s) {
   LogprobGradArgs a{};
   a.z = z; a.dz = dz; a.N = N; a.ld = ld; a.ld_dz = ld_dz; a.V = int(V); a.M = M;
-  a.tokens = tokens; a.mask = mask; a.inv_tau = 1.0f / tau; a.k = float(1.4426950408889634 / double(tau));
+  a.tokens = tokens; a.mask = mask; a.inv_tau = inverse_tau(tau); a.k = log2e_over_tau(tau);
   a.lse = lse; a.entropy = entropy; a.g_logp = g_logp; a.g_ent = g_ent; a.err = err;
   // blocks per row: more than one where the rows alone leave SMs idle, while each thread keeps two
   // groups of vectors; one in place, since a block may have to read the whole row first
@@ -683,7 +683,7 @@ cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, i
   if (grid > most) grid = most;
   if (grid > max_units) grid = max_units;
   *units = int(grid);
-  const float k = float(1.4426950408889634 / double(tau));
+  const float k = log2e_over_tau(tau);
   prof_before("kd_logprob_few", s);
   cudaError_t e = cudaSuccess;
 #define KD_FEW(R_)                                                                                                   \
@@ -692,7 +692,7 @@ cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, i
     e = smem_attr_once(done, reinterpret_cast<const void*>(kd_logprob_few_kernel<R_>), FEW_MAX_SMEM);                \
     if (e == cudaSuccess)                                                                                            \
       kd_logprob_few_kernel<R_><<<unsigned(grid), FEW_THREADS, size_t(R_) * d * 4, s>>>(                             \
-          H, W, rows, d, V, tokens, mask, k, 1.0f / tau, partials, BM);                                              \
+          H, W, rows, d, V, tokens, mask, k, inverse_tau(tau), partials, BM);                                              \
   } while (0)
   if (rows == 1) KD_FEW(1);
   else if (rows == 2) KD_FEW(2);

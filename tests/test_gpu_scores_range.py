@@ -153,3 +153,19 @@ def test_gradient_where_the_logsumexp_overflows(kd, cuda_device):
     check_grad(dz, ref, torch.float32)
     assert r.lse.tolist() == [-math.inf, -math.inf, math.inf]
     near(r.logp.cpu()[[0, 2]], np.full((2, 1), -math.log(1003)), 5e-5)
+
+
+@pytest.mark.parametrize("tau", [1e-38, 1e-40, 1e-45, 1e38])
+def test_temperatures_at_the_ends_of_fp32(kd, cuda_device, tau):
+    """1 / tau above or near fp32's largest: one-hot rows, uniform at the other end; no NaN."""
+    z = draw(4, 515, torch.float32, 9)
+    tok = torch.stack([z.argmax(1), z.argmin(1)], 1).to(torch.int32)
+    r, dz, _, _ = run_both(kd, z, tok, tau=tau)
+    zero = kd.token_logprobs_backward(z, tok, r.lse, torch.zeros_like(r.logp), tau=tau)
+    assert not zero.any()
+    if tau < 1:
+        assert r.logp[:, 0].tolist() == [0.0] * 4 and (r.logp[:, 1] < -1e37).all() and not r.entropy.any()
+    else:
+        near(r.logp.cpu(), np.full((4, 2), -math.log(515)), 5e-5)
+        near(r.entropy.cpu(), np.full(4, math.log(515)), 4e-4)
+        assert torch.isfinite(dz).all()
