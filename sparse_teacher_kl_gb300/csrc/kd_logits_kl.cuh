@@ -57,7 +57,7 @@ struct LkEntries {
   uint32_t* bits;   // S within the block's vectors: byte i is vector i, a bit per element
   int32_t* loc;     // [K] element (grid index - e_lo), or -1: absent or another block's;
                     // -2 - element: its id repeats that of another entry
-  float* t;         // [K] t / tau - shift
+  float* t;         // [K] (t - shift) / tau, shift the row's largest t (0 with the rest class)
   float* e;         // [K] probability, but for the factor 1 / sum
   float* z;         // [K] the student's logit, for entries of this block
 };
@@ -140,7 +140,7 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
     tm = sh.t_max[0];
 #pragma unroll
     for (int w = 1; w < EW; ++w) tm = fmaxf(tm, sh.t_max[w]);
-    if (tm != -INFINITY) shift = __fmul_rn(tm, a.inv_tau);
+    if (tm != -INFINITY) shift = tm;
   }
   LkSummary o = lk_nothing();
   o.t_lse = ahead.t_lse;
@@ -153,7 +153,7 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
       if (uint32_t(id) >= uint32_t(a.V)) {
         if (report) raise_error(a.err, KD_DEVERR_BAD_ID, uint32_t(r));
       } else {
-        ts = fmaf(tj, a.inv_tau, -shift);
+        ts = (tj - shift) * a.inv_tau;  // the difference first: t / tau may round by more than 1
         e = expf(REST ? ts - ahead.t_lse : ts);
         const int at = row.lead + id - e_lo;
         if (at >= 0 && at < e_hi - e_lo && KD_DCHECK(at / VE / 16 < words, a.err, 0x7701)) {
@@ -222,7 +222,7 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
 // One warp, whose first lanes hold parts of a row's entries: all of them together.
 __device__ __forceinline__ void lk_merge(const LogitsKlArgs& a, LkSummary& o) {
   const float ref = warp_max(o.z_ref);
-  o.d = warp_sum(o.z_ref == -INFINITY ? o.d : fmaf(-o.e, (o.z_ref - ref) * a.inv_tau, o.d));
+  o.d = warp_sum(o.z_ref == -INFINITY || o.e == 0.f ? o.d : fmaf(-o.e, (o.z_ref - ref) * a.inv_tau, o.d));
   o.z_ref = ref;
   o.e = warp_sum(o.e);
   o.e_sum = warp_sum(o.e_sum);

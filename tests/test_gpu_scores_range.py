@@ -169,3 +169,13 @@ def test_temperatures_at_the_ends_of_fp32(kd, cuda_device, tau):
         near(r.logp.cpu(), np.full((4, 2), -math.log(515)), 5e-5)
         near(r.entropy.cpu(), np.full(4, math.log(515)), 4e-4)
         assert torch.isfinite(dz).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tau", [1e-30, 1e-10, 4e-9, 1e-7, 1e-5, 1e-3])
+def test_kl_at_small_temperatures(kd, cuda_device, dtype, tau):
+    z = draw(40, 1003, dtype, 6)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ids = torch.argsort(torch.rand((40, 1003), generator=g, device="cuda"), dim=1)[:, :9].to(torch.int32).contiguous()
+    t = torch.randn((40, 9), generator=g, device="cuda") * 2
+    check_kl(kd, z, ids, t, None, f32(tau))
