@@ -475,10 +475,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             }
           } else if (EPI == EPI_LSE_H) {
             if (row < p.rows && col0 < p.N) {
-              if (col0 + 32 > p.N) {
+              const bool tail = col0 + 32 > p.N;  // columns past the vocabulary: weight 0
+              if (tail) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (col0 + i >= p.N) x[i] = -1e30f;  // past the vocabulary: weight 0, exponent finite
+                  if (col0 + i >= p.N) x[i] = -INFINITY;
               }
               float cm = x[0];
 #pragma unroll
@@ -492,14 +493,23 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               }
               const float off = -run_m * scale2;
               float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+              if (tail) {  // their exponents are kept finite
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float t0 = fmaf(x[i], scale2, off), t1 = fmaf(x[i + 1], scale2, off);
-                const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
-                s0 += e0;
-                s1 += e1;
-                u0 = fmaf(e0, t0, u0);
-                u1 = fmaf(e1, t1, u1);
+                for (int i = 0; i < 32; ++i) {
+                  const float t0 = fmaf(x[i], scale2, off), e0 = ex2_approx(t0);
+                  s0 += e0;
+                  u0 = fmaf(e0, fmaxf(t0, -200.f), u0);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const float t0 = fmaf(x[i], scale2, off), t1 = fmaf(x[i + 1], scale2, off);
+                  const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+                  s0 += e0;
+                  s1 += e1;
+                  u0 = fmaf(e0, t0, u0);
+                  u1 = fmaf(e1, t1, u1);
+                }
               }
               run_s += s0 + s1;
               run_u += u0 + u1;

@@ -179,3 +179,19 @@ def test_kl_at_small_temperatures(kd, cuda_device, dtype, tau):
     ids = torch.argsort(torch.rand((40, 1003), generator=g, device="cuda"), dim=1)[:, :9].to(torch.int32).contiguous()
     t = torch.randn((40, 9), generator=g, device="cuda") * 2
     check_kl(kd, z, ids, t, None, f32(tau))
+
+
+# ------------------------------------------------------------- from hidden states
+
+@pytest.mark.parametrize("N", [1, 4, 5, 300])
+@pytest.mark.parametrize("V", [33, 1000, 1024, 5003])
+@pytest.mark.parametrize("tau", [1e-30, 1e-10, 1.0])
+def test_fused_entropy_of_equal_logits(kd, cuda_device, N, V, tau):
+    """Logits of 0: the columns past the vocabulary in its last tile weigh nothing at any temperature."""
+    H = torch.zeros((N, 64), dtype=torch.bfloat16, device="cuda")
+    W = torch.ones((V, 64), dtype=torch.bfloat16, device="cuda")
+    tok = torch.full((N,), V - 1, dtype=torch.int32, device="cuda")
+    logp, lse, ent, _ = kd.fused_logprobs_forward(H, W, tok, tau=tau, entropy=True)
+    near(ent.cpu(), np.full(N, math.log(V)), 4e-5 * (1 + math.log(V)))
+    near(lse.cpu(), np.full(N, math.log(V)), 5e-5)
+    near(logp.cpu(), np.full(N, -math.log(V)), 5e-5)
