@@ -425,7 +425,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   float* negent = reinterpret_cast<float*>(w8 + L.negent);
   float* kl = kl_per_token_out ? kl_per_token_out : reinterpret_cast<float*>(w8 + L.kl);
   float4* partials = reinterpret_cast<float4*>(w8 + (lp ? sizeof(Ctrl) : L.partials));
-  const float inv_tau = 1.0f / tau;
+  const float inv_tau = lp ? inverse_tau(tau) : 1.0f / tau;
   const uint16_t* H = static_cast<const uint16_t*>(H_bf16);
 
   if (lp && N <= FEW_ROWS && FEW_ROWS * d * 4 <= FEW_MAX_SMEM) {
@@ -435,7 +435,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     cudaError_t e = launch_logprob_few(H, static_cast<const uint16_t*>(W_bf16), int(N), int(d), V, lp->tokens, mask,
                                        tau, partials, L.n_groups, &units, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
-    return map_cuda(launch_logprob_combine(partials, units, int(N), V, lp->tokens, mask, lp->logp, lse_out,
+    return map_cuda(launch_logprob_combine(partials, units, int(N), V, lp->tokens, mask, tau, lp->logp, lse_out,
                                            lp->entropy, &ctrl->err, 0, s));
   }
 
@@ -477,6 +477,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     p.ids_sorted = ids_sorted; p.p_sorted = p_sorted; p.Kt = K; p.inv_tau = inv_tau;
     p.partials = partials; p.rows = n; p.err = &ctrl->err;
     if (lp) {
+      p.k = log2e_over_tau(tau);
       p.tokens = lp->tokens + c0;
       p.mask = mask ? mask + c0 : nullptr;
     }
@@ -486,7 +487,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
                     grid_max, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
     if (lp)
-      e = launch_logprob_combine(partials, L.n_groups, n, V, lp->tokens + c0, mask ? mask + c0 : nullptr,
+      e = launch_logprob_combine(partials, L.n_groups, n, V, lp->tokens + c0, mask ? mask + c0 : nullptr, tau,
                                  lp->logp + c0, lse_out + c0, lp->entropy ? lp->entropy + c0 : nullptr, &ctrl->err,
                                  c0, s);
     else
@@ -526,7 +527,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   float* p_sorted = reinterpret_cast<float*>(w8 + L.p_sorted);
   float* negent = reinterpret_cast<float*>(w8 + L.negent);
   uint16_t* dz = reinterpret_cast<uint16_t*>(w8 + L.dz);
-  const float inv_tau = 1.0f / tau;
+  const float inv_tau = lp ? inverse_tau(tau) : 1.0f / tau;
   const uint16_t* H = static_cast<const uint16_t*>(H_bf16);
   const size_t gh_elt = grad_H_is_fp32 ? 4 : 2;
 
@@ -598,6 +599,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     p.lse = lse + c0; p.mask = mask ? mask + c0 : nullptr; p.grad_loss = grad_loss; p.n_valid = &ctrl->n_valid;
     p.dz = dz; p.ldz = L.ldz; p.rows = n; p.err = &ctrl->err;
     if (lp) {
+      p.k = log2e_over_tau(tau);
       p.tokens = lp->tokens + c0;
       p.g_logp = lp->g_logp + c0;
       p.g_entropy = lp->g_entropy ? lp->g_entropy + c0 : nullptr;

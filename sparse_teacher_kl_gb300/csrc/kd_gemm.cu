@@ -30,6 +30,7 @@
 #include "kd_device.cuh"
 #include "kd_host_state.h"
 #include "kd_internal.h"
+#include "kd_rows.cuh"
 
 namespace kd {
 
@@ -323,7 +324,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const uint32_t quarter = warp & 3u;  // tensor-memory lane quarter this warp may access
     const int r_local = int(quarter * 32u + lane);
     const uint32_t t_lane = tmem_base + ((quarter * 32u) << 16);
-    const float scale2 = 1.4426950408889634f * p.inv_tau;  // log2(e) / tau
+    // log2(e) / tau; the score epilogues' is rounded once, as the combine's
+    const float scale2 = EPI == EPI_LSE_H || EPI == EPI_DZ_LP ? p.k : 1.4426950408889634f * p.inv_tau;
     uint8_t* my_staging = staging + quarter * 8192u;        // two 4 KB boxes of this warp
     uint32_t sbuf = 0;
     uint32_t acc_it = 0;
@@ -485,18 +487,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
               for (int i = 1; i < 32; ++i) cm = fmaxf(cm, x[i]);
               if (cm > run_m) {
-                const float t = fmaxf((run_m - cm) * scale2, -200.f);  // 2^-200 is 0
+                const float t = fmaxf(stats_shift(run_m, cm, scale2), -200.f);  // 2^-200 is 0
                 const float f = ex2_approx(t);
                 run_u = fmaf(t, run_s, run_u) * f;
                 run_s *= f;
                 run_m = cm;
               }
-              const float off = -run_m * scale2;
+              const float off = -__fmul_rn(run_m, scale2);
               float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
-              if (tail) {  // their exponents are kept finite
+              if (tail || fabsf(off) > kPlainMax || scale2 > 1e8f) {
+                // the last columns, logits far from zero, small temperatures: exponents from differences, kept
+                // finite (see kd_rows.cuh)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                  const float t0 = fmaf(x[i], scale2, off), e0 = ex2_approx(t0);
+                  const float t0 = stats_t(x[i], run_m, scale2), e0 = ex2_approx(t0);
                   s0 += e0;
                   u0 = fmaf(e0, fmaxf(t0, -200.f), u0);
                 }
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       }
       if (EPI == EPI_LSE_H && ok && row < p.rows)
         p.partials[size_t(n_first / p.n_group) * (p.m_tiles * BM) + row] =
-            make_float4(run_m * scale2, run_s, run_g * p.inv_tau, run_u);
+            make_float4(run_m, run_s, run_g * p.inv_tau, run_u);
     }
     if ((EPI == EPI_DZ || EPI == EPI_DZ_LP || EPI == EPI_LSE_Z || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
       bulk_wait_all();  // output boxes done before exit

@@ -121,7 +121,8 @@ struct GemmProblem {
   const float* p_sorted;      // [rows, K] teacher probabilities matching ids_sorted
   int Kt;                     // teacher K
   float inv_tau;
-  float4* partials;           // EPI_LSE: [n_units_per_row, rows] (m2, s, G, 0); EPI_LSE_H: (m2, s, z_token, u)
+  float k;                    // EPI_LSE_H / EPI_DZ_LP: log2(e) / tau
+  float4* partials;           // EPI_LSE: [n_units_per_row, rows] (m2, s, G, 0); EPI_LSE_H: (m, s, z_token / tau, u)
   // EPI_LSE_H / EPI_DZ_LP (chunk-relative): the given token of each row; the gradients that
   // reach its log probability and (NULL: none) the entropy
   const int32_t* tokens;
@@ -217,7 +218,7 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
                                float inv_tau, float* lse_out, float* kl_out, cudaStream_t s);
 // Log probability, logsumexp and entropy (NULL: not wanted) of each row from EPI_LSE_H's partials.
 cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, int rows, int64_t V,
-                                   const int32_t* tokens, const uint8_t* mask, float* logp, float* lse,
+                                   const int32_t* tokens, const uint8_t* mask, float tau, float* logp, float* lse,
                                    float* entropy, uint32_t* err, int64_t row0, cudaStream_t s);
 // EPI_LSE_H's partials for up to FEW_ROWS rows without the tensor cores; *units: how many per row
 // were written (at most max_units).

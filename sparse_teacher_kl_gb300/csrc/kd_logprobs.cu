@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(FEW_THREADS, FEW_PER_SM)
             if (z != z) st[r].s = z;
             else stats_rescale(st[r], z, k);
           }
-          const float t = fmaf(z, k, -__fmul_rn(st[r].m, k)), p = ex2_approx(t);
+          const float t = stats_t(z, st[r].m, k), p = ex2_approx(t);
           st[r].s += p;
           st[r].u = fmaf(p, fmaxf(t, -200.f), st[r].u);
         }
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(FEW_THREADS, FEW_PER_SM)
     stats_warp<true>(s, k);
     if (lane == 0)
       partials[size_t(blockIdx.x) * rows_pad + warp] =
-          make_float4(__fmul_rn(s.m, k), s.s, z_token[warp] * inv_tau, s.u);
+          make_float4(s.m, s.s, z_token[warp] * inv_tau, s.u);
   }
 }
 

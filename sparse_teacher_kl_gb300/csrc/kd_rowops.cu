@@ -7,6 +7,7 @@
 
 #include "kd_device.cuh"
 #include "kd_internal.h"
+#include "kd_rows.cuh"
 
 namespace kd {
 
@@ -229,9 +230,9 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
 }
 
 // --------------------------------------------------- logprob combine ---
-// Merge the per-unit (max, s, z_token, u) partials of a position, s = sum 2^t and u = sum 2^t t
-// with t = (z / tau) log2 e - max:
-//   lse = ln 2 (M + log2 s),  logp = z_token / tau - lse,  entropy = ln 2 (log2 s - u / s)
+// Merge the per-unit (m, s, z_token / tau, u) partials of a position, m the largest logit, s and u the
+// sums of kd_rows.cuh:
+//   lse = ln 2 (O(m) + log2 s),  logp = z_token / tau - lse,  entropy = ln 2 (log2 s - u / s)
 // Threads as in the lse combine, with more phases: a thread's partials are a chain of dependent
 // exponentials, and rows are often few.  Measured (events around the launch): 300 rows of 391 units
 // 14.7 us with 32 phases, 29.7 with 8; one row of 304 units: the call of one hidden state 187 against
@@ -241,8 +242,8 @@ constexpr int LPC_PHASES = 32;
 
 __global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
     kd_logprob_combine_kernel(const float4* __restrict__ partials, int n_units, int rows, int rows_pad, int64_t V,
-                              const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask,
-                              float* __restrict__ logp, float* __restrict__ lse_out, float* __restrict__ entropy,
+                              const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, float k,
+                              float tau, float* __restrict__ logp, float* __restrict__ lse_out, float* __restrict__ entropy,
                               uint32_t* __restrict__ err, int64_t row0) {
   __shared__ float4 sm[LPC_PHASES][LC_ROWS];
   const int x = threadIdx.x, y = threadIdx.y;
@@ -251,12 +252,12 @@ __global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
   auto fold = [&](const float4& q) {
     G += q.z;
     if (q.x > M) {
-      const float t = fmaxf(M - q.x, -200.f), f = exp2f(t);  // 2^-200 is 0 in fp32
+      const float t = fmaxf(stats_shift(M, q.x, k), -200.f), f = exp2f(t);  // 2^-200 is 0 in fp32
       U = fmaf(t, S, U) * f + q.w;
       S = S * f + q.y;
       M = q.x;
     } else {
-      const float t = fmaxf(q.x - M, -200.f), f = exp2f(t);
+      const float t = fmaxf(stats_shift(q.x, M, k), -200.f), f = exp2f(t);
       U += fmaf(t, q.y, q.w) * f;
       S += q.y * f;
     }
@@ -268,15 +269,25 @@ __global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
   sm[y][x] = make_float4(M, S, G, U);
   __syncthreads();
   if (y == 0 && r < rows) {
+    // the phases against their common maximum, so that their exponentials do not wait for one another
     const int units = n_units < LPC_PHASES ? n_units : LPC_PHASES;
-    for (int k = 1; k < units; ++k) fold(sm[k][x]);
+    for (int q = 1; q < units; ++q) M = fmaxf(M, sm[q][x].x);
+    S = G = U = 0.f;
+#pragma unroll 4
+    for (int q = 0; q < units; ++q) {
+      const float4 v = sm[q][x];
+      const float t = fmaxf(stats_shift(v.x, M, k), -200.f), f = exp2f(t);
+      U = fmaf(fmaf(t, v.y, v.w), f, U);
+      S = fmaf(v.y, f, S);
+      G += v.z;
+    }
     if (mask && mask[r] == 0) {
       logp[r] = 0.f;
       lse_out[r] = 0.f;
       if (entropy) entropy[r] = 0.f;
       return;
     }
-    const float l2s = log2f(S), lse = (M + l2s) * 0.69314718055994531f;
+    const float l2s = log2f(S), lse = stats_lse(M, l2s, k, tau);
     const int32_t id = tokens[r];
     const bool bad = id < 0 || int64_t(id) >= V;
     if (bad) raise_error(err, KD_DEVERR_BAD_ID, uint32_t(row0 + r));
@@ -287,12 +298,13 @@ __global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
 }
 
 cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, int rows, int64_t V,
-                                   const int32_t* tokens, const uint8_t* mask, float* logp, float* lse,
+                                   const int32_t* tokens, const uint8_t* mask, float tau, float* logp, float* lse,
                                    float* entropy, uint32_t* err, int64_t row0, cudaStream_t s) {
   const int rows_pad = ((rows + BM - 1) / BM) * BM;
   prof_before("kd_logprob_combine", s);
   kd_logprob_combine_kernel<<<(rows + LC_ROWS - 1) / LC_ROWS, dim3(LC_ROWS, LPC_PHASES), 0, s>>>(
-      partials, n_units_per_row, rows, rows_pad, V, tokens, mask, logp, lse, entropy, err, row0);
+      partials, n_units_per_row, rows, rows_pad, V, tokens, mask, log2e_over_tau(tau), tau, logp, lse, entropy, err,
+      row0);
   prof_after(s);
   return cudaGetLastError();
 }

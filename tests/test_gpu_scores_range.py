@@ -195,3 +195,24 @@ def test_fused_entropy_of_equal_logits(kd, cuda_device, N, V, tau):
     near(ent.cpu(), np.full(N, math.log(V)), 4e-5 * (1 + math.log(V)))
     near(lse.cpu(), np.full(N, math.log(V)), 5e-5)
     near(logp.cpu(), np.full(N, -math.log(V)), 5e-5)
+
+
+def exact_case(N, V, d=64, seed=0, scale=4.0):
+    """Hidden states and a head whose logits are exact in fp32 whatever the order of the sum."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    H = (torch.randint(-16, 17, (N, d), generator=g, device="cuda") / 16.0 * scale).to(torch.bfloat16)
+    W = (torch.randint(-16, 17, (V, d), generator=g, device="cuda") / 32.0).to(torch.bfloat16)
+    tok = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    z = (H.double() @ W.double().T).cpu().numpy()
+    tok[::2] = torch.from_numpy(z.argmax(1)).to(torch.int32).cuda()[::2]
+    return H, W, tok, z
+
+
+@pytest.mark.parametrize("N,V", [(1, 1000), (3, 1003), (4, 4096), (5, 1000), (40, 1024), (300, 1000)])
+@pytest.mark.parametrize("tau", [1e-30, 1e-10, 4e-9, 1e-5])
+def test_fused_entropy_and_logsumexp_at_small_temperatures(kd, cuda_device, N, V, tau):
+    H, W, tok, z = exact_case(N, V)
+    s = oracle.token_logprobs(z, tok.cpu().numpy(), None, f32(tau))
+    _, lse, ent, _ = kd.fused_logprobs_forward(H, W, tok, tau=tau, entropy=True)
+    near(lse.double().cpu(), s.lse, 4e-5 + 4e-7 * np.abs(s.lse))
+    near(ent.double().cpu(), s.entropy, 4e-5 * (1 + s.entropy))
