@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       }
       if (EPI == EPI_LSE_H && ok && row < p.rows)
         p.partials[size_t(n_first / p.n_group) * (p.m_tiles * BM) + row] =
-            make_float4(run_m, run_s, run_g * p.inv_tau, run_u);
+            make_float4(run_m, run_s, run_g, run_u);
     }
     if ((EPI == EPI_DZ || EPI == EPI_DZ_LP || EPI == EPI_LSE_Z || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
       bulk_wait_all();  // output boxes done before exit

@@ -122,7 +122,7 @@ struct GemmProblem {
   int Kt;                     // teacher K
   float inv_tau;
   float k;                    // EPI_LSE_H / EPI_DZ_LP: log2(e) / tau
-  float4* partials;           // EPI_LSE: [n_units_per_row, rows] (m2, s, G, 0); EPI_LSE_H: (m, s, z_token / tau, u)
+  float4* partials;           // EPI_LSE: [n_units_per_row, rows] (m2, s, G, 0); EPI_LSE_H: (m, s, z_token, u)
   // EPI_LSE_H / EPI_DZ_LP (chunk-relative): the given token of each row; the gradients that
   // reach its log probability and (NULL: none) the entropy
   const int32_t* tokens;

@@ -599,7 +599,7 @@ constexpr int FEW_PER_SM = 2;  // blocks on an SM
 template <int R>
 __global__ void __launch_bounds__(FEW_THREADS, FEW_PER_SM)
     kd_logprob_few_kernel(const uint16_t* __restrict__ H, const uint16_t* __restrict__ W, int rows, int d, int64_t V,
-                          const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, float k, float inv_tau,
+                          const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, float k,
                           float4* __restrict__ partials, int rows_pad) {
   extern __shared__ __align__(16) float few_h[];  // [R][d] hidden states
   __shared__ RowStats sh[R][FEW_THREADS / 32];
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(FEW_THREADS, FEW_PER_SM)
     stats_warp<true>(s, k);
     if (lane == 0)
       partials[size_t(blockIdx.x) * rows_pad + warp] =
-          make_float4(s.m, s.s, z_token[warp] * inv_tau, s.u);
+          make_float4(s.m, s.s, z_token[warp], s.u);
   }
 }
 
@@ -692,7 +692,7 @@ cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, i
     e = smem_attr_once(done, reinterpret_cast<const void*>(kd_logprob_few_kernel<R_>), FEW_MAX_SMEM);                \
     if (e == cudaSuccess)                                                                                            \
       kd_logprob_few_kernel<R_><<<unsigned(grid), FEW_THREADS, size_t(R_) * d * 4, s>>>(                             \
-          H, W, rows, d, V, tokens, mask, k, inverse_tau(tau), partials, BM);                                              \
+          H, W, rows, d, V, tokens, mask, k, partials, BM);                                                                \
   } while (0)
   if (rows == 1) KD_FEW(1);
   else if (rows == 2) KD_FEW(2);

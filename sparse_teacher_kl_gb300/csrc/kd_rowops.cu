@@ -230,9 +230,10 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
 }
 
 // --------------------------------------------------- logprob combine ---
-// Merge the per-unit (m, s, z_token / tau, u) partials of a position, m the largest logit, s and u the
+// Merge the per-unit (m, s, z_token, u) partials of a position, m the largest logit, s and u the
 // sums of kd_rows.cuh:
-//   lse = ln 2 (O(m) + log2 s),  logp = z_token / tau - lse,  entropy = ln 2 (log2 s - u / s)
+//   lse = ln 2 (O(m) + log2 s),  logp = ln 2 (t(z_token) - log2 s),  entropy = ln 2 (log2 s - u / s)
+// (logp as a difference of logits: z_token / tau and lse would each be rounded at their own size)
 // Threads as in the lse combine, with more phases: a thread's partials are a chain of dependent
 // exponentials, and rows are often few.  Measured (events around the launch): 300 rows of 391 units
 // 14.7 us with 32 phases, 29.7 with 8; one row of 304 units: the call of one hidden state 187 against
@@ -287,12 +288,12 @@ __global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
       if (entropy) entropy[r] = 0.f;
       return;
     }
-    const float l2s = log2f(S), lse = stats_lse(M, l2s, k, tau);
+    const float l2s = log2f(S);
     const int32_t id = tokens[r];
     const bool bad = id < 0 || int64_t(id) >= V;
     if (bad) raise_error(err, KD_DEVERR_BAD_ID, uint32_t(row0 + r));
-    logp[r] = bad ? __int_as_float(0x7FC00000) : G - lse;
-    lse_out[r] = lse;
+    logp[r] = bad ? __int_as_float(0x7FC00000) : stats_logp(G, M, l2s, k, tau);
+    lse_out[r] = stats_lse(M, l2s, k, tau);
     if (entropy) entropy[r] = (l2s - U / S) * 0.69314718055994531f;
   }
 }

@@ -216,3 +216,22 @@ def test_fused_entropy_and_logsumexp_at_small_temperatures(kd, cuda_device, N, V
     _, lse, ent, _ = kd.fused_logprobs_forward(H, W, tok, tau=tau, entropy=True)
     near(lse.double().cpu(), s.lse, 4e-5 + 4e-7 * np.abs(s.lse))
     near(ent.double().cpu(), s.entropy, 4e-5 * (1 + s.entropy))
+
+
+@pytest.mark.parametrize("N,V", [(1, 1000), (3, 1003), (4, 4096), (5, 1000), (40, 1024), (300, 1000)])
+@pytest.mark.parametrize("tau", [1e-30, 1e-10, 4e-9, 1e-5])
+def test_fused_scores_at_small_temperatures(kd, cuda_device, N, V, tau):
+    H, W, tok, z = exact_case(N, V)
+    s = oracle.token_logprobs(z, tok.cpu().numpy(), None, f32(tau))
+    logp, lse, ent, _ = kd.fused_logprobs_forward(H, W, tok, tau=tau, entropy=True)
+    check_forward(kd.TokenLogprobs(logp, lse, ent, None, None), s, 0)
+
+
+@pytest.mark.parametrize("N,V", [(1, 1000), (4, 1003), (5, 1000), (300, 4096)])
+@pytest.mark.parametrize("tau", [0.001, 0.01, 0.5])
+def test_fused_log_probabilities_keep_their_digits(kd, cuda_device, N, V, tau):
+    """The log probability's error is that of the difference to the largest logit, not of the logit over tau."""
+    H, W, tok, z = exact_case(N, V, seed=1)
+    s = oracle.token_logprobs(z, tok.cpu().numpy(), None, f32(tau))
+    logp, _, _, _ = kd.fused_logprobs_forward(H, W, tok, tau=tau)
+    near(logp.double().cpu(), s.logp[:, 0], 4e-5 + 4e-7 * np.abs(s.logp[:, 0]))
