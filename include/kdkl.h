@@ -401,7 +401,9 @@ KD_API int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V
  *   dZ_v = (1 / tau) (g [v = token] - p_v (g + h (ln p_v + H)))
  * with g = grad_logp, h = grad_entropy ([N] fp32; grad_entropy and entropy may be NULL
  * together); grad_H and the rounding of dZ to bf16 as for kd_fused_kl_bwd; grad_W as
- * grad_W_kind (kd_grad_kind) says.
+ * grad_W_kind (kd_grad_kind) says.  p is taken from lse, so it is as exact as fp32 holds lse
+ * (|lse| 2^-24 of itself); for tau < 1/64 the rows' statistics are taken again instead (the
+ * projection runs once more).
  * Workspace: `backward` != 0 asks for what the backward pass needs (both calls may use
  * it; it grows with chunk * V), 0 for the forward pass alone (chunk * V / 16 bytes).
  * ------------------------------------------------------------------------ */

@@ -398,6 +398,11 @@ static kd_status check_logprob_args(const void* H, const void* W, const int32_t*
                                                                                                  : KD_OK;
 }
 
+// Temperatures below this take the statistics of a chunk's rows again for the gradient: an fp32
+// logsumexp holds p to |lse| 2^-24 of itself, which for logits of 64 passes 2^-12 there (dZ is
+// rounded to 2^-9) and has no digit left below 1e-6.
+constexpr float kRestateTau = 1.0f / 64;
+
 // Forward pass of both modes: z_store == NULL is the fused chunked loss; otherwise
 // each chunk's raw logits are also written (bf16, blocked) for a backward pass that
 // reads them instead of recomputing them.  lp (else NULL): log probabilities of given
@@ -606,9 +611,20 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
       p.entropy = lp->entropy_in ? lp->entropy_in + c0 : nullptr;
     }
     p.a_k3d = p.b_k3d = p.cta_pair && d64;
-    e = launch_gemm(p, p.a_k3d ? th_k2 : th_k,
-                    p.b_k3d ? tw_k2 : (p.cta_pair ? tw_k_half : tw_k), tdz_st,
-                    grid_max, s);
+    const CUtensorMap& ta = p.a_k3d ? th_k2 : th_k;
+    const CUtensorMap& tb = p.b_k3d ? tw_k2 : (p.cta_pair ? tw_k_half : tw_k);
+    if (lp && tau < kRestateTau) {
+      // the rows' statistics once more, in the place of the teacher's sorted ids and probabilities (K = 1)
+      float2* row_stats = reinterpret_cast<float2*>(ids_sorted);
+      p.epi = EPI_LSE_H;
+      p.partials = reinterpret_cast<float4*>(w8 + L.partials);
+      e = launch_gemm(p, ta, tb, tw_k, grid_max, s);
+      if (e == cudaSuccess) e = launch_logprob_row_stats(p.partials, L.n_groups, n, tau, row_stats, s);
+      if (e != cudaSuccess) return KD_ERR_CUDA;
+      p.epi = EPI_DZ_LP;
+      p.row_stats = row_stats;
+    }
+    e = launch_gemm(p, ta, tb, tdz_st, grid_max, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
     }
 

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         if (EPI == EPI_DZ_LP) {
           lse2 = 1e30f;  // p = 0
           if (valid) {
-            lse2 = p.lse[row] * 1.4426950408889634f;
+            lse2 = p.row_stats ? p.row_stats[row].y : p.lse[row] * 1.4426950408889634f;
             const float g = nid == 0x7fffffff ? 0.f : p.g_logp[row] * p.inv_tau;
             const float h = p.g_entropy ? p.g_entropy[row] * p.inv_tau : 0.f;
             np_ = g;
@@ -526,9 +526,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             if (EPI == EPI_DZ_LP) {
               if (row < p.rows) {
                 const int off = nid - col0;
+                float slope = scale2, shift = lse2;
+                if (p.row_stats) {  // small temperatures: the exponents from differences, kept finite
+                  const float m = p.row_stats[row].x;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) x[i] = max_nan((x[i] - m) * scale2 - lse2, -200.f);
+                  slope = 1.f;
+                  shift = 0.f;
+                }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                  const float t = fmaf(x[i], scale2, -lse2);
+                  const float t = fmaf(x[i], slope, -shift);
                   q[i] = ex2_approx(t) * fmaf(c1, t, c0);
                   q[i] = (i == off) ? q[i] + np_ : q[i];
                   if (col0 + i >= p.N) q[i] = 0.f;

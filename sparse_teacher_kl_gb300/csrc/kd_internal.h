@@ -129,6 +129,7 @@ struct GemmProblem {
   const float* g_logp;
   const float* g_entropy;
   const float* entropy;
+  const float2* row_stats;    // EPI_DZ_LP: [rows] (m, log2 s - (m k - O(m))), in the place of lse; or null
   const float* lse;           // EPI_DZ: [rows] natural-log lse (chunk-relative pointer)
   const uint8_t* mask;        // EPI_DZ: [rows] or null (chunk-relative pointer)
   const float* grad_loss;     // EPI_DZ: device scalar
@@ -220,6 +221,9 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
 cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, int rows, int64_t V,
                                    const int32_t* tokens, const uint8_t* mask, float tau, float* logp, float* lse,
                                    float* entropy, uint32_t* err, int64_t row0, cudaStream_t s);
+// GemmProblem::row_stats of each row from EPI_LSE_H's partials.
+cudaError_t launch_logprob_row_stats(const float4* partials, int n_units_per_row, int rows, float tau, float2* row_stats,
+                                     cudaStream_t s);
 // EPI_LSE_H's partials for up to FEW_ROWS rows without the tensor cores; *units: how many per row
 // were written (at most max_units).
 constexpr int FEW_ROWS = 4;

@@ -241,14 +241,11 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
 
 constexpr int LPC_PHASES = 32;
 
-__global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
-    kd_logprob_combine_kernel(const float4* __restrict__ partials, int n_units, int rows, int rows_pad, int64_t V,
-                              const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, float k,
-                              float tau, float* __restrict__ logp, float* __restrict__ lse_out, float* __restrict__ entropy,
-                              uint32_t* __restrict__ err, int64_t row0) {
+// Thread (row r, phase y): the row's partials put together in phase 0's thread, as (m, s, z_token, u).
+__device__ __forceinline__ float4 combine_partials(const float4* __restrict__ partials, int n_units, int rows,
+                                                   int rows_pad, int r, float k) {
   __shared__ float4 sm[LPC_PHASES][LC_ROWS];
   const int x = threadIdx.x, y = threadIdx.y;
-  const int r = blockIdx.x * LC_ROWS + x;
   float M = -INFINITY, S = 0.f, G = 0.f, U = 0.f;
   auto fold = [&](const float4& q) {
     G += q.z;
@@ -282,20 +279,39 @@ __global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
       S = fmaf(v.y, f, S);
       G += v.z;
     }
-    if (mask && mask[r] == 0) {
-      logp[r] = 0.f;
-      lse_out[r] = 0.f;
-      if (entropy) entropy[r] = 0.f;
-      return;
-    }
-    const float l2s = log2f(S);
-    const int32_t id = tokens[r];
-    const bool bad = id < 0 || int64_t(id) >= V;
-    if (bad) raise_error(err, KD_DEVERR_BAD_ID, uint32_t(row0 + r));
-    logp[r] = bad ? __int_as_float(0x7FC00000) : stats_logp(G, M, l2s, k, tau);
-    lse_out[r] = stats_lse(M, l2s, k, tau);
-    if (entropy) entropy[r] = (l2s - U / S) * 0.69314718055994531f;
   }
+  return make_float4(M, S, G, U);
+}
+
+__global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
+    kd_logprob_combine_kernel(const float4* __restrict__ partials, int n_units, int rows, int rows_pad, int64_t V,
+                              const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, float k,
+                              float tau, float* __restrict__ logp, float* __restrict__ lse_out,
+                              float* __restrict__ entropy, uint32_t* __restrict__ err, int64_t row0) {
+  const int r = blockIdx.x * LC_ROWS + threadIdx.x;
+  const float4 st = combine_partials(partials, n_units, rows, rows_pad, r, k);
+  if (threadIdx.y != 0 || r >= rows) return;
+  if (mask && mask[r] == 0) {
+    logp[r] = 0.f;
+    lse_out[r] = 0.f;
+    if (entropy) entropy[r] = 0.f;
+    return;
+  }
+  const float l2s = log2f(st.y);
+  const int32_t id = tokens[r];
+  const bool bad = id < 0 || int64_t(id) >= V;
+  if (bad) raise_error(err, KD_DEVERR_BAD_ID, uint32_t(row0 + r));
+  logp[r] = bad ? __int_as_float(0x7FC00000) : stats_logp(st.z, st.x, l2s, k, tau);
+  lse_out[r] = stats_lse(st.x, l2s, k, tau);
+  if (entropy) entropy[r] = (l2s - st.w / st.y) * 0.69314718055994531f;
+}
+
+__global__ void __launch_bounds__(LC_ROWS * LPC_PHASES)
+    kd_logprob_row_stats_kernel(const float4* __restrict__ partials, int n_units, int rows, int rows_pad, float k,
+                                float2* __restrict__ row_stats) {
+  const int r = blockIdx.x * LC_ROWS + threadIdx.x;
+  const float4 st = combine_partials(partials, n_units, rows, rows_pad, r, k);
+  if (threadIdx.y == 0 && r < rows) row_stats[r] = make_float2(st.x, log2f(st.y) - stats_rounding(st.x, k));
 }
 
 cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, int rows, int64_t V,
@@ -306,6 +322,16 @@ cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, 
   kd_logprob_combine_kernel<<<(rows + LC_ROWS - 1) / LC_ROWS, dim3(LC_ROWS, LPC_PHASES), 0, s>>>(
       partials, n_units_per_row, rows, rows_pad, V, tokens, mask, log2e_over_tau(tau), tau, logp, lse, entropy, err,
       row0);
+  prof_after(s);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_logprob_row_stats(const float4* partials, int n_units_per_row, int rows, float tau, float2* row_stats,
+                                     cudaStream_t s) {
+  const int rows_pad = ((rows + BM - 1) / BM) * BM;
+  prof_before("kd_logprob_row_stats", s);
+  kd_logprob_row_stats_kernel<<<(rows + LC_ROWS - 1) / LC_ROWS, dim3(LC_ROWS, LPC_PHASES), 0, s>>>(
+      partials, n_units_per_row, rows, rows_pad, log2e_over_tau(tau), row_stats);
   prof_after(s);
   return cudaGetLastError();
 }

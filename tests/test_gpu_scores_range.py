@@ -235,3 +235,30 @@ def test_fused_log_probabilities_keep_their_digits(kd, cuda_device, N, V, tau):
     s = oracle.token_logprobs(z, tok.cpu().numpy(), None, f32(tau))
     logp, _, _, _ = kd.fused_logprobs_forward(H, W, tok, tau=tau)
     near(logp.double().cpu(), s.logp[:, 0], 4e-5 + 4e-7 * np.abs(s.logp[:, 0]))
+
+
+@pytest.mark.parametrize("N,V,chunk", [(1, 1000, 128), (5, 1003, 128), (300, 1000, 128), (300, 4096, 512)])
+@pytest.mark.parametrize("tau", [1e-30, 1e-10, 1e-7, 1e-4, 0.02, 0.05])
+def test_fused_gradients_at_small_temperatures(kd, cuda_device, N, V, chunk, tau):
+    """Each entry within bf16's rounding of dZ (2^-9 of its terms, one binade of slack) and 1e-3 of the terms."""
+    H, W, tok, z = exact_case(N, V, seed=2)
+    tau = f32(tau)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    gl = torch.randn((N,), generator=g, device="cuda")
+    ge = torch.randn((N,), generator=g, device="cuda") * 0.2
+    mask = (torch.rand((N,), generator=g, device="cuda") < 0.8).to(torch.uint8)
+    logp, lse, ent, _ = kd.fused_logprobs_forward(H, W, tok, mask, chunk, tau, entropy=True)
+    gH, gW = kd.fused_logprobs_backward(H, W, tok, lse, gl, mask, chunk, tau, ent, ge, grad_H_fp32=True)
+    lp = torch.log_softmax(torch.from_numpy(z) / tau, 1).numpy()
+    p = np.exp(lp)
+    slope = np.where(p > 0, np.maximum(lp, -1e300), 0)
+    H_row = -(p * slope).sum(1, keepdims=True)
+    on = mask.cpu().numpy()[:, None] / tau
+    l, e = gl.double().cpu().numpy()[:, None], ge.double().cpu().numpy()[:, None]
+    one = np.zeros_like(p)
+    one[np.arange(N), tok.cpu().numpy()] = 1
+    dz = on * (l * one - p * (l + e * (slope + H_row)))
+    bound = on * (np.abs(l) * one + p * (np.abs(l) + np.abs(e) * (np.abs(slope) + H_row)))
+    h, w = H.double().cpu().numpy(), W.double().cpu().numpy()
+    for got, ref, size in ((gH, dz @ w, bound @ np.abs(w)), (gW, dz.T @ h, bound.T @ np.abs(h))):
+        near(got.double().cpu(), ref, (2.0 ** -8 + 1e-3) * size + 1e-30)
