@@ -433,9 +433,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   const float inv_tau = lp ? inverse_tau(tau) : 1.0f / tau;
   const uint16_t* H = static_cast<const uint16_t*>(H_bf16);
 
-  if (lp && N <= FEW_ROWS && FEW_ROWS * d * 4 <= FEW_MAX_SMEM) {
-    // a few positions: bound by reading W, which CUDA cores do faster than 128-row tiles (one
-    // position of the gpt-oss head: 196 against 263 us; four: 269 against 286)
+  if (lp && N <= FEW_ROWS && V * d * 2 > N * FEW_ROW_BYTES && FEW_ROWS * d * 4 <= FEW_MAX_SMEM) {
     int units = 0;
     cudaError_t e = launch_logprob_few(H, static_cast<const uint16_t*>(W_bf16), int(N), int(d), V, lp->tokens, mask,
                                        tau, partials, L.n_groups, &units, s);

@@ -225,8 +225,15 @@ cudaError_t launch_logprob_combine(const float4* partials, int n_units_per_row, 
 cudaError_t launch_logprob_row_stats(const float4* partials, int n_units_per_row, int rows, float tau, float2* row_stats,
                                      cudaStream_t s);
 // EPI_LSE_H's partials for up to FEW_ROWS rows without the tensor cores; *units: how many per row
-// were written (at most max_units).
-constexpr int FEW_ROWS = 4;
+// were written (at most max_units).  Faster than the engine's 128-row tiles for one row where W has
+// to come from HBM, and for two where that takes longer than their logits' sums: where W has more
+// than FEW_ROW_BYTES for each row (us, this / the engine; W in MB):
+//   W         2    66   131   206   262   311   622   1051  1158  1245
+//   one row   18/13 25/25 41/43 51/65 66/64 60/78 102/140 162/205 190/230 186/249
+//   two       25/13 33/25 49/41 69/60 75/66 74/79 113/141 170/244 209/229 196/248
+// (three rows 298 against 224, four 298 against 227 at 1158 MB)
+constexpr int FEW_ROWS = 2;
+constexpr int64_t FEW_ROW_BYTES = 150000000;
 constexpr int FEW_MAX_SMEM = 200 * 1024;  // the hidden states in fp32: a limit on rows * d
 cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, int d, int64_t V, const int32_t* tokens,
                                const uint8_t* mask, float tau, float4* partials, int max_units, int* units,

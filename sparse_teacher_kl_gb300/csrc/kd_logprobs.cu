@@ -583,14 +583,13 @@ cudaError_t launch_logprobs_bwd(const void* z, int dtype, int64_t N, int64_t V, 
 }
 
 // ---------------------------------------------------- few hidden states ---
-// The same scores straight from a few hidden states (fused_logprobs with up to FEW_ROWS rows, a
-// generated token or so): z_v = H W_v^T is then bound by reading W once, V d elements.  A warp
-// takes FEW_VOCAB rows of W at a time, a lane 16 bytes of each in turn, sums the products over the
-// lanes and keeps running statistics of the logits; a block leaves one partial per hidden state,
-// as the projection engine's epilogue does per tile.
-// Measured, whole calls, V = 201088, d = 2880 (1.16 GB): one row 187 us (6.2 TB/s, 91 % of the copy
-// bandwidth).  With a slower combine kernel 1 / 2 / 4 rows 196 / 214 / 269 us; the engine's 128-row
-// tiles 263 / 269 / 286, and 265 for 5; two blocks on an SM 196, three 203, four 226.
+// The same scores straight from one or two hidden states (fused_logprobs with a large head): z_v =
+// H W_v^T is then bound by reading W once, V d elements.  A warp takes FEW_VOCAB rows of W at a time,
+// a lane 16 bytes of each in turn, sums the products over the lanes and keeps running statistics of
+// the logits; a block leaves one partial per hidden state, as the projection engine's epilogue does
+// per tile.
+// Measured, whole calls, V = 201088, d = 2880 (1.16 GB): one row 190 us (6.1 TB/s, 90 % of the copy
+// bandwidth), two 209.  One row with three blocks on an SM 3 % slower, with four 15 %.
 
 constexpr int FEW_THREADS = 256;
 constexpr int FEW_VOCAB = 4;
@@ -695,8 +694,8 @@ cudaError_t launch_logprob_few(const uint16_t* H, const uint16_t* W, int rows, i
           H, W, rows, d, V, tokens, mask, k, partials, BM);                                                                \
   } while (0)
   if (rows == 1) KD_FEW(1);
-  else if (rows == 2) KD_FEW(2);
-  else KD_FEW(4);
+  else KD_FEW(2);
+  static_assert(FEW_ROWS == 2, "instances");
 #undef KD_FEW
   prof_after(s);
   return e != cudaSuccess ? e : cudaGetLastError();
