@@ -345,9 +345,10 @@ KD_API size_t kd_logits_kl_workspace(int64_t N, int64_t V, int K);
  *   t_lse == NULL : p = softmax(t / tau) over S, as kd_fused_kl_fwd;
  *                   KL_t = sum_k p_k (ln p_k - ln q_k).
  *   t_lse given   : the teacher's mass outside its cache is kept as one more class:
- *                   p_k = exp(t_k / tau - t_lse), p_R = max(0, 1 - sum_k p_k), q_R = the
- *                   student's mass outside S;  KL_t gains p_R (ln p_R - ln q_R).  Where S
- *                   is the whole vocabulary there is no such class.
+ *                   p_k = exp(t_k / tau - t_lse), p_R = 1 - sum_k p_k, q_R = the student's
+ *                   mass outside S;  KL_t gains p_R (ln p_R - ln q_R).  Where S is the whole
+ *                   vocabulary there is no such class, and a p_R below 2^-21 (1 + |t_lse|),
+ *                   which is the rounding of t_lse and the sum, is taken as 0.
  *                   t_lse: [N] fp32, logsumexp of the teacher's full row of logits / tau
  *                   (for tau = 1 the lse_out of kd_topk_cache and kd_teacher_topk).
  *   loss          = sum over valid t of KL_t / N_valid   (0 when N_valid == 0).

@@ -13,6 +13,7 @@ from typing import Optional
 import numpy as np
 
 F64 = np.float64
+REST_RESOLUTION = 2.0 ** -21  # of 1 + |t_lse|
 
 
 def _log_softmax(x: np.ndarray):
@@ -92,7 +93,8 @@ def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=1.0) 
 
     A teacher entry of logit -inf is absent; entries that share an id add up; a row without
     entries (and without t_lse) has KL 0 and no gradient; entries that cover the whole
-    vocabulary leave no rest class.
+    vocabulary leave no rest class, and a remainder below the resolution of an fp32 t_lse has
+    no mass.
     """
     z = np.asarray(logits, dtype=F64)
     N, V = z.shape
@@ -118,7 +120,9 @@ def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=1.0) 
         if t_lse is not None:
             outside = np.ones(V, bool)
             outside[at] = False
-            p_rest = max(0.0, 1.0 - float(p.sum())) if outside.any() else 0.0
+            p_rest = 1.0 - float(p.sum())
+            if not outside.any() or p_rest < REST_RESOLUTION * (1.0 + abs(float(t_lse[r]))):
+                p_rest = 0.0
             lq_out, lq_rest = _log_softmax(lq[outside]) if outside.any() else (None, -np.inf)
             if p_rest > 0:
                 kl[r] += p_rest * (np.log(p_rest) - lq_rest)

@@ -2,9 +2,9 @@
 // gradient.  Per position, with x = z / tau, q = softmax(x) over the V logits and S the K cached
 // ids:
 //   without the rest: p = softmax(t / tau) over S (the mass outside dropped)
-//   with the rest   : p_k = exp(t_k / tau - t_lse), p_R = 1 - sum_k p_k >= 0, t_lse the
-//                     teacher's logsumexp over its whole vocabulary; every id outside S is one
-//                     more class R, q_R = sum of q outside S
+//   with the rest   : p_k = exp(t_k / tau - t_lse), p_R = 1 - sum_k p_k (0 where that is below
+//                     2^-21 (1 + |t_lse|)), t_lse the teacher's logsumexp over its whole
+//                     vocabulary; every id outside S is one more class R, q_R = sum of q outside S
 //   KL   = sum_k p_k (ln p_k - ln q_k) [+ p_R (ln p_R - ln q_R)]
 //   dz_v = c (q_v - p_v) on S;  off S: c q_v, or with the rest c (q_R - p_R) e^(x_v - lse_R),
 //          lse_R the logsumexp of x outside S;  c = grad_loss / (N_valid tau)
@@ -257,8 +257,12 @@ __device__ __forceinline__ LkRow lk_row(const LogitsKlArgs& a, const RowStats& a
   if (REST) {
     w.log_norm = t_lse;
     w.inv_sum = 1.f;
-    // the entries may cover the whole vocabulary (K = V, one block): there is no rest then
-    const float p_rest = t.distinct == a.V ? 0.f : fmaxf(1.f - t.e_sum, 0.f);
+    // Below the resolution of its inputs a remainder is rounding, not mass (a teacher whose cache holds
+    // everything leaves some 1e-6 of either sign, and a student without mass there would be infinitely
+    // wrong): t_lse is rounded by |t_lse| 2^-24, t / tau by as much and half more, the exponentials and
+    // their sum by 2^-21 in all.  The entries may also cover the whole vocabulary (K = V, one block).
+    const float left = 1.f - t.e_sum;
+    const float p_rest = t.distinct == a.V || left < 4.76837158e-7f * (1.f + fabsf(t_lse)) ? 0.f : left;
     float log_q = -INFINITY;  // of the rest
     if (b.s > 0.f) {
       log_q = kLn2 * (stats_shift(b.m, all.m, a.k) + log2f(b.s) - w.log2_s);
