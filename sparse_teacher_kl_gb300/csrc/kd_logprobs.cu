@@ -261,8 +261,10 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
         }
     };
     if (own_max >= floor_v) {
+      // the slots that this thread has written: the last one's rounds may have no vector for it
       const int slots = rounds > 0 ? ((rounds - 1) >> shift) + 1 : 0;
-      for (int q = 0; q < slots; ++q)
+      const int own = body_lo + (slots - 1) * (STEP << shift) + tid < body_hi ? slots : slots - 1;
+      for (int q = 0; q < own; ++q)
         if (slot_max[q * LP_THREADS + tid] >= floor_v) {
           const int at = atomicAdd(&ts.groups, 1);
           if (at < LP_LIST) ts.list[at] = uint32_t(q * LP_THREADS + tid);
