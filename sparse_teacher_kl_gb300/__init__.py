@@ -261,19 +261,27 @@ def _fresh_ws(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
-_control = {}  # device index -> control block
+_blocks = {}  # device index -> control block
 
 
-def control_block(device) -> torch.Tensor:
-    """The control block that token_logprobs calls without a workspace share on a device: its only content is the
-    error word, which ``device_error(control_block(device))`` reads."""
-    ws = _control.get(device.index)
+def _control(device: torch.device) -> torch.Tensor:
+    """The control block of a call without a workspace."""
+    ws = _blocks.get(device.index)
     if ws is None:
         ws = _fresh_ws(256, device)
         if not torch.cuda.is_current_stream_capturing():  # memory of a capture belongs to its graph
             torch.cuda.current_stream(device).synchronize()  # cleared before another stream uses it
-            _control[device.index] = ws
+            _blocks[device.index] = ws
     return ws
+
+
+def control_block(device=None) -> torch.Tensor:
+    """The control block that token_logprobs calls without a workspace share on a device: its only content is the
+    error word, which ``device_error(control_block(device))`` reads."""
+    device = torch.device("cuda" if device is None else device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return _control(device)
 
 
 class TokenLogprobs(NamedTuple):
@@ -301,7 +309,7 @@ def token_logprobs_forward(logits, tokens, mask=None, tau=1.0, top=0, entropy=Fa
     top_ids = torch.empty((N, top), dtype=torch.int32, device=dev) if top else None
     top_logp = torch.empty((N, top), **f32) if top else None
     if ws is None:
-        ws = control_block(dev)
+        ws = _control(dev)
     st = _abi.kd_token_logprobs_fwd(_ptr(logits), dt, N, V, ld, _ptr(tokens), M, _ptr(mask), float(tau), int(top),
                                     _ptr(logp), _ptr(lse), _ptr(ent), _ptr(top_ids), _ptr(top_logp), _ptr(ws),
                                     ws.numel(), _stream(dev))
@@ -323,7 +331,7 @@ def token_logprobs_backward(logits, tokens, lse, grad_logp, mask=None, tau=1.0, 
     _check(mask, "mask", torch.uint8, (N,), dev)
     grad_logits, ldg = _grad_like(logits, grad_logits)
     if ws is None:
-        ws = control_block(dev)
+        ws = _control(dev)
     st = _abi.kd_token_logprobs_bwd(_ptr(logits), dt, N, V, ld, _ptr(tokens), M, _ptr(mask), float(tau), _ptr(lse),
                                     _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_logits), ldg,
                                     _ptr(ws), ws.numel(), _stream(dev))
