@@ -11,6 +11,7 @@ runs in the CUDA kernels of ``libkdkl.so`` (see ``include/kdkl.h``).
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -261,27 +262,49 @@ def _fresh_ws(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
-_blocks = {}  # device index -> control block
+class _Blocks(threading.local):
+    """A thread's control blocks, by device index and stream."""
+
+    def __init__(self):
+        self.by_stream = {}
 
 
-def _control(device: torch.device) -> torch.Tensor:
-    """The control block of a call without a workspace."""
-    ws = _blocks.get(device.index)
-    if ws is None:
-        ws = _fresh_ws(256, device)
-        if not torch.cuda.is_current_stream_capturing():  # memory of a capture belongs to its graph
-            torch.cuda.current_stream(device).synchronize()  # cleared before another stream uses it
-            _blocks[device.index] = ws
+_blocks = _Blocks()
+_captured = {}  # device index -> the control block of calls captured into graphs
+
+
+def _cleared(device: torch.device) -> torch.Tensor:
+    ws = _fresh_ws(256, device)
+    torch.cuda.current_stream(device).synchronize()  # cleared before another stream uses it
     return ws
 
 
-def control_block(device=None) -> torch.Tensor:
-    """The control block that token_logprobs calls without a workspace share on a device: its only content is the
-    error word, which ``device_error(control_block(device))`` reads."""
+def _control(device: torch.device) -> torch.Tensor:
+    """The control block of a call without a workspace, on the current stream."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = _captured.get(device.index)
+        # memory of a capture belongs to its graph: without an earlier call outside, nobody can read it
+        return _fresh_ws(256, device) if ws is None else ws
+    key = (device.index, _stream(device))
+    ws = _blocks.by_stream.get(key)
+    if ws is None:
+        ws = _blocks.by_stream[key] = _cleared(device)
+        if device.index not in _captured:
+            _captured.setdefault(device.index, _cleared(device))
+    return ws
+
+
+def control_block(device=None, captured: bool = False) -> torch.Tensor:
+    """The control block that token_logprobs calls report to when they are given no workspace: its only content is
+    the error word, which ``device_error(control_block(device))`` reads and clears.
+    Each thread has one for every device and stream (this is the current stream's; a backward pass reports to the
+    block of its forward pass).  With ``captured``, the one that calls captured into graphs on the device share,
+    where a call outside a capture (a warm-up) came first."""
     device = torch.device("cuda" if device is None else device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    return _control(device)
+    block = _control(device)
+    return _captured[device.index] if captured else block
 
 
 class TokenLogprobs(NamedTuple):
@@ -346,7 +369,9 @@ def _f32c(g):
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, mask, tau):
-        r = token_logprobs_forward(logits, tokens, mask, tau, entropy=True)
+        _check_logits(logits)
+        ctx.control = _control(logits.device)
+        r = token_logprobs_forward(logits, tokens, mask, tau, entropy=True, ws=ctx.control)
         ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
         ctx.mask, ctx.tau = mask, tau
         ctx.set_materialize_grads(False)
@@ -359,7 +384,8 @@ class _TokenLogprobs(torch.autograd.Function):
             return None, None, None, None
         if g_logp is None:
             g_logp = torch.zeros(tokens.shape, dtype=torch.float32, device=logits.device)
-        g = token_logprobs_backward(logits, tokens, lse, _f32c(g_logp), ctx.mask, ctx.tau, ent, _f32c(g_entropy))
+        g = token_logprobs_backward(logits, tokens, lse, _f32c(g_logp), ctx.mask, ctx.tau, ent, _f32c(g_entropy),
+                                    ws=ctx.control)
         return g, None, None, None
 
 
