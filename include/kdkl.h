@@ -388,6 +388,23 @@ KD_API int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V
                     float tau, const float* grad_loss, float* loss_out, float* kl_per_token_out,
                     void* grad_logits, int64_t ld_grad, void* ws, size_t ws_bytes, void* stream);
 
+/* The same calls with the error word in a control block of the caller's (256 bytes, 256-byte
+ * aligned, cleared once by kd_workspace_clear) instead of the workspace's first bytes: for callers
+ * whose workspaces do not outlive the call.  `ws` may then be memory of any content.  `control` may
+ * be `ws` itself, and may serve any number of calls: it holds the first error since it was read. */
+KD_API int kd_logits_kl_fwd_ctl(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* t_ids, const float* t_logits, int K, const float* t_lse, const uint8_t* mask,
+                    float tau, float* loss_out, float* stats_out, float* kl_per_token_out,
+                    void* ws, size_t ws_bytes, void* control, void* stream);
+KD_API int kd_logits_kl_bwd_ctl(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* t_ids, const float* t_logits, int K, const float* t_lse, const uint8_t* mask,
+                    float tau, const float* stats, const float* grad_loss, void* grad_logits, int64_t ld_grad,
+                    void* ws, size_t ws_bytes, void* control, void* stream);
+KD_API int kd_logits_kl_step_ctl(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                    const int32_t* t_ids, const float* t_logits, int K, const float* t_lse, const uint8_t* mask,
+                    float tau, const float* grad_loss, float* loss_out, float* kl_per_token_out,
+                    void* grad_logits, int64_t ld_grad, void* ws, size_t ws_bytes, void* control, void* stream);
+
 /* ------------------------------------------------------------------------ *
  * The same scores straight from hidden states: log probability of one given token per
  * position and the entropy under softmax(H W^T / tau), formed `chunk` positions at a
@@ -420,6 +437,17 @@ KD_API int kd_fused_logprobs_bwd(const void* H_bf16, const void* W_bf16, const i
                     const float* lse, const float* entropy, const float* grad_logp, const float* grad_entropy,
                     void* grad_H, int grad_H_is_fp32, void* grad_W, int grad_W_kind,
                     void* ws, size_t ws_bytes, void* stream);
+
+/* With the error word in a control block of the caller's, as kd_logits_kl_fwd_ctl. */
+KD_API int kd_fused_logprobs_fwd_ctl(const void* H_bf16, const void* W_bf16, const int32_t* tokens,
+                    const uint8_t* mask, int64_t N, int64_t d, int64_t V, int64_t chunk, float tau,
+                    float* logp_out, float* lse_out, float* entropy_out, void* ws, size_t ws_bytes,
+                    void* control, void* stream);
+KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, const int32_t* tokens,
+                    const uint8_t* mask, int64_t N, int64_t d, int64_t V, int64_t chunk, float tau,
+                    const float* lse, const float* entropy, const float* grad_logp, const float* grad_entropy,
+                    void* grad_H, int grad_H_is_fp32, void* grad_W, int grad_W_kind,
+                    void* ws, size_t ws_bytes, void* control, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * On-disk teacher cache ([ART] paragraph on the first fix: run the teacher once,

@@ -257,9 +257,14 @@ def _grad_like(z: torch.Tensor, grad: Optional[torch.Tensor]):
 
 def _fresh_ws(nbytes: int, device) -> torch.Tensor:
     """A workspace with its control block zeroed and the rest left as it is (the allocator's blocks are aligned)."""
-    ws = torch.empty((int(nbytes),), dtype=torch.uint8, device=device)
+    ws = _scratch(nbytes, device)
     _abi.check(_abi.kd_workspace_clear(ws.data_ptr(), ws.numel(), _stream(device)), "kd_workspace_clear")
     return ws
+
+
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    """A workspace of any content, for calls that report to a control block of its own."""
+    return torch.empty((int(nbytes),), dtype=torch.uint8, device=device)
 
 
 class _Blocks(threading.local):
@@ -295,8 +300,8 @@ def _control(device: torch.device) -> torch.Tensor:
 
 
 def control_block(device=None, captured: bool = False) -> torch.Tensor:
-    """The control block that token_logprobs calls report to when they are given no workspace: its only content is
-    the error word, which ``device_error(control_block(device))`` reads and clears.
+    """The control block that calls on dense logits, and the differentiable calls, report to when they are given no
+    workspace: its only content is the error word, which ``device_error(control_block(device))`` reads and clears.
     Each thread has one for every device and stream (this is the current stream's; a backward pass reports to the
     block of its forward pass).  With ``captured``, the one that calls captured into graphs on the device share,
     where a call outside a capture (a warm-up) came first."""
@@ -408,50 +413,67 @@ def _check_kl(logits, ids, tlog, mask, t_lse, kl_out=None):
     return dt, N, V, ld, K, dev
 
 
-def logits_kl_forward(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, ws=None, kl_out=None):
-    """kd_logits_kl_fwd: KL of the cached teacher (``ids`` int32, ``tlog`` fp32 [N, K]; with ``t_lse`` its mass
-    outside the cache as one more class) against softmax(logits / tau): (loss [1], stats [N, 4], ws)."""
+def _kl_forward(logits, ids, tlog, mask, tau, t_lse, ws, control, kl_out=None):
     dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse, kl_out)
     if ws is None:
-        ws = _fresh_ws(_abi.kd_logits_kl_workspace(N, V, K), dev)
+        ws = (_fresh_ws if control is None else _scratch)(_abi.kd_logits_kl_workspace(N, V, K), dev)
+    if control is None:
+        control = ws
     loss = torch.empty((1,), dtype=torch.float32, device=dev)
     stats = torch.empty((N, 4), dtype=torch.float32, device=dev)
-    st = _abi.kd_logits_kl_fwd(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
-                               float(tau), _ptr(loss), _ptr(stats), _ptr(kl_out), _ptr(ws), ws.numel(), _stream(dev))
+    st = _abi.kd_logits_kl_fwd_ctl(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
+                                   float(tau), _ptr(loss), _ptr(stats), _ptr(kl_out), _ptr(ws), ws.numel(),
+                                   _ptr(control), _stream(dev))
     _abi.check(st, "kd_logits_kl_fwd")
     return loss, stats, ws
 
 
-def logits_kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau=1.0, t_lse=None, ws=None, grad_logits=None):
-    """kd_logits_kl_bwd: the gradient of the logits, in their type (``grad_logits`` may be the logits themselves)."""
+def logits_kl_forward(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, ws=None, kl_out=None):
+    """kd_logits_kl_fwd: KL of the cached teacher (``ids`` int32, ``tlog`` fp32 [N, K]; with ``t_lse`` its mass
+    outside the cache as one more class) against softmax(logits / tau): (loss [1], stats [N, 4], ws)."""
+    return _kl_forward(logits, ids, tlog, mask, tau, t_lse, ws, None, kl_out)
+
+
+def _kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau, t_lse, ws, control, grad_logits=None):
     dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse)
     _check(stats, "stats", torch.float32, (N, 4), dev)
     _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
     grad_logits, ldg = _grad_like(logits, grad_logits)
-    if ws is None:  # not returned: nobody reads its error word
-        ws = torch.empty((_abi.kd_logits_kl_workspace(N, V, K),), dtype=torch.uint8, device=dev)
-    st = _abi.kd_logits_kl_bwd(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
-                               float(tau), _ptr(stats), _ptr(grad_loss), _ptr(grad_logits), ldg, _ptr(ws), ws.numel(),
-                               _stream(dev))
+    if control is None:
+        control = _control(dev) if ws is None else ws
+    if ws is None:
+        ws = _scratch(_abi.kd_logits_kl_workspace(N, V, K), dev)
+    st = _abi.kd_logits_kl_bwd_ctl(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
+                                   float(tau), _ptr(stats), _ptr(grad_loss), _ptr(grad_logits), ldg, _ptr(ws),
+                                   ws.numel(), _ptr(control), _stream(dev))
     _abi.check(st, "kd_logits_kl_bwd")
     return grad_logits
+
+
+def logits_kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau=1.0, t_lse=None, ws=None, grad_logits=None):
+    """kd_logits_kl_bwd: the gradient of the logits, in their type (``grad_logits`` may be the logits themselves).
+    Without a workspace errors go to the stream's control_block."""
+    return _kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau, t_lse, ws, None, grad_logits)
 
 
 def logits_kl_step(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=None, ws=None, kl_out=None,
                    grad_logits=None):
     """kd_logits_kl_step: loss and gradient in one pass over the logits, for a ``grad_loss`` ([1] fp32, default 1)
-    known beforehand: (loss [1], grad_logits).  ``grad_logits`` may be the logits themselves."""
+    known beforehand: (loss [1], grad_logits).  ``grad_logits`` may be the logits themselves.  Without a workspace
+    errors go to the stream's control_block."""
     dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse, kl_out)
     if grad_loss is None:
         grad_loss = torch.ones((1,), dtype=torch.float32, device=dev)
     _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
     grad_logits, ldg = _grad_like(logits, grad_logits)
-    if ws is None:  # not returned: nobody reads its error word
-        ws = torch.empty((_abi.kd_logits_kl_workspace(N, V, K),), dtype=torch.uint8, device=dev)
+    control = ws
+    if ws is None:
+        control = _control(dev)
+        ws = _scratch(_abi.kd_logits_kl_workspace(N, V, K), dev)
     loss = torch.empty((1,), dtype=torch.float32, device=dev)
-    st = _abi.kd_logits_kl_step(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
-                                float(tau), _ptr(grad_loss), _ptr(loss), _ptr(kl_out), _ptr(grad_logits), ldg,
-                                _ptr(ws), ws.numel(), _stream(dev))
+    st = _abi.kd_logits_kl_step_ctl(_ptr(logits), dt, N, V, ld, _ptr(ids), _ptr(tlog), K, _ptr(t_lse), _ptr(mask),
+                                    float(tau), _ptr(grad_loss), _ptr(loss), _ptr(kl_out), _ptr(grad_logits), ldg,
+                                    _ptr(ws), ws.numel(), _ptr(control), _stream(dev))
     _abi.check(st, "kd_logits_kl_step")
     return loss, grad_logits
 
@@ -459,7 +481,9 @@ def logits_kl_step(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=
 class _LogitsKL(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, tlog, mask, tau, t_lse):
-        loss, stats, ws = logits_kl_forward(logits, ids, tlog, mask, tau, t_lse)
+        _check_logits(logits)
+        ctx.control = _control(logits.device)
+        loss, stats, ws = _kl_forward(logits, ids, tlog, mask, tau, t_lse, None, ctx.control)
         ctx.save_for_backward(logits, ids, tlog, stats)
         ctx.mask, ctx.tau, ctx.t_lse, ctx.ws = mask, tau, t_lse, ws
         return loss[0]
@@ -467,8 +491,8 @@ class _LogitsKL(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_out):
         logits, ids, tlog, stats = ctx.saved_tensors
-        g = logits_kl_backward(logits, ids, tlog, ctx.mask, stats, _f32c(grad_out.reshape(1)), ctx.tau, ctx.t_lse,
-                               ws=ctx.ws)
+        g = _kl_backward(logits, ids, tlog, ctx.mask, stats, _f32c(grad_out.reshape(1)), ctx.tau, ctx.t_lse, ctx.ws,
+                         ctx.control)
         return g, None, None, None, None, None
 
 
@@ -489,30 +513,37 @@ def _check_projection(H, W, tokens, mask):
     return N, d, W.shape[0], H.device
 
 
-def fused_logprobs_forward(H, W, tokens, mask=None, chunk=4096, tau=1.0, entropy=False, ws=None):
-    """kd_fused_logprobs_fwd: (logp [N], lse [N], entropy [N] or None, ws) of ``tokens`` (int32 [N]) under
-    softmax(H W^T / tau), the logits never stored."""
+def _fused_forward(H, W, tokens, mask, chunk, tau, entropy, ws, control):
     N, d, V, dev = _check_projection(H, W, tokens, mask)
     if ws is None:
-        ws = _fresh_ws(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 0), dev)
+        ws = (_fresh_ws if control is None else _scratch)(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 0), dev)
+    if control is None:
+        control = ws
     logp = torch.empty((N,), dtype=torch.float32, device=dev)
     lse = torch.empty((N,), dtype=torch.float32, device=dev)
     ent = torch.empty((N,), dtype=torch.float32, device=dev) if entropy else None
-    st = _abi.kd_fused_logprobs_fwd(_ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), N, d, V, chunk, float(tau), _ptr(logp),
-                                    _ptr(lse), _ptr(ent), _ptr(ws), ws.numel(), _stream(dev))
+    st = _abi.kd_fused_logprobs_fwd_ctl(_ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), N, d, V, chunk, float(tau),
+                                        _ptr(logp), _ptr(lse), _ptr(ent), _ptr(ws), ws.numel(), _ptr(control),
+                                        _stream(dev))
     _abi.check(st, "kd_fused_logprobs_fwd")
     return logp, lse, ent, ws
 
 
-def fused_logprobs_backward(H, W, tokens, lse, grad_logp, mask=None, chunk=4096, tau=1.0, entropy=None,
-                            grad_entropy=None, ws=None, grad_H=None, grad_W=None, grad_H_fp32=False, grad_W_bf16=False):
-    """kd_fused_logprobs_bwd: (grad_H [N, d] bf16 or fp32, grad_W [V, d]).  A ``grad_W`` of the caller's (fp32) is
-    added into; without one it is a new tensor, fp32 or with ``grad_W_bf16`` (one chunk only) bf16."""
+def fused_logprobs_forward(H, W, tokens, mask=None, chunk=4096, tau=1.0, entropy=False, ws=None):
+    """kd_fused_logprobs_fwd: (logp [N], lse [N], entropy [N] or None, ws) of ``tokens`` (int32 [N]) under
+    softmax(H W^T / tau), the logits never stored."""
+    return _fused_forward(H, W, tokens, mask, chunk, tau, entropy, ws, None)
+
+
+def _fused_backward(H, W, tokens, lse, grad_logp, mask, chunk, tau, entropy, grad_entropy, ws, control, grad_H=None,
+                    grad_W=None, grad_H_fp32=False, grad_W_bf16=False):
     N, d, V, dev = _check_projection(H, W, tokens, mask)
     for t, name in ((lse, "lse"), (grad_logp, "grad_logp"), (entropy, "entropy"), (grad_entropy, "grad_entropy")):
         _check(t, name, torch.float32, (N,), dev)
+    if control is None:
+        control = _control(dev) if ws is None else ws
     if ws is None:
-        ws = _fresh_ws(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 1), dev)
+        ws = _scratch(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 1), dev)
     if grad_H is None:
         grad_H = torch.empty((N, d), dtype=torch.float32 if grad_H_fp32 else torch.bfloat16, device=dev)
     kind = _abi.KD_GRAD_ADD_F32
@@ -522,18 +553,29 @@ def fused_logprobs_backward(H, W, tokens, lse, grad_logp, mask=None, chunk=4096,
     else:
         _check(grad_W, "grad_W", torch.float32, (V, d), dev)
     _check(grad_H, "grad_H", torch.float32 if grad_H.dtype == torch.float32 else torch.bfloat16, (N, d), dev)
-    st = _abi.kd_fused_logprobs_bwd(_ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), N, d, V, chunk, float(tau), _ptr(lse),
-                                    _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_H),
-                                    1 if grad_H.dtype == torch.float32 else 0, _ptr(grad_W), kind, _ptr(ws),
-                                    ws.numel(), _stream(dev))
+    st = _abi.kd_fused_logprobs_bwd_ctl(_ptr(H), _ptr(W), _ptr(tokens), _ptr(mask), N, d, V, chunk, float(tau),
+                                        _ptr(lse), _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_H),
+                                        1 if grad_H.dtype == torch.float32 else 0, _ptr(grad_W), kind, _ptr(ws),
+                                        ws.numel(), _ptr(control), _stream(dev))
     _abi.check(st, "kd_fused_logprobs_bwd")
     return grad_H, grad_W
+
+
+def fused_logprobs_backward(H, W, tokens, lse, grad_logp, mask=None, chunk=4096, tau=1.0, entropy=None,
+                            grad_entropy=None, ws=None, grad_H=None, grad_W=None, grad_H_fp32=False, grad_W_bf16=False):
+    """kd_fused_logprobs_bwd: (grad_H [N, d] bf16 or fp32, grad_W [V, d]).  A ``grad_W`` of the caller's (fp32) is
+    added into; without one it is a new tensor, fp32 or with ``grad_W_bf16`` (one chunk only) bf16.  Without a
+    workspace errors go to the stream's control_block."""
+    return _fused_backward(H, W, tokens, lse, grad_logp, mask, chunk, tau, entropy, grad_entropy, ws, None, grad_H,
+                           grad_W, grad_H_fp32, grad_W_bf16)
 
 
 class _FusedLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, tokens, mask, chunk, tau):
-        logp, lse, ent, _ = fused_logprobs_forward(H, W, tokens, mask, chunk, tau, entropy=True)
+        _check_projection(H, W, tokens, mask)
+        ctx.control = _control(H.device)
+        logp, lse, ent, _ = _fused_forward(H, W, tokens, mask, chunk, tau, True, None, ctx.control)
         ctx.save_for_backward(H, W, tokens, lse, ent)
         ctx.mask, ctx.chunk, ctx.tau = mask, chunk, tau
         ctx.set_materialize_grads(False)
@@ -546,8 +588,8 @@ class _FusedLogprobs(torch.autograd.Function):
             return None, None, None, None, None, None
         if g_logp is None:
             g_logp = torch.zeros_like(lse)
-        grad_H, grad_W = fused_logprobs_backward(H, W, tokens, lse, _f32c(g_logp), ctx.mask, ctx.chunk, ctx.tau, ent,
-                                                 _f32c(g_entropy), grad_W_bf16=H.shape[0] <= ctx.chunk)
+        grad_H, grad_W = _fused_backward(H, W, tokens, lse, _f32c(g_logp), ctx.mask, ctx.chunk, ctx.tau, ent,
+                                         _f32c(g_entropy), None, ctx.control, grad_W_bf16=H.shape[0] <= ctx.chunk)
         return grad_H, grad_W.to(W.dtype), None, None, None, None
 
 

@@ -98,6 +98,9 @@ _SIGNATURES = {
     "kd_profile_end": (_c_int, []),
     "kd_profile_read": (_c_int, [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(_c_float), _c_int]),
 }
+# the forms with a control block of the caller's: one pointer more, before the stream
+for _name in ("kd_logits_kl_fwd", "kd_logits_kl_bwd", "kd_logits_kl_step", "kd_fused_logprobs_fwd", "kd_fused_logprobs_bwd"):
+    _SIGNATURES[_name + "_ctl"] = (_SIGNATURES[_name][0], [*_SIGNATURES[_name][1], _c_ptr])
 
 _lib = None
 
@@ -166,11 +169,16 @@ kd_token_logprobs_fwd = _wrap("kd_token_logprobs_fwd")
 kd_token_logprobs_bwd = _wrap("kd_token_logprobs_bwd")
 kd_logits_kl_workspace = _wrap("kd_logits_kl_workspace")
 kd_logits_kl_fwd = _wrap("kd_logits_kl_fwd")
+kd_logits_kl_fwd_ctl = _wrap("kd_logits_kl_fwd_ctl")
 kd_logits_kl_bwd = _wrap("kd_logits_kl_bwd")
+kd_logits_kl_bwd_ctl = _wrap("kd_logits_kl_bwd_ctl")
 kd_logits_kl_step = _wrap("kd_logits_kl_step")
+kd_logits_kl_step_ctl = _wrap("kd_logits_kl_step_ctl")
 kd_fused_logprobs_workspace = _wrap("kd_fused_logprobs_workspace")
 kd_fused_logprobs_fwd = _wrap("kd_fused_logprobs_fwd")
+kd_fused_logprobs_fwd_ctl = _wrap("kd_fused_logprobs_fwd_ctl")
 kd_fused_logprobs_bwd = _wrap("kd_fused_logprobs_bwd")
+kd_fused_logprobs_bwd_ctl = _wrap("kd_fused_logprobs_bwd_ctl")
 kd_workspace_clear = _wrap("kd_workspace_clear")
 kd_get_device_error = _wrap("kd_get_device_error")
 kd_gemm_bf16 = _wrap("kd_gemm_bf16")

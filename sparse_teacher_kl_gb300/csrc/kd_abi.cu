@@ -376,6 +376,7 @@ size_t kd_chunked_kl_logits_bytes(int64_t N, int64_t V) {
 // What fused_logprobs puts in the place of the teacher: the given tokens, and the outputs of
 // the forward or the gradients of the backward pass.
 struct LogprobTerm {
+  Ctrl* control;  // of the error word
   const int32_t* tokens;
   float *logp, *entropy;                       // forward outputs (entropy may be NULL)
   const float *g_logp, *g_entropy, *entropy_in;  // backward
@@ -387,13 +388,13 @@ static size_t logprob_fwd_ws(int64_t N, int64_t V, int64_t chunk) {
   return sizeof(Ctrl) + size_t((V + BN - 1) / BN) * size_t((c + BM - 1) / BM * BM) * 16;
 }
 
-static kd_status check_logprob_args(const void* H, const void* W, const int32_t* tokens, int64_t N, int64_t d,
+static kd_status check_logprob_args(const void* H, const void* W, const LogprobTerm& lp, int64_t N, int64_t d,
                                     int64_t V, int64_t chunk, float tau, const void* ws, size_t ws_bytes,
                                     bool backward) {
   const kd_status st = check_proj_args(H, W, N, d, V, chunk, tau);
   if (st != KD_OK) return st;
-  if (!tokens || !aligned(tokens, 4)) return KD_ERR_INVALID_ARG;
-  if (!ws || !aligned(ws, 256)) return KD_ERR_WORKSPACE;
+  if (!lp.tokens || !aligned(lp.tokens, 4)) return KD_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || !lp.control || !aligned(lp.control, 256)) return KD_ERR_WORKSPACE;
   return ws_bytes < (backward ? kl_layout(N, d, V, 1, chunk).total : logprob_fwd_ws(N, V, chunk)) ? KD_ERR_WORKSPACE
                                                                                                  : KD_OK;
 }
@@ -411,7 +412,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
                     const uint8_t* mask, int64_t N, int64_t d, int64_t V, int K, int64_t chunk, float tau,
                     float* loss_out, float* lse_out, float* kl_per_token_out, void* z_store, size_t z_bytes,
                     void* ws, size_t ws_bytes, void* stream, const LogprobTerm* lp = nullptr) {
-  kd_status st = lp ? check_logprob_args(H_bf16, W_bf16, lp->tokens, N, d, V, chunk, tau, ws, ws_bytes, false)
+  kd_status st = lp ? check_logprob_args(H_bf16, W_bf16, *lp, N, d, V, chunk, tau, ws, ws_bytes, false)
                     : check_kl_args(H_bf16, W_bf16, t_ids, t_logits, N, d, V, K, chunk, tau, ws, ws_bytes);
   if (st != KD_OK) return st;
   if (!lse_out || !aligned(lse_out, 4)) return KD_ERR_INVALID_ARG;
@@ -425,6 +426,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   const KlLayout L = kl_layout(N, d, V, K, chunk);
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(w8);
+  uint32_t* const err = lp ? &lp->control->err : &ctrl->err;
   int32_t* ids_sorted = reinterpret_cast<int32_t*>(w8 + L.ids_sorted);
   float* p_sorted = reinterpret_cast<float*>(w8 + L.p_sorted);
   float* negent = reinterpret_cast<float*>(w8 + L.negent);
@@ -439,7 +441,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
                                        tau, partials, L.n_groups, &units, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
     return map_cuda(launch_logprob_combine(partials, units, int(N), V, lp->tokens, mask, tau, lp->logp, lse_out,
-                                           lp->entropy, &ctrl->err, 0, s));
+                                           lp->entropy, err, 0, s));
   }
 
   alignas(64) CUtensorMap tw, tw_half, th, tz;
@@ -462,7 +464,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     const int n = int((N - c0) < chunk ? (N - c0) : chunk);
     if (!lp)
       e = launch_teacher_prologue(t_ids + c0 * K, t_logits + c0 * K, n, K, V, inv_tau, ids_sorted, p_sorted, negent,
-                                  &ctrl->err, c0, s);
+                                  err, c0, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
     if (!make_tmap_2d_bf16(&th, H + c0 * d, uint64_t(d), uint64_t(n), uint64_t(d) * 2, BK, BM)) return KD_ERR_CUDA;
     if (d64 && !make_tmap_mn2_bf16(&th2, H + c0 * d, uint64_t(d), uint64_t(n), uint64_t(d) * 2, BM))
@@ -478,7 +480,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     p.n_units = ((p.m_tiles + p.cluster - 1) / p.cluster) * ((p.n_tiles + p.n_group - 1) / p.n_group);
     p.k_splits = 1;
     p.ids_sorted = ids_sorted; p.p_sorted = p_sorted; p.Kt = K; p.inv_tau = inv_tau;
-    p.partials = partials; p.rows = n; p.err = &ctrl->err;
+    p.partials = partials; p.rows = n; p.err = err;
     if (lp) {
       p.k = log2e_over_tau(tau);
       p.tokens = lp->tokens + c0;
@@ -491,7 +493,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     if (e != cudaSuccess) return KD_ERR_CUDA;
     if (lp)
       e = launch_logprob_combine(partials, L.n_groups, n, V, lp->tokens + c0, mask ? mask + c0 : nullptr, tau,
-                                 lp->logp + c0, lse_out + c0, lp->entropy ? lp->entropy + c0 : nullptr, &ctrl->err,
+                                 lp->logp + c0, lse_out + c0, lp->entropy ? lp->entropy + c0 : nullptr, err,
                                  c0, s);
     else
       e = launch_lse_combine(partials, L.n_groups, n, negent, inv_tau, lse_out + c0, kl + c0, s);
@@ -510,7 +512,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
                     const float* lse, const float* grad_loss, const void* z_store, void* grad_H, int grad_H_is_fp32,
                     void* grad_W, void* ws, size_t ws_bytes, void* stream, const LogprobTerm* lp = nullptr,
                     int w_kind = KD_GRAD_ADD_F32) {
-  kd_status st = lp ? check_logprob_args(H_bf16, W_bf16, lp->tokens, N, d, V, chunk, tau, ws, ws_bytes, true)
+  kd_status st = lp ? check_logprob_args(H_bf16, W_bf16, *lp, N, d, V, chunk, tau, ws, ws_bytes, true)
                     : check_kl_args(H_bf16, W_bf16, t_ids, t_logits, N, d, V, K, chunk, tau, ws, ws_bytes);
   if (st != KD_OK) return st;
   if (!lse || !grad_H || !grad_W) return KD_ERR_INVALID_ARG;
@@ -526,6 +528,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   const KlLayout L = kl_layout(N, d, V, K, chunk);
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(w8);
+  uint32_t* const err = lp ? &lp->control->err : &ctrl->err;
   int32_t* ids_sorted = reinterpret_cast<int32_t*>(w8 + L.ids_sorted);
   float* p_sorted = reinterpret_cast<float*>(w8 + L.p_sorted);
   float* negent = reinterpret_cast<float*>(w8 + L.negent);
@@ -563,7 +566,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     const int n = int((N - c0) < chunk ? (N - c0) : chunk);
     if (!lp)
       e = launch_teacher_prologue(t_ids + c0 * K, t_logits + c0 * K, n, K, V, inv_tau, ids_sorted, p_sorted, negent,
-                                  &ctrl->err, c0, s);
+                                  err, c0, s);
     if (e != cudaSuccess) return KD_ERR_CUDA;
     const uint16_t* Hc = H + c0 * d;
     if (!make_tmap_2d_bf16(&th_k, Hc, uint64_t(d), uint64_t(n), uint64_t(d) * 2, BK, BM)) return KD_ERR_CUDA;
@@ -600,7 +603,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     p.k_splits = 1;
     p.ids_sorted = ids_sorted; p.p_sorted = p_sorted; p.Kt = K; p.inv_tau = inv_tau;
     p.lse = lse + c0; p.mask = mask ? mask + c0 : nullptr; p.grad_loss = grad_loss; p.n_valid = &ctrl->n_valid;
-    p.dz = dz; p.ldz = L.ldz; p.rows = n; p.err = &ctrl->err;
+    p.dz = dz; p.ldz = L.ldz; p.rows = n; p.err = err;
     if (lp) {
       p.k = log2e_over_tau(tau);
       p.tokens = lp->tokens + c0;
@@ -646,7 +649,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
       q.ldc = d; q.c_bf16 = 0;
       q.split_stride = L.rows_pad * d;
     }
-    q.err = &ctrl->err;
+    q.err = err;
     q.b_box2 = q.cta_pair && d64;
     e = launch_gemm(q, q.cta_pair ? tdz_k_p : tdz_k, q.b_box2 ? tw_mn2 : (q.cta_pair ? tw_mn_p : tw_mn), tw_mn,
                     grid_max, s);
@@ -669,7 +672,7 @@ static int bwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
     r.k_splits = 1;
     set_cluster(r);
     r.n_units = ((r.m_tiles + r.cluster - 1) / r.cluster) * r.n_tiles;
-    r.C = grad_W; r.ldc = d; r.err = &ctrl->err;
+    r.C = grad_W; r.ldc = d; r.err = err;
     r.c_bf16 = r.c_tma = w_kind == KD_GRAD_STORE_BF16;
     r.b_box2 = r.cta_pair && d64;
     e = launch_gemm(r, r.cta_pair ? tdz_mn_p : tdz_mn, r.b_box2 ? th_mn2 : (r.cta_pair ? th_mn_p : th_mn), tgw,
@@ -705,7 +708,16 @@ size_t kd_fused_logprobs_workspace(int64_t N, int64_t d, int64_t V, int64_t chun
 int kd_fused_logprobs_fwd(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
                           int64_t N, int64_t d, int64_t V, int64_t chunk, float tau, float* logp_out, float* lse_out,
                           float* entropy_out, void* ws, size_t ws_bytes, void* stream) {
+  return kd_fused_logprobs_fwd_ctl(H_bf16, W_bf16, tokens, mask, N, d, V, chunk, tau, logp_out, lse_out, entropy_out,
+                                   ws, ws_bytes, ws, stream);
+}
+
+int kd_fused_logprobs_fwd_ctl(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
+                              int64_t N, int64_t d, int64_t V, int64_t chunk, float tau, float* logp_out,
+                              float* lse_out, float* entropy_out, void* ws, size_t ws_bytes, void* control,
+                              void* stream) {
   LogprobTerm lp{};
+  lp.control = static_cast<Ctrl*>(control);
   lp.tokens = tokens;
   lp.logp = logp_out;
   lp.entropy = entropy_out;
@@ -718,9 +730,20 @@ int kd_fused_logprobs_bwd(const void* H_bf16, const void* W_bf16, const int32_t*
                           const float* entropy, const float* grad_logp, const float* grad_entropy, void* grad_H,
                           int grad_H_is_fp32, void* grad_W, int grad_W_kind, void* ws, size_t ws_bytes,
                           void* stream) {
+  return kd_fused_logprobs_bwd_ctl(H_bf16, W_bf16, tokens, mask, N, d, V, chunk, tau, lse, entropy, grad_logp,
+                                   grad_entropy, grad_H, grad_H_is_fp32, grad_W, grad_W_kind, ws, ws_bytes, ws,
+                                   stream);
+}
+
+int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, const int32_t* tokens, const uint8_t* mask,
+                              int64_t N, int64_t d, int64_t V, int64_t chunk, float tau, const float* lse,
+                              const float* entropy, const float* grad_logp, const float* grad_entropy, void* grad_H,
+                              int grad_H_is_fp32, void* grad_W, int grad_W_kind, void* ws, size_t ws_bytes,
+                              void* control, void* stream) {
   if (grad_W_kind < KD_GRAD_ADD_F32 || grad_W_kind > KD_GRAD_STORE_BF16) return KD_ERR_INVALID_ARG;
   if (grad_W_kind == KD_GRAD_STORE_BF16 && N > chunk) return KD_ERR_INVALID_ARG;
   LogprobTerm lp{};
+  lp.control = static_cast<Ctrl*>(control);
   lp.tokens = tokens;
   lp.g_logp = grad_logp;
   lp.g_entropy = grad_entropy;

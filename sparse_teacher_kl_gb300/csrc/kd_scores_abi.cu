@@ -42,6 +42,11 @@ kd_status check_ws(const void* ws, size_t have, size_t need) {
   return (ws && aligned(ws, 256) && have >= need) ? KD_OK : KD_ERR_WORKSPACE;
 }
 
+// The block that holds the error word: the workspace's own, or the caller's.
+kd_status check_control(const void* control) {
+  return (control && aligned(control, 256)) ? KD_OK : KD_ERR_WORKSPACE;
+}
+
 size_t logits_kl_ws(int64_t N) { return sizeof(Ctrl) + align_up(size_t(N) * 4, 256); }
 
 kd_status check_teacher(const int32_t* ids, const float* tlog, int K, const float* t_lse, int64_t V, int dtype) {
@@ -116,18 +121,26 @@ int kd_logits_kl_fwd(const void* logits, int dtype, int64_t N, int64_t V, int64_
                      const float* t_logits, int K, const float* t_lse, const uint8_t* mask, float tau,
                      float* loss_out, float* stats_out, float* kl_per_token_out, void* ws, size_t ws_bytes,
                      void* stream) {
+  return kd_logits_kl_fwd_ctl(logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, loss_out, stats_out,
+                              kl_per_token_out, ws, ws_bytes, ws, stream);
+}
+
+int kd_logits_kl_fwd_ctl(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* t_ids,
+                         const float* t_logits, int K, const float* t_lse, const uint8_t* mask, float tau,
+                         float* loss_out, float* stats_out, float* kl_per_token_out, void* ws, size_t ws_bytes,
+                         void* control, void* stream) {
   kd_status st = check_logits(logits, dtype, N, V, ld, tau);
   if (st != KD_OK) return st;
   if ((st = check_teacher(t_ids, t_logits, K, t_lse, V, dtype)) != KD_OK) return st;
   if (!ok4(loss_out) || !stats_out || !aligned(stats_out, 16) || !ok4_or_null(kl_per_token_out))
     return KD_ERR_INVALID_ARG;
   if ((st = check_ws(ws, ws_bytes, logits_kl_ws(N))) != KD_OK) return st;
+  if ((st = check_control(control)) != KD_OK) return st;
   if ((st = check_device()) != KD_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Ctrl* ctrl = static_cast<Ctrl*>(ws);
-  float* kl = kl_per_token_out ? kl_per_token_out : reinterpret_cast<float*>(ctrl + 1);
+  float* kl = kl_per_token_out ? kl_per_token_out : reinterpret_cast<float*>(static_cast<Ctrl*>(ws) + 1);
   if (launch_logits_kl(1, logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, stats_out, kl, nullptr,
-                       nullptr, nullptr, 0, &ctrl->err, s) != cudaSuccess)
+                       nullptr, nullptr, 0, &static_cast<Ctrl*>(control)->err, s) != cudaSuccess)
     return KD_ERR_CUDA;
   return map_cuda(launch_masked_mean(kl, mask, N, loss_out, s));
 }
@@ -136,32 +149,49 @@ int kd_logits_kl_bwd(const void* logits, int dtype, int64_t N, int64_t V, int64_
                      const float* t_logits, int K, const float* t_lse, const uint8_t* mask, float tau,
                      const float* stats, const float* grad_loss, void* grad_logits, int64_t ld_grad, void* ws,
                      size_t ws_bytes, void* stream) {
+  return kd_logits_kl_bwd_ctl(logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, stats, grad_loss,
+                              grad_logits, ld_grad, ws, ws_bytes, ws, stream);
+}
+
+int kd_logits_kl_bwd_ctl(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* t_ids,
+                         const float* t_logits, int K, const float* t_lse, const uint8_t* mask, float tau,
+                         const float* stats, const float* grad_loss, void* grad_logits, int64_t ld_grad, void* ws,
+                         size_t ws_bytes, void* control, void* stream) {
   kd_status st = check_logits(logits, dtype, N, V, ld, tau);
   if (st != KD_OK) return st;
   if ((st = check_teacher(t_ids, t_logits, K, t_lse, V, dtype)) != KD_OK) return st;
   if (!stats || !aligned(stats, 16) || !ok4(grad_loss)) return KD_ERR_INVALID_ARG;
   if ((st = check_grad(logits, dtype, N, V, ld, grad_logits, ld_grad)) != KD_OK) return st;
   if ((st = check_ws(ws, ws_bytes, logits_kl_ws(N))) != KD_OK) return st;
+  if ((st = check_control(control)) != KD_OK) return st;
   if ((st = check_device()) != KD_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Ctrl* ctrl = static_cast<Ctrl*>(ws);
   const int32_t* n_valid;
-  if ((st = count_valid(mask, N, ctrl, &n_valid, s)) != KD_OK) return st;
+  if ((st = count_valid(mask, N, static_cast<Ctrl*>(ws), &n_valid, s)) != KD_OK) return st;
   return map_cuda(launch_logits_kl(2, logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau,
                                    const_cast<float*>(stats), nullptr, grad_loss, n_valid, grad_logits, ld_grad,
-                                   &ctrl->err, s));
+                                   &static_cast<Ctrl*>(control)->err, s));
 }
 
 int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* t_ids,
                       const float* t_logits, int K, const float* t_lse, const uint8_t* mask, float tau,
                       const float* grad_loss, float* loss_out, float* kl_per_token_out, void* grad_logits,
                       int64_t ld_grad, void* ws, size_t ws_bytes, void* stream) {
+  return kd_logits_kl_step_ctl(logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, grad_loss, loss_out,
+                               kl_per_token_out, grad_logits, ld_grad, ws, ws_bytes, ws, stream);
+}
+
+int kd_logits_kl_step_ctl(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int32_t* t_ids,
+                          const float* t_logits, int K, const float* t_lse, const uint8_t* mask, float tau,
+                          const float* grad_loss, float* loss_out, float* kl_per_token_out, void* grad_logits,
+                          int64_t ld_grad, void* ws, size_t ws_bytes, void* control, void* stream) {
   kd_status st = check_logits(logits, dtype, N, V, ld, tau);
   if (st != KD_OK) return st;
   if ((st = check_teacher(t_ids, t_logits, K, t_lse, V, dtype)) != KD_OK) return st;
   if (!ok4(loss_out) || !ok4(grad_loss) || !ok4_or_null(kl_per_token_out)) return KD_ERR_INVALID_ARG;
   if ((st = check_grad(logits, dtype, N, V, ld, grad_logits, ld_grad)) != KD_OK) return st;
   if ((st = check_ws(ws, ws_bytes, logits_kl_ws(N))) != KD_OK) return st;
+  if ((st = check_control(control)) != KD_OK) return st;
   if ((st = check_device()) != KD_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Ctrl* ctrl = static_cast<Ctrl*>(ws);
@@ -169,7 +199,7 @@ int kd_logits_kl_step(const void* logits, int dtype, int64_t N, int64_t V, int64
   const int32_t* n_valid = nullptr;
   if (N > kCountInBlock && (st = count_valid(mask, N, ctrl, &n_valid, s)) != KD_OK) return st;
   if (launch_logits_kl(3, logits, dtype, N, V, ld, t_ids, t_logits, K, t_lse, mask, tau, nullptr, kl, grad_loss,
-                       n_valid, grad_logits, ld_grad, &ctrl->err, s) != cudaSuccess)
+                       n_valid, grad_logits, ld_grad, &static_cast<Ctrl*>(control)->err, s) != cudaSuccess)
     return KD_ERR_CUDA;
   return map_cuda(launch_masked_mean(kl, mask, N, loss_out, s));
 }
