@@ -377,19 +377,19 @@ class _TokenLogprobs(torch.autograd.Function):
         _check_logits(logits)
         ctx.control = _control(logits.device)
         r = token_logprobs_forward(logits, tokens, mask, tau, entropy=True, ws=ctx.control)
-        ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
-        ctx.mask, ctx.tau = mask, tau
+        ctx.save_for_backward(logits, tokens, mask, r.lse, r.entropy)
+        ctx.tau = tau
         ctx.set_materialize_grads(False)
         return r.logp, r.entropy
 
     @staticmethod
     def backward(ctx, g_logp, g_entropy):
-        logits, tokens, lse, ent = ctx.saved_tensors
+        logits, tokens, mask, lse, ent = ctx.saved_tensors
         if g_logp is None and g_entropy is None:
             return None, None, None, None
         if g_logp is None:
             g_logp = torch.zeros(tokens.shape, dtype=torch.float32, device=logits.device)
-        g = token_logprobs_backward(logits, tokens, lse, _f32c(g_logp), ctx.mask, ctx.tau, ent, _f32c(g_entropy),
+        g = token_logprobs_backward(logits, tokens, lse, _f32c(g_logp), mask, ctx.tau, ent, _f32c(g_entropy),
                                     ws=ctx.control)
         return g, None, None, None
 
@@ -484,14 +484,14 @@ class _LogitsKL(torch.autograd.Function):
         _check_logits(logits)
         ctx.control = _control(logits.device)
         loss, stats, ws = _kl_forward(logits, ids, tlog, mask, tau, t_lse, None, ctx.control)
-        ctx.save_for_backward(logits, ids, tlog, stats)
-        ctx.mask, ctx.tau, ctx.t_lse, ctx.ws = mask, tau, t_lse, ws
+        ctx.save_for_backward(logits, ids, tlog, mask, t_lse, stats)
+        ctx.tau, ctx.ws = tau, ws
         return loss[0]
 
     @staticmethod
     def backward(ctx, grad_out):
-        logits, ids, tlog, stats = ctx.saved_tensors
-        g = _kl_backward(logits, ids, tlog, ctx.mask, stats, _f32c(grad_out.reshape(1)), ctx.tau, ctx.t_lse, ctx.ws,
+        logits, ids, tlog, mask, t_lse, stats = ctx.saved_tensors
+        g = _kl_backward(logits, ids, tlog, mask, stats, _f32c(grad_out.reshape(1)), ctx.tau, t_lse, ctx.ws,
                          ctx.control)
         return g, None, None, None, None, None
 
@@ -576,19 +576,19 @@ class _FusedLogprobs(torch.autograd.Function):
         _check_projection(H, W, tokens, mask)
         ctx.control = _control(H.device)
         logp, lse, ent, _ = _fused_forward(H, W, tokens, mask, chunk, tau, True, None, ctx.control)
-        ctx.save_for_backward(H, W, tokens, lse, ent)
-        ctx.mask, ctx.chunk, ctx.tau = mask, chunk, tau
+        ctx.save_for_backward(H, W, tokens, mask, lse, ent)
+        ctx.chunk, ctx.tau = chunk, tau
         ctx.set_materialize_grads(False)
         return logp, ent
 
     @staticmethod
     def backward(ctx, g_logp, g_entropy):
-        H, W, tokens, lse, ent = ctx.saved_tensors
+        H, W, tokens, mask, lse, ent = ctx.saved_tensors
         if g_logp is None and g_entropy is None:
             return None, None, None, None, None, None
         if g_logp is None:
             g_logp = torch.zeros_like(lse)
-        grad_H, grad_W = _fused_backward(H, W, tokens, lse, _f32c(g_logp), ctx.mask, ctx.chunk, ctx.tau, ent,
+        grad_H, grad_W = _fused_backward(H, W, tokens, lse, _f32c(g_logp), mask, ctx.chunk, ctx.tau, ent,
                                          _f32c(g_entropy), None, ctx.control, grad_W_bf16=H.shape[0] <= ctx.chunk)
         return grad_H, grad_W.to(W.dtype), None, None, None, None
 
