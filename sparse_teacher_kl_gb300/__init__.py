@@ -255,6 +255,14 @@ def _grad_like(z: torch.Tensor, grad: Optional[torch.Tensor]):
     return grad, _check_logits(grad, "grad_logits")[3]
 
 
+def _written(*ts):
+    """Tells autograd that a kernel wrote to these tensors of the caller's: where one of them was saved for a backward
+    pass, that pass raises in place of reading what took its values' place."""
+    for t in ts:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _fresh_ws(nbytes: int, device) -> torch.Tensor:
     """A workspace with its control block zeroed and the rest left as it is (the allocator's blocks are aligned)."""
     ws = _scratch(nbytes, device)
@@ -357,6 +365,7 @@ def token_logprobs_backward(logits, tokens, lse, grad_logp, mask=None, tau=1.0, 
     for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_entropy, "grad_entropy")):
         _check(t, name, torch.float32, (N,), dev)
     _check(mask, "mask", torch.uint8, (N,), dev)
+    given = grad_logits
     grad_logits, ldg = _grad_like(logits, grad_logits)
     if ws is None:
         ws = _control(dev)
@@ -364,6 +373,7 @@ def token_logprobs_backward(logits, tokens, lse, grad_logp, mask=None, tau=1.0, 
                                     _ptr(entropy), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_logits), ldg,
                                     _ptr(ws), ws.numel(), _stream(dev))
     _abi.check(st, "kd_token_logprobs_bwd")
+    _written(given)
     return grad_logits
 
 
@@ -425,6 +435,7 @@ def _kl_forward(logits, ids, tlog, mask, tau, t_lse, ws, control, kl_out=None):
                                    float(tau), _ptr(loss), _ptr(stats), _ptr(kl_out), _ptr(ws), ws.numel(),
                                    _ptr(control), _stream(dev))
     _abi.check(st, "kd_logits_kl_fwd")
+    _written(kl_out)
     return loss, stats, ws
 
 
@@ -438,6 +449,7 @@ def _kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau, t_lse, ws, cont
     dt, N, V, ld, K, dev = _check_kl(logits, ids, tlog, mask, t_lse)
     _check(stats, "stats", torch.float32, (N, 4), dev)
     _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
+    given = grad_logits
     grad_logits, ldg = _grad_like(logits, grad_logits)
     if control is None:
         control = _control(dev) if ws is None else ws
@@ -447,6 +459,7 @@ def _kl_backward(logits, ids, tlog, mask, stats, grad_loss, tau, t_lse, ws, cont
                                    float(tau), _ptr(stats), _ptr(grad_loss), _ptr(grad_logits), ldg, _ptr(ws),
                                    ws.numel(), _ptr(control), _stream(dev))
     _abi.check(st, "kd_logits_kl_bwd")
+    _written(given)
     return grad_logits
 
 
@@ -465,6 +478,7 @@ def logits_kl_step(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=
     if grad_loss is None:
         grad_loss = torch.ones((1,), dtype=torch.float32, device=dev)
     _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
+    given = grad_logits
     grad_logits, ldg = _grad_like(logits, grad_logits)
     control = ws
     if ws is None:
@@ -475,6 +489,7 @@ def logits_kl_step(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=
                                     float(tau), _ptr(grad_loss), _ptr(loss), _ptr(kl_out), _ptr(grad_logits), ldg,
                                     _ptr(ws), ws.numel(), _ptr(control), _stream(dev))
     _abi.check(st, "kd_logits_kl_step")
+    _written(given, kl_out)
     return loss, grad_logits
 
 
@@ -544,6 +559,7 @@ def _fused_backward(H, W, tokens, lse, grad_logp, mask, chunk, tau, entropy, gra
         control = _control(dev) if ws is None else ws
     if ws is None:
         ws = _scratch(_abi.kd_fused_logprobs_workspace(N, d, V, chunk, 1), dev)
+    given = grad_H, grad_W
     if grad_H is None:
         grad_H = torch.empty((N, d), dtype=torch.float32 if grad_H_fp32 else torch.bfloat16, device=dev)
     kind = _abi.KD_GRAD_ADD_F32
@@ -558,6 +574,7 @@ def _fused_backward(H, W, tokens, lse, grad_logp, mask, chunk, tau, entropy, gra
                                         1 if grad_H.dtype == torch.float32 else 0, _ptr(grad_W), kind, _ptr(ws),
                                         ws.numel(), _ptr(control), _stream(dev))
     _abi.check(st, "kd_fused_logprobs_bwd")
+    _written(*given)
     return grad_H, grad_W
 
 

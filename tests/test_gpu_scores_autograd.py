@@ -43,3 +43,62 @@ def test_inputs_rewritten_before_the_backward_pass_are_noticed(kd, cuda_device):
         inputs[name].add_(1)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             out.backward()
+
+
+def test_gradients_written_over_the_logits_are_noticed(kd, cuda_device):
+    """token_logprobs keeps the logits for its backward pass; a gradient of another call takes their place."""
+    z, ids, t, _ = case(6, 200, 5, torch.float32)
+    one = torch.ones(1, device="cuda")
+    tok = tokens_for(6, 200, 1, 1)
+    r = kd.token_logprobs_forward(z, tok)
+    _, stats, _ = kd.logits_kl_forward(z, ids, t)
+
+    def step(x):
+        kd.logits_kl_step(x, ids, t, grad_logits=x)
+
+    def kl_backward(x):
+        kd.logits_kl_backward(x, ids, t, None, stats, one, grad_logits=x)
+
+    def score_backward(x):
+        kd.token_logprobs_backward(x, tok, r.lse, torch.ones_like(r.logp), grad_logits=x)
+
+    for write in (step, kl_backward, score_backward):
+        leaf = z.clone().requires_grad_(True)
+        logits = leaf * 1.0
+        logp, _ = kd.token_logprobs(logits, tok)
+        write(logits.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            logp.sum().backward()
+
+
+def test_gradients_written_into_a_callers_tensors_are_noticed(kd, cuda_device):
+    H = torch.randn((5, 64), device="cuda").to(torch.bfloat16)
+    W = torch.randn((300, 64), device="cuda").to(torch.bfloat16)
+    tok = tokens_for(5, 300, 1, 1)[:, 0].contiguous()
+    logp, lse, _, _ = kd.fused_logprobs_forward(H, W, tok)
+    gH, gW = torch.zeros((5, 64), device="cuda"), torch.zeros((300, 64), device="cuda")
+    before = gH._version, gW._version
+    kd.fused_logprobs_backward(H, W, tok, lse, torch.ones_like(logp), grad_H=gH, grad_W=gW)
+    assert gH._version > before[0] and gW._version > before[1]
+    kl = torch.zeros((6,), device="cuda")
+    z, ids, t, _ = case(6, 200, 5, torch.float32)
+    before = kl._version
+    kd.logits_kl_step(z, ids, t, kl_out=kl)
+    assert kl._version > before
+    before = kl._version
+    kd.logits_kl_forward(z, ids, t, kl_out=kl)
+    assert kl._version > before
+
+
+def test_in_place_gradients_under_inference_mode(kd, cuda_device):
+    z, ids, t, _ = case(6, 200, 5, torch.float32)
+    want = kd.logits_kl_step(z, ids, t)[1]
+    with torch.inference_mode():
+        x = z.clone()
+        kd.logits_kl_step(x, ids, t, grad_logits=x)
+    assert torch.equal(x, want)
+    x = None
+    with torch.inference_mode():
+        x = z.clone()
+    kd.logits_kl_step(x, ids, t, grad_logits=x)       # an inference tensor outside inference mode
+    assert torch.equal(x, want)
