@@ -11,6 +11,7 @@ runs in the CUDA kernels of ``libkdkl.so`` (see ``include/kdkl.h``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 from typing import NamedTuple, Optional
 
@@ -381,6 +382,29 @@ def _f32c(g):
     return None if g is None else g.to(torch.float32).contiguous()
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, g):
+        return g.view_as(g)
+
+    @staticmethod
+    def backward(ctx, g):
+        raise RuntimeError("trying to differentiate twice a function that is once_differentiable")
+
+
+def _once_differentiable(backward):
+    """A backward pass whose gradients, under create_graph, raise when they are differentiated in turn, by the inputs
+    as by the incoming gradients (torch's own decorator sees the latter alone)."""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        return tuple(None if g is None else _NoSecondDerivative.apply(g.detach().requires_grad_()) for g in out)
+    return run
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, mask, tau):
@@ -393,6 +417,7 @@ class _TokenLogprobs(torch.autograd.Function):
         return r.logp, r.entropy
 
     @staticmethod
+    @_once_differentiable
     def backward(ctx, g_logp, g_entropy):
         logits, tokens, mask, lse, ent = ctx.saved_tensors
         if g_logp is None and g_entropy is None:
@@ -504,6 +529,7 @@ class _LogitsKL(torch.autograd.Function):
         return loss[0]
 
     @staticmethod
+    @_once_differentiable
     def backward(ctx, grad_out):
         logits, ids, tlog, mask, t_lse, stats = ctx.saved_tensors
         g = _kl_backward(logits, ids, tlog, mask, stats, _f32c(grad_out.reshape(1)), ctx.tau, t_lse, ctx.ws,
@@ -599,6 +625,7 @@ class _FusedLogprobs(torch.autograd.Function):
         return logp, ent
 
     @staticmethod
+    @_once_differentiable
     def backward(ctx, g_logp, g_entropy):
         H, W, tokens, mask, lse, ent = ctx.saved_tensors
         if g_logp is None and g_entropy is None:

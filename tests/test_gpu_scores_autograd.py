@@ -102,3 +102,20 @@ def test_in_place_gradients_under_inference_mode(kd, cuda_device):
         x = z.clone()
     kd.logits_kl_step(x, ids, t, grad_logits=x)       # an inference tensor outside inference mode
     assert torch.equal(x, want)
+
+
+def test_second_derivatives_are_refused(kd, cuda_device):
+    for i in range(3):
+        out, x, _ = list(calls(kd))[i]
+        (g,) = torch.autograd.grad(out, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (g.float() * x.float()).sum().backward()
+
+
+def test_first_derivatives_with_create_graph_keep_their_values(kd, cuda_device):
+    for i in range(2):
+        out, x, _ = list(calls(kd))[i]
+        out2, x2, _ = list(calls(kd))[i]
+        (a,) = torch.autograd.grad(out, x, create_graph=True)
+        (b,) = torch.autograd.grad(out2, x2)
+        assert torch.equal(a, b)
