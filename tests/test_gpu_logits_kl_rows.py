@@ -104,3 +104,70 @@ def test_forward_with_a_padding_row_between_two_of_a_block(kd, cuda_device, V, o
         _, stats, ws = kd.logits_kl_forward(z, ids, t, mask, kl_out=got)
         close(got, kl, tol)
         close_grad(kd.logits_kl_backward(z, ids, t, mask, stats, torch.ones(1, device="cuda"), ws=ws), dz, z.dtype)
+
+
+def test_reference_is_the_oracle(cuda_device):
+    for tail in (False, True):
+        z, ids, t, t_lse = case(30, 300, 7, torch.float32, tail=tail, seed=3)
+        mask = stripes(30, 3, 2, 3)
+        kl, dz = reference(z, ids, t, mask, t_lse, 0.75)
+        ref = oracle.logits_kl(host(z), host(ids), host(t), host(mask), 1.0, host(t_lse), 0.75)
+        assert np.allclose(host(kl), ref.kl, atol=1e-12) and np.allclose(host(dz), ref.grad, atol=1e-14)
+
+
+# rows of up to 16, 48, 96, 208 and 416 KB, and of more (clusters of two): how many resident blocks or
+# clusters of an SM take them
+VARIANTS = [
+    ("10 blocks on an SM", 700, torch.float32, 10, 4597),
+    ("10 blocks on an SM", 2053, torch.bfloat16, 10, 3500),
+    ("8 blocks on an SM", 9001, torch.float16, 8, 2600),
+    ("4 blocks on an SM", 32000, torch.bfloat16, 4, 1500),
+    ("2 blocks on an SM", 70001, torch.bfloat16, 2, 800),
+    ("one block on an SM", 150000, torch.bfloat16, 1, 400),
+    ("clusters of two", 201088, torch.float32, 0.5, 230),
+]
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("pattern", ["all", "random", "stripes"])
+@pytest.mark.parametrize("V,dtype,per_sm,N", [v[1:] for v in VARIANTS], ids=[f"{v[0]}, V={v[1]}" for v in VARIANTS])
+def test_every_variant_with_several_rows_a_block(kd, cuda_device, V, dtype, per_sm, N, pattern, tail):
+    z, ids, t, t_lse = case(N, V, 20, dtype, tail=tail, seed=V)
+    mask = None
+    if pattern == "random":
+        g = torch.Generator(device="cuda").manual_seed(2)
+        mask = (torch.rand((N,), generator=g, device="cuda") < 0.7).to(torch.uint8)
+    elif pattern == "stripes":
+        mask = stripes(N, int(per_sm * torch.cuda.get_device_properties(0).multi_processor_count))
+    check(kd, z, ids, t, t_lse, mask)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V,dtype", [(515, torch.bfloat16), (9001, torch.float32)])
+def test_padding_is_not_looked_at_in_any_pass(kd, cuda_device, V, dtype, tail):
+    N = 3100 if V < 1000 else 1300
+    z, ids, t, t_lse = case(N, V, 9, dtype, tail=tail)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    mask = (torch.rand((N,), generator=g, device="cuda") < 0.6).to(torch.uint8)
+    zc, idc, tc, lc = padded(z, ids, t, t_lse, mask)
+    kl, dz = reference(zc, idc, tc, mask, lc, 0.75)
+    one = torch.full((1,), 0.75, device="cuda")
+    ws = kd.workspace(kd._abi.kd_logits_kl_workspace(N, V, 9), "cuda")
+    got = torch.full((N,), -1.0, device="cuda")
+    _, stats, _ = kd.logits_kl_forward(z, ids, t, mask, 1.0, t_lse, ws=ws, kl_out=got)
+    close(got, kl, 4e-5 + 4e-7 * (kl + 40))
+    close_grad(kd.logits_kl_backward(z, ids, t, mask, stats, one, 1.0, t_lse, ws=ws), dz, dtype)
+    _, grad = kd.logits_kl_step(z, ids, t, mask, 1.0, t_lse, one, ws=ws, kl_out=got)
+    close(got, kl, 4e-5 + 4e-7 * (kl + 40))
+    close_grad(grad, dz, dtype)
+    _, same = kd.logits_kl_step(z, ids, t, mask, 1.0, t_lse, one, ws=ws, grad_logits=z)   # in place
+    assert same is z and torch.equal(z, grad)
+    assert kd.device_error(ws)[0] == 0
+
+
+@pytest.mark.parametrize("N", [8192, 8193, 20011])
+def test_the_valid_rows_are_counted_either_way(kd, cuda_device, N):
+    """Steps of up to 8192 rows count their valid rows in every block, longer ones ahead."""
+    z, ids, t, t_lse = case(N, 128, 5, torch.bfloat16, tail=True)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    check(kd, z, ids, t, t_lse, (torch.rand((N,), generator=g, device="cuda") < 0.5).to(torch.uint8))
