@@ -177,15 +177,22 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
     o.z_ref = fmaxf(o.z_ref, z);
   }
   // the sums relative to the warp's largest logit; only with an entry that repeats an id do they
-  // wait for every entry's logit
-  auto sums = [&] {
+  // wait for every entry's logit.  An id counts once in S: with its entry that came first to the
+  // bitmap or, where there are more, with its lowest one, so that the order of the sum is fixed.
+  auto sums = [&](bool repeats) {
     o.z_ref = warp_max(o.z_ref);
     o.s_s = o.e = o.d = 0.f;
     for (int j = et; j < a.K; j += ET) {
       const int loc = t.loc[j];
       if (loc == -1) continue;
       const float z = t.z[j], e = t.e[j];
-      if (loc >= 0) {
+      bool once = loc >= 0;
+      if (repeats) {
+        const int at = loc >= 0 ? loc : -2 - loc;
+        once = true;
+        for (int q = 0; q < j; ++q) once &= t.loc[q] != at && t.loc[q] != -2 - at;
+      }
+      if (once) {
         if (!(fabsf(z) <= 3.402823466e38f) && z != -INFINITY) o.s_s = __int_as_float(0x7FC00000);  // NaN or +inf
         else if (z != -INFINITY) o.s_s += ex2_approx(stats_t(z, o.z_ref, a.k));
       }
@@ -203,7 +210,7 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
   o.e_sum = warp_sum(o.e_sum);
   o.distinct = __reduce_add_sync(0xffffffffu, o.distinct);
   o.repeats = __reduce_add_sync(0xffffffffu, o.repeats);
-  sums();
+  sums(false);
   sync();
   if (sh.repeated(EW)) {
     sync();  // every thread has read the summaries
@@ -214,7 +221,7 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
         o.z_ref = fmaxf(o.z_ref, t.z[j]);
       }
     __syncwarp();
-    sums();
+    sums(true);
     sync();
   }
 }
