@@ -121,7 +121,8 @@ def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None, grad_loss=1.0) 
             outside = np.ones(V, bool)
             outside[at] = False
             p_rest = 1.0 - float(p.sum())
-            if not outside.any() or p_rest < REST_RESOLUTION * (1.0 + abs(float(t_lse[r]))):
+            least = 0.0 if t_lse[r] == -np.inf else REST_RESOLUTION * (1.0 + abs(float(t_lse[r])))
+            if not outside.any() or p_rest < least:
                 p_rest = 0.0
             lq_out, lq_rest = _log_softmax(lq[outside]) if outside.any() else (None, -np.inf)
             if p_rest > 0:

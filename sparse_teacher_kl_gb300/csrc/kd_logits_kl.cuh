@@ -267,9 +267,11 @@ __device__ __forceinline__ LkRow lk_row(const LogitsKlArgs& a, const RowStats& a
     // Below the resolution of its inputs a remainder is rounding, not mass (a teacher whose cache holds
     // everything leaves some 1e-6 of either sign, and a student without mass there would be infinitely
     // wrong): t_lse is rounded by |t_lse| 2^-24, t / tau by as much and half more, the exponentials and
-    // their sum by 2^-21 in all.  The entries may also cover the whole vocabulary (K = V, one block).
+    // their sum by 2^-21 in all.  (A teacher row of nothing but -inf has all its mass there, wherever that
+    // is: KL 0 and no gradient, as without the rest class.)  The entries may also cover the whole vocabulary (K = V, one block).
     const float left = 1.f - t.e_sum;
-    const float p_rest = t.distinct == a.V || left < 4.76837158e-7f * (1.f + fabsf(t_lse)) ? 0.f : left;
+    const float least = t_lse == -INFINITY ? 0.f : 4.76837158e-7f * (1.f + fabsf(t_lse));
+    const float p_rest = t.distinct == a.V || left < least ? 0.f : left;
     float log_q = -INFINITY;  // of the rest
     if (b.s > 0.f) {
       log_q = kLn2 * (stats_shift(b.m, all.m, a.k) + log2f(b.s) - w.log2_s);

@@ -64,3 +64,21 @@ def test_a_small_rest_is_still_mass(kd, cuda_device, rest):
     # p_R within 2^-21 (1 + t_lse) of the float64 value, times |ln p_R / q_R| + 1
     near(kl.cpu(), ref.kl, 6e-5 + 2.0 ** -21 * (1 + np.abs(host(t_lse))) * (1 + abs(math.log(rest))))
     assert (ref.kl - oracle.logits_kl(host(z), host(ids), host(t)).kl).min() < -1e-6   # the rest is seen
+
+
+def test_a_teacher_row_of_nothing(kd, cuda_device):
+    """Every teacher logit of a row -inf, its logsumexp too: no divergence and no gradient in that row."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.randn((6, 900), generator=g, device="cuda")
+    ids = torch.argsort(torch.rand((6, 900), generator=g, device="cuda"), dim=1)[:, :7].to(torch.int32).contiguous()
+    t = torch.randn((6, 7), generator=g, device="cuda")
+    t_lse = torch.logsumexp(t, 1) + 0.3
+    t[2], t_lse[2] = -math.inf, -math.inf
+    ref = oracle.logits_kl(host(z), host(ids), host(t), None, 1.0, host(t_lse))
+    kl = torch.empty((6,), device="cuda")
+    _, dz = kd.logits_kl_step(z, ids, t, None, 1.0, t_lse, kl_out=kl)
+    near(kl.cpu(), ref.kl, 6e-5)
+    rows = [0, 1, 3, 4, 5]
+    check_grad(dz[rows], ref.grad[rows], torch.float32)
+    # q_R - 1 is the rounding of the row's sum (2^-22), spread over the row
+    assert abs(float(kl[2])) <= 1e-6 and float(dz[2].abs().max()) <= 1e-6 / 6

@@ -59,3 +59,14 @@ def test_a_rest_above_the_resolution_is_kept():
         q_s = np.take_along_axis(np.exp(lq), ids, 1)
         kl = (p * (np.log(p) - np.log(q_s))).sum(1) + rest * (np.log(rest) - np.log(1 - q_s.sum(1)))
         assert np.allclose(got.kl, kl, atol=1e-10)
+
+
+def test_a_teacher_row_of_nothing():
+    """Every teacher logit -inf, its logsumexp too: no divergence, no gradient."""
+    rng = np.random.default_rng(6)
+    z = rng.normal(0, 1, (2, 20))
+    ids = np.stack([rng.permutation(20)[:3] for _ in range(2)])
+    t = np.full((2, 3), -np.inf)
+    for t_lse in (np.full(2, -np.inf), None):
+        got = oracle.logits_kl(z, ids, t, t_lse=t_lse)
+        assert np.allclose(got.kl, 0, atol=1e-12) and np.allclose(got.grad, 0, atol=1e-12)
