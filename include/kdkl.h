@@ -350,7 +350,8 @@ KD_API size_t kd_logits_kl_workspace(int64_t N, int64_t V, int K);
  *                   vocabulary there is no such class, and a p_R below 2^-21 (1 + |t_lse|),
  *                   which is the rounding of t_lse and the sum, is taken as 0.
  *                   t_lse: [N] fp32, logsumexp of the teacher's full row of logits / tau
- *                   (for tau = 1 the lse_out of kd_topk_cache and kd_teacher_topk).
+ *                   (for tau = 1 the lse_out of kd_topk_cache and kd_teacher_topk); p_k is as
+ *                   exact as fp32 holds it (|t_lse| 2^-24 of itself).
  *   loss          = sum over valid t of KL_t / N_valid   (0 when N_valid == 0).
  *   t_ids    : [N, K] int32, 1 <= K <= min(V, KD_MAX_K).  An id that repeats within a row
  *              adds up its entries' probabilities.  One outside [0, V) is recorded in the
@@ -414,7 +415,8 @@ KD_API int kd_logits_kl_step_ctl(const void* logits, int dtype, int64_t N, int64
  *   tokens : [N] int32 in [0, V) (one outside is recorded in the error word with its
  *            row; its log probability is NaN, its one-hot gradient is left out).
  *   logp_out, lse_out : [N] fp32.   entropy_out: [N] fp32 or NULL.  Padding rows give 0;
- *            their tokens are not looked at.
+ *            their tokens are not looked at (their hidden states are multiplied by zeros in
+ *            the backward pass, and so have to be finite).
  * The backward pass recomputes each chunk's logits and takes, per valid position,
  *   dZ_v = (1 / tau) (g [v = token] - p_v (g + h (ln p_v + H)))
  * with g = grad_logp, h = grad_entropy ([N] fp32; grad_entropy and entropy may be NULL

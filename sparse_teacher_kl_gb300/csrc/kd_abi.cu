@@ -162,8 +162,9 @@ static KlLayout kl_layout(int64_t N, int64_t d, int64_t V, int K, int64_t chunk)
 
 // CTA pairs (GemmProblem::cta_pair, clusters of two) for every launch with at least two
 // row tiles (measured on the gpt-oss shape: 342k against 295k tokens/s for single-CTA
-// tiles).  The loss epilogues also need an even number of row tiles (no phantom tile
-// writing past the chunk); the gradient products check their rows themselves.
+// tiles).  The fused loss's epilogues also need an even number of row tiles (no phantom tile
+// writing past the chunk); the score epilogues and the gradient products run one, and check
+// their rows themselves (the stores of dZ boxes are clipped at the chunk's last row).
 static void set_cluster(GemmProblem& p) {
   const bool loss_epi = (p.epi == EPI_LSE || p.epi == EPI_DZ || p.epi == EPI_LSE_Z);
   p.cta_pair = (p.m_tiles >= 2 && !(loss_epi && p.m_tiles % 2 != 0)) ? 1 : 0;
@@ -435,6 +436,7 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   const float inv_tau = lp ? inverse_tau(tau) : 1.0f / tau;
   const uint16_t* H = static_cast<const uint16_t*>(H_bf16);
 
+  // one or two positions of a large head: bound by reading W (see FEW_ROW_BYTES)
   if (lp && N <= FEW_ROWS && V * d * 2 > N * FEW_ROW_BYTES && FEW_ROWS * d * 4 <= FEW_MAX_SMEM) {
     int units = 0;
     cudaError_t e = launch_logprob_few(H, static_cast<const uint16_t*>(W_bf16), int(N), int(d), V, lp->tokens, mask,

@@ -23,6 +23,10 @@
 //   EPI_LSE_H / EPI_DZ_LP  log probabilities of given tokens with the entropy, and their
 //             gradient: as EPI_LSE / EPI_DZ with one token per row in the teacher's place;
 //             the entropy takes one more sum, u = sum 2^t t, t the term's exponent.
+//             dZ is rounded to bf16 here too: the tensor cores take both operands of the
+//             gradient products in one 16-bit type, and H and W are bf16.  Measured on 8192 x
+//             2048 x 32000: gradients within 2.3e-3 (2-norm) of float64, 1.7e-3 of which is the
+//             rounding of bf16 outputs; a second bf16 term of dZ would run the products twice.
 //   EPI_STORE / EPI_ACCUM  plain C = acc / C += acc for the gradient products.
 #include <math.h>
 #include <stdio.h>

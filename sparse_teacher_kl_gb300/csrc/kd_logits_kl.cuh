@@ -13,11 +13,12 @@
 //
 // Loss and gradient in one call must read each logit once and write each gradient once
 // (2 N V elements): bound by HBM.  Measured, bf16, K = 100: 4096 x 201088 with the rest class
-// 0.635 ms (5.2 TB/s, 77 % of the copy bandwidth; DRAM reads 13 % over the row's own bytes), 8192 x
-// 32000 with 5 % padding 0.217 ms (4.7 TB/s, 70 %); what is left are the joins of a row's
-// statistics, where a block's loads run dry.  Tried and slower: the row kept in the shared memory
-// of a cluster by bulk copies (0.83 ms at best, the joins cost more), the next row's statistics
-// and this row's gradient in one loop (1.04 ms: too few loads in flight).
+// 0.641 ms (5.1 TB/s, 76 % of the copy bandwidth; DRAM reads 12 % over the row's own bytes), 8192 x
+// 32000 with 5 % padding 0.211 ms (4.8 TB/s, 71 %); what is left are the joins of a row's
+// statistics, where a block's loads run dry.  Tried at 4096 x 201088 and slower: the row kept in
+// the shared memory of a cluster by bulk copies (0.83 ms at best, the joins cost more), the next
+// row's statistics and this row's gradient in one loop (1.04 ms: too few loads in flight).  Rows
+// that fit into one SM were not tried that way; they are read twice like the others.
 #pragma once
 
 #include "kd_rows.cuh"
@@ -642,14 +643,15 @@ static cudaError_t lk_launch(LogitsKlArgs a, int ctas, cudaStream_t s) {
 // How a row is shared out, by its bytes (measured: bf16, K = 100, the rest class, N x V; us):
 //   up to 16 KB   ten blocks of 4 warps on an SM, a row each: little of a row is its logits
 //                 (8192 x 4096: 69; blocks of 5 warps 88, of 9 140)
-//   up to 48 KB   eight of 5 warps (4096 x 16000: 79; of 9 warps 95)
-//   up to 96 KB   four of 9 (8192 x 32000, 5 % padding, no rest: 217; of 16 warps 241, of 32 373)
-//   up to 208 KB  two of 16 (4096 x 100000: 350; of 9 warps 378, of 32 373)
-//   longer        one of 32 (2048 x 201088: 334; of 16 warps 377); over 416 KB a cluster of two or
-//                 more (1024 x 201088 fp32: 343; without 363), so that the rows in flight
+//   up to 48 KB   eight of 5 warps (4096 x 16000, no rest: 69; of 9 warps some 16 more)
+//   up to 96 KB   four of 9 (8192 x 32000, 5 % padding, no rest: 211; of 16 warps some 24 more, of 32
+//                 156 more)
+//   up to 208 KB  two of 16 (4096 x 100000, no rest: 342; of 9 warps some 28 more, of 32 23 more)
+//   longer        one of 32 (2048 x 201088: 339; of 16 warps some 43 more); over 416 KB a cluster of two
+//                 or more (1024 x 201088 fp32: 349; without some 20 more), so that the rows in flight
 //                 (at most 152 x 4 x 96 KB = 58 MB, 152 x 416 KB = 63 MB) stay in half of L2
 // With few rows a cluster takes each, while a thread keeps more than a group of vectors
-// (8 x 201088: 22.6; a block each 28.7).
+// (8 x 201088: 22.5; a block each 28.7).
 template <int DT, bool REST, bool STEP>
 static cudaError_t lk_one(const LogitsKlArgs& a, cudaStream_t s) {
   const int64_t nv = a.V / Elt<DT>::kVec + 2, kb = nv * 16 / 1024;

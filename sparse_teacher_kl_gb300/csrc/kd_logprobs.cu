@@ -9,17 +9,17 @@
 //
 // The forward pass reads each logit once: what it must move is N V elements.  The backward
 // pass reads and writes each once (2 N V elements).  Both are bound by HBM.  Measured, bf16:
-// 4096 x 151936 with the entropy and 5 alternatives 0.222 ms (5.6 TB/s, 83 % of the copy
-// bandwidth; 92 % with the softmax terms left out, so the rest is their issue slots and the
-// joins of a row), its gradient 0.379 ms (6.6 TB/s, 97 %); one row of 201088 logits 4.4 us, with
-// 20 alternatives 9.2 us.
+// 4096 x 151936 with the entropy and 5 alternatives 0.211 ms (5.9 TB/s, 87 % of the copy
+// bandwidth; fp16 the same; the softmax terms' issue slots and the joins of a row are the rest), its
+// gradient 0.376 ms (6.6 TB/s, 98 %); 2048 x 151936 fp32 0.230 ms (5.4 TB/s, 80 %); one row of 201088
+// logits 4.4 us, with 20 alternatives 9.2 us.
 #include "kd_rows.cuh"
 
 namespace kd {
 
 constexpr int LP_THREADS = 256;      // forward
 constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_PER_SM = 6;         // blocks on an SM (4096 x 151936: 222 us; 4: 232, 5: 229)
+constexpr int LP_PER_SM = 6;         // blocks on an SM (4096 x 151936, an earlier loop: 222 us; 4: 232, 5: 229)
 constexpr int LP_SLOTS = 32;         // group maxima kept per thread
 constexpr int LP_CAND = 1024;        // candidates for the top alternatives
 constexpr int LP_LIST = 512;         // groups that may hold one
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_PER_SM) kd_logprobs_fwd_kernel(
 
 // CTAs per row: one where the rows alone give every SM its blocks; otherwise as many as
 // would, up to the largest cluster, while each thread still has two groups of vectors (1 x 201088:
-// 6.8 us, without clusters 18.7; 128 x 151936 with 5 alternatives 18.7, 26.7; 512 rows 39 either way).
+// 6.8 us, without clusters 18.7; 128 x 151936 with 5 alternatives 18.5, 26.7; 512 rows 35).
 static int logprobs_cluster(int64_t N, int64_t nv) {
   const int64_t want = int64_t(gemm_max_grid()) * LP_PER_SM;
   int c = 1;

@@ -236,8 +236,8 @@ cudaError_t launch_lse_combine(const float4* partials, int n_units_per_row, int 
 // (logp as a difference of logits: z_token / tau and lse would each be rounded at their own size)
 // Threads as in the lse combine, with more phases: a thread's partials are a chain of dependent
 // exponentials, and rows are often few.  Measured (events around the launch): 300 rows of 391 units
-// 14.7 us with 32 phases, 29.7 with 8; one row of 304 units: the call of one hidden state 187 against
-// 196 us.
+// 14.7 us with 32 phases, 29.7 with 8; one row of 304 units: the call of one hidden state 190 us, 9 more
+// with 8.
 
 constexpr int LPC_PHASES = 32;
 
