@@ -437,7 +437,8 @@ static int fwd_impl(const void* H_bf16, const void* W_bf16, const int32_t* t_ids
   const uint16_t* H = static_cast<const uint16_t*>(H_bf16);
 
   // one or two positions of a large head: bound by reading W (see FEW_ROW_BYTES)
-  if (lp && N <= FEW_ROWS && V * d * 2 > N * FEW_ROW_BYTES && FEW_ROWS * d * 4 <= FEW_MAX_SMEM) {
+  if (lp && N <= FEW_ROWS && V * d * 2 > N * FEW_ROW_BYTES && L.n_groups >= gemm_max_grid() &&
+      FEW_ROWS * d * 4 <= FEW_MAX_SMEM) {
     int units = 0;
     cudaError_t e = launch_logprob_few(H, static_cast<const uint16_t*>(W_bf16), int(N), int(d), V, lp->tokens, mask,
                                        tau, partials, L.n_groups, &units, s);

@@ -227,11 +227,14 @@ cudaError_t launch_logprob_row_stats(const float4* partials, int n_units_per_row
 // EPI_LSE_H's partials for up to FEW_ROWS rows without the tensor cores; *units: how many per row
 // were written (at most max_units).  Faster than the engine's 128-row tiles for one row where W has
 // to come from HBM, and for two where that takes longer than their logits' sums: where W has more
-// than FEW_ROW_BYTES for each row (us, this / the engine; W in MB):
-//   W         2    66   131   206   262   311   622   1051  1158  1245
-//   one row   18/13 25/25 41/43 51/65 66/64 60/78 102/140 162/205 190/230 186/249
-//   two       25/13 33/25 49/41 69/60 75/66 74/79 113/141 170/244 209/229 196/248
-// (three rows 298 against 224, four 298 against 227 at 1158 MB)
+// than FEW_ROW_BYTES for each row, and the vocabulary a unit (BN tokens, as many as the partials have
+// room for) for every SM.  us, this / the engine, for a V x d head:
+//              4096x256 50257x768 50257x1600 201088x512 151936x1024 50257x4096 151936x2048 201088x2880
+//   W in MB       2        77        161        206        311         412        622        1158
+//   one row     18/13     29/26      45/49      52/62      60/80      78/103     102/147    190/230
+//   two         25/13     37/27      54/51      69/62      74/84      90/102     113/148    209/229
+// and with too few units: 32000 x 4096 66/69 and 76/68, 32000 x 8192 117/110 and 130/110, 10000 x 8192
+// 105/65 and 118/64; three rows at 1158 MB 298/224, four 298/227.
 constexpr int FEW_ROWS = 2;
 constexpr int64_t FEW_ROW_BYTES = 150000000;
 constexpr int FEW_MAX_SMEM = 200 * 1024;  // the hidden states in fp32: a limit on rows * d
