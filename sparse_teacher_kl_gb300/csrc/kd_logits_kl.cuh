@@ -78,12 +78,16 @@ __device__ __forceinline__ LkEntries lk_entries(uint8_t* at, int n, int K) {
   return t;
 }
 
+// The sums below are of e times this (KD_MAX_K entries of at most 1, so that no sum passes a single
+// entry's size: student logits of a type's lowest value on cached ids make entries of up to 3e38).
+constexpr float kEntryScale = 1.f / KD_MAX_K;
+
 // What a warp's entries come to.
 struct LkSummary {
   float e_sum;             // over all of them
   float s_m, s_s;          // the student's logits on the block's part of S, each id once
-  float z_ref, e, d;       // over the block's: sum of e, and of e (t - (z - z_ref) / tau); z_ref
-                           // the largest z (-inf where there is none)
+  float z_ref, e, d;       // over the block's: sum of e, and of e (t - (z - z_ref) / tau), scaled;
+                           // z_ref the largest z (-inf where there is none)
   int distinct, repeats;   // ids that came first, and again
   float t_lse;
 };
@@ -198,8 +202,9 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
         else if (z != -INFINITY) o.s_s += ex2_approx(stats_t(z, o.z_ref, a.k));
       }
       if (!(e <= 0.f)) {
-        o.e += e;
-        o.d += z == -INFINITY ? INFINITY : e * (t.t[j] - (z - o.z_ref) * a.inv_tau);
+        const float es = e * kEntryScale;
+        o.e += es;
+        o.d += z == -INFINITY ? INFINITY : fmaf(-es * a.inv_tau, z - o.z_ref, es * t.t[j]);
       }
     }
     o.s_s = warp_sum(o.s_s);
@@ -230,7 +235,7 @@ __device__ __forceinline__ void lk_teacher(const LogitsKlArgs& a, int64_t r, con
 // One warp, whose first lanes hold parts of a row's entries: all of them together.
 __device__ __forceinline__ void lk_merge(const LogitsKlArgs& a, LkSummary& o) {
   const float ref = warp_max(o.z_ref);
-  o.d = warp_sum(o.z_ref == -INFINITY || o.e == 0.f ? o.d : fmaf(-o.e, (o.z_ref - ref) * a.inv_tau, o.d));
+  o.d = warp_sum(o.z_ref == -INFINITY || o.e == 0.f ? o.d : fmaf(-o.e * a.inv_tau, o.z_ref - ref, o.d));
   o.z_ref = ref;
   o.e = warp_sum(o.e);
   o.e_sum = warp_sum(o.e_sum);
@@ -277,7 +282,11 @@ __device__ __forceinline__ LkRow lk_row(const LogitsKlArgs& a, const RowStats& a
     if (b.s > 0.f) {
       log_q = kLn2 * (stats_shift(b.m, all.m, a.k) + log2f(b.s) - w.log2_s);
     }
-    if (p_rest > 0.f) w.rest_kl = p_rest * (logf(p_rest) - log_q);
+    if (p_rest > 0.f) {
+      w.rest_kl = p_rest * (logf(p_rest) - log_q);
+      // a logarithm beyond fp32's range, which its share of the mass may bring back into it
+      if (log_q == -INFINITY && b.s > 0.f) w.rest_kl = -(p_rest * a.inv_tau) * (b.m - all.m);
+    }
     w.scale = b.s == 0.f ? 0.f : c * (expf(log_q) - p_rest) / b.s;
     if (b.s != b.s) w.rest_kl = w.scale = b.s;
   } else {
@@ -296,7 +305,8 @@ __device__ __forceinline__ float lk_kl(const LogitsKlArgs& a, const LkRow& w, fl
   if (w.none || e_here == 0.f) return 0.f;
   if (d_here != d_here) return d_here;
   if (w.empty || z_ref == -INFINITY) return INFINITY;
-  return w.inv_sum * (d_here - e_here * (w.log_norm + stats_logp(z_ref, w.m, w.log2_s, a.k, a.tau)));
+  const float log_q = stats_logp(z_ref, w.m, w.log2_s, a.k, a.tau);
+  return w.inv_sum * (1.f / kEntryScale) * (d_here - e_here * (w.log_norm + log_q));
 }
 
 // Vectors [lo, hi) of a row by the block's first THREADS threads: the gradient outside S.

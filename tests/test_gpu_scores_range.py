@@ -262,3 +262,35 @@ def test_fused_gradients_at_small_temperatures(kd, cuda_device, N, V, chunk, tau
     h, w = H.double().cpu().numpy(), W.double().cpu().numpy()
     for got, ref, size in ((gH, dz @ w, bound @ np.abs(w)), (gW, dz.T @ h, bound.T @ np.abs(h))):
         near(got.double().cpu(), ref, (2.0 ** -8 + 1e-3) * size + 1e-30)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tau", [1.0, 0.3])
+def test_kl_of_cached_ids_masked_with_the_lowest_value(kd, cuda_device, dtype, tau, tail):
+    """The teacher keeps a little mass on tokens that the student masks with its type's lowest value, cached or
+    (with the rest class) not: the KL is that mass times 3e38 / tau, in range although its unnormalised sums are
+    not.  To 4e-6 of itself, and the rest's mass to 2^-21 (1 + t_lse)."""
+    N, V, K = 20, 2000, 300
+    low = torch.finfo(dtype).min
+    g = torch.Generator(device="cuda").manual_seed(8)
+    z = torch.randn((N, V), generator=g, device="cuda").to(dtype)
+    ids = torch.argsort(torch.rand((N, V), generator=g, device="cuda"), dim=1)[:, :K].to(torch.int32).contiguous()
+    t = torch.sort(torch.randn((N, K), generator=g, device="cuda") * 0.3, dim=1, descending=True)[0].contiguous()
+    t_lse = torch.logsumexp(t / tau, 1) + 0.05 if tail else None
+    if tail:
+        z.masked_fill_(torch.ones_like(z, dtype=torch.bool).scatter_(1, ids.long(), False), low)
+    z.scatter_(1, ids[:, K - 60:].long(), low)
+    host = [x.double().cpu().numpy() if x is not None and x.is_floating_point() else x for x in (z, t, t_lse)]
+    ref = oracle.logits_kl(host[0], ids.cpu().numpy(), host[1], None, f32(tau), host[2])
+    assert (ref.kl > 1e36).all() and (ref.kl < 3e38).all()
+    tol = 4e-6 * ref.kl
+    if tail:
+        tol = tol + 2.0 ** -21 * (1 + np.abs(host[2])) * 3.4e38 / tau
+    kl = torch.empty((N,), device="cuda")
+    kd.logits_kl_forward(z, ids, t, None, tau, t_lse, kl_out=kl)
+    near(kl.cpu(), ref.kl, tol)
+    loss, dz = kd.logits_kl_step(z, ids, t, None, tau, t_lse, kl_out=kl)
+    near(kl.cpu(), ref.kl, tol)
+    near(loss.cpu(), [ref.loss], tol.max())
+    check_grad(dz, ref.grad, dtype)
