@@ -360,7 +360,8 @@ KD_API size_t kd_logits_kl_workspace(int64_t N, int64_t V, int K);
  *              at).  Without t_lse, a row with no entry has KL 0 and zero gradient.
  *   loss_out : device fp32 scalar.     kl_per_token_out: [N] fp32 or NULL.
  *   stats_out: [N, 4] fp32, the row statistics that the backward pass takes: the largest
- *              logit and sum exp((logit - largest) / tau) over the row, then over the ids
+ *              logit and sum exp((logit - largest) / tau) over the row (to the rounding of
+ *              largest / tau, which cancels where they are used together), then over the ids
  *              outside S (with t_lse; -inf and 0 without).
  * KD_ERR_UNSUPPORTED when the bitmap of S and the K entries of two rows do not fit into the
  * shared memory of an SM (V over about 0.7 million, 0.35 million for fp32).
