@@ -453,6 +453,48 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
                     void* ws, size_t ws_bytes, void* control, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * Softmax cross entropy against hard labels from hidden states and the LM head: the hard-label term of
+ * a distillation loss, the [N, V] logits never formed (no page has a counterpart).  With z' = h W^T, or
+ * c tanh(h W^T / c) for a softcap c, and lse = logsumexp(z'),
+ *   loss_n = lse - (1 - e) z'_y - (e / V) sum_v z'_v + l lse^2     e label_smoothing, l z_loss
+ *   loss   = sum over valid n of loss_n / n_valid                  (0 when none is)
+ *   H_bf16, W_bf16, chunk : as for kd_fused_kl_fwd.
+ *   labels : [N] int32.  A position is valid if its label is not ignore_index and mask ([N] uint8, NULL:
+ *            all) is not 0; only those are projected, the hidden states of the others are not read.
+ *            A valid position's label outside [0, V) is recorded in the error word with its position;
+ *            its loss is NaN, its gradient left out.
+ *   0 <= label_smoothing < 1; z_loss >= 0; softcap > 0, or 0 for none.
+ *   loss_out: device fp32 scalar.  lse_out, loss_per_token_out: [N] fp32 (the latter may be NULL), 0 for
+ *            positions that are not valid.
+ * kd_fused_cross_entropy_step returns the gradients with the loss, for a grad_loss (device fp32 scalar,
+ * NULL: 1) known beforehand: one projection and two products in place of the two and two that a
+ * separate backward pass needs.
+ *   grad_H : [N, d] bf16 or fp32, zero rows where not valid.  grad_W, grad_W_kind as for
+ *            kd_fused_logprobs_bwd.  dZ is rounded to bf16; probabilities below e^-32 of the
+ *            largest of their 256 columns are taken as that.
+ * Workspace: `step` != 0 asks for the step's (it grows with chunk * V), 0 for the forward pass's
+ * (chunk * (V / 16 + 2 d) bytes).  `ws` may be memory of any content; the error word is in `control`
+ * (see kd_logits_kl_fwd_ctl), which may be `ws` itself once kd_workspace_clear has cleared it.
+ * ------------------------------------------------------------------------ */
+
+KD_API size_t kd_fused_cross_entropy_workspace(int64_t N, int64_t d, int64_t V, int64_t chunk, int step);
+
+KD_API int kd_fused_cross_entropy_fwd(const void* H_bf16, const void* W_bf16, const int32_t* labels,
+                    const uint8_t* mask, int64_t N, int64_t d, int64_t V, int64_t chunk, float label_smoothing,
+                    float z_loss, float softcap, int ignore_index, float* loss_out, float* lse_out,
+                    float* loss_per_token_out, void* ws, size_t ws_bytes, void* control, void* stream);
+
+KD_API int kd_fused_cross_entropy_step(const void* H_bf16, const void* W_bf16, const int32_t* labels,
+                    const uint8_t* mask, int64_t N, int64_t d, int64_t V, int64_t chunk, float label_smoothing,
+                    float z_loss, float softcap, int ignore_index, const float* grad_loss, float* loss_out,
+                    float* lse_out, float* loss_per_token_out, void* grad_H, int grad_H_is_fp32, void* grad_W,
+                    int grad_W_kind, void* ws, size_t ws_bytes, void* control, void* stream);
+
+/* x[0 .. n) *= *factor (device fp32 scalar), bf16 or fp32, n a multiple of 8; nothing is read or
+ * written where the factor is 1.  What a backward pass does to a step's gradients. */
+KD_API int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* factor, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * On-disk teacher cache ([ART] paragraph on the first fix: run the teacher once,
  * keep its top-K logits per position on disk, reuse them across experiments).
  * HOST memory and host files only; no CUDA call.  One file per contiguous range

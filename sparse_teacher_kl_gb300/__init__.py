@@ -39,6 +39,9 @@ __all__ = [
     "fused_logprobs",
     "fused_logprobs_forward",
     "fused_logprobs_backward",
+    "fused_cross_entropy",
+    "fused_cross_entropy_forward",
+    "fused_cross_entropy_step",
     "gemm_bf16",
     "cache_write",
     "cache_info",
@@ -542,14 +545,14 @@ def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None):
     return _LogitsKL.apply(logits, ids, tlog, mask, float(tau), t_lse)
 
 
-def _check_projection(H, W, tokens, mask):
+def _check_projection(H, W, tokens, mask, name="tokens"):
     for t, name in ((H, "H"), (W, "W")):
         if not t.is_cuda or t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous 2-D bf16 CUDA tensor")
     N, d = H.shape
     if W.shape[1] != d or W.device != H.device:
         raise ValueError("W must be [V, d] on the device of H [N, d]")
-    _check(tokens, "tokens", torch.int32, (N,), H.device)
+    _check(tokens, name, torch.int32, (N,), H.device)
     _check(mask, "mask", torch.uint8, (N,), H.device)
     return N, d, W.shape[0], H.device
 
@@ -640,6 +643,119 @@ class _FusedLogprobs(torch.autograd.Function):
 def fused_logprobs(H, W, tokens, mask=None, chunk=4096, tau=1.0):
     """Differentiable (log probability of ``tokens`` [N], entropy [N]) of softmax(H W^T / tau)."""
     return _FusedLogprobs.apply(H, W, tokens, mask, int(chunk), float(tau))
+
+
+def _ce_step(H, W, labels, mask, chunk, options, grad_loss, ws, control, loss_out=None, grad_H=None, grad_W=None,
+             grad_H_fp32=False, grad_W_bf16=False):
+    N, d, V, dev = _check_projection(H, W, labels, mask, "labels")
+    _check(loss_out, "loss_out", torch.float32, (N,), dev)
+    _check(grad_loss, "grad_loss", torch.float32, (1,), dev)
+    if ws is None:
+        ws = _scratch(_abi.kd_fused_cross_entropy_workspace(N, d, V, chunk, 1), dev)
+    given = loss_out, grad_H, grad_W
+    if grad_H is None:
+        grad_H = torch.empty((N, d), dtype=torch.float32 if grad_H_fp32 else torch.bfloat16, device=dev)
+    kind = _abi.KD_GRAD_ADD_F32
+    if grad_W is None:
+        kind = _abi.KD_GRAD_STORE_BF16 if grad_W_bf16 else _abi.KD_GRAD_STORE_F32
+        grad_W = torch.empty((V, d), dtype=torch.bfloat16 if grad_W_bf16 else torch.float32, device=dev)
+    else:
+        _check(grad_W, "grad_W", torch.float32, (V, d), dev)
+    _check(grad_H, "grad_H", torch.float32 if grad_H.dtype == torch.float32 else torch.bfloat16, (N, d), dev)
+    loss = torch.empty((1,), dtype=torch.float32, device=dev)
+    lse = torch.empty((N,), dtype=torch.float32, device=dev)
+    st = _abi.kd_fused_cross_entropy_step(_ptr(H), _ptr(W), _ptr(labels), _ptr(mask), N, d, V, chunk, *options,
+                                          _ptr(grad_loss), _ptr(loss), _ptr(lse), _ptr(loss_out), _ptr(grad_H),
+                                          1 if grad_H.dtype == torch.float32 else 0, _ptr(grad_W), kind, _ptr(ws),
+                                          ws.numel(), _ptr(control), _stream(dev))
+    _abi.check(st, "kd_fused_cross_entropy_step")
+    _written(*given)
+    return loss, grad_H, grad_W
+
+
+def _ce_forward(H, W, labels, mask, chunk, options, ws, control, loss_out=None):
+    N, d, V, dev = _check_projection(H, W, labels, mask, "labels")
+    _check(loss_out, "loss_out", torch.float32, (N,), dev)
+    if ws is None:
+        ws = (_fresh_ws if control is None else _scratch)(_abi.kd_fused_cross_entropy_workspace(N, d, V, chunk, 0), dev)
+    if control is None:
+        control = ws
+    loss = torch.empty((1,), dtype=torch.float32, device=dev)
+    lse = torch.empty((N,), dtype=torch.float32, device=dev)
+    st = _abi.kd_fused_cross_entropy_fwd(_ptr(H), _ptr(W), _ptr(labels), _ptr(mask), N, d, V, chunk, *options,
+                                         _ptr(loss), _ptr(lse), _ptr(loss_out), _ptr(ws), ws.numel(), _ptr(control),
+                                         _stream(dev))
+    _abi.check(st, "kd_fused_cross_entropy_fwd")
+    _written(loss_out)
+    return loss, lse, ws
+
+
+def fused_cross_entropy_forward(H, W, labels, mask=None, chunk=4096, label_smoothing=0.0, z_loss=0.0, softcap=0.0,
+                                ignore_index=-100, ws=None, loss_out=None):
+    """kd_fused_cross_entropy_fwd: (loss [1], lse [N], ws).  Cross entropy of ``labels`` (int32 [N]) against
+    softmax(H W^T), the logits never stored: the mean over the positions whose label is not ``ignore_index`` and
+    whose ``mask`` is not 0; each position's own loss goes to ``loss_out`` ([N] fp32) when given."""
+    return _ce_forward(H, W, labels, mask, chunk,
+                       (float(label_smoothing), float(z_loss), float(softcap), int(ignore_index)), ws, None, loss_out)
+
+
+def fused_cross_entropy_step(H, W, labels, mask=None, chunk=4096, label_smoothing=0.0, z_loss=0.0, softcap=0.0,
+                             ignore_index=-100, grad_loss=None, ws=None, loss_out=None, grad_H=None, grad_W=None,
+                             grad_H_fp32=False, grad_W_bf16=False):
+    """kd_fused_cross_entropy_step: loss and gradients in one call, for a ``grad_loss`` ([1] fp32, default 1) known
+    beforehand: (loss [1], grad_H [N, d] bf16 or fp32, grad_W [V, d]).  A ``grad_W`` of the caller's (fp32) is added
+    into; without one it is a new tensor, fp32 or with ``grad_W_bf16`` (one chunk only) bf16.  Without a workspace
+    errors go to the stream's control_block."""
+    _check_projection(H, W, labels, mask, "labels")
+    control = _control(H.device) if ws is None else ws
+    return _ce_step(H, W, labels, mask, chunk, (float(label_smoothing), float(z_loss), float(softcap), int(ignore_index)),
+                    grad_loss, ws, control, loss_out, grad_H, grad_W, grad_H_fp32, grad_W_bf16)
+
+
+class _FusedCrossEntropy(torch.autograd.Function):
+    """The forward pass takes the gradients of a factor 1 with the loss (one projection in place of two); the
+    backward pass multiplies them by the factor that arrives, which costs nothing where that is 1."""
+
+    @staticmethod
+    def forward(ctx, H, W, labels, mask, chunk, options, wanted):
+        _check_projection(H, W, labels, mask, "labels")
+        ctx.control = _control(H.device)
+        ctx.chunk, ctx.options, ctx.grads = chunk, options, None
+        ctx.save_for_backward(H, W, labels, mask)
+        if not wanted:
+            return _ce_forward(H, W, labels, mask, chunk, options, None, ctx.control)[0][0]
+        loss, grads = _FusedCrossEntropy.step(ctx, H, W, labels, mask)
+        ctx.grads = grads
+        return loss[0]
+
+    @staticmethod
+    def step(ctx, H, W, labels, mask):
+        loss, *grads = _ce_step(H, W, labels, mask, ctx.chunk, ctx.options, None, None, ctx.control,
+                                grad_W_bf16=H.shape[0] <= ctx.chunk)
+        return loss, grads
+
+    @staticmethod
+    @_once_differentiable
+    def backward(ctx, grad_out):
+        H, W, labels, mask = ctx.saved_tensors
+        # handed out once: what becomes of them is the caller's, so a second pass takes them anew
+        grads, ctx.grads = ctx.grads, None
+        if grads is None:
+            grads = _FusedCrossEntropy.step(ctx, H, W, labels, mask)[1]
+        g = _f32c(grad_out.reshape(1))
+        for t in grads:
+            _abi.check(_abi.kd_scale_gradient(_ptr(t), t.numel(), int(t.dtype == torch.float32), _ptr(g),
+                                              _stream(H.device)), "kd_scale_gradient")
+        return grads[0], grads[1].to(W.dtype), None, None, None, None, None
+
+
+def fused_cross_entropy(H, W, labels, mask=None, chunk=4096, label_smoothing=0.0, z_loss=0.0, softcap=0.0,
+                        ignore_index=-100):
+    """Differentiable cross entropy of ``labels`` (int32 [N]) against softmax(H W^T): the mean over the positions
+    whose label is not ``ignore_index`` and whose ``mask`` is not 0 (scalar tensor)."""
+    wanted = torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)
+    return _FusedCrossEntropy.apply(H, W, labels, mask, int(chunk), (float(label_smoothing), float(z_loss),
+                                    float(softcap), int(ignore_index)), wanted)
 
 
 def gemm_bf16(A, B, M, N, K, a_mn_major=False, b_mn_major=False, C=None):

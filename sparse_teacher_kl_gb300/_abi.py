@@ -79,6 +79,14 @@ _SIGNATURES = {
     "kd_fused_logprobs_bwd": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_float,
                                        _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int, _c_ptr, _c_size,
                                        _c_ptr]),
+    "kd_fused_cross_entropy_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
+    "kd_fused_cross_entropy_fwd": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_float,
+                                            _c_float, _c_float, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size,
+                                            _c_ptr, _c_ptr]),
+    "kd_fused_cross_entropy_step": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_float,
+                                             _c_float, _c_float, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                             _c_int, _c_ptr, _c_int, _c_ptr, _c_size, _c_ptr, _c_ptr]),
+    "kd_scale_gradient": (_c_int, [_c_ptr, _c_i64, _c_int, _c_ptr, _c_ptr]),
     "kd_workspace_clear": (_c_int, [_c_ptr, _c_size, _c_ptr]),
     "kd_get_device_error": (_c_int, [_c_ptr, _c_ptr, ctypes.POINTER(_c_i64)]),
     "kd_gemm_bf16": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_ptr, _c_size,
@@ -179,6 +187,10 @@ kd_fused_logprobs_fwd = _wrap("kd_fused_logprobs_fwd")
 kd_fused_logprobs_fwd_ctl = _wrap("kd_fused_logprobs_fwd_ctl")
 kd_fused_logprobs_bwd = _wrap("kd_fused_logprobs_bwd")
 kd_fused_logprobs_bwd_ctl = _wrap("kd_fused_logprobs_bwd_ctl")
+kd_fused_cross_entropy_workspace = _wrap("kd_fused_cross_entropy_workspace")
+kd_fused_cross_entropy_fwd = _wrap("kd_fused_cross_entropy_fwd")
+kd_fused_cross_entropy_step = _wrap("kd_fused_cross_entropy_step")
+kd_scale_gradient = _wrap("kd_scale_gradient")
 kd_workspace_clear = _wrap("kd_workspace_clear")
 kd_get_device_error = _wrap("kd_get_device_error")
 kd_gemm_bf16 = _wrap("kd_gemm_bf16")

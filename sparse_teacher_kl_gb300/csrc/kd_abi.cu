@@ -165,7 +165,7 @@ static KlLayout kl_layout(int64_t N, int64_t d, int64_t V, int K, int64_t chunk)
 // tiles).  The fused loss's epilogues also need an even number of row tiles (no phantom tile
 // writing past the chunk); the score epilogues and the gradient products run one, and check
 // their rows themselves (the stores of dZ boxes are clipped at the chunk's last row).
-static void set_cluster(GemmProblem& p) {
+void set_cluster(GemmProblem& p) {
   const bool loss_epi = (p.epi == EPI_LSE || p.epi == EPI_DZ || p.epi == EPI_LSE_Z);
   p.cta_pair = (p.m_tiles >= 2 && !(loss_epi && p.m_tiles % 2 != 0)) ? 1 : 0;
   p.cluster = p.cta_pair ? 2 : 1;
@@ -178,7 +178,7 @@ static void set_cluster(GemmProblem& p) {
 // K-major boxes (a_k3d / b_k3d) for CTA pairs.
 static_assert(pair_kblocks(0, 0) == 2, "K-major operand pairs take two k-blocks per pair stage");
 
-static int choose_splits(int64_t tiles, int k_blocks, int grid) {
+int choose_splits(int64_t tiles, int k_blocks, int grid) {
   int best = 1;
   double best_cost = 1e300;
   for (int S = 1; S <= KD_MAX_SPLITS; ++S) {
@@ -193,7 +193,7 @@ static int choose_splits(int64_t tiles, int k_blocks, int grid) {
   return best;
 }
 
-static kd_status check_proj_args(const void* H, const void* W, int64_t N, int64_t d, int64_t V, int64_t chunk,
+kd_status check_proj_args(const void* H, const void* W, int64_t N, int64_t d, int64_t V, int64_t chunk,
                                  float tau) {
   if (N < 1 || d < 8 || V < 1 || chunk < BM) return KD_ERR_INVALID_ARG;
   if (d % 8 != 0 || chunk % BM != 0) return KD_ERR_INVALID_ARG;

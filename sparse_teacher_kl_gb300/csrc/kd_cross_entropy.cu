@@ -1,0 +1,602 @@
+// Softmax cross entropy from hidden states: the row-wise steps around the projection engine, and the
+// host side of kd_fused_cross_entropy_*.  With z' = z, or c tanh(z / c) for a softcap c, over the V
+// logits z = h W^T of a position with label y,
+//   lse    = logsumexp(z')
+//   loss_n = lse - (1 - e) z'_y - (e / V) sum_v z'_v + l lse^2       (e label smoothing, l z-loss)
+//   loss   = sum_n loss_n / n_valid
+//   dZ_v   = G ((1 + 2 l lse) p_v - e / V - (1 - e) [v = y]) (1 - (z'_v / c)^2),   G = grad / n_valid
+//   grad_H = dZ W,   grad_W = dZ^T H
+//
+// What a step cannot do without is 6 N d V operations (one projection, two gradient products); what it
+// must move is H, W and the two gradients.  The usual way to keep no logits is to project twice (8 N d V).
+// Here the projection's epilogue leaves each chunk's logits as 16-bit distances from the largest of
+// their 256-column tile (CE_STEPS; 2 bytes each, in the buffer that dZ needs anyway), and once a row's sum is
+// known one pass over that buffer turns them into bf16 dZ where they lie: 6 bytes moved for each logit
+// against 2 d operations, 0.9 ns against 3.3 ns per thousand at d = 2880.  The label's own entry, where
+// p_y - 1 would cancel, comes from its fp32 logit.
+//
+// Positions without a loss (mask 0, or the ignored label) cost nothing: the others are gathered to the
+// front, in order, and the products stop after the last of them (GemmProblem::rows_dev).  Their hidden states
+// are never read, so they may hold anything.
+#include <math.h>
+
+#include "kd_device.cuh"
+#include "kd_internal.h"
+
+namespace kd {
+
+namespace {
+
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2f = 0.69314718055994531f;
+
+__device__ __forceinline__ bool has_loss(const int32_t* labels, const uint8_t* mask, int64_t i, int ignore) {
+  return labels[i] != ignore && (mask == nullptr || mask[i] != 0);
+}
+
+// ------------------------------------------------------------------ positions ---
+// list[0 .. n_valid): the positions that have a loss, ascending.  The others' outputs are set to 0.  One block,
+// eight positions a thread and sweep, so that each sweep's loads are in flight together.
+constexpr int LIST_THREADS = 1024, LIST_EACH = 8;
+
+__global__ void __launch_bounds__(LIST_THREADS)
+    kd_ce_list_kernel(const int32_t* __restrict__ labels, const uint8_t* __restrict__ mask, int64_t N, int ignore,
+                      int32_t* __restrict__ list, int32_t* __restrict__ n_valid, float* __restrict__ lse,
+                      float* __restrict__ losses) {
+  __shared__ int warp_sum[LIST_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0;
+  for (int64_t i0 = 0; i0 < N; i0 += int64_t(LIST_THREADS) * LIST_EACH) {
+    const int64_t first = i0 + int64_t(threadIdx.x) * LIST_EACH;
+    uint32_t on = 0;
+#pragma unroll
+    for (int j = 0; j < LIST_EACH; ++j)
+      if (first + j < N && has_loss(labels, mask, first + j, ignore)) on |= 1u << j;
+    const int mine = __popc(on);
+    int sum = mine;  // inclusive over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll 8
+    for (int w = 0; w < LIST_THREADS / 32; ++w) {
+      const int v = warp_sum[w];
+      before += w < warp ? v : 0;
+      total += v;
+    }
+    int at = base + before + sum - mine;
+#pragma unroll
+    for (int j = 0; j < LIST_EACH; ++j) {
+      if (first + j >= N) break;
+      if (on >> j & 1u) {
+        list[at++] = int32_t(first + j);
+      } else {
+        lse[first + j] = 0.f;
+        losses[first + j] = 0.f;
+      }
+    }
+    base += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *n_valid = base;
+}
+
+__device__ __forceinline__ int chunk_rows(const int32_t* n_valid, int64_t c0, int cap) {
+  const int64_t n = int64_t(*n_valid) - c0;
+  return int(n < 0 ? 0 : n > cap ? cap : n);
+}
+
+// Rows that the products read: whole 64-row blocks, one at least.
+__device__ __forceinline__ int read_rows(int n) { return n < 1 ? 64 : (n + 63) / 64 * 64; }
+
+// A chunk's hidden states and labels to the front; zero rows after the last, as far as the products read.  With
+// zero_H (first chunk of a step): the gradients of positions without a loss.  A warp copies a row.
+constexpr int GATHER_WARPS = 8;
+
+__global__ void __launch_bounds__(GATHER_WARPS * 32)
+    kd_ce_gather_kernel(const uint16_t* __restrict__ H, const int32_t* __restrict__ labels,
+                        const uint8_t* __restrict__ mask, int64_t N, int64_t d, int ignore,
+                        const int32_t* __restrict__ list, const int32_t* __restrict__ n_valid, int64_t c0, int cap,
+                        int rows_pad, uint16_t* __restrict__ Hc, int32_t* __restrict__ labels_c,
+                        void* __restrict__ zero_H, int64_t zero_vecs) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w0 = int64_t(blockIdx.x) * GATHER_WARPS + (threadIdx.x >> 5), step = int64_t(gridDim.x) * GATHER_WARPS;
+  const int n = chunk_rows(n_valid, c0, cap);
+  const int end = min(read_rows(n), rows_pad);
+  const int64_t vecs = d / 8;
+  for (int64_t r = w0; r < end; r += step) {
+    uint4* dst = reinterpret_cast<uint4*>(Hc + r * d);
+    if (r < n) {
+      const int64_t i = list[c0 + r];
+      const uint4* src = reinterpret_cast<const uint4*>(H + i * d);
+      if (lane == 0) labels_c[r] = labels[i];
+#pragma unroll 4
+      for (int64_t v = lane; v < vecs; v += 32) dst[v] = __ldg(src + v);
+    } else {
+      for (int64_t v = lane; v < vecs; v += 32) dst[v] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  if (zero_H == nullptr) return;
+  for (int64_t i = w0; i < N; i += step) {
+    if (has_loss(labels, mask, i, ignore)) continue;
+    uint4* dst = reinterpret_cast<uint4*>(zero_H) + i * zero_vecs;
+    for (int64_t v = lane; v < zero_vecs; v += 32) dst[v] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// ------------------------------------------------------------------ row sums ---
+// A row's tiles put together: its loss and logsumexp to the position's place and, for a step, what dZ
+// takes of it: (lse, a, b, dz_y) with dZ_v = (a p_v - b) slope_v.  32 threads share a row's tiles (as
+// the other combines: a thread's tiles are a chain of dependent exponentials).
+constexpr int CC_ROWS = 32, CC_PHASES = 32;
+
+struct CeCombine {
+  const float4* partials;
+  int tiles, rows_pad, cap;
+  int64_t c0, V;
+  const int32_t *list, *n_valid, *labels_c;
+  float smooth, z_loss, softcap;
+  const float* grad_loss;
+  float *lse, *losses;
+  float4* row_stats;
+  uint32_t* err;
+};
+
+__global__ void __launch_bounds__(CC_ROWS * CC_PHASES) kd_ce_combine_kernel(const CeCombine a) {
+  __shared__ float4 sm[CC_PHASES][CC_ROWS];
+  const int x = threadIdx.x, y = threadIdx.y;
+  const int r = blockIdx.x * CC_ROWS + x;
+  const int n = chunk_rows(a.n_valid, a.c0, a.cap);
+  if (int(blockIdx.x) * CC_ROWS >= n) return;
+  float M = -INFINITY, S = 0.f, Y = 0.f, Z = 0.f;
+  if (r < n) {
+#pragma unroll 4
+    for (int u = y; u < a.tiles; u += CC_PHASES) {
+      const float4 q = a.partials[size_t(u) * a.rows_pad + r];
+      Y += q.z;
+      Z += q.w;
+      if (q.x > M) {
+        S = fmaf(S, exp2f((M - q.x) * kLog2E), q.y);
+        M = q.x;
+      } else if (q.x != -INFINITY) {
+        S = fmaf(q.y, exp2f((q.x - M) * kLog2E), S);
+      } else {
+        S += q.y;  // 0, or NaN of a tile that holds one
+      }
+    }
+  }
+  sm[y][x] = make_float4(M, S, Y, Z);
+  __syncthreads();
+  if (y != 0 || r >= n) return;
+  for (int k = 1; k < CC_PHASES; ++k) M = fmaxf(M, sm[k][x].x);
+  S = Y = Z = 0.f;
+  for (int k = 0; k < CC_PHASES; ++k) {
+    const float4 q = sm[k][x];
+    S += q.x == -INFINITY ? q.y : q.y * exp2f((q.x - M) * kLog2E);
+    Y += q.z;
+    Z += q.w;
+  }
+  const int64_t pos = a.list[a.c0 + r];
+  const int32_t label = a.labels_c[r];
+  const bool bad = label < 0 || int64_t(label) >= a.V;
+  if (bad) raise_error(a.err, KD_DEVERR_BAD_ID, uint32_t(pos));
+  const float ln_s = logf(S), lse = M + ln_s;
+  // as a difference of logits: lse and z_y would each be rounded at their own size
+  const float nll = ln_s - (Y - M);
+  const float mean_off = a.smooth > 0.f ? Y - Z / float(a.V) : 0.f;
+  a.lse[pos] = lse;
+  a.losses[pos] = bad ? __int_as_float(0x7FC00000) : nll + a.smooth * mean_off + a.z_loss * lse * lse;
+  if (a.row_stats == nullptr) return;
+  float4 st = make_float4(lse, 0.f, 0.f, 0.f);
+  if (!bad) {
+    const float G = (a.grad_loss ? *a.grad_loss : 1.f) / float(*a.n_valid);
+    st.y = G * fmaf(2.f * a.z_loss, lse, 1.f);
+    st.z = G * (a.smooth / float(a.V));
+    const float t = a.softcap > 0.f ? Y / a.softcap : 0.f;
+    st.w = (st.y * exp2f(-nll * kLog2E) - st.z - G * (1.f - a.smooth)) * fmaf(-t, t, 1.f);
+  }
+  a.row_stats[r] = st;
+}
+
+// ------------------------------------------------------------------ dZ ---
+// The chunk's 16-bit distances to bf16 dZ, in place ([V / 64][row][64], both).  A block takes 64 rows of
+// one 256-column tile: 8 lanes to a 128-byte row of a 64-column block, 8 vectors of 16 bytes in flight a thread.
+// Bound by HBM: 4 bytes a logit.
+constexpr int DQ_ROWS = 64;
+
+__device__ __forceinline__ float dz_of(uint32_t q, float shift, float m, const float4& st, float cap2) {
+  const float far = float(q);
+  const float p = ex2_approx(fmaf(far, -kLog2E / CE_STEPS, shift));
+  const float z = fmaf(far, -1.f / CE_STEPS, m);
+  return fmaf(st.y, p, -st.z) * fmaf(-z * z, cap2, 1.f);
+}
+
+__global__ void __launch_bounds__(256)
+    kd_ce_dz_kernel(uint4* __restrict__ dz, int rows_pad, int64_t nvb, const float4* __restrict__ partials, int ld_part,
+                    const float4* __restrict__ row_stats, const int32_t* __restrict__ labels_c,
+                    const int32_t* __restrict__ n_valid, int64_t c0, int cap, float softcap) {
+  const int n = chunk_rows(n_valid, c0, cap);
+  const int end = min(read_rows(n), rows_pad);
+  const uint32_t row_blocks = uint32_t(cap + DQ_ROWS - 1) / DQ_ROWS;
+  const int tile = int(blockIdx.x / row_blocks), lane8 = threadIdx.x & 7;
+  const int first = int(blockIdx.x - uint32_t(tile) * row_blocks) * DQ_ROWS, r0 = first + (threadIdx.x >> 3);
+  const float cap2 = softcap > 0.f ? 1.f / (softcap * softcap) : 0.f;
+  if (first >= end) return;
+#pragma unroll
+  for (int h = 0; h < DQ_ROWS / 32; ++h) {
+    const int r = r0 + h * 32;
+    if (r >= end) continue;
+    uint4 v[4];
+    const int vb0 = tile * 4;
+    if (r >= n) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (vb0 + b < nvb) dz[(size_t(vb0 + b) * rows_pad + r) * 8 + lane8] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (vb0 + b < nvb) v[b] = dz[(size_t(vb0 + b) * rows_pad + r) * 8 + lane8];
+    const float4 st = row_stats[r];
+    const float m = partials[size_t(tile) * ld_part + r].x;
+    const int label = labels_c[r];
+    // a tile of nothing but -inf has no probability, whatever its distances (then m - lse is -inf)
+    const float shift = (m - st.x) * kLog2E;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (vb0 + b >= nvb) break;
+      const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+      const int off = label - (vb0 + b) * 64 - lane8 * 8;
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo = dz_of(w[i] & 0xFFFFu, shift, m, st, cap2), hi = dz_of(w[i] >> 16, shift, m, st, cap2);
+        lo = off == 2 * i ? st.w : lo;
+        hi = off == 2 * i + 1 ? st.w : hi;
+        o[i] = pack_bf16x2(lo, hi);
+      }
+      dz[(size_t(vb0 + b) * rows_pad + r) * 8 + lane8] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ split sums ---
+// grad_H of a chunk from its fp32 partials, summed in split order, each row to its position.
+__global__ void __launch_bounds__(256)
+    kd_ce_split_kernel(const float4* __restrict__ parts, int splits, int64_t stride4, int64_t d4,
+                       const int32_t* __restrict__ list, const int32_t* __restrict__ n_valid, int64_t c0, int cap,
+                       void* __restrict__ out, int out_bf16) {
+  const int64_t n = chunk_rows(n_valid, c0, cap);
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n * d4; i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t r = i / d4, o = int64_t(list[c0 + r]) * d4 + (i - r * d4);
+    float4 a = parts[i];
+    for (int sp = 1; sp < splits; ++sp) {
+      const float4 b = parts[sp * stride4 + i];
+      a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+    }
+    if (out_bf16) reinterpret_cast<uint2*>(out)[o] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    else reinterpret_cast<float4*>(out)[o] = a;
+  }
+}
+
+// ------------------------------------------------------------------ scaling ---
+// x *= *g, nothing at all where g is 1 (the gradients of a loss that nothing follows).
+template <class T>
+__global__ void __launch_bounds__(256) kd_ce_scale_kernel(T* __restrict__ x, int64_t n, const float* __restrict__ g) {
+  const float f = *g;
+  if (f == 1.f) return;
+  constexpr int E = 16 / sizeof(T);
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n / E; i += int64_t(gridDim.x) * blockDim.x) {
+    uint4 v = reinterpret_cast<uint4*>(x)[i];
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(w[j]) * f)
+                            : pack_bf16x2(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xFFFF0000u) * f);
+    reinterpret_cast<uint4*>(x)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ------------------------------------------------------------------ host side ---
+
+struct CeLayout {
+  size_t list, losses, labels, stats, partials, hidden, dz, gh_part, total;
+  int64_t rows_pad, nvb;
+  int tiles;
+};
+
+CeLayout ce_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool step) {
+  CeLayout L{};
+  const int64_t c = chunk < N ? chunk : N;
+  L.rows_pad = (c + BM - 1) / BM * BM;
+  L.tiles = int((V + BN - 1) / BN);
+  L.nvb = (V + 63) / 64;
+  size_t off = sizeof(Ctrl);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  L.list = take(size_t(N) * 4);
+  L.losses = take(size_t(N) * 4);
+  L.labels = take(size_t(L.rows_pad) * 4);
+  L.stats = take(size_t(L.rows_pad) * 16);
+  L.partials = take(size_t(L.tiles) * L.rows_pad * 16);
+  L.hidden = take(size_t(L.rows_pad) * size_t(d) * 2);
+  if (step) {
+    L.dz = take(size_t(L.nvb) * L.rows_pad * 128);
+    L.gh_part = take(size_t(KD_MAX_SPLITS) * L.rows_pad * size_t(d) * 4);
+  }
+  L.total = off;
+  return L;
+}
+
+struct CeCall {
+  const void *H, *W;
+  const int32_t* labels;
+  const uint8_t* mask;
+  int64_t N, d, V, chunk;
+  float smooth, z_loss, softcap;
+  int ignore;
+  const float* grad_loss;
+  float *loss, *lse, *losses;
+  void* grad_H;
+  int grad_H_f32;
+  void* grad_W;
+  int w_kind;
+  void* ws;
+  size_t ws_bytes;
+  void *control, *stream;
+};
+
+#define KD_TRY(call)                      \
+  do {                                    \
+    if ((call) != cudaSuccess) return KD_ERR_CUDA; \
+  } while (0)
+
+// The two gradient products of a chunk, from dZ and the gathered hidden states.
+int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int n, cudaStream_t s) {
+  Ctrl* ctrl = static_cast<Ctrl*>(a.ws);
+  uint32_t* err = &static_cast<Ctrl*>(a.control)->err;
+  const int32_t* list = reinterpret_cast<const int32_t*>(w8 + L.list);
+  const uint16_t* Hc = reinterpret_cast<const uint16_t*>(w8 + L.hidden);
+  const void* dz = w8 + L.dz;
+  const uint64_t d = uint64_t(a.d), V = uint64_t(a.V), row_bytes = d * 2;
+  const int grid = gemm_max_grid();
+  const bool d64 = a.d % 64 == 0;
+  alignas(64) CUtensorMap ta, tb, tc;
+
+  // grad_H = dZ W  (dZ K-major over the vocabulary, W with d contiguous)
+  GemmProblem q{};
+  q.M = n; q.N = int(a.d); q.K = int(a.V);
+  q.b_mn = 1; q.epi = EPI_STORE; q.a_blocked = 1;
+  q.m_tiles = (n + BM - 1) / BM;
+  q.n_tiles = int((a.d + BN - 1) / BN);
+  q.n_group = 1;
+  q.k_splits = choose_splits(int64_t(q.m_tiles) * q.n_tiles, int((a.V + BK - 1) / BK), grid);
+  set_cluster(q);
+  q.n_units = ((q.m_tiles + q.cluster - 1) / q.cluster) * q.n_tiles * q.k_splits;
+  q.rows = n; q.rows_dev = &ctrl->n_valid; q.row_first = int(c0);
+  q.err = err;
+  q.ldc = a.d;
+  if (q.k_splits == 1) {
+    q.C = a.grad_H;
+    q.c_bf16 = a.grad_H_f32 ? 0 : 1;
+    q.row_map = list + c0;
+  } else {
+    q.C = w8 + L.gh_part;  // fp32 partial per split, summed in split order below
+    q.split_stride = L.rows_pad * a.d;
+  }
+  q.b_box2 = q.cta_pair && d64;
+  const int kq = q.cta_pair ? pair_kblocks(0, 1) : 1;
+  if (!make_tmap_dz_blocked(&ta, dz, uint64_t(n), uint64_t(L.rows_pad), uint64_t(L.nvb), BM, uint32_t(kq)) ||
+      !(q.b_box2 ? make_tmap_mn2_bf16(&tb, a.W, d, V, row_bytes, uint32_t(BK * kq))
+                 : make_tmap_2d_bf16(&tb, a.W, d, V, row_bytes, 64, uint32_t(BK * kq))))
+    return KD_ERR_CUDA;
+  KD_TRY(launch_gemm(q, ta, tb, tb, grid, s));
+  if (q.k_splits > 1) {
+    const int64_t work = (int64_t(n) * (a.d / 4) + 255) / 256;
+    prof_before("kd_ce_split", s);
+    kd_ce_split_kernel<<<unsigned(work < 4 * grid ? work : 4 * grid), 256, 0, s>>>(
+        reinterpret_cast<const float4*>(w8 + L.gh_part), q.k_splits, L.rows_pad * a.d / 4, a.d / 4, list,
+        &ctrl->n_valid, c0, n, a.grad_H, a.grad_H_f32 ? 0 : 1);
+    prof_after(s);
+    KD_TRY(cudaGetLastError());
+  }
+
+  // grad_W (+)= dZ^T H  (dZ with the vocabulary contiguous, H with d contiguous)
+  GemmProblem r{};
+  r.M = int(a.V); r.N = int(a.d); r.K = n;
+  r.a_mn = r.b_mn = 1; r.a_blocked = 1;
+  r.epi = (a.w_kind != KD_GRAD_ADD_F32 && c0 == 0) ? EPI_STORE : EPI_ACCUM;
+  r.m_tiles = int((a.V + BM - 1) / BM);
+  r.n_tiles = int((a.d + BN - 1) / BN);
+  r.n_group = 1;
+  r.k_splits = 1;
+  set_cluster(r);
+  r.n_units = ((r.m_tiles + r.cluster - 1) / r.cluster) * r.n_tiles;
+  r.rows = n; r.rows_dev = &ctrl->n_valid; r.row_first = int(c0);
+  r.C = a.grad_W; r.ldc = a.d; r.err = err;
+  r.c_bf16 = r.c_tma = a.w_kind == KD_GRAD_STORE_BF16;
+  r.b_box2 = r.cta_pair && d64;
+  const int kr = r.cta_pair ? pair_kblocks(1, 1) : 1;
+  if (!(r.cta_pair ? make_tmap_dz_blocked(&ta, dz, uint64_t(n), uint64_t(L.rows_pad), uint64_t(L.nvb),
+                                          uint32_t(BK * kr), 2)
+                   : make_tmap_dz_blocked(&ta, dz, uint64_t(n), uint64_t(L.rows_pad), uint64_t(L.nvb), BK)) ||
+      !(r.b_box2 ? make_tmap_mn2_bf16(&tb, Hc, d, uint64_t(n), row_bytes, uint32_t(BK * kr))
+                 : make_tmap_2d_bf16(&tb, Hc, d, uint64_t(n), row_bytes, 64, uint32_t(BK * kr))) ||
+      !(r.c_bf16 ? make_tmap_2d_bf16(&tc, a.grad_W, d, V, row_bytes, 64, 32)
+                 : make_tmap_2d_f32(&tc, a.grad_W, d, V, d * 4, 32, 32)))
+    return KD_ERR_CUDA;
+  KD_TRY(launch_gemm(r, ta, tb, tc, grid, s));
+  return KD_OK;
+}
+
+bool ok4(const void* p) { return p != nullptr && aligned(p, 4); }
+
+int ce_run(const CeCall& a, bool step) {
+  kd_status st = check_proj_args(a.H, a.W, a.N, a.d, a.V, a.chunk, 1.f);
+  if (st != KD_OK) return st;
+  if (!(a.smooth >= 0.f && a.smooth < 1.f) || !(a.z_loss >= 0.f && isfinite(a.z_loss)) ||
+      !(a.softcap >= 0.f && isfinite(a.softcap)))
+    return KD_ERR_INVALID_ARG;
+  if (!ok4(a.labels) || !ok4(a.loss) || !ok4(a.lse) || !aligned(a.losses, 4)) return KD_ERR_INVALID_ARG;
+  if (step) {
+    if (!aligned(a.grad_loss, 4) || !a.grad_H || !aligned(a.grad_H, 16) || !a.grad_W || !aligned(a.grad_W, 16))
+      return KD_ERR_INVALID_ARG;
+    if (a.w_kind < KD_GRAD_ADD_F32 || a.w_kind > KD_GRAD_STORE_BF16) return KD_ERR_INVALID_ARG;
+    if (a.w_kind == KD_GRAD_STORE_BF16 && a.N > a.chunk) return KD_ERR_INVALID_ARG;
+  }
+  const CeLayout L = ce_layout(a.N, a.d, a.V, a.chunk, step);
+  if (!a.ws || !aligned(a.ws, 256) || a.ws_bytes < L.total || !a.control || !aligned(a.control, 256))
+    return KD_ERR_WORKSPACE;
+  if ((st = check_device()) != KD_OK) return st;
+
+  cudaStream_t s = static_cast<cudaStream_t>(a.stream);
+  uint8_t* w8 = static_cast<uint8_t*>(a.ws);
+  Ctrl* ctrl = static_cast<Ctrl*>(a.ws);
+  uint32_t* err = &static_cast<Ctrl*>(a.control)->err;
+  int32_t* list = reinterpret_cast<int32_t*>(w8 + L.list);
+  float* losses = a.losses ? a.losses : reinterpret_cast<float*>(w8 + L.losses);
+  int32_t* labels_c = reinterpret_cast<int32_t*>(w8 + L.labels);
+  float4* row_stats = reinterpret_cast<float4*>(w8 + L.stats);
+  float4* partials = reinterpret_cast<float4*>(w8 + L.partials);
+  uint16_t* Hc = reinterpret_cast<uint16_t*>(w8 + L.hidden);
+  const uint64_t d = uint64_t(a.d), V = uint64_t(a.V), row_bytes = d * 2;
+  const bool d64 = a.d % 64 == 0;  // two k-blocks per box for CTA pairs
+  const int grid = gemm_max_grid();
+
+  prof_before("kd_ce_list", s);
+  kd_ce_list_kernel<<<1, LIST_THREADS, 0, s>>>(a.labels, a.mask, a.N, a.ignore, list, &ctrl->n_valid, a.lse, losses);
+  prof_after(s);
+  KD_TRY(cudaGetLastError());
+
+  for (int64_t c0 = 0; c0 < a.N; c0 += a.chunk) {
+    const int n = int((a.N - c0) < a.chunk ? (a.N - c0) : a.chunk);  // at most
+    const bool zero = step && c0 == 0;
+    const int64_t warps = (zero && a.N > L.rows_pad ? a.N : L.rows_pad);
+    const int64_t blocks = (warps + GATHER_WARPS - 1) / GATHER_WARPS;
+    prof_before("kd_ce_gather", s);
+    kd_ce_gather_kernel<<<unsigned(blocks < 8 * grid ? blocks : 8 * grid), GATHER_WARPS * 32, 0, s>>>(
+        static_cast<const uint16_t*>(a.H), a.labels, a.mask, a.N, a.d, a.ignore, list, &ctrl->n_valid, c0, n,
+        int(L.rows_pad), Hc, labels_c, zero ? a.grad_H : nullptr, a.d * (a.grad_H_f32 ? 4 : 2) / 16);
+    prof_after(s);
+    KD_TRY(cudaGetLastError());
+
+    alignas(64) CUtensorMap th, tw, tq;
+    GemmProblem p{};
+    p.M = n; p.N = int(a.V); p.K = int(a.d);
+    p.epi = EPI_CE;
+    p.m_tiles = (n + BM - 1) / BM;
+    p.n_tiles = L.tiles;
+    p.n_group = 1;
+    p.k_splits = 1;
+    set_cluster(p);
+    p.n_units = ((p.m_tiles + p.cluster - 1) / p.cluster) * p.n_tiles;
+    p.partials = partials;
+    p.rows = n; p.rows_dev = &ctrl->n_valid; p.row_first = int(c0);
+    p.tokens = labels_c;
+    p.ce_cap = a.softcap;
+    p.ce_sum = a.smooth > 0.f;
+    p.ce_q = step;
+    p.err = err;
+    p.a_k3d = p.b_k3d = p.cta_pair && d64;
+    if (!(p.a_k3d ? make_tmap_mn2_bf16(&th, Hc, d, uint64_t(n), row_bytes, BM)
+                  : make_tmap_2d_bf16(&th, Hc, d, uint64_t(n), row_bytes, BK, BM)) ||
+        !(p.b_k3d ? make_tmap_mn2_bf16(&tw, a.W, d, V, row_bytes, BN / 2)
+                  : make_tmap_2d_bf16(&tw, a.W, d, V, row_bytes, BK, p.cta_pair ? BN / 2 : BN)))
+      return KD_ERR_CUDA;
+    if (step && !make_tmap_dz_blocked(&tq, w8 + L.dz, uint64_t(n), uint64_t(L.rows_pad), uint64_t(L.nvb), 32))
+      return KD_ERR_CUDA;
+    KD_TRY(launch_gemm(p, th, tw, step ? tq : tw, grid, s));
+
+    CeCombine c{};
+    c.partials = partials;
+    c.tiles = L.tiles; c.rows_pad = int((n + BM - 1) / BM * BM); c.cap = n;
+    c.c0 = c0; c.V = a.V;
+    c.list = list; c.n_valid = &ctrl->n_valid; c.labels_c = labels_c;
+    c.smooth = a.smooth; c.z_loss = a.z_loss; c.softcap = a.softcap;
+    c.grad_loss = a.grad_loss;
+    c.lse = a.lse; c.losses = losses;
+    c.row_stats = step ? row_stats : nullptr;
+    c.err = err;
+    prof_before("kd_ce_combine", s);
+    kd_ce_combine_kernel<<<unsigned((n + CC_ROWS - 1) / CC_ROWS), dim3(CC_ROWS, CC_PHASES), 0, s>>>(c);
+    prof_after(s);
+    KD_TRY(cudaGetLastError());
+    if (!step) continue;
+
+    prof_before("kd_ce_dz", s);
+    kd_ce_dz_kernel<<<unsigned((n + DQ_ROWS - 1) / DQ_ROWS) * unsigned(L.tiles), 256, 0, s>>>(
+        reinterpret_cast<uint4*>(w8 + L.dz), int(L.rows_pad), L.nvb, partials, c.rows_pad, row_stats, labels_c,
+        &ctrl->n_valid, c0, n, a.softcap);
+    prof_after(s);
+    KD_TRY(cudaGetLastError());
+    if ((st = kd_status(ce_products(a, L, w8, c0, n, s))) != KD_OK) return st;
+  }
+  return map_cuda(launch_loss_reduce(losses, nullptr, a.N, &ctrl->n_valid, a.loss, s));
+}
+
+}  // namespace
+
+}  // namespace kd
+
+using namespace kd;
+
+extern "C" {
+
+size_t kd_fused_cross_entropy_workspace(int64_t N, int64_t d, int64_t V, int64_t chunk, int step) {
+  if (N < 1 || d < 1 || V < 1 || chunk < 1) return 0;
+  return ce_layout(N, d, V, chunk, step != 0).total;
+}
+
+int kd_fused_cross_entropy_fwd(const void* H_bf16, const void* W_bf16, const int32_t* labels, const uint8_t* mask,
+                               int64_t N, int64_t d, int64_t V, int64_t chunk, float label_smoothing, float z_loss,
+                               float softcap, int ignore_index, float* loss_out, float* lse_out,
+                               float* loss_per_token_out, void* ws, size_t ws_bytes, void* control, void* stream) {
+  CeCall a{};
+  a.H = H_bf16; a.W = W_bf16; a.labels = labels; a.mask = mask;
+  a.N = N; a.d = d; a.V = V; a.chunk = chunk;
+  a.smooth = label_smoothing; a.z_loss = z_loss; a.softcap = softcap; a.ignore = ignore_index;
+  a.loss = loss_out; a.lse = lse_out; a.losses = loss_per_token_out;
+  a.ws = ws; a.ws_bytes = ws_bytes; a.control = control; a.stream = stream;
+  return ce_run(a, false);
+}
+
+int kd_fused_cross_entropy_step(const void* H_bf16, const void* W_bf16, const int32_t* labels, const uint8_t* mask,
+                                int64_t N, int64_t d, int64_t V, int64_t chunk, float label_smoothing, float z_loss,
+                                float softcap, int ignore_index, const float* grad_loss, float* loss_out,
+                                float* lse_out, float* loss_per_token_out, void* grad_H, int grad_H_is_fp32,
+                                void* grad_W, int grad_W_kind, void* ws, size_t ws_bytes, void* control,
+                                void* stream) {
+  CeCall a{};
+  a.H = H_bf16; a.W = W_bf16; a.labels = labels; a.mask = mask;
+  a.N = N; a.d = d; a.V = V; a.chunk = chunk;
+  a.smooth = label_smoothing; a.z_loss = z_loss; a.softcap = softcap; a.ignore = ignore_index;
+  a.grad_loss = grad_loss;
+  a.loss = loss_out; a.lse = lse_out; a.losses = loss_per_token_out;
+  a.grad_H = grad_H; a.grad_H_f32 = grad_H_is_fp32; a.grad_W = grad_W; a.w_kind = grad_W_kind;
+  a.ws = ws; a.ws_bytes = ws_bytes; a.control = control; a.stream = stream;
+  return ce_run(a, true);
+}
+
+int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* factor, void* stream) {
+  if (n < 8 || n % 8 != 0 || !x || !aligned(x, 16) || !ok4(factor)) return KD_ERR_INVALID_ARG;
+  kd_status st = check_device();
+  if (st != KD_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t blocks = (n / (is_fp32 ? 4 : 8) + 255) / 256, most = 8 * gemm_max_grid();
+  prof_before("kd_ce_scale", s);
+  if (is_fp32)
+    kd_ce_scale_kernel<<<unsigned(blocks < most ? blocks : most), 256, 0, s>>>(static_cast<float*>(x), n, factor);
+  else
+    kd_ce_scale_kernel<<<unsigned(blocks < most ? blocks : most), 256, 0, s>>>(static_cast<uint16_t*>(x), n, factor);
+  prof_after(s);
+  return map_cuda(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -27,6 +27,10 @@
 //             gradient products in one 16-bit type, and H and W are bf16.  Measured on 8192 x
 //             2048 x 32000: gradients within 2.3e-3 (2-norm) of float64, 1.7e-3 of which is the
 //             rounding of bf16 outputs; a second bf16 term of dZ would run the products twice.
+//   EPI_CE    cross entropy: per row and tile the largest (capped) logit, the sum of exponentials
+//             against it, the label's logit and the sum of logits; for a training step also every
+//             logit as a 16-bit distance from the tile's largest, which kd_cross_entropy.cu turns
+//             into dZ where it lies once the rows' sums are known (no second projection).
 //   EPI_STORE / EPI_ACCUM  plain C = acc / C += acc for the gradient products.
 #include <math.h>
 #include <stdio.h>
@@ -75,15 +79,40 @@ struct Geo {
   static_assert(kSmem <= 232448, "shared memory budget of one CTA");
 };
 
+// What of the problem exists: all of it, or as much as rows_dev says.
+struct Extent {
+  int M, K, rows, m_tiles, n_units;
+};
+
+__device__ __forceinline__ Extent problem_extent(const GemmProblem& p) {
+  Extent e{p.M, p.K, p.rows, p.m_tiles, p.n_units};
+  if (p.rows_dev != nullptr) {
+    const int n = min(max(__ldg(p.rows_dev) - p.row_first, 0), p.rows);
+    if (p.a_mn) {
+      e.K = n;
+      if (n == 0) {
+        if (p.epi == EPI_STORE) e.K = 1; else e.n_units = 0;
+      }
+    } else {
+      e.M = e.rows = n;
+      e.m_tiles = (n + BM - 1) / BM;
+      e.n_units = (e.m_tiles + p.cluster - 1) / p.cluster * p.n_tiles * p.k_splits;
+    }
+  }
+  return e;
+}
+
 // Unit u -> tile coordinates.  LSE/DZ walk the vocabulary (n) slowly so that
 // every CTA in flight reads the same few W tiles while the small H chunk stays
 // in L2; the gradient products walk n fastest so that CTAs in flight share A.
 // K ranges are in steps of kkb 64-deep k-blocks (one ring stage each).
-__device__ __forceinline__ void unit_coords(const GemmProblem& p, int u, uint32_t crank, int kkb, int& m_blk,
-                                            int& n_first, int& n_count, int& kb_lo, int& kb_hi, int& split) {
-  const int k_blocks = ((p.K + BK - 1) / BK + kkb - 1) / kkb;
-  const int m_groups = (p.m_tiles + p.cluster - 1) / p.cluster;
-  if (p.epi == EPI_LSE || p.epi == EPI_DZ || p.epi == EPI_LSE_Z || p.epi == EPI_LSE_H || p.epi == EPI_DZ_LP) {
+__device__ __forceinline__ void unit_coords(const GemmProblem& p, const Extent& e, int u, uint32_t crank, int kkb,
+                                            int& m_blk, int& n_first, int& n_count, int& kb_lo, int& kb_hi,
+                                            int& split) {
+  const int k_blocks = ((e.K + BK - 1) / BK + kkb - 1) / kkb;
+  const int m_groups = (e.m_tiles + p.cluster - 1) / p.cluster;
+  if (p.epi == EPI_LSE || p.epi == EPI_DZ || p.epi == EPI_LSE_Z || p.epi == EPI_LSE_H || p.epi == EPI_DZ_LP ||
+      p.epi == EPI_CE) {
     const int g = u / m_groups;
     m_blk = (u - g * m_groups) * p.cluster + int(crank);
     n_first = g * p.n_group;
@@ -116,6 +145,102 @@ __device__ __forceinline__ void unit_coords(const GemmProblem& p, int u, uint32_
   }
 }
 
+// One tile of EPI_CE for the row of this thread: two sweeps over the accumulator, the first for the
+// largest logit, so that the sum needs no rescaling and the distances their final reference.
+__device__ __forceinline__ void ce_tile(const GemmProblem& p, const CUtensorMap& tmap_c, uint32_t t_acc, int nb,
+                                        int m_blk, int row, int rows, int nid, uint8_t* staging, uint32_t& sbuf,
+                                        uint32_t lane, uint32_t quarter) {
+  constexpr float kL2E = 1.4426950408889634f;
+  const bool last = (nb + 1) * BN > p.N;  // columns past the vocabulary: weight 0
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t raw[32];
+    tmem_ld_32x32b_x32(t_acc + c * 32, raw);
+    tmem_ld_wait();
+    if (last) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (nb * BN + c * 32 + i < p.N) m = fmaxf(m, __uint_as_float(raw[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(raw[i]));
+    }
+  }
+  const float cap = p.ce_cap, cap_k = cap > 0.f ? 2.f * kL2E / cap : 0.f;
+  if (cap > 0.f) m = ce_capped(m, cap, cap_k);
+  const float ref = m == -INFINITY ? 0.f : m;  // nothing but -inf: distances stay infinite, not NaN
+  float s0 = 0.f, s1 = 0.f, zs = 0.f, zy = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    const int col0 = nb * BN + c * 32;
+    uint32_t raw[32];
+    tmem_ld_32x32b_x32(t_acc + c * 32, raw);
+    tmem_ld_wait();
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
+    if (cap > 0.f) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = ce_capped(x[i], cap, cap_k);
+    }
+    if (p.ce_sum) {
+      float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        z0 += !last || col0 + i < p.N ? x[i] : 0.f;
+        z1 += !last || col0 + i + 1 < p.N ? x[i + 1] : 0.f;
+      }
+      zs += z0 + z1;
+    }
+    if (uint32_t(nid - col0) < 32u) zy = select32(x, uint32_t(nid - col0));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = ref - x[i];
+    if (last) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col0 + i >= p.N) x[i] = INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      s0 += ex2_approx(x[i] * -kL2E);
+      s1 += ex2_approx(x[i + 1] * -kL2E);
+    }
+    if (p.ce_q) {
+      uint8_t* box = staging + sbuf * 4096u;
+      if ((c & 1) == 0) {
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+      }
+      // 2^23 added: the distance in whole steps, rounded, in the low bits of the sum
+      uint32_t q[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        q[i] = __float_as_uint(fminf(fmaxf(fmaf(x[i], CE_STEPS, 8388608.f), 8388608.f), 8388608.f + 65535.f));
+#pragma unroll
+      for (int g8 = 0; g8 < 4; ++g8) {
+        uint4 v;
+        v.x = __byte_perm(q[g8 * 8 + 0], q[g8 * 8 + 1], 0x5410);
+        v.y = __byte_perm(q[g8 * 8 + 2], q[g8 * 8 + 3], 0x5410);
+        v.z = __byte_perm(q[g8 * 8 + 4], q[g8 * 8 + 5], 0x5410);
+        v.w = __byte_perm(q[g8 * 8 + 6], q[g8 * 8 + 7], 0x5410);
+        const uint32_t j = uint32_t((c & 1) * 4 + g8);
+        *reinterpret_cast<uint4*>(box + lane * 128u + ((j ^ (lane & 7u)) * 16u)) = v;
+      }
+      if (c & 1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tmap_c, box, 0, m_blk * BM + int(quarter) * 32, (col0 - 32) / 64);
+          bulk_commit();
+        }
+        sbuf ^= 1u;
+      }
+    }
+  }
+  if (row < rows) p.partials[size_t(nb) * (p.m_tiles * BM) + row] = make_float4(m, s0 + s1, zy, zs);
+}
+
 template <int EPI, int CG, int KKB>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     kd_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -131,6 +256,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = lane_id();
   const uint32_t crank = CG == 2 ? cluster_ctarank() : 0u;
+  const Extent ext = problem_extent(p);
   const int u_first = int(blockIdx.x) / p.cluster;
   const int u_step = int(gridDim.x) / p.cluster;
 
@@ -152,7 +278,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tmap_a);
     tma_prefetch_map(&tmap_b);
-    if (EPI == EPI_DZ || EPI == EPI_LSE_Z || EPI == EPI_DZ_LP) tma_prefetch_map(&tmap_c);
+    if (EPI == EPI_DZ || EPI == EPI_LSE_Z || EPI == EPI_DZ_LP || EPI == EPI_CE) tma_prefetch_map(&tmap_c);
   }
   if (warp == 1) {
     if (CG == 2) tmem_alloc_pair(&tail->tmem_base, TMEM_COLS); else tmem_alloc(&tail->tmem_base, TMEM_COLS);
@@ -168,9 +294,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = u_first; u < p.n_units && ok; u += u_step) {
+      for (int u = u_first; u < ext.n_units && ok; u += u_step) {
         int m_blk, n_first, n_count, kb_lo, kb_hi, split;
-        unit_coords(p, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
+        unit_coords(p, ext, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
         for (int nb = n_first; nb < n_first + n_count && ok; ++nb) {
           for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
             const uint32_t s = it % G::kStages;
@@ -275,9 +401,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       const uint32_t b_lbo = p.b_mn ? uint32_t(BK * G::kKB * 128) : 16u;
       uint32_t it = 0, acc_it = 0;
       bool ok = true;
-      for (int u = u_first; u < p.n_units && ok; u += u_step) {
+      for (int u = u_first; u < ext.n_units && ok; u += u_step) {
         int m_blk, n_first, n_count, kb_lo, kb_hi, split;
-        unit_coords(p, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
+        unit_coords(p, ext, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
         for (int nb = n_first; nb < n_first + n_count && ok; ++nb, ++acc_it) {
           const uint32_t a = acc_it & 1u;
           const uint32_t aph = (acc_it >> 1) & 1u;
@@ -299,7 +425,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const uint32_t sb = sa + G::kA;
             // 16-deep steps of this stage inside K (a pair's last stage may hold one
             // k-block of zeros past the end of K: skip its MMAs)
-            const int ksteps = (p.K - kb * BK * G::kKB + 15) / 16;
+            const int ksteps = (ext.K - kb * BK * G::kKB + 15) / 16;
 #pragma unroll
             for (int k = 0; k < G::kKB * (BK / 16); ++k) {
               if (CG == 2 && k >= BK / 16 && k >= ksteps) break;
@@ -334,9 +460,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     uint32_t sbuf = 0;
     uint32_t acc_it = 0;
     bool ok = true;
-    for (int u = u_first; u < p.n_units && ok; u += u_step) {
+    for (int u = u_first; u < ext.n_units && ok; u += u_step) {
       int m_blk, n_first, n_count, kb_lo, kb_hi, split;
-      unit_coords(p, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
+      unit_coords(p, ext, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
       const int row = m_blk * BM + r_local;
 
       // Per-row state for the loss epilogues.
@@ -374,6 +500,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         }
       }
 
+      if (EPI == EPI_CE && row < ext.rows) {
+        nid = __ldg(p.tokens + row);
+        if (nid < 0 || nid >= p.N) nid = 0x7fffffff;  // out of range: reported by the combine
+      }
       if (EPI == EPI_LSE_H || EPI == EPI_DZ_LP) {
         // a padding row (its token is not looked at): no token, no gradient
         const bool valid = row < p.rows && (p.mask == nullptr || p.mask[row] != 0);
@@ -406,8 +536,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         tc_fence_after();
         const uint32_t t_acc = t_lane + a * BN;
 
+        if (EPI == EPI_CE) ce_tile(p, tmap_c, t_acc, nb, m_blk, row, ext.rows, nid, my_staging, sbuf, lane, quarter);
+
 #pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
+        for (int c = 0; c < (EPI == EPI_CE ? 0 : BN / 32); ++c) {
           uint32_t raw[32];
           tmem_ld_32x32b_x32(t_acc + c * 32, raw);
           tmem_ld_wait();
@@ -692,10 +824,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             }
           } else {
             // EPI_STORE: C[row, col0 + i]
-            if (row < p.M) {
+            if (row < ext.M) {
+              const int crow = p.row_map ? __ldg(p.row_map + row) : row;
               if (p.c_bf16) {
                 uint16_t* dst =
-                    reinterpret_cast<uint16_t*>(p.C) + size_t(split) * p.split_stride + size_t(row) * p.ldc + col0;
+                    reinterpret_cast<uint16_t*>(p.C) + size_t(split) * p.split_stride + size_t(crow) * p.ldc + col0;
 #pragma unroll
                 for (int g8 = 0; g8 < 4; ++g8) {
                   // whole 8-column groups that start inside the matrix; the row stride ldc is
@@ -711,7 +844,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 }
               } else {
                 float* dst =
-                    reinterpret_cast<float*>(p.C) + size_t(split) * p.split_stride + size_t(row) * p.ldc + col0;
+                    reinterpret_cast<float*>(p.C) + size_t(split) * p.split_stride + size_t(crow) * p.ldc + col0;
 #pragma unroll
                 for (int g4 = 0; g4 < 8; ++g4) {
                   if (col0 + g4 * 4 < p.N && col0 + g4 * 4 + 4 <= p.ldc) {
@@ -740,7 +873,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         p.partials[size_t(n_first / p.n_group) * (p.m_tiles * BM) + row] =
             make_float4(run_m, run_s, run_g, run_u);
     }
-    if ((EPI == EPI_DZ || EPI == EPI_DZ_LP || EPI == EPI_LSE_Z || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
+    if ((EPI == EPI_DZ || EPI == EPI_DZ_LP || EPI == EPI_LSE_Z || EPI == EPI_CE || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
       bulk_wait_all();  // output boxes done before exit
   }
 
@@ -836,6 +969,7 @@ static const char* gemm_name(int epi, int a_mn, int b_mn) {
     case EPI_DZ: return "kd_proj_dz_bwd";
     case EPI_LSE_H: return "kd_proj_logprob_fwd";
     case EPI_DZ_LP: return "kd_proj_logprob_bwd";
+    case EPI_CE: return "kd_proj_ce";
     case EPI_STORE: return (a_mn == 0 && b_mn == 1) ? "kd_gemm_dz_w" : "kd_gemm_store";
     default: return (a_mn == 1 && b_mn == 1) ? "kd_gemm_dzT_h" : "kd_gemm_accum";
   }
@@ -857,6 +991,7 @@ cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUten
       case EPI_DZ: e = two ? launch_one<EPI_DZ, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_LSE_H: e = two ? launch_one<EPI_LSE_H, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_DZ_LP: e = two ? launch_one<EPI_DZ_LP, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
+      case EPI_CE: e = two ? launch_one<EPI_CE, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_STORE:
         e = two ? launch_one<EPI_STORE, 2, 2>(p, ta, tb, tc, grid, s) : launch_one<EPI_STORE, 2, 1>(p, ta, tb, tc, grid, s);
         break;
@@ -871,6 +1006,7 @@ cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUten
       case EPI_DZ: e = launch_one<EPI_DZ, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_LSE_H: e = launch_one<EPI_LSE_H, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_DZ_LP: e = launch_one<EPI_DZ_LP, 1>(p, ta, tb, tc, grid, s); break;
+      case EPI_CE: e = launch_one<EPI_CE, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_STORE: e = launch_one<EPI_STORE, 1>(p, ta, tb, tc, grid, s); break;
       default: e = launch_one<EPI_ACCUM, 1>(p, ta, tb, tc, grid, s); break;
     }

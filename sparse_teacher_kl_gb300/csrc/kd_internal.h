@@ -56,6 +56,8 @@ enum EpiKind : int {
   EPI_LSE_Z = 4,  // forward-chunked: EPI_LSE plus the raw logits z -> bf16, blocked [V/64][N][64]
   EPI_LSE_H = 5,  // log probabilities: online logsumexp and entropy sum, the token's logit -> partials
   EPI_DZ_LP = 6,  // their gradient: dZ = p (c0 + c1 log2 p) + [v = token] g / tau -> bf16, blocked
+  EPI_CE = 7,     // cross entropy: a tile's (max, sum, label's logit, sum of logits) -> partials; with ce_q the
+                  // logits as 16-bit distances from the tile's largest, blocked as dZ
 };
 
 // 64-deep k-blocks per ring stage of a CTA-pair launch: two when both operands are
@@ -137,8 +139,24 @@ struct GemmProblem {
   uint16_t* dz;               // EPI_DZ: bf16 [rows, ldz]
   int64_t ldz;
   int rows;                   // valid rows of A (tokens in this chunk) for LSE/DZ
+  // rows_dev (NULL: none): only the first clamp(*rows_dev - row_first, 0, rows) rows of the chunk
+  // exist: the M extent of a product whose A is K-major, the K extent of one whose A is MN-major
+  // (there an EPI_STORE takes one k-block of zeros when none exists).
+  const int32_t* rows_dev;
+  int row_first;
+  const int32_t* row_map;     // EPI_STORE without c_tma and splits (NULL: none): row of C that row i goes to
+  // EPI_CE: tokens as above; logits capped to ce_cap tanh(z / ce_cap) (0: not); ce_sum: the sum of
+  // logits is wanted; ce_q: the 16-bit logits go out through tmap_c
+  float ce_cap;
+  int ce_sum, ce_q;
   uint32_t* err;
 };
+
+// EPI_CE's 16-bit logits: the distance from the tile's largest in steps of 1 / CE_STEPS, 65535 for
+// anything 32 and further below (e^-32 of the largest, 1.3e-14).  Half a step makes 2.4e-4 of a
+// probability, an eighth of the rounding of bf16 dZ; bf16 logits would make 2^-8 of every unit of |z|.
+constexpr float CE_STEPS = 2048.f;
+
 
 // Host helpers of the C ABI.
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -151,6 +169,8 @@ inline float log2e_over_tau(float tau) {
   const double k = 1.4426950408889634 / double(tau);
   return k <= double(FLT_MAX) ? float(k) : FLT_MAX;
 }
+// What every call on hidden states and a head checks: sizes, chunk, alignment, temperature.
+kd_status check_proj_args(const void* H, const void* W, int64_t N, int64_t d, int64_t V, int64_t chunk, float tau);
 // KD_OK if the current device is an sm_103 GPU.
 kd_status check_device();
 
@@ -187,6 +207,8 @@ inline cudaError_t smem_attr_once(PerDevice<int>& done, const void* func, int by
 // tc: output map for the epilogues that write through TMA (EPI_ACCUM: fp32 C,
 // box 32 x 32; EPI_DZ: bf16 dZ, box 64 x 32; both 128-byte swizzle); ignored
 // by the others.
+void set_cluster(GemmProblem& p);
+int choose_splits(int64_t tiles, int k_blocks, int grid);
 cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                         int grid, cudaStream_t s);
 int gemm_max_grid();
