@@ -471,7 +471,7 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
  * separate backward pass needs.
  *   grad_H : [N, d] bf16 or fp32, zero rows where not valid.  grad_W, grad_W_kind as for
  *            kd_fused_logprobs_bwd.  dZ is rounded to bf16; probabilities below e^-32 of the
- *            largest of their 256 columns are taken as that.
+ *            largest of their 128 columns are taken as that.
  * Workspace: `step` != 0 asks for the step's (it grows with chunk * V), 0 for the forward pass's
  * (chunk * (V / 16 + 2 d) bytes).  `ws` may be memory of any content; the error word is in `control`
  * (see kd_logits_kl_fwd_ctl), which may be `ws` itself once kd_workspace_clear has cleared it.

@@ -178,7 +178,7 @@ void set_cluster(GemmProblem& p) {
 // K-major boxes (a_k3d / b_k3d) for CTA pairs.
 static_assert(pair_kblocks(0, 0) == 2, "K-major operand pairs take two k-blocks per pair stage");
 
-int choose_splits(int64_t tiles, int k_blocks, int grid) {
+static int choose_splits(int64_t tiles, int k_blocks, int grid) {
   int best = 1;
   double best_cost = 1e300;
   for (int S = 1; S <= KD_MAX_SPLITS; ++S) {

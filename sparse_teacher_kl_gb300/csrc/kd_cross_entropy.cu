@@ -10,7 +10,7 @@
 // What a step cannot do without is 6 N d V operations (one projection, two gradient products); what it
 // must move is H, W and the two gradients.  The usual way to keep no logits is to project twice (8 N d V).
 // Here the projection's epilogue leaves each chunk's logits as 16-bit distances from the largest of
-// their 256-column tile (CE_STEPS; 2 bytes each, in the buffer that dZ needs anyway), and once a row's sum is
+// their CE_COLS columns (CE_STEPS; 2 bytes each, in the buffer that dZ needs anyway), and once a row's sum is
 // known one pass over that buffer turns them into bf16 dZ where they lie: 6 bytes moved for each logit
 // against 2 d operations, 0.9 ns against 3.3 ns per thousand at d = 2880.  The label's own entry, where
 // p_y - 1 would cancel, comes from its fp32 logit.
@@ -203,10 +203,10 @@ __global__ void __launch_bounds__(CC_ROWS * CC_PHASES) kd_ce_combine_kernel(cons
 }
 
 // ------------------------------------------------------------------ dZ ---
-// The chunk's 16-bit distances to bf16 dZ, in place ([V / 64][row][64], both).  A block takes 64 rows of
-// one 256-column tile: 8 lanes to a 128-byte row of a 64-column block, 8 vectors of 16 bytes in flight a thread.
+// The chunk's 16-bit distances to bf16 dZ, in place ([V / 64][row][64], both).  A block takes 128 rows of
+// CE_COLS columns: 8 lanes to a 128-byte row of a 64-column block, 8 vectors of 16 bytes in flight a thread.
 // Bound by HBM: 4 bytes a logit.
-constexpr int DQ_ROWS = 64;
+constexpr int DQ_ROWS = 128, DQ_BLOCKS = CE_COLS / 64;
 
 __device__ __forceinline__ float dz_of(uint32_t q, float shift, float m, const float4& st, float cap2) {
   const float far = float(q);
@@ -226,30 +226,32 @@ __global__ void __launch_bounds__(256)
   const int first = int(blockIdx.x - uint32_t(tile) * row_blocks) * DQ_ROWS, r0 = first + (threadIdx.x >> 3);
   const float cap2 = softcap > 0.f ? 1.f / (softcap * softcap) : 0.f;
   if (first >= end) return;
+  const int vb0 = tile * DQ_BLOCKS;
+  uint4 v[DQ_ROWS / 32][DQ_BLOCKS];
+#pragma unroll
+  for (int h = 0; h < DQ_ROWS / 32; ++h)
+#pragma unroll
+    for (int b = 0; b < DQ_BLOCKS; ++b)
+      if (r0 + h * 32 < n && vb0 + b < nvb) v[h][b] = dz[(size_t(vb0 + b) * rows_pad + r0 + h * 32) * 8 + lane8];
 #pragma unroll
   for (int h = 0; h < DQ_ROWS / 32; ++h) {
     const int r = r0 + h * 32;
-    if (r >= end) continue;
-    uint4 v[4];
-    const int vb0 = tile * 4;
+    if (r >= end) return;
     if (r >= n) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
+      for (int b = 0; b < DQ_BLOCKS; ++b)
         if (vb0 + b < nvb) dz[(size_t(vb0 + b) * rows_pad + r) * 8 + lane8] = make_uint4(0, 0, 0, 0);
       continue;
     }
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      if (vb0 + b < nvb) v[b] = dz[(size_t(vb0 + b) * rows_pad + r) * 8 + lane8];
     const float4 st = row_stats[r];
     const float m = partials[size_t(tile) * ld_part + r].x;
     const int label = labels_c[r];
-    // a tile of nothing but -inf has no probability, whatever its distances (then m - lse is -inf)
+    // columns of nothing but -inf have no probability, whatever their distances (then m - lse is -inf)
     const float shift = (m - st.x) * kLog2E;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < DQ_BLOCKS; ++b) {
       if (vb0 + b >= nvb) break;
-      const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+      const uint32_t w[4] = {v[h][b].x, v[h][b].y, v[h][b].z, v[h][b].w};
       const int off = label - (vb0 + b) * 64 - lane8 * 8;
       uint32_t o[4];
 #pragma unroll
@@ -313,7 +315,7 @@ CeLayout ce_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool step) {
   CeLayout L{};
   const int64_t c = chunk < N ? chunk : N;
   L.rows_pad = (c + BM - 1) / BM * BM;
-  L.tiles = int((V + BN - 1) / BN);
+  L.tiles = int((V + CE_COLS - 1) / CE_COLS);
   L.nvb = (V + 63) / 64;
   size_t off = sizeof(Ctrl);
   auto take = [&](size_t bytes) {
@@ -358,6 +360,26 @@ struct CeCall {
     if ((call) != cudaSuccess) return KD_ERR_CUDA; \
   } while (0)
 
+// Splits of grad_H's reduction over the vocabulary.  In units of one 64-deep k-block of a tile (0.27 us):
+// the waves of tiles, each with about 8 blocks of ramp and epilogue, and for a split the reading of its fp32
+// partials and one more launch.  8 k-blocks are the least that pays for a split.
+int ce_splits(const GemmProblem& q, int slots, int k_blocks) {
+  const int64_t tiles = int64_t((q.m_tiles + q.cluster - 1) / q.cluster) * q.n_tiles;
+  const double part = double(q.M) * q.N * 4 / 6.5e6 / 0.27;
+  int best = 1;
+  double best_cost = 1e300;
+  for (int S = 1; S <= KD_MAX_SPLITS; ++S) {
+    if (S > 1 && k_blocks / S < 8) break;
+    const double waves = double((tiles * S + slots - 1) / slots);
+    const double cost = waves * (double(k_blocks) / S + 8) + (S > 1 ? S * part + 11 : 0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = S;
+    }
+  }
+  return best;
+}
+
 // The two gradient products of a chunk, from dZ and the gathered hidden states.
 int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int n, cudaStream_t s) {
   Ctrl* ctrl = static_cast<Ctrl*>(a.ws);
@@ -377,8 +399,8 @@ int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int
   q.m_tiles = (n + BM - 1) / BM;
   q.n_tiles = int((a.d + BN - 1) / BN);
   q.n_group = 1;
-  q.k_splits = choose_splits(int64_t(q.m_tiles) * q.n_tiles, int((a.V + BK - 1) / BK), grid);
   set_cluster(q);
+  q.k_splits = ce_splits(q, grid / q.cluster, int((a.V + BK - 1) / BK));
   q.n_units = ((q.m_tiles + q.cluster - 1) / q.cluster) * q.n_tiles * q.k_splits;
   q.rows = n; q.rows_dev = &ctrl->n_valid; q.row_first = int(c0);
   q.err = err;
@@ -492,7 +514,7 @@ int ce_run(const CeCall& a, bool step) {
     p.M = n; p.N = int(a.V); p.K = int(a.d);
     p.epi = EPI_CE;
     p.m_tiles = (n + BM - 1) / BM;
-    p.n_tiles = L.tiles;
+    p.n_tiles = int((a.V + BN - 1) / BN);
     p.n_group = 1;
     p.k_splits = 1;
     set_cluster(p);

@@ -386,9 +386,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// 1 / x on the special-function unit (approximate; 0 for an infinity).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // c tanh(z / c) = c - 2 c / (e^(2 z / c) + 1), k = 2 log2(e) / c: within a few roundings of c at any z.
 __device__ __forceinline__ float ce_capped(float z, float c, float k) {
-  return fmaf(-2.f * c, __frcp_rn(ex2_approx(z * k) + 1.f), c);
+  return fmaf(-2.f * c, rcp_approx(ex2_approx(z * k) + 1.f), c);
 }
 
 // Value of r[i] for a run-time i in [0, 32), by a tree of selects so that the

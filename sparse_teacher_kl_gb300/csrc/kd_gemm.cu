@@ -27,9 +27,9 @@
 //             gradient products in one 16-bit type, and H and W are bf16.  Measured on 8192 x
 //             2048 x 32000: gradients within 2.3e-3 (2-norm) of float64, 1.7e-3 of which is the
 //             rounding of bf16 outputs; a second bf16 term of dZ would run the products twice.
-//   EPI_CE    cross entropy: per row and tile the largest (capped) logit, the sum of exponentials
+//   EPI_CE    cross entropy: per row and half tile the largest (capped) logit, the sum of exponentials
 //             against it, the label's logit and the sum of logits; for a training step also every
-//             logit as a 16-bit distance from the tile's largest, which kd_cross_entropy.cu turns
+//             logit as a 16-bit distance from that largest, which kd_cross_entropy.cu turns
 //             into dZ where it lies once the rows' sums are known (no second projection).
 //   EPI_STORE / EPI_ACCUM  plain C = acc / C += acc for the gradient products.
 #include <math.h>
@@ -145,23 +145,33 @@ __device__ __forceinline__ void unit_coords(const GemmProblem& p, const Extent& 
   }
 }
 
-// One tile of EPI_CE for the row of this thread: two sweeps over the accumulator, the first for the
-// largest logit, so that the sum needs no rescaling and the distances their final reference.
-__device__ __forceinline__ void ce_tile(const GemmProblem& p, const CUtensorMap& tmap_c, uint32_t t_acc, int nb,
-                                        int m_blk, int row, int rows, int nid, uint8_t* staging, uint32_t& sbuf,
-                                        uint32_t lane, uint32_t quarter) {
+// Warps that drain finished accumulators.  The cross entropy's take two sweeps and, with a softcap, three
+// special-function results for each logit: two warps on each of the SM's four schedulers, each with half of
+// the columns, hide their latency (509 x 50257, d = 1000, capped: EPI_CE_MEASURED).
+template <int EPI>
+constexpr int kEpiWarps = EPI == EPI_CE ? 8 : 4;
+template <int EPI>
+constexpr int kThreads = 64 + 32 * kEpiWarps<EPI>;
+static_assert(kThreads<EPI_STORE> == GEMM_THREADS, "TMA warp, MMA warp, 4 epilogue warps");
+
+// A warp's half of a tile of EPI_CE (CE_COLS columns from `first`), for the row of this thread: two sweeps
+// over the accumulator, the first for the largest logit, so that the sum needs no rescaling and the
+// distances have their final reference.
+__device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap& tmap_c, uint32_t t_acc, int first,
+                                        int m_blk, int row, int rows, int nid, uint8_t* box, uint32_t lane,
+                                        uint32_t quarter) {
   constexpr float kL2E = 1.4426950408889634f;
-  const bool last = (nb + 1) * BN > p.N;  // columns past the vocabulary: weight 0
+  const bool last = first + CE_COLS > p.N;  // columns past the vocabulary: weight 0
   float m = -INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
+  for (int c = 0; c < CE_COLS / 32; ++c) {
     uint32_t raw[32];
     tmem_ld_32x32b_x32(t_acc + c * 32, raw);
     tmem_ld_wait();
     if (last) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (nb * BN + c * 32 + i < p.N) m = fmaxf(m, __uint_as_float(raw[i]));
+        if (first + c * 32 + i < p.N) m = fmaxf(m, __uint_as_float(raw[i]));
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(raw[i]));
@@ -172,8 +182,8 @@ __device__ __forceinline__ void ce_tile(const GemmProblem& p, const CUtensorMap&
   const float ref = m == -INFINITY ? 0.f : m;  // nothing but -inf: distances stay infinite, not NaN
   float s0 = 0.f, s1 = 0.f, zs = 0.f, zy = 0.f;
 #pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
-    const int col0 = nb * BN + c * 32;
+  for (int c = 0; c < CE_COLS / 32; ++c) {
+    const int col0 = first + c * 32;
     uint32_t raw[32];
     tmem_ld_32x32b_x32(t_acc + c * 32, raw);
     tmem_ld_wait();
@@ -207,9 +217,8 @@ __device__ __forceinline__ void ce_tile(const GemmProblem& p, const CUtensorMap&
       s1 += ex2_approx(x[i + 1] * -kL2E);
     }
     if (p.ce_q) {
-      uint8_t* box = staging + sbuf * 4096u;
       if ((c & 1) == 0) {
-        if (lane == 0) bulk_wait_read<1>();
+        if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
       }
       // 2^23 added: the distance in whole steps, rounded, in the low bits of the sum
@@ -234,15 +243,15 @@ __device__ __forceinline__ void ce_tile(const GemmProblem& p, const CUtensorMap&
           tma_store_3d(&tmap_c, box, 0, m_blk * BM + int(quarter) * 32, (col0 - 32) / 64);
           bulk_commit();
         }
-        sbuf ^= 1u;
       }
     }
   }
-  if (row < rows) p.partials[size_t(nb) * (p.m_tiles * BM) + row] = make_float4(m, s0 + s1, zy, zs);
+  if (row < rows && first < p.N)
+    p.partials[size_t(first / CE_COLS) * (p.m_tiles * BM) + row] = make_float4(m, s0 + s1, zy, zs);
 }
 
 template <int EPI, int CG, int KKB>
-__global__ void __launch_bounds__(GEMM_THREADS, 1)
+__global__ void __launch_bounds__(kThreads<EPI>, 1)
     kd_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                    const __grid_constant__ CUtensorMap tmap_c, const GemmProblem p) {
   extern __shared__ uint8_t smem_raw[];
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tail->tfull[a], 1);
       // the pair's MMA thread waits for both CTAs' epilogues
-      mbar_init(&tail->tempty[a], (CG == 2 && crank == 0) ? 256u : 128u);
+      mbar_init(&tail->tempty[a], ((CG == 2 && crank == 0) ? 64u : 32u) * kEpiWarps<EPI>);
     }
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
@@ -536,7 +545,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         tc_fence_after();
         const uint32_t t_acc = t_lane + a * BN;
 
-        if (EPI == EPI_CE) ce_tile(p, tmap_c, t_acc, nb, m_blk, row, ext.rows, nid, my_staging, sbuf, lane, quarter);
+        if (EPI == EPI_CE) {
+          const int half = int(warp - 2u) >> 2;
+          ce_half(p, tmap_c, t_acc + half * CE_COLS, nb * BN + half * CE_COLS, m_blk, row, ext.rows, nid,
+                  staging + (warp - 2u) * 4096u, lane, quarter);
+        }
 
 #pragma unroll 1
         for (int c = 0; c < (EPI == EPI_CE ? 0 : BN / 32); ++c) {
@@ -925,7 +938,7 @@ static cudaError_t launch_one(const GemmProblem& p, const CUtensorMap& ta, const
       qa[0].val.clusterDim.z = 1;
       q.attrs = qa;
       q.numAttrs = 1;
-      q.blockDim = dim3(GEMM_THREADS, 1, 1);
+      q.blockDim = dim3(kThreads<EPI>, 1, 1);
       q.dynamicSmemBytes = Geo<CG, KKB>::kSmem;
       q.gridDim = dim3(unsigned((gemm_max_grid() / 2) * 2), 1, 1);
       int n = 0;
@@ -936,7 +949,7 @@ static cudaError_t launch_one(const GemmProblem& p, const CUtensorMap& ta, const
   if (rc != 0) return rc > 0 ? cudaError_t(rc) : cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.blockDim = dim3(GEMM_THREADS, 1, 1);
+  cfg.blockDim = dim3(kThreads<EPI>, 1, 1);
   cfg.dynamicSmemBytes = Geo<CG, KKB>::kSmem;
   cfg.stream = s;
   if (CG == 2) {

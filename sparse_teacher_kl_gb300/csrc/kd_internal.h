@@ -152,9 +152,11 @@ struct GemmProblem {
   uint32_t* err;
 };
 
-// EPI_CE's 16-bit logits: the distance from the tile's largest in steps of 1 / CE_STEPS, 65535 for
+// EPI_CE's partials and 16-bit logits belong to CE_COLS columns (half a tile).  The latter are the distance
+// from the largest of those columns in steps of 1 / CE_STEPS, 65535 for
 // anything 32 and further below (e^-32 of the largest, 1.3e-14).  Half a step makes 2.4e-4 of a
 // probability, an eighth of the rounding of bf16 dZ; bf16 logits would make 2^-8 of every unit of |z|.
+constexpr int CE_COLS = BN / 2;
 constexpr float CE_STEPS = 2048.f;
 
 
@@ -208,7 +210,6 @@ inline cudaError_t smem_attr_once(PerDevice<int>& done, const void* func, int by
 // box 32 x 32; EPI_DZ: bf16 dZ, box 64 x 32; both 128-byte swizzle); ignored
 // by the others.
 void set_cluster(GemmProblem& p);
-int choose_splits(int64_t tiles, int k_blocks, int grid);
 cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                         int grid, cudaStream_t s);
 int gemm_max_grid();
