@@ -495,6 +495,45 @@ KD_API int kd_fused_cross_entropy_step(const void* H_bf16, const void* W_bf16, c
 KD_API int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* factor, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * 8-bit integers with one scale a row: a quantised teacher head (no page has a counterpart).
+ *
+ * kd_quantize_int8: rows of x [N, d] (bf16, fp16 or fp32, kd_dtype, any row stride ld >= d) to integers,
+ *   scale_n = max |x_n| / 127 (fp32),   q_nk = the whole number nearest to x_nk / scale_n, ties to even,
+ * the quotient taken exactly.  A row of zeros has scale 0; one that holds a NaN or an infinity has
+ * scale NaN and integers 0.  q_out: [N, d] with row stride ld_q >= d.
+ *
+ * kd_gemm_int8: C_mn = (sum_k A_mk B_nk) a_scale_m b_scale_n, A [M, K] the tokens and B [N, K] the channels,
+ * 1 <= K <= KD_MAX_INT8_K, any row strides lda, ldb >= K, ldc >= N; C bf16, fp16 or fp32 (kd_dtype).  The
+ * integer sum is exact below 2^24 (always for K <= 1024) and rounded to fp32 from there on; each of the two
+ * products with a scale rounds once to fp32, and the result once to C's type.  Weights whose rows start on
+ * 16-byte boundaries (B and ldb multiples of 16) are read in place, others are copied to such rows
+ * in the workspace by every call.  Workspace: `b_rows_aligned` as B's rows are; memory of any content,
+ * the error word in `control` (see kd_logits_kl_fwd_ctl).
+ *
+ * kd_teacher_topk_int8: kd_teacher_topk from quantised hidden states Ht [N, dt] and head Wt [V, dt]; any
+ * chunk >= 1.
+ * ------------------------------------------------------------------------ */
+
+#define KD_MAX_INT8_K 65536
+
+KD_API int kd_quantize_int8(const void* x, int dtype, int64_t N, int64_t d, int64_t ld, int8_t* q_out, int64_t ld_q,
+                    float* scale_out, void* stream);
+
+KD_API size_t kd_gemm_int8_workspace(int64_t M, int64_t N, int64_t K, int b_rows_aligned);
+
+KD_API int kd_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
+                    const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                    void* ws, size_t ws_bytes, void* control, void* stream);
+
+KD_API size_t kd_teacher_topk_int8_workspace(int64_t N, int64_t dt, int64_t V, int K, int64_t chunk,
+                    int w_rows_aligned);
+
+KD_API int kd_teacher_topk_int8(const int8_t* Ht, int64_t ld_h, const float* h_scale, const int8_t* Wt, int64_t ld_w,
+                    const float* w_scale, int64_t N, int64_t dt, int64_t V, int K, int64_t chunk,
+                    int32_t* ids_out, float* vals_out, float* lse_out, float* dropped_out,
+                    void* ws, size_t ws_bytes, void* control, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * On-disk teacher cache ([ART] paragraph on the first fix: run the teacher once,
  * keep its top-K logits per position on disk, reuse them across experiments).
  * HOST memory and host files only; no CUDA call.  One file per contiguous range

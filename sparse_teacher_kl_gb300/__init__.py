@@ -43,6 +43,9 @@ __all__ = [
     "fused_cross_entropy_forward",
     "fused_cross_entropy_step",
     "gemm_bf16",
+    "quantize_int8",
+    "gemm_int8",
+    "teacher_topk_int8",
     "cache_write",
     "cache_info",
     "cache_read",
@@ -771,6 +774,98 @@ def gemm_bf16(A, B, M, N, K, a_mn_major=False, b_mn_major=False, C=None):
                            ws.numel(), _stream(A.device))
     _abi.check(st, "kd_gemm_bf16")
     return C, ws
+
+
+# ------------------------------------------------------------------ 8 bits
+
+def quantize_int8(x, q=None, scale=None):
+    """kd_quantize_int8: (q int8 [N, d], scale fp32 [N]) of the rows of ``x`` ([N, d] bf16, fp16 or fp32, any row
+    stride): scale = max |x| / 127, q = x / scale to the nearest whole number."""
+    dt, N, d, ld = _check_logits(x, "x")
+    given = q, scale
+    if q is None:
+        q = torch.empty((N, d), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((N,), dtype=torch.float32, device=x.device)
+    ldq = _check_int8(q, "q", x.device)
+    if q.shape != x.shape:
+        raise ValueError("q must have the shape of x")
+    _check(scale, "scale", torch.float32, (N,), x.device)
+    st = _abi.kd_quantize_int8(_ptr(x), dt, N, d, ld, _ptr(q), ldq, _ptr(scale), _stream(x.device))
+    _abi.check(st, "kd_quantize_int8")
+    _written(*given)
+    return q, scale
+
+
+def _check_int8(t, name: str, device=None) -> int:
+    """The row stride of a 2-D int8 CUDA matrix whose rows are contiguous."""
+    if not t.is_cuda or t.dim() != 2 or t.dtype != torch.int8 or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a 2-D int8 CUDA tensor" + ("" if device is None else f" on {device}"))
+    if t.shape[0] < 1 or t.shape[1] < 1:
+        raise ValueError(f"{name} must not be empty")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if (t.stride(1) != 1 and t.shape[1] > 1) or ld < t.shape[1]:
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    return ld
+
+
+def _rows_aligned(t, ld: int) -> int:
+    return int(t.data_ptr() % 16 == 0 and ld % 16 == 0)
+
+
+def gemm_int8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, ws=None):
+    """kd_gemm_int8: [M, N] = (A B^T) a_scale[:, None] b_scale of int8 matrices A [M, K] (tokens) and B [N, K]
+    (channels), rows of any stride, in bf16, fp16 or fp32 (``out_dtype``, or that of a given ``out``).  Weights
+    B whose rows start on 16-byte boundaries are read in place.  Without a workspace errors go to the stream's
+    control_block."""
+    lda, ldb = _check_int8(A, "A"), _check_int8(B, "B", A.device)
+    (M, K), N, dev = A.shape, B.shape[0], A.device
+    if B.shape[1] != K:
+        raise ValueError("A and B must have the same number of columns")
+    _check(a_scale, "a_scale", torch.float32, (M,), dev)
+    _check(b_scale, "b_scale", torch.float32, (N,), dev)
+    given = out
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise ValueError("out_dtype must be bf16, fp16 or fp32")
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    if out.device != dev or out.shape != (M, N):
+        raise ValueError(f"out must be [{M}, {N}] on {dev}")
+    dt, _, _, ldc = _check_logits(out, "out")
+    control = ws
+    if ws is None:
+        control = _control(dev)
+        ws = _scratch(_abi.kd_gemm_int8_workspace(M, N, K, _rows_aligned(B, ldb)), dev)
+    st = _abi.kd_gemm_int8(_ptr(A), lda, _ptr(a_scale), _ptr(B), ldb, _ptr(b_scale), _ptr(out), dt, ldc, M, N, K,
+                           _ptr(ws), ws.numel(), _ptr(control), _stream(dev))
+    _abi.check(st, "kd_gemm_int8")
+    _written(given)
+    return out
+
+
+def teacher_topk_int8(Ht, h_scale, Wt, w_scale, K: int, chunk: int = 1024, with_lse: bool = False,
+                      with_dropped: bool = False, ws: Optional[torch.Tensor] = None):
+    """Top-K cache from quantised teacher hidden states Ht [N, dt] and LM-head Wt [V, dt] (int8 with their rows'
+    scales, see quantize_int8): the teacher logits exist only one chunk at a time, in bf16.  Returns as topk_cache."""
+    ld_h, ld_w = _check_int8(Ht, "Ht"), _check_int8(Wt, "Wt", Ht.device)
+    (N, dt), V, dev = Ht.shape, Wt.shape[0], Ht.device
+    if Wt.shape[1] != dt:
+        raise ValueError("Ht and Wt must have the same number of columns")
+    _check(h_scale, "h_scale", torch.float32, (N,), dev)
+    _check(w_scale, "w_scale", torch.float32, (V,), dev)
+    ids = torch.empty((N, K), dtype=torch.int32, device=dev)
+    vals = torch.empty((N, K), dtype=torch.float32, device=dev)
+    lse = torch.empty((N,), dtype=torch.float32, device=dev) if with_lse else None
+    dropped = torch.empty((N,), dtype=torch.float32, device=dev) if with_dropped else None
+    control = ws
+    if ws is None:
+        control = _control(dev)
+        ws = _scratch(_abi.kd_teacher_topk_int8_workspace(N, dt, V, K, chunk, _rows_aligned(Wt, ld_w)), dev)
+    st = _abi.kd_teacher_topk_int8(_ptr(Ht), ld_h, _ptr(h_scale), _ptr(Wt), ld_w, _ptr(w_scale), N, dt, V, K, chunk,
+                                   _ptr(ids), _ptr(vals), _ptr(lse), _ptr(dropped), _ptr(ws), ws.numel(),
+                                   _ptr(control), _stream(dev))
+    _abi.check(st, "kd_teacher_topk_int8")
+    return (ids, vals) + ((lse,) if with_lse else ()) + ((dropped,) if with_dropped else ())
 
 
 def device_error(ws: torch.Tensor):

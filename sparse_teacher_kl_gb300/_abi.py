@@ -31,6 +31,7 @@ KD_GRAD_STORE_F32 = 1
 KD_GRAD_STORE_BF16 = 2
 KD_MAX_K = 1024
 KD_MAX_TOP = 128
+KD_MAX_INT8_K = 65536
 KD_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 _c_i64 = ctypes.c_int64
@@ -87,6 +88,13 @@ _SIGNATURES = {
                                              _c_float, _c_float, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
                                              _c_int, _c_ptr, _c_int, _c_ptr, _c_size, _c_ptr, _c_ptr]),
     "kd_scale_gradient": (_c_int, [_c_ptr, _c_i64, _c_int, _c_ptr, _c_ptr]),
+    "kd_quantize_int8": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr]),
+    "kd_gemm_int8_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "kd_gemm_int8": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_int, _c_i64, _c_i64, _c_i64,
+                              _c_i64, _c_ptr, _c_size, _c_ptr, _c_ptr]),
+    "kd_teacher_topk_int8_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_i64, _c_int]),
+    "kd_teacher_topk_int8": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_i64, _c_i64, _c_i64, _c_int,
+                                      _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr, _c_ptr]),
     "kd_workspace_clear": (_c_int, [_c_ptr, _c_size, _c_ptr]),
     "kd_get_device_error": (_c_int, [_c_ptr, _c_ptr, ctypes.POINTER(_c_i64)]),
     "kd_gemm_bf16": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_ptr, _c_size,
@@ -191,6 +199,11 @@ kd_fused_cross_entropy_workspace = _wrap("kd_fused_cross_entropy_workspace")
 kd_fused_cross_entropy_fwd = _wrap("kd_fused_cross_entropy_fwd")
 kd_fused_cross_entropy_step = _wrap("kd_fused_cross_entropy_step")
 kd_scale_gradient = _wrap("kd_scale_gradient")
+kd_quantize_int8 = _wrap("kd_quantize_int8")
+kd_gemm_int8_workspace = _wrap("kd_gemm_int8_workspace")
+kd_gemm_int8 = _wrap("kd_gemm_int8")
+kd_teacher_topk_int8_workspace = _wrap("kd_teacher_topk_int8_workspace")
+kd_teacher_topk_int8 = _wrap("kd_teacher_topk_int8")
 kd_workspace_clear = _wrap("kd_workspace_clear")
 kd_get_device_error = _wrap("kd_get_device_error")
 kd_gemm_bf16 = _wrap("kd_gemm_bf16")

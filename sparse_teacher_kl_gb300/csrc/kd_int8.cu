@@ -1,0 +1,549 @@
+// 8-bit integers: rows quantised with one scale each, and the product of two such matrices,
+//   quantize   s_n = max_k |x_nk| / 127,  q_nk = x_nk / s_n to the nearest whole number (ties to even)
+//   product    C_mn = (sum_k A_mk B_nk) sa_m sb_n
+// A: [M, K], the tokens; B: [N, K], the channels (a head's vocabulary, a layer's outputs).
+//
+// sm_103a's fast tensor path takes no 8-bit integers, but every one of them is a 16-bit floating-point
+// number, and so is their product a sum of exact terms: fp16 operands and fp32 accumulators give the integer
+// sums themselves as long as those stay below 2^24 (always for K <= 1024; K = 4096 of random integers stays
+// a hundred times below it), and beyond that sums rounded to fp32.  So the operations cannot go
+// faster than the 16-bit rate, but the weights keep their single byte all the way from HBM to the SM:
+// they are widened on their way from shared to tensor memory, where tcgen05.mma takes its A operand from.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "kd_device.cuh"
+#include "kd_internal.h"
+
+namespace kd {
+
+namespace {
+
+// ------------------------------------------------------------------ geometry ---
+// A tile is 128 channels (the MMA's M side, from tensor memory) by TN tokens (its N side, from shared
+// memory); a pair of CTAs computes 256 channels, each loading half of the tokens.  The reduction goes 128
+// deep a stage.
+constexpr int T8_ROWS = 128;
+constexpr int T8_K = 128;
+constexpr int T8_W_BYTES = T8_ROWS * T8_K;      // a stage's weights: 16 KB
+constexpr int T8_MAX_TOKENS = 192;
+constexpr int T8_MAX_STAGES = 10;
+constexpr int T8_MAX_WIDE = 4;                  // stages of widened weights in tensor memory, 64 columns each
+constexpr int T8_THREADS = 320;                 // TMA, MMA, 4 epilogue and 4 widening warps
+constexpr int T8_SMEM = 224 * 1024;
+
+struct __align__(8) T8Tail {
+  uint64_t full[T8_MAX_STAGES], empty[T8_MAX_STAGES];
+  uint64_t wide[T8_MAX_WIDE], wfree[T8_MAX_WIDE];
+  uint64_t tfull[2], tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base, abort_flag;
+};
+
+struct T8Problem {
+  int M, N, K;
+  int tokens;        // TN: tokens of a tile, a multiple of 16 (a pair's: of 32)
+  int token_tiles, units, stages, wide_stages, stage_bytes;
+  const float *a_scale, *b_scale;
+  void* C;
+  int64_t ldc;
+  uint32_t* err;
+};
+
+// Four integers to two pairs of fp16: with the sign bit flipped a byte is x + 128, the low mantissa bits of
+// 1024 + that; 1152 taken away again is exact.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__half* p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = uint16_t(pack_bf16x2(v, v)); }
+
+template <int CG, class OUT>
+__global__ void __launch_bounds__(T8_THREADS, 1)
+    kd_gemm8_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_t,
+                    const T8Problem p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  T8Tail* tail = reinterpret_cast<T8Tail*>(smem + size_t(p.stages) * p.stage_bytes);
+  volatile uint32_t* abort_flag = &tail->abort_flag;
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  const uint32_t crank = CG == 2 ? cluster_ctarank() : 0u;
+  const int u_first = int(blockIdx.x) / CG, u_step = int(gridDim.x) / CG;
+  const int k_stages = (p.K + T8_K - 1) / T8_K;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->empty[s], 1);
+    }
+    for (int t = 0; t < p.wide_stages; ++t) {
+      mbar_init(&tail->wide[t], 4 * CG);  // a lane of each widening warp, of both CTAs
+      mbar_init(&tail->wfree[t], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tail->tfull[a], 1);
+      mbar_init(&tail->tempty[a], 4 * CG);
+    }
+    mbar_init(&tail->drain, 1);
+    tail->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&tmap_w);
+    tma_prefetch_map(&tmap_t);
+  }
+  if (warp == 1) {
+    if (CG == 2) tmem_alloc_pair(&tail->tmem_base, TMEM_COLS); else tmem_alloc(&tail->tmem_base, TMEM_COLS);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();  // the peer's barriers exist before any commit reaches them
+  tc_fence_after();
+  const uint32_t tmem_base = tail->tmem_base;
+  // tensor memory: the widened weights' stages, then two accumulators
+  const uint32_t acc_col = uint32_t(p.wide_stages) * 64u, acc_step = (512u - acc_col) / 2u;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      const int rows_t = p.tokens / CG;
+      for (int u = u_first; u < p.units && ok; u += u_step) {
+        const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
+        const int row = (wg * CG + int(crank)) * T8_ROWS, tok = tt * p.tokens + int(crank) * rows_t;
+        for (int kb = 0; kb < k_stages; ++kb, ++it) {
+          const uint32_t s = it % uint32_t(p.stages), ph = (it / uint32_t(p.stages)) & 1u;
+          if (!mbar_wait(&tail->empty[s], ph ^ 1u, abort_flag, p.err, 0x1100u)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sw = smem + size_t(s) * p.stage_bytes;
+          mbar_arrive_expect_tx(&tail->full[s], uint32_t(T8_W_BYTES + rows_t * 256));
+          tma_load_2d(sw, &tmap_w, &tail->full[s], kb * T8_K, row);
+          tma_load_3d(sw + T8_W_BYTES, &tmap_t, &tail->full[s], 0, tok, kb * 2);
+        }
+      }
+      if (!ok) {
+        // let the copies already issued land before the CTA can exit
+        const uint32_t n = uint32_t(p.stages), first = it > n ? it - n : 0;
+        for (uint32_t j = first; j < it; ++j) {
+          volatile uint32_t never = 0;
+          mbar_wait(&tail->full[j % n], (j / n) & 1u, &never, nullptr, 0);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && crank == 0) {
+      const uint32_t idesc = idesc_f16_f32(T8_ROWS * CG, uint32_t(p.tokens));
+      const uint32_t kblock_bytes = uint32_t(p.tokens / CG) * 128u;
+      uint32_t it = 0, acc_it = 0;
+      bool ok = true;
+      for (int u = u_first; u < p.units && ok; u += u_step, ++acc_it) {
+        const uint32_t a = acc_it & 1u, aph = (acc_it >> 1) & 1u;
+        if (!mbar_wait<CG == 2>(&tail->tempty[a], aph ^ 1u, abort_flag, p.err, 0x1200u)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc_col + a * acc_step;
+        for (int kb = 0; kb < k_stages; ++kb, ++it) {
+          const uint32_t s = it % uint32_t(p.stages);
+          const uint32_t t = it % uint32_t(p.wide_stages), tph = (it / uint32_t(p.wide_stages)) & 1u;
+          // both CTAs' weights are in tensor memory, so their tokens are in shared memory too
+          if (!mbar_wait<CG == 2>(&tail->wide[t], tph, abort_flag, p.err, 0x1300u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sb = smem_u32(smem + size_t(s) * p.stage_bytes + T8_W_BYTES);
+          const int steps = min(T8_K / 16, (p.K - kb * T8_K + 15) / 16);
+          for (int k = 0; k < steps; ++k) {
+            const uint64_t bd = sdesc_sw128(sb + uint32_t(k >> 2) * kblock_bytes + uint32_t(k & 3) * 32u, 16u);
+            umma_f16_ts<CG>(d_tmem, tmem_base + t * 64u + uint32_t(k) * 8u, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+          }
+          if (CG == 2) {
+            umma_commit_pair_mc(&tail->empty[s], 0x3);
+            umma_commit_pair_mc(&tail->wfree[t], 0x3);
+          } else {
+            umma_commit(&tail->empty[s]);
+            umma_commit(&tail->wfree[t]);
+          }
+        }
+        if (ok) {
+          if (CG == 2) umma_commit_pair_mc(&tail->tfull[a], 0x3); else umma_commit(&tail->tfull[a]);
+        }
+      }
+      // every MMA issued above has completed once this arrives
+      if (CG == 2) umma_commit_pair_mc(&tail->drain, 0x1); else umma_commit(&tail->drain);
+      volatile uint32_t never = 0;
+      mbar_wait(&tail->drain, 0, &never, p.err, 0x1400u);
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------------------ epilogue
+    // lanes are channels, columns tokens: a token's 32 channels go out as one coalesced store
+    const uint32_t quarter = warp & 3u;
+    uint32_t acc_it = 0;
+    for (int u = u_first; u < p.units; u += u_step, ++acc_it) {
+      const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
+      const int n = (wg * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
+      const int tok0 = tt * p.tokens, toks = min(p.tokens, p.M - tok0);
+      const uint32_t a = acc_it & 1u, aph = (acc_it >> 1) & 1u;
+      const float sb = n < p.N ? __ldg(p.b_scale + n) : 0.f;
+      const bool got = mbar_wait(&tail->tfull[a], aph, abort_flag, p.err, 0x1500u);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after();
+      const uint32_t t_acc = tmem_base + ((quarter * 32u) << 16) + acc_col + a * acc_step;
+      OUT* out = reinterpret_cast<OUT*>(p.C) + size_t(tok0) * size_t(p.ldc) + n;
+#pragma unroll 1
+      for (int c = 0; c < toks; c += 32) {
+        const float sa_lane = c + int(lane) < toks ? __ldg(p.a_scale + tok0 + c + lane) : 0.f;
+        uint32_t raw[32];
+        tmem_ld_32x32b_x32(t_acc + c, raw);
+        tmem_ld_wait();
+        if (c + 32 >= toks) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->tempty[a], 0));
+            else mbar_arrive(&tail->tempty[a]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          // (sum sa) sb, each product rounded once: the order that a plain form takes
+          const float sa = __shfl_sync(0xffffffffu, sa_lane, i);
+          const float v = __fmul_rn(__fmul_rn(__uint_as_float(raw[i]), sa), sb);
+          if (c + i < toks && n < p.N) store_out(out + size_t(c + i) * size_t(p.ldc), v);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ widening
+    // A thread takes a channel's 128 bytes of a stage (128-byte rows, 16-byte chunks swizzled by row) to 64
+    // columns of its lane in tensor memory, two consecutive k a column.
+    const uint32_t quarter = warp & 3u, row = quarter * 32u + lane;
+    const uint32_t t_lane = tmem_base + ((quarter * 32u) << 16);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = u_first; u < p.units && ok; u += u_step) {
+      for (int kb = 0; kb < k_stages; ++kb, ++it) {
+        const uint32_t s = it % uint32_t(p.stages), ph = (it / uint32_t(p.stages)) & 1u;
+        const uint32_t t = it % uint32_t(p.wide_stages), tph = (it / uint32_t(p.wide_stages)) & 1u;
+        const bool got = mbar_wait(&tail->full[s], ph, abort_flag, p.err, 0x1600u);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = smem + size_t(s) * p.stage_bytes + row * 128u;
+        uint32_t lo[32], hi[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + ((uint32_t(c) ^ (row & 7u)) * 16u));
+          uint32_t* d = (c < 4 ? lo : hi) + (c & 3) * 8;
+          widen4(v.x, d[0], d[1]);
+          widen4(v.y, d[2], d[3]);
+          widen4(v.z, d[4], d[5]);
+          widen4(v.w, d[6], d[7]);
+        }
+        const bool free = mbar_wait(&tail->wfree[t], tph ^ 1u, abort_flag, p.err, 0x1700u);
+        if (!__all_sync(0xffffffffu, free)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st_32x32b_x32(t_lane + t * 64u, lo);
+        tmem_st_32x32b_x32(t_lane + t * 64u + 32u, hi);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->wide[t], 0));
+          else mbar_arrive(&tail->wide[t]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();  // no commit or remote arrival of the peer can still target this CTA
+  tc_fence_after();
+  if (warp == 1) {
+    if (CG == 2) tmem_dealloc_pair(tmem_base, TMEM_COLS); else tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ operands ---
+// The tokens as fp16, rows of Kp (K to the next 64, zeros behind): small beside the weights, read by every
+// tile.  A thread takes 8 elements; rows that start unaligned are read byte by byte.
+__global__ void __launch_bounds__(256)
+    kd_int8_tokens_kernel(const int8_t* __restrict__ A, int64_t lda, int M, int K, int Kp, int aligned8,
+                          uint4* __restrict__ out) {
+  const int per_row = Kp / 8;
+  const int64_t total = int64_t(M) * per_row;
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t m = i / per_row;
+    const int k = int(i - m * per_row) * 8;
+    const int8_t* src = A + m * lda + k;
+    uint32_t w[2] = {0, 0};
+    if (aligned8 && k + 8 <= K) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k + j < K) w[j >> 2] |= uint32_t(uint8_t(src[j])) << (8 * (j & 3));
+    }
+    uint4 o;
+    widen4(w[0], o.x, o.y);
+    widen4(w[1], o.z, o.w);
+    out[i] = o;
+  }
+}
+
+// Weights whose rows do not start on 16-byte boundaries, copied to rows that do (K to the next 16).  A thread
+// makes 16 bytes from the two 4-byte-aligned words either side of each of its four.
+__global__ void __launch_bounds__(256)
+    kd_int8_rows_kernel(const int8_t* __restrict__ B, int64_t ldb, int64_t N, int K, int Kp, uint4* __restrict__ out) {
+  const int per_row = Kp / 16;
+  const int64_t total = N * per_row;
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t n = i / per_row;
+    const int k = int(i - n * per_row) * 16;
+    const int8_t* src = B + n * ldb + k;
+    const int left = K - k;  // elements of this row from k on
+    uint32_t o[4];
+    if (left >= 20) {
+      // the word behind the sixteenth element still lies in this row
+      const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(src) & 3u);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(src - off);
+      uint32_t v[5];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __ldg(w + j);
+      v[4] = off ? __ldg(w + 4) : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = __funnelshift_r(v[j], v[j + 1], off * 8u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[j] = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (j * 4 + b < left) o[j] |= uint32_t(uint8_t(src[j * 4 + b])) << (8 * b);
+      }
+    }
+    out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ------------------------------------------------------------------ quantisation ---
+// A block takes a row at a time: its largest magnitude, then the row again (from cache) as integers.  x / s
+// is correctly rounded to fp32 first; where that lands on a tie, the sign of what the division left over says
+// on which side the quotient lies, so that the integer is the exact quotient's nearest.  A row that holds a
+// NaN or an infinity has scale NaN and integers 0, a row of zeros scale 0.
+template <class T>
+__device__ __forceinline__ float q_load(const T* p);
+template <>
+__device__ __forceinline__ float q_load<float>(const float* p) { return __ldg(p); }
+template <>
+__device__ __forceinline__ float q_load<__half>(const __half* p) { return __half2float(__ldg(p)); }
+template <>
+__device__ __forceinline__ float q_load<uint16_t>(const uint16_t* p) {
+  return __uint_as_float(uint32_t(__ldg(p)) << 16);
+}
+
+__device__ __forceinline__ int quantized(float x, float s) {
+  const float v = __fdiv_rn(x, s);
+  float r = rintf(v);
+  if (fabsf(v - truncf(v)) == 0.5f) {
+    const float up = s < 1.f ? 16777216.f : 1.f;       // so that nothing below is rounded away
+    const float rest = fmaf(-v, s * up, x * up);       // exact: x - v s
+    if (rest != 0.f) r = rest > 0.f ? ceilf(v) : floorf(v);
+  }
+  return int(fminf(fmaxf(r, -127.f), 127.f));
+}
+
+constexpr int Q_THREADS = 256;
+
+template <class T>
+__global__ void __launch_bounds__(Q_THREADS)
+    kd_quantize_kernel(const T* __restrict__ x, int64_t N, int64_t d, int64_t ld, int8_t* __restrict__ q, int64_t ldq,
+                       float* __restrict__ scale) {
+  __shared__ float part[Q_THREADS / 32];
+  __shared__ int bad[Q_THREADS / 32];
+  for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
+    const T* row = x + n * ld;
+    float most = 0.f;
+    int odd = 0;
+    for (int64_t i = threadIdx.x; i < d; i += Q_THREADS) {
+      const float v = fabsf(q_load(row + i));
+      odd |= !(v < INFINITY);
+      most = fmaxf(most, v);
+    }
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    odd = __any_sync(0xffffffffu, odd);
+    if ((threadIdx.x & 31) == 0) {
+      part[threadIdx.x >> 5] = most;
+      bad[threadIdx.x >> 5] = odd;
+    }
+    __syncthreads();
+    for (int w = 0; w < Q_THREADS / 32; ++w) {
+      most = fmaxf(most, part[w]);
+      odd |= bad[w];
+    }
+    const float s = odd ? __int_as_float(0x7FC00000) : __fdiv_rn(most, 127.f);
+    if (threadIdx.x == 0) scale[n] = s;
+    for (int64_t i = threadIdx.x; i < d; i += Q_THREADS)
+      q[n * ldq + i] = s > 0.f ? int8_t(quantized(q_load(row + i), s)) : int8_t(0);
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ host side ---
+
+template <int CG, class OUT>
+cudaError_t launch_t8(const T8Problem& p, const CUtensorMap& tw, const CUtensorMap& tt, cudaStream_t s) {
+  static PerDevice<int> resident;  // clusters (CTAs) on the device at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(T8_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = T8_SMEM;
+  cfg.stream = s;
+  int most = 1;
+  const int rc = resident.get(dev, &most, [&](int, int* v) {
+    const cudaError_t r =
+        cudaFuncSetAttribute(kd_gemm8_kernel<CG, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T8_SMEM);
+    if (r != cudaSuccess) return int(r);
+    *v = gemm_max_grid() / CG;
+    if (CG == 2) {
+      cudaLaunchConfig_t q = cfg;
+      q.gridDim = dim3(unsigned(gemm_max_grid() / 2 * 2), 1, 1);
+      q.stream = nullptr;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kd_gemm8_kernel<CG, OUT>, &q) == cudaSuccess && n >= 1) *v = n;
+    }
+    return 0;
+  });
+  if (rc != 0) return rc > 0 ? cudaError_t(rc) : cudaErrorInvalidDevice;
+  cfg.gridDim = dim3(unsigned((p.units < most ? p.units : most) * CG), 1, 1);
+  e = cudaLaunchKernelEx(&cfg, kd_gemm8_kernel<CG, OUT>, tw, tt, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int CG>
+cudaError_t launch_t8_typed(int dtype, const T8Problem& p, const CUtensorMap& tw, const CUtensorMap& tt,
+                            cudaStream_t s) {
+  prof_before("kd_gemm8", s);
+  const cudaError_t e = dtype == KD_F32   ? launch_t8<CG, float>(p, tw, tt, s)
+                        : dtype == KD_F16 ? launch_t8<CG, __half>(p, tw, tt, s)
+                                          : launch_t8<CG, uint16_t>(p, tw, tt, s);
+  prof_after(s);
+  return e;
+}
+
+// Tokens up to which single CTAs compute a tile; a pair halves the loads of more.
+constexpr int T8_SINGLE = 64;
+
+struct I8Layout {
+  size_t tokens, weights, total;
+  int64_t Kp, Kw;
+};
+
+I8Layout int8_layout(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
+  I8Layout L{};
+  L.Kp = (K + 63) / 64 * 64;
+  L.Kw = (K + 15) / 16 * 16;
+  L.tokens = sizeof(Ctrl);
+  L.weights = align_up(L.tokens + size_t(M) * size_t(L.Kp) * 2, 256);
+  L.total = aligned_rows ? L.weights : align_up(L.weights + size_t(N) * size_t(L.Kw), 256);
+  return L;
+}
+
+unsigned blocks_for(int64_t work, int per_sm) {
+  const int64_t b = (work + 255) / 256, most = int64_t(per_sm) * gemm_max_grid();
+  return unsigned(b < 1 ? 1 : b < most ? b : most);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
+                             const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                             uint8_t* ws, uint32_t* err, cudaStream_t s) {
+  const bool rows16 = aligned(B, 16) && ldb % 16 == 0;
+  const I8Layout L = int8_layout(M, N, K, rows16);
+  uint4* tokens = reinterpret_cast<uint4*>(ws + L.tokens);
+  prof_before("kd_int8_tokens", s);
+  kd_int8_tokens_kernel<<<blocks_for(M * L.Kp / 8, 8), 256, 0, s>>>(A, lda, int(M), int(K), int(L.Kp),
+                                                                  aligned(A, 8) && lda % 8 == 0, tokens);
+  prof_after(s);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const void* weights = B;
+  uint64_t w_stride = uint64_t(ldb);
+  if (!rows16) {
+    prof_before("kd_int8_rows", s);
+    kd_int8_rows_kernel<<<blocks_for(N * (L.Kw / 16), 16), 256, 0, s>>>(B, ldb, N, int(K), int(L.Kw),
+                                                                       reinterpret_cast<uint4*>(ws + L.weights));
+    prof_after(s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    weights = ws + L.weights;
+    w_stride = uint64_t(L.Kw);
+  }
+
+  T8Problem p{};
+  p.M = int(M); p.N = int(N); p.K = int(K);
+  p.token_tiles = int((M + T8_MAX_TOKENS - 1) / T8_MAX_TOKENS);
+  const int64_t even = (M + p.token_tiles - 1) / p.token_tiles;  // tiles of nearly the same size
+  const int cg = even <= T8_SINGLE ? 1 : 2;
+  p.tokens = int((even + 16 * cg - 1) / (16 * cg) * (16 * cg));
+  p.wide_stages = p.tokens <= 128 ? 4 : 2;
+  p.stage_bytes = T8_W_BYTES + p.tokens / cg * 256;
+  p.stages = (T8_SMEM - 1024 - int(sizeof(T8Tail))) / p.stage_bytes;
+  if (p.stages > T8_MAX_STAGES) p.stages = T8_MAX_STAGES;
+  const int64_t channel_tiles = (N + T8_ROWS - 1) / T8_ROWS;
+  p.units = int((channel_tiles + cg - 1) / cg * p.token_tiles);
+  p.a_scale = a_scale; p.b_scale = b_scale;
+  p.C = C; p.ldc = ldc;
+  p.err = err;
+  alignas(64) CUtensorMap tw, tt;
+  if (!make_tmap_2d_u8(&tw, weights, uint64_t(K), uint64_t(N), w_stride, T8_K, T8_ROWS) ||
+      !make_tmap_mn2_bf16(&tt, tokens, uint64_t(L.Kp), uint64_t(M), uint64_t(L.Kp) * 2, uint32_t(p.tokens / cg)))
+    return cudaErrorInvalidValue;
+  return cg == 1 ? launch_t8_typed<1>(dtype, p, tw, tt, s) : launch_t8_typed<2>(dtype, p, tw, tt, s);
+}
+
+size_t gemm_int8_scratch(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
+  return int8_layout(M, N, K, aligned_rows).total;
+}
+
+cudaError_t launch_quantize_int8(const void* x, int dtype, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq,
+                                 float* scale, cudaStream_t s) {
+  const int64_t most = int64_t(8) * gemm_max_grid();
+  const unsigned grid = unsigned(N < most ? N : most);
+  prof_before("kd_quantize_int8", s);
+  if (dtype == KD_F32)
+    kd_quantize_kernel<<<grid, Q_THREADS, 0, s>>>(static_cast<const float*>(x), N, d, ld, q, ldq, scale);
+  else if (dtype == KD_F16)
+    kd_quantize_kernel<<<grid, Q_THREADS, 0, s>>>(static_cast<const __half*>(x), N, d, ld, q, ldq, scale);
+  else
+    kd_quantize_kernel<<<grid, Q_THREADS, 0, s>>>(static_cast<const uint16_t*>(x), N, d, ld, q, ldq, scale);
+  prof_after(s);
+  return cudaGetLastError();
+}
+
+}  // namespace kd

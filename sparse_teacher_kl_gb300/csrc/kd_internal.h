@@ -188,6 +188,8 @@ bool make_tmap_dz_blocked(CUtensorMap* map, const void* base, uint64_t rows, uin
 // of a K-major operand, or two column blocks of an MN-major one).
 bool make_tmap_mn2_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t row_stride_bytes,
                         uint32_t box_rows);
+bool make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
+                     uint32_t box_inner, uint32_t box_outer);
 bool make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                       uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 
@@ -292,6 +294,15 @@ cudaError_t launch_logits_kl(int mode, const void* z, int dtype, int64_t N, int6
 
 // loss = mean of kl over the valid rows, 0 if there are none.
 cudaError_t launch_masked_mean(const float* kl, const uint8_t* mask, int64_t N, float* loss, cudaStream_t s);
+
+// 8-bit integers (kd_int8.cu).  ws: gemm_int8_scratch bytes, its first 256 left alone; aligned_rows: the rows of
+// B start on 16-byte boundaries.
+size_t gemm_int8_scratch(int64_t M, int64_t N, int64_t K, bool aligned_rows);
+cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
+                             const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                             uint8_t* ws, uint32_t* err, cudaStream_t s);
+cudaError_t launch_quantize_int8(const void* x, int dtype, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq,
+                                 float* scale, cudaStream_t s);
 
 constexpr int KD_MAX_SPLITS = 8;
 
