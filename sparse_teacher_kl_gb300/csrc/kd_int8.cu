@@ -29,7 +29,10 @@ constexpr int T8_W_BYTES = T8_ROWS * T8_K;      // a stage's weights: 16 KB
 constexpr int T8_MAX_TOKENS = 192;
 constexpr int T8_MAX_STAGES = 10;
 constexpr int T8_MAX_WIDE = 4;                  // stages of widened weights in tensor memory, 64 columns each
-constexpr int T8_THREADS = 320;                 // TMA, MMA, 4 epilogue and 4 widening warps
+// Sets of 4 widening warps, taking stages in turn; at most as many as there are stages of widened weights, so
+// that a set never waits for a phase two ahead of the barrier's (parity cannot tell the two apart).
+constexpr int T8_SETS = 2;
+constexpr int T8_THREADS = 32 * (6 + 4 * T8_SETS);  // TMA, MMA, 4 epilogue warps, the widening ones
 constexpr int T8_SMEM = 224 * 1024;
 
 struct __align__(8) T8Tail {
@@ -64,6 +67,18 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = uint16_t(pack_bf16x2(v, v)); }
+
+// A place in a ring of `n` stages and the parity of its turn; by steps of at most n.
+struct Turn {
+  uint32_t at, parity;
+  __device__ __forceinline__ void step(uint32_t by, uint32_t n) {
+    at += by;
+    if (at >= n) {
+      at -= n;
+      parity ^= 1u;
+    }
+  }
+};
 
 template <int CG, class OUT>
 __global__ void __launch_bounds__(T8_THREADS, 1)
@@ -114,14 +129,15 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t it = 0;
+      Turn r{0, 0};
       bool ok = true;
       const int rows_t = p.tokens / CG;
       for (int u = u_first; u < p.units && ok; u += u_step) {
         const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
         const int row = (wg * CG + int(crank)) * T8_ROWS, tok = tt * p.tokens + int(crank) * rows_t;
-        for (int kb = 0; kb < k_stages; ++kb, ++it) {
-          const uint32_t s = it % uint32_t(p.stages), ph = (it / uint32_t(p.stages)) & 1u;
-          if (!mbar_wait(&tail->empty[s], ph ^ 1u, abort_flag, p.err, 0x1100u)) {
+        for (int kb = 0; kb < k_stages; ++kb, ++it, r.step(1, uint32_t(p.stages))) {
+          const uint32_t s = r.at;
+          if (!mbar_wait(&tail->empty[s], r.parity ^ 1u, abort_flag, p.err, 0x1100u)) {
             ok = false;
             break;
           }
@@ -144,36 +160,48 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && crank == 0) {
       const uint32_t idesc = idesc_f16_f32(T8_ROWS * CG, uint32_t(p.tokens));
-      const uint32_t kblock_bytes = uint32_t(p.tokens / CG) * 128u;
-      uint32_t it = 0, acc_it = 0;
+      // The tensor cores finish a step of 16 in 64 to 96 cycles (TN tokens), so the thread has few
+      // instructions for each: descriptors by adding to a ready one (the address field counts 16 bytes).
+      const uint64_t desc0 = sdesc_sw128(smem_u32(smem + T8_W_BYTES), 16u);
+      const uint64_t stage_step = uint64_t(uint32_t(p.stage_bytes) >> 4);
+      const uint64_t kblock = uint64_t((uint32_t(p.tokens / CG) * 128u) >> 4);
+      Turn r{0, 0}, w{0, 0};
+      uint32_t acc_it = 0;
       bool ok = true;
       for (int u = u_first; u < p.units && ok; u += u_step, ++acc_it) {
         const uint32_t a = acc_it & 1u, aph = (acc_it >> 1) & 1u;
         if (!mbar_wait<CG == 2>(&tail->tempty[a], aph ^ 1u, abort_flag, p.err, 0x1200u)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc_col + a * acc_step;
-        for (int kb = 0; kb < k_stages; ++kb, ++it) {
-          const uint32_t s = it % uint32_t(p.stages);
-          const uint32_t t = it % uint32_t(p.wide_stages), tph = (it / uint32_t(p.wide_stages)) & 1u;
+        for (int kb = 0; kb < k_stages; ++kb) {
           // both CTAs' weights are in tensor memory, so their tokens are in shared memory too
-          if (!mbar_wait<CG == 2>(&tail->wide[t], tph, abort_flag, p.err, 0x1300u)) {
+          if (!mbar_wait<CG == 2>(&tail->wide[w.at], w.parity, abort_flag, p.err, 0x1300u)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sb = smem_u32(smem + size_t(s) * p.stage_bytes + T8_W_BYTES);
-          const int steps = min(T8_K / 16, (p.K - kb * T8_K + 15) / 16);
-          for (int k = 0; k < steps; ++k) {
-            const uint64_t bd = sdesc_sw128(sb + uint32_t(k >> 2) * kblock_bytes + uint32_t(k & 3) * 32u, 16u);
-            umma_f16_ts<CG>(d_tmem, tmem_base + t * 64u + uint32_t(k) * 8u, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+          const uint64_t bd = desc0 + r.at * stage_step;
+          const uint32_t at = tmem_base + w.at * 64u;
+          const int steps = (p.K - kb * T8_K + 15) / 16;
+          if (steps >= T8_K / 16) {
+#pragma unroll
+            for (int k = 0; k < T8_K / 16; ++k)
+              umma_f16_ts<CG>(d_tmem, at + uint32_t(k) * 8u, bd + (k >> 2) * kblock + uint64_t((k & 3) * 2), idesc,
+                              (k != 0 || kb != 0) ? 1u : 0u);
+          } else {
+            for (int k = 0; k < steps; ++k)
+              umma_f16_ts<CG>(d_tmem, at + uint32_t(k) * 8u, bd + uint64_t(k >> 2) * kblock + uint64_t((k & 3) * 2),
+                              idesc, (kb | k) != 0 ? 1u : 0u);
           }
           if (CG == 2) {
-            umma_commit_pair_mc(&tail->empty[s], 0x3);
-            umma_commit_pair_mc(&tail->wfree[t], 0x3);
+            umma_commit_pair_mc(&tail->empty[r.at], 0x3);
+            umma_commit_pair_mc(&tail->wfree[w.at], 0x3);
           } else {
-            umma_commit(&tail->empty[s]);
-            umma_commit(&tail->wfree[t]);
+            umma_commit(&tail->empty[r.at]);
+            umma_commit(&tail->wfree[w.at]);
           }
+          r.step(1, uint32_t(p.stages));
+          w.step(1, uint32_t(p.wide_stages));
         }
         if (ok) {
           if (CG == 2) umma_commit_pair_mc(&tail->tfull[a], 0x3); else umma_commit(&tail->tfull[a]);
@@ -229,43 +257,36 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     // columns of its lane in tensor memory, two consecutive k a column.
     const uint32_t quarter = warp & 3u, row = quarter * 32u + lane;
     const uint32_t t_lane = tmem_base + ((quarter * 32u) << 16);
-    uint32_t it = 0;
-    bool ok = true;
-    for (int u = u_first; u < p.units && ok; u += u_step) {
-      for (int kb = 0; kb < k_stages; ++kb, ++it) {
-        const uint32_t s = it % uint32_t(p.stages), ph = (it / uint32_t(p.stages)) & 1u;
-        const uint32_t t = it % uint32_t(p.wide_stages), tph = (it / uint32_t(p.wide_stages)) & 1u;
-        const bool got = mbar_wait(&tail->full[s], ph, abort_flag, p.err, 0x1600u);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
-        const uint8_t* src = smem + size_t(s) * p.stage_bytes + row * 128u;
-        uint32_t lo[32], hi[32];
+    const uint32_t set = (warp - 6u) >> 2;
+    const uint32_t total = u_first < p.units ? uint32_t((p.units - 1 - u_first) / u_step + 1) * uint32_t(k_stages) : 0;
+    Turn r{set, 0}, w{set, 0};
+    for (uint32_t it = set; it < total;
+         it += T8_SETS, r.step(T8_SETS, uint32_t(p.stages)), w.step(T8_SETS, uint32_t(p.wide_stages))) {
+      const uint32_t s = r.at, t = w.at;
+      const bool got = mbar_wait(&tail->full[s], r.parity, abort_flag, p.err, 0x1600u);
+      if (!__all_sync(0xffffffffu, got)) break;
+      const uint8_t* src = smem + size_t(s) * p.stage_bytes + row * 128u;
+      uint32_t lo[32], hi[32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + ((uint32_t(c) ^ (row & 7u)) * 16u));
-          uint32_t* d = (c < 4 ? lo : hi) + (c & 3) * 8;
-          widen4(v.x, d[0], d[1]);
-          widen4(v.y, d[2], d[3]);
-          widen4(v.z, d[4], d[5]);
-          widen4(v.w, d[6], d[7]);
-        }
-        const bool free = mbar_wait(&tail->wfree[t], tph ^ 1u, abort_flag, p.err, 0x1700u);
-        if (!__all_sync(0xffffffffu, free)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        tmem_st_32x32b_x32(t_lane + t * 64u, lo);
-        tmem_st_32x32b_x32(t_lane + t * 64u + 32u, hi);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->wide[t], 0));
-          else mbar_arrive(&tail->wide[t]);
-        }
+      for (int c = 0; c < 8; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + ((uint32_t(c) ^ (row & 7u)) * 16u));
+        uint32_t* d = (c < 4 ? lo : hi) + (c & 3) * 8;
+        widen4(v.x, d[0], d[1]);
+        widen4(v.y, d[2], d[3]);
+        widen4(v.z, d[4], d[5]);
+        widen4(v.w, d[6], d[7]);
+      }
+      const bool free = mbar_wait(&tail->wfree[t], w.parity ^ 1u, abort_flag, p.err, 0x1700u);
+      if (!__all_sync(0xffffffffu, free)) break;
+      tc_fence_after();
+      tmem_st_32x32b_x32(t_lane + t * 64u, lo);
+      tmem_st_32x32b_x32(t_lane + t * 64u + 32u, hi);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->wide[t], 0));
+        else mbar_arrive(&tail->wide[t]);
       }
     }
   }
