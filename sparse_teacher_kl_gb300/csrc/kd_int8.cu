@@ -22,22 +22,33 @@ namespace {
 // ------------------------------------------------------------------ geometry ---
 // A tile is 128 channels (the MMA's M side, from tensor memory) by TN tokens (its N side, from shared
 // memory); a pair of CTAs computes 256 channels, each loading half of the tokens.  The reduction goes 128
-// deep a stage.
+// deep a stage.  Tensor memory's 512 columns: four stages of widened weights, which cover the way from an
+// MMA's end over the barriers to the next weights' arrival (about 1300 cycles; two stages left the tensor
+// cores waiting a third of the time), and one accumulator of up to 256 tokens, or two of up to 128.  One large
+// accumulator, whose draining the next tile waits for, beats two of 192: the thread that issues the MMAs
+// needs about 60 cycles for each, so short ones (96 cycles for 192 tokens) leave it none for its barriers.
 constexpr int T8_ROWS = 128;
 constexpr int T8_K = 128;
 constexpr int T8_W_BYTES = T8_ROWS * T8_K;      // a stage's weights: 16 KB
-constexpr int T8_MAX_TOKENS = 192;
+constexpr int T8_MAX_TOKENS = 256;
+constexpr int T8_TWO_ACC = 128;                 // tokens up to which there are two accumulators
+// Shared memory: two rings of stages, since a stage's weights are free as soon as they have been widened and its
+// tokens only when its MMAs are done.
 constexpr int T8_MAX_STAGES = 10;
-constexpr int T8_MAX_WIDE = 4;                  // stages of widened weights in tensor memory, 64 columns each
-// Sets of 4 widening warps, taking stages in turn; at most as many as there are stages of widened weights, so
-// that a set never waits for a phase two ahead of the barrier's (parity cannot tell the two apart).
+constexpr int T8_WIDE = 4;                      // stages of widened weights, 64 columns each
+constexpr int T8_ACC_COL = T8_WIDE * 64;
+// Sets of 4 widening warps, taking stages in turn; at most T8_WIDE, so that a set never waits for a phase two
+// ahead of the barrier's (parity cannot tell the two apart).
 constexpr int T8_SETS = 2;
-constexpr int T8_THREADS = 32 * (6 + 4 * T8_SETS);  // TMA, MMA, 4 epilogue warps, the widening ones
+constexpr int T8_EPI = 8;                       // epilogue warps, two to a quarter of the lanes
+// Warps: weights' and tokens' TMA (0, 2), MMA (1), none (3), epilogue, widening.
+constexpr int T8_THREADS = 32 * (4 + T8_EPI + 4 * T8_SETS);
 constexpr int T8_SMEM = 224 * 1024;
 
 struct __align__(8) T8Tail {
-  uint64_t full[T8_MAX_STAGES], empty[T8_MAX_STAGES];
-  uint64_t wide[T8_MAX_WIDE], wfree[T8_MAX_WIDE];
+  uint64_t wgot[T8_MAX_STAGES], wempty[T8_MAX_STAGES];  // weights
+  uint64_t tgot[T8_MAX_STAGES], tdone[T8_MAX_STAGES];   // tokens
+  uint64_t wide[T8_WIDE], wfree[T8_WIDE];
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem_base, abort_flag;
@@ -46,7 +57,7 @@ struct __align__(8) T8Tail {
 struct T8Problem {
   int M, N, K;
   int tokens;        // TN: tokens of a tile, a multiple of 16 (a pair's: of 32)
-  int token_tiles, units, stages, wide_stages, stage_bytes;
+  int token_tiles, units, w_stages, t_stages, t_bytes;
   const float *a_scale, *b_scale;
   void* C;
   int64_t ldc;
@@ -80,13 +91,25 @@ struct Turn {
   }
 };
 
+template <class OUT>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+  return pack_bf16x2(lo, hi);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_out<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 template <int CG, class OUT>
 __global__ void __launch_bounds__(T8_THREADS, 1)
     kd_gemm8_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_t,
                     const T8Problem p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  T8Tail* tail = reinterpret_cast<T8Tail*>(smem + size_t(p.stages) * p.stage_bytes);
+  uint8_t* smem_t = smem + size_t(p.w_stages) * T8_W_BYTES;
+  T8Tail* tail = reinterpret_cast<T8Tail*>(smem_t + size_t(p.t_stages) * p.t_bytes);
+  const uint32_t w_stages = uint32_t(p.w_stages), t_stages = uint32_t(p.t_stages);
   volatile uint32_t* abort_flag = &tail->abort_flag;
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t crank = CG == 2 ? cluster_ctarank() : 0u;
@@ -94,17 +117,21 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
   const int k_stages = (p.K + T8_K - 1) / T8_K;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&tail->full[s], 1);
-      mbar_init(&tail->empty[s], 1);
+    for (int s = 0; s < p.w_stages; ++s) {
+      mbar_init(&tail->wgot[s], 1);
+      mbar_init(&tail->wempty[s], 4);  // a lane of each warp of the set that widened them
     }
-    for (int t = 0; t < p.wide_stages; ++t) {
+    for (int s = 0; s < p.t_stages; ++s) {
+      mbar_init(&tail->tgot[s], 1);
+      mbar_init(&tail->tdone[s], 1);
+    }
+    for (int t = 0; t < T8_WIDE; ++t) {
       mbar_init(&tail->wide[t], 4 * CG);  // a lane of each widening warp, of both CTAs
       mbar_init(&tail->wfree[t], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tail->tfull[a], 1);
-      mbar_init(&tail->tempty[a], 4 * CG);
+      mbar_init(&tail->tempty[a], T8_EPI * CG);
     }
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
@@ -122,37 +149,42 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
   if (CG == 2) cluster_sync();  // the peer's barriers exist before any commit reaches them
   tc_fence_after();
   const uint32_t tmem_base = tail->tmem_base;
-  // tensor memory: the widened weights' stages, then two accumulators
-  const uint32_t acc_col = uint32_t(p.wide_stages) * 64u, acc_step = (512u - acc_col) / 2u;
+  const uint32_t accs = p.tokens <= T8_TWO_ACC ? 2u : 1u;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA producers
     if (lane == 0) {
+      const bool tokens = warp == 2;
+      const uint32_t stages = tokens ? t_stages : w_stages;
+      uint64_t* got = tokens ? tail->tgot : tail->wgot;
+      uint64_t* empty = tokens ? tail->tdone : tail->wempty;
+      const int rows_t = p.tokens / CG;
       uint32_t it = 0;
       Turn r{0, 0};
       bool ok = true;
-      const int rows_t = p.tokens / CG;
       for (int u = u_first; u < p.units && ok; u += u_step) {
         const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
         const int row = (wg * CG + int(crank)) * T8_ROWS, tok = tt * p.tokens + int(crank) * rows_t;
-        for (int kb = 0; kb < k_stages; ++kb, ++it, r.step(1, uint32_t(p.stages))) {
-          const uint32_t s = r.at;
-          if (!mbar_wait(&tail->empty[s], r.parity ^ 1u, abort_flag, p.err, 0x1100u)) {
+        for (int kb = 0; kb < k_stages; ++kb, ++it, r.step(1, stages)) {
+          if (!mbar_wait(&empty[r.at], r.parity ^ 1u, abort_flag, p.err, 0x1100u + warp)) {
             ok = false;
             break;
           }
-          uint8_t* sw = smem + size_t(s) * p.stage_bytes;
-          mbar_arrive_expect_tx(&tail->full[s], uint32_t(T8_W_BYTES + rows_t * 256));
-          tma_load_2d(sw, &tmap_w, &tail->full[s], kb * T8_K, row);
-          tma_load_3d(sw + T8_W_BYTES, &tmap_t, &tail->full[s], 0, tok, kb * 2);
+          if (tokens) {
+            mbar_arrive_expect_tx(&got[r.at], uint32_t(p.t_bytes));
+            tma_load_3d(smem_t + size_t(r.at) * p.t_bytes, &tmap_t, &got[r.at], 0, tok, kb * 2);
+          } else {
+            mbar_arrive_expect_tx(&got[r.at], uint32_t(T8_W_BYTES));
+            tma_load_2d(smem + size_t(r.at) * T8_W_BYTES, &tmap_w, &got[r.at], kb * T8_K, row);
+          }
         }
       }
       if (!ok) {
         // let the copies already issued land before the CTA can exit
-        const uint32_t n = uint32_t(p.stages), first = it > n ? it - n : 0;
+        const uint32_t first = it > stages ? it - stages : 0;
         for (uint32_t j = first; j < it; ++j) {
           volatile uint32_t never = 0;
-          mbar_wait(&tail->full[j % n], (j / n) & 1u, &never, nullptr, 0);
+          mbar_wait(&got[j % stages], (j / stages) & 1u, &never, nullptr, 0);
         }
       }
     }
@@ -162,17 +194,15 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       const uint32_t idesc = idesc_f16_f32(T8_ROWS * CG, uint32_t(p.tokens));
       // The tensor cores finish a step of 16 in 64 to 96 cycles (TN tokens), so the thread has few
       // instructions for each: descriptors by adding to a ready one (the address field counts 16 bytes).
-      const uint64_t desc0 = sdesc_sw128(smem_u32(smem + T8_W_BYTES), 16u);
-      const uint64_t stage_step = uint64_t(uint32_t(p.stage_bytes) >> 4);
+      const uint64_t desc0 = sdesc_sw128(smem_u32(smem_t), 16u);
+      const uint64_t stage_step = uint64_t(uint32_t(p.t_bytes) >> 4);
       const uint64_t kblock = uint64_t((uint32_t(p.tokens / CG) * 128u) >> 4);
-      Turn r{0, 0}, w{0, 0};
-      uint32_t acc_it = 0;
+      Turn r{0, 0}, w{0, 0}, acc{0, 0};
       bool ok = true;
-      for (int u = u_first; u < p.units && ok; u += u_step, ++acc_it) {
-        const uint32_t a = acc_it & 1u, aph = (acc_it >> 1) & 1u;
-        if (!mbar_wait<CG == 2>(&tail->tempty[a], aph ^ 1u, abort_flag, p.err, 0x1200u)) break;
+      for (int u = u_first; u < p.units && ok; u += u_step, acc.step(1, accs)) {
+        if (!mbar_wait<CG == 2>(&tail->tempty[acc.at], acc.parity ^ 1u, abort_flag, p.err, 0x1200u)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc_col + a * acc_step;
+        const uint32_t d_tmem = tmem_base + T8_ACC_COL + acc.at * T8_TWO_ACC;
         for (int kb = 0; kb < k_stages; ++kb) {
           // both CTAs' weights are in tensor memory, so their tokens are in shared memory too
           if (!mbar_wait<CG == 2>(&tail->wide[w.at], w.parity, abort_flag, p.err, 0x1300u)) {
@@ -194,17 +224,17 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
                               idesc, (kb | k) != 0 ? 1u : 0u);
           }
           if (CG == 2) {
-            umma_commit_pair_mc(&tail->empty[r.at], 0x3);
             umma_commit_pair_mc(&tail->wfree[w.at], 0x3);
+            umma_commit_pair_mc(&tail->tdone[r.at], 0x3);
           } else {
-            umma_commit(&tail->empty[r.at]);
             umma_commit(&tail->wfree[w.at]);
+            umma_commit(&tail->tdone[r.at]);
           }
-          r.step(1, uint32_t(p.stages));
-          w.step(1, uint32_t(p.wide_stages));
+          r.step(1, t_stages);
+          w.step(1, T8_WIDE);
         }
         if (ok) {
-          if (CG == 2) umma_commit_pair_mc(&tail->tfull[a], 0x3); else umma_commit(&tail->tfull[a]);
+          if (CG == 2) umma_commit_pair_mc(&tail->tfull[acc.at], 0x3); else umma_commit(&tail->tfull[acc.at]);
         }
       }
       // every MMA issued above has completed once this arrives
@@ -212,60 +242,102 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       volatile uint32_t never = 0;
       mbar_wait(&tail->drain, 0, &never, p.err, 0x1400u);
     }
-  } else if (warp < 6) {
+  } else if (warp >= 4 && warp < 4 + T8_EPI) {
     // ------------------------------------------------------------ epilogue
-    // lanes are channels, columns tokens: a token's 32 channels go out as one coalesced store
+    // lanes are channels, columns tokens: a token's 32 channels go out as one coalesced store.  A warp takes
+    // half of the tokens.
     const uint32_t quarter = warp & 3u;
-    uint32_t acc_it = 0;
-    for (int u = u_first; u < p.units; u += u_step, ++acc_it) {
+    const int half = int(warp - 4u) >> 2;
+    const int first = half == 0 ? 0 : (p.tokens / 2 + 15) / 16 * 16;
+    const int end = half == 0 ? (p.tokens / 2 + 15) / 16 * 16 : p.tokens;
+    Turn acc{0, 0};
+    for (int u = u_first; u < p.units; u += u_step, acc.step(1, accs)) {
       const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
       const int n = (wg * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
-      const int tok0 = tt * p.tokens, toks = min(p.tokens, p.M - tok0);
-      const uint32_t a = acc_it & 1u, aph = (acc_it >> 1) & 1u;
+      const int tok0 = tt * p.tokens + first, toks = min(end - first, p.M - tok0);  // <= 128, may be below 1
       const float sb = n < p.N ? __ldg(p.b_scale + n) : 0.f;
-      const bool got = mbar_wait(&tail->tfull[a], aph, abort_flag, p.err, 0x1500u);
+      const bool got = mbar_wait(&tail->tfull[acc.at], acc.parity, abort_flag, p.err, 0x1500u);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
-      const uint32_t t_acc = tmem_base + ((quarter * 32u) << 16) + acc_col + a * acc_step;
-      OUT* out = reinterpret_cast<OUT*>(p.C) + size_t(tok0) * size_t(p.ldc) + n;
-#pragma unroll 1
-      for (int c = 0; c < toks; c += 32) {
-        const float sa_lane = c + int(lane) < toks ? __ldg(p.a_scale + tok0 + c + lane) : 0.f;
-        uint32_t raw[32];
-        tmem_ld_32x32b_x32(t_acc + c, raw);
+      const uint32_t t_acc = tmem_base + ((quarter * 32u) << 16) + T8_ACC_COL + acc.at * T8_TWO_ACC + uint32_t(first);
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->tempty[acc.at], 0));
+          else mbar_arrive(&tail->tempty[acc.at]);
+        }
+      };
+      OUT* out = reinterpret_cast<OUT*>(p.C) + int64_t(tok0) * p.ldc + n;
+      // 16 tokens' values: (sum a_scale) b_scale, each product rounded once
+      auto values = [&](int c, float (&v)[16]) {
+        const float sa_lane = lane < 16u && c + int(lane) < toks ? __ldg(p.a_scale + tok0 + c + lane) : 0.f;
+        uint32_t raw[16];
+        tmem_ld_32x32b_x16(t_acc + c, raw);
         tmem_ld_wait();
-        if (c + 32 >= toks) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->tempty[a], 0));
-            else mbar_arrive(&tail->tempty[a]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[i] = __fmul_rn(__fmul_rn(__uint_as_float(raw[i]), __shfl_sync(0xffffffffu, sa_lane, i)), sb);
+      };
+      if (sizeof(OUT) == 2 && accs == 1) {
+        // the accumulator is waited for: all of it to registers, in the output's type, before any store
+        uint32_t packed[64];
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          if (c < toks) {
+            float v[16];
+            values(c, v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) packed[(c + i) / 2] = pack_out<OUT>(v[i], v[i + 1]);
           }
         }
+        release();
+        if (n < p.N) {
+          uint16_t* o = reinterpret_cast<uint16_t*>(out);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          // (sum sa) sb, each product rounded once: the order that a plain form takes
-          const float sa = __shfl_sync(0xffffffffu, sa_lane, i);
-          const float v = __fmul_rn(__fmul_rn(__uint_as_float(raw[i]), sa), sb);
-          if (c + i < toks && n < p.N) store_out(out + size_t(c + i) * size_t(p.ldc), v);
+          for (int c = 0; c < 128; c += 2) {
+            if (c < toks) o[0] = uint16_t(packed[c / 2] & 0xFFFFu);
+            if (c + 1 < toks) o[p.ldc] = uint16_t(packed[c / 2] >> 16);
+            o += 2 * p.ldc;
+          }
+        }
+      } else {
+        if (toks < 1) release();
+#pragma unroll 1
+        for (int c = 0; c < toks; c += 16) {
+          float v[16];
+          values(c, v);
+          if (c + 16 >= toks) release();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i < toks && n < p.N) store_out(out, v[i]);
+            out += p.ldc;
+          }
         }
       }
     }
-  } else {
+  } else if (warp >= 4 + T8_EPI) {
     // ------------------------------------------------------------ widening
     // A thread takes a channel's 128 bytes of a stage (128-byte rows, 16-byte chunks swizzled by row) to 64
     // columns of its lane in tensor memory, two consecutive k a column.
     const uint32_t quarter = warp & 3u, row = quarter * 32u + lane;
     const uint32_t t_lane = tmem_base + ((quarter * 32u) << 16);
-    const uint32_t set = (warp - 6u) >> 2;
+    const uint32_t set = (warp - 4u - T8_EPI) >> 2;
     const uint32_t total = u_first < p.units ? uint32_t((p.units - 1 - u_first) / u_step + 1) * uint32_t(k_stages) : 0;
-    Turn r{set, 0}, w{set, 0};
-    for (uint32_t it = set; it < total;
-         it += T8_SETS, r.step(T8_SETS, uint32_t(p.stages)), w.step(T8_SETS, uint32_t(p.wide_stages))) {
-      const uint32_t s = r.at, t = w.at;
-      const bool got = mbar_wait(&tail->full[s], r.parity, abort_flag, p.err, 0x1600u);
+    // a set's first stage may lie behind the ring's end: turns by steps, never by more than a ring
+    Turn r{0, 0}, b{0, 0}, w{0, 0};
+    auto step = [&](uint32_t n) {
+      for (uint32_t i = 0; i < n; ++i) {
+        r.step(1, w_stages);
+        b.step(1, t_stages);
+        w.step(1, T8_WIDE);
+      }
+    };
+    step(set);
+    for (uint32_t it = set; it < total; it += T8_SETS, step(T8_SETS)) {
+      const bool got = mbar_wait(&tail->wgot[r.at], r.parity, abort_flag, p.err, 0x1600u);
       if (!__all_sync(0xffffffffu, got)) break;
-      const uint8_t* src = smem + size_t(s) * p.stage_bytes + row * 128u;
+      const uint8_t* src = smem + size_t(r.at) * T8_W_BYTES + row * 128u;
       uint32_t lo[32], hi[32];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -276,17 +348,22 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
         widen4(v.z, d[4], d[5]);
         widen4(v.w, d[6], d[7]);
       }
-      const bool free = mbar_wait(&tail->wfree[t], w.parity ^ 1u, abort_flag, p.err, 0x1700u);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->wempty[r.at]);
+      const bool free = mbar_wait(&tail->wfree[w.at], w.parity ^ 1u, abort_flag, p.err, 0x1700u);
       if (!__all_sync(0xffffffffu, free)) break;
       tc_fence_after();
-      tmem_st_32x32b_x32(t_lane + t * 64u, lo);
-      tmem_st_32x32b_x32(t_lane + t * 64u + 32u, hi);
+      tmem_st_32x32b_x32(t_lane + w.at * 64u, lo);
+      tmem_st_32x32b_x32(t_lane + w.at * 64u + 32u, hi);
+      // the stage's tokens, so that the MMA thread needs no barrier of the other CTA's for them
+      const bool toks = mbar_wait(&tail->tgot[b.at], b.parity, abort_flag, p.err, 0x1800u);
       tmem_st_wait();
+      if (!__all_sync(0xffffffffu, toks)) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->wide[t], 0));
-        else mbar_arrive(&tail->wide[t]);
+        if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->wide[w.at], 0));
+        else mbar_arrive(&tail->wide[w.at]);
       }
     }
   }
@@ -532,10 +609,13 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
   const int64_t even = (M + p.token_tiles - 1) / p.token_tiles;  // tiles of nearly the same size
   const int cg = even <= T8_SINGLE ? 1 : 2;
   p.tokens = int((even + 16 * cg - 1) / (16 * cg) * (16 * cg));
-  p.wide_stages = p.tokens <= 128 ? 4 : 2;
-  p.stage_bytes = T8_W_BYTES + p.tokens / cg * 256;
-  p.stages = (T8_SMEM - 1024 - int(sizeof(T8Tail))) / p.stage_bytes;
-  if (p.stages > T8_MAX_STAGES) p.stages = T8_MAX_STAGES;
+  // tokens' stages first, up to what hides a load from L2, the rest to the weights
+  p.t_bytes = p.tokens / cg * 256;
+  const int room = T8_SMEM - 1024 - int(sizeof(T8Tail));
+  p.t_stages = room * 5 / 8 / p.t_bytes;
+  if (p.t_stages > 6) p.t_stages = 6;
+  p.w_stages = (room - p.t_stages * p.t_bytes) / T8_W_BYTES;
+  if (p.w_stages > T8_MAX_STAGES) p.w_stages = T8_MAX_STAGES;
   const int64_t channel_tiles = (N + T8_ROWS - 1) / T8_ROWS;
   p.units = int((channel_tiles + cg - 1) / cg * p.token_tiles);
   p.a_scale = a_scale; p.b_scale = b_scale;
