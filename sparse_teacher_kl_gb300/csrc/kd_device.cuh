@@ -89,15 +89,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same for a barrier that threads of the cluster's other CTAs arrive at.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// The same, with the thread suspended for up to `ns` until the phase completes: a role that waits long leaves
+// its scheduler's issue slots to the others.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
       : "memory");
   return ok != 0;
 }
@@ -106,14 +107,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 // after kWaitLimitNs of wall time, or as soon as another role of the CTA has
 // raised `abort_flag`; returns false in both cases (and raises the flag and the
 // workspace error word on a timeout).  Never spins without a bound.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
                                           uint32_t* err, uint32_t where, uint64_t limit_ns = kWaitLimitNs) {
-  auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-  if (done()) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (done()) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0u) {
       if (*abort_flag) return false;
       if (globaltimer_ns() - t0 > limit_ns) {
@@ -121,6 +120,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
         raise_error(err, KD_DEVERR_TIMEOUT, where);
         return false;
       }
+    }
+  }
+}
+
+// The same bounded wait, suspended: the abort flag and the clock are looked at after each of the tries.
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                                    uint32_t* err, uint32_t where, uint64_t limit_ns = kWaitLimitNs) {
+  constexpr uint32_t kTryNs = 100000;
+  if (mbar_try_wait_for(bar, parity, kTryNs)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait_for(bar, parity, kTryNs)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort_flag = 1u;
+      raise_error(err, KD_DEVERR_TIMEOUT, where);
+      return false;
     }
   }
 }
@@ -318,6 +334,13 @@ __device__ __forceinline__ uint32_t mapa_u32(const void* p, uint32_t rank) {
 
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The same for an MMA thread that waits there: what passes with the arrival lies in tensor memory, ordered by the
+// tcgen05 fences on both sides, so it need not wait for the thread's stores in flight, as a release at cluster
+// scope does (measured in the 8-bit product: 2000 cycles between two arrivals).
+__device__ __forceinline__ void mbar_arrive_remote_tc(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // TMA loads into this CTA's shared memory that complete bytes on a barrier of

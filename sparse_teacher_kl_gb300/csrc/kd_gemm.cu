@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
           }
         }
         tc_fence_before();
-        if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->tempty[a], 0));
+        if (CG == 2 && crank != 0) mbar_arrive_remote_tc(mapa_u32(&tail->tempty[a], 0));
         else mbar_arrive(&tail->tempty[a]);
         if (EPI == EPI_STORE && p.tile_max && ok && row < p.M) {
           p.tile_max[size_t(row) * p.ld_tile_max + nb] = uint16_t(pack_bf16x2(tmax, tmax) & 0xFFFFu);

@@ -43,15 +43,16 @@ constexpr int T8_SETS = 2;
 constexpr int T8_EPI = 8;                       // epilogue warps, two to a quarter of the lanes
 // Warps: weights' and tokens' TMA (0, 2), MMA (1), none (3), epilogue, widening.
 constexpr int T8_THREADS = 32 * (4 + T8_EPI + 4 * T8_SETS);
-constexpr int T8_SMEM = 224 * 1024;
+constexpr int T8_SMEM = 227 * 1024;
 
-struct __align__(8) T8Tail {
+struct __align__(16) T8Tail {
   uint64_t wgot[T8_MAX_STAGES], wempty[T8_MAX_STAGES];  // weights
   uint64_t tgot[T8_MAX_STAGES], tdone[T8_MAX_STAGES];   // tokens
   uint64_t wide[T8_WIDE], wfree[T8_WIDE];
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem_base, abort_flag;
+  float a_scale[T8_EPI][128];  // of each epilogue warp's tokens
 };
 
 struct T8Problem {
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
         const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
         const int row = (wg * CG + int(crank)) * T8_ROWS, tok = tt * p.tokens + int(crank) * rows_t;
         for (int kb = 0; kb < k_stages; ++kb, ++it, r.step(1, stages)) {
-          if (!mbar_wait(&empty[r.at], r.parity ^ 1u, abort_flag, p.err, 0x1100u + warp)) {
+          if (!mbar_wait_suspended(&empty[r.at], r.parity ^ 1u, abort_flag, p.err, 0x1100u + warp)) {
             ok = false;
             break;
           }
@@ -184,63 +185,71 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
         const uint32_t first = it > stages ? it - stages : 0;
         for (uint32_t j = first; j < it; ++j) {
           volatile uint32_t never = 0;
-          mbar_wait(&got[j % stages], (j / stages) & 1u, &never, nullptr, 0);
+          mbar_wait_suspended(&got[j % stages], (j / stages) & 1u, &never, nullptr, 0);
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && crank == 0) {
+    // The whole warp goes through the loop, so that what an MMA takes stays in uniform registers; one lane issues.
+    if (crank == 0) {
       const uint32_t idesc = idesc_f16_f32(T8_ROWS * CG, uint32_t(p.tokens));
-      // The tensor cores finish a step of 16 in 64 to 96 cycles (TN tokens), so the thread has few
-      // instructions for each: descriptors by adding to a ready one (the address field counts 16 bytes).
+      // descriptors by adding to a ready one (the address field counts 16 bytes)
       const uint64_t desc0 = sdesc_sw128(smem_u32(smem_t), 16u);
       const uint64_t stage_step = uint64_t(uint32_t(p.t_bytes) >> 4);
       const uint64_t kblock = uint64_t((uint32_t(p.tokens / CG) * 128u) >> 4);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
       Turn r{0, 0}, w{0, 0}, acc{0, 0};
       bool ok = true;
       for (int u = u_first; u < p.units && ok; u += u_step, acc.step(1, accs)) {
-        if (!mbar_wait<CG == 2>(&tail->tempty[acc.at], acc.parity ^ 1u, abort_flag, p.err, 0x1200u)) break;
+        bool go = mbar_wait_suspended(&tail->tempty[acc.at], acc.parity ^ 1u, abort_flag, p.err, 0x1200u);
+        if (!__all_sync(0xffffffffu, go)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + T8_ACC_COL + acc.at * T8_TWO_ACC;
+        const uint32_t d_tmem = tm + T8_ACC_COL + acc.at * T8_TWO_ACC;
         for (int kb = 0; kb < k_stages; ++kb) {
           // both CTAs' weights are in tensor memory, so their tokens are in shared memory too
-          if (!mbar_wait<CG == 2>(&tail->wide[w.at], w.parity, abort_flag, p.err, 0x1300u)) {
+          go = mbar_wait_suspended(&tail->wide[w.at], w.parity, abort_flag, p.err, 0x1300u);
+          if (!__all_sync(0xffffffffu, go)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t bd = desc0 + r.at * stage_step;
-          const uint32_t at = tmem_base + w.at * 64u;
+          const uint32_t at = tm + w.at * 64u;
           const int steps = (p.K - kb * T8_K + 15) / 16;
-          if (steps >= T8_K / 16) {
+          if (elect_one()) {
+            if (steps >= T8_K / 16) {
 #pragma unroll
-            for (int k = 0; k < T8_K / 16; ++k)
-              umma_f16_ts<CG>(d_tmem, at + uint32_t(k) * 8u, bd + (k >> 2) * kblock + uint64_t((k & 3) * 2), idesc,
-                              (k != 0 || kb != 0) ? 1u : 0u);
-          } else {
-            for (int k = 0; k < steps; ++k)
-              umma_f16_ts<CG>(d_tmem, at + uint32_t(k) * 8u, bd + uint64_t(k >> 2) * kblock + uint64_t((k & 3) * 2),
-                              idesc, (kb | k) != 0 ? 1u : 0u);
+              for (int k = 0; k < T8_K / 16; ++k)
+                umma_f16_ts<CG>(d_tmem, at + uint32_t(k) * 8u, bd + (k >> 2) * kblock + uint64_t((k & 3) * 2), idesc,
+                                (k != 0 || kb != 0) ? 1u : 0u);
+            } else {
+              for (int k = 0; k < steps; ++k)
+                umma_f16_ts<CG>(d_tmem, at + uint32_t(k) * 8u, bd + uint64_t(k >> 2) * kblock + uint64_t((k & 3) * 2),
+                                idesc, (kb | k) != 0 ? 1u : 0u);
+            }
+            if (CG == 2) {
+              umma_commit_pair_mc(&tail->wfree[w.at], 0x3);
+              umma_commit_pair_mc(&tail->tdone[r.at], 0x3);
+              if (kb == k_stages - 1) umma_commit_pair_mc(&tail->tfull[acc.at], 0x3);
+            } else {
+              umma_commit(&tail->wfree[w.at]);
+              umma_commit(&tail->tdone[r.at]);
+              if (kb == k_stages - 1) umma_commit(&tail->tfull[acc.at]);
+            }
           }
-          if (CG == 2) {
-            umma_commit_pair_mc(&tail->wfree[w.at], 0x3);
-            umma_commit_pair_mc(&tail->tdone[r.at], 0x3);
-          } else {
-            umma_commit(&tail->wfree[w.at]);
-            umma_commit(&tail->tdone[r.at]);
-          }
+          __syncwarp();
           r.step(1, t_stages);
           w.step(1, T8_WIDE);
         }
-        if (ok) {
-          if (CG == 2) umma_commit_pair_mc(&tail->tfull[acc.at], 0x3); else umma_commit(&tail->tfull[acc.at]);
-        }
       }
       // every MMA issued above has completed once this arrives
-      if (CG == 2) umma_commit_pair_mc(&tail->drain, 0x1); else umma_commit(&tail->drain);
+      if (elect_one()) {
+        if (CG == 2) umma_commit_pair_mc(&tail->drain, 0x1); else umma_commit(&tail->drain);
+      }
+      __syncwarp();
       volatile uint32_t never = 0;
-      mbar_wait(&tail->drain, 0, &never, p.err, 0x1400u);
+      mbar_wait_suspended(&tail->drain, 0, &never, p.err, 0x1400u);
     }
   } else if (warp >= 4 && warp < 4 + T8_EPI) {
     // ------------------------------------------------------------ epilogue
@@ -256,7 +265,13 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       const int n = (wg * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
       const int tok0 = tt * p.tokens + first, toks = min(end - first, p.M - tok0);  // <= 128, may be below 1
       const float sb = n < p.N ? __ldg(p.b_scale + n) : 0.f;
-      const bool got = mbar_wait(&tail->tfull[acc.at], acc.parity, abort_flag, p.err, 0x1500u);
+      float* sa = tail->a_scale[warp - 4u];
+      __syncwarp();  // the last tile's have been read
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        sa[32 * j + lane] = 32 * j + int(lane) < toks ? __ldg(p.a_scale + tok0 + 32 * j + lane) : 0.f;
+      __syncwarp();
+      const bool got = mbar_wait_suspended(&tail->tfull[acc.at], acc.parity, abort_flag, p.err, 0x1500u);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const uint32_t t_acc = tmem_base + ((quarter * 32u) << 16) + T8_ACC_COL + acc.at * T8_TWO_ACC + uint32_t(first);
@@ -264,20 +279,24 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->tempty[acc.at], 0));
+          if (CG == 2 && crank != 0) mbar_arrive_remote_tc(mapa_u32(&tail->tempty[acc.at], 0));
           else mbar_arrive(&tail->tempty[acc.at]);
         }
       };
       OUT* out = reinterpret_cast<OUT*>(p.C) + int64_t(tok0) * p.ldc + n;
       // 16 tokens' values: (sum a_scale) b_scale, each product rounded once
       auto values = [&](int c, float (&v)[16]) {
-        const float sa_lane = lane < 16u && c + int(lane) < toks ? __ldg(p.a_scale + tok0 + c + lane) : 0.f;
         uint32_t raw[16];
         tmem_ld_32x32b_x16(t_acc + c, raw);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[i] = __fmul_rn(__fmul_rn(__uint_as_float(raw[i]), __shfl_sync(0xffffffffu, sa_lane, i)), sb);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(sa + c + i);
+          v[i] = __fmul_rn(__fmul_rn(__uint_as_float(raw[i]), f.x), sb);
+          v[i + 1] = __fmul_rn(__fmul_rn(__uint_as_float(raw[i + 1]), f.y), sb);
+          v[i + 2] = __fmul_rn(__fmul_rn(__uint_as_float(raw[i + 2]), f.z), sb);
+          v[i + 3] = __fmul_rn(__fmul_rn(__uint_as_float(raw[i + 3]), f.w), sb);
+        }
       };
       if (sizeof(OUT) == 2 && accs == 1) {
         // the accumulator is waited for: all of it to registers, in the output's type, before any store
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     };
     step(set);
     for (uint32_t it = set; it < total; it += T8_SETS, step(T8_SETS)) {
-      const bool got = mbar_wait(&tail->wgot[r.at], r.parity, abort_flag, p.err, 0x1600u);
+      const bool got = mbar_wait_suspended(&tail->wgot[r.at], r.parity, abort_flag, p.err, 0x1600u);
       if (!__all_sync(0xffffffffu, got)) break;
       const uint8_t* src = smem + size_t(r.at) * T8_W_BYTES + row * 128u;
       uint32_t lo[32], hi[32];
@@ -350,19 +369,19 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->wempty[r.at]);
-      const bool free = mbar_wait(&tail->wfree[w.at], w.parity ^ 1u, abort_flag, p.err, 0x1700u);
+      const bool free = mbar_wait_suspended(&tail->wfree[w.at], w.parity ^ 1u, abort_flag, p.err, 0x1700u);
       if (!__all_sync(0xffffffffu, free)) break;
       tc_fence_after();
       tmem_st_32x32b_x32(t_lane + w.at * 64u, lo);
       tmem_st_32x32b_x32(t_lane + w.at * 64u + 32u, hi);
       // the stage's tokens, so that the MMA thread needs no barrier of the other CTA's for them
-      const bool toks = mbar_wait(&tail->tgot[b.at], b.parity, abort_flag, p.err, 0x1800u);
+      const bool toks = mbar_wait_suspended(&tail->tgot[b.at], b.parity, abort_flag, p.err, 0x1800u);
       tmem_st_wait();
       if (!__all_sync(0xffffffffu, toks)) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2 && crank != 0) mbar_arrive_remote(mapa_u32(&tail->wide[w.at], 0));
+        if (CG == 2 && crank != 0) mbar_arrive_remote_tc(mapa_u32(&tail->wide[w.at], 0));
         else mbar_arrive(&tail->wide[w.at]);
       }
     }
