@@ -12,6 +12,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "kd_device.cuh"
 #include "kd_internal.h"
 
@@ -396,6 +398,102 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------------ few tokens ---
+// Up to F8_TOKENS tokens: bound by reading the weights once, which the tensor cores' tiles do at 5.0 TB/s (an
+// MMA takes about 60 cycles however few tokens it has).  Here the lanes of a group walk a weight row's 16-byte
+// pieces with the tokens' integers in shared memory, four products an instruction into exact 32-bit sums.
+// A group is as wide as a row has pieces (32 lanes at most) and takes F8_ROWS rows at a time, so that each
+// piece of the tokens serves all of them and their loads are in flight together.  Rows may start anywhere: a
+// piece then comes from the two aligned ones that it lies in, shifted; the second is in L1, as the next lane's.
+constexpr int F8_THREADS = 256, F8_ROWS = 4, F8_PER_SM = 3;
+constexpr int F8_TOKENS = 4;
+constexpr int F8_MAX_SMEM = 64 * 1024;
+
+template <bool ANY>
+__device__ __forceinline__ uint4 load_piece(const int8_t* p, int left) {
+  // the piece's 16 bytes from p on, of which `left` >= 1 belong to the row (what follows meets zeros)
+  if (!ANY) return __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* a = reinterpret_cast<const uint4*>(p - off);
+  const uint4 x = __ldg(a);
+  uint4 y = make_uint4(0, 0, 0, 0);
+  if (off != 0 && int(16u - off) < left) y = __ldg(a + 1);
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t v[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    const uint32_t lo = (off & 4u) ? w[j + 1] : w[j];
+    const uint32_t hi = (off & 4u) ? w[j + 3 > 7 ? 7 : j + 3] : w[j + 2 > 7 ? 7 : j + 2];
+    v[j] = (off & 8u) ? hi : lo;
+  }
+  const uint32_t bits = (off & 3u) * 8u;
+  return make_uint4(__funnelshift_r(v[0], v[1], bits), __funnelshift_r(v[1], v[2], bits),
+                    __funnelshift_r(v[2], v[3], bits), __funnelshift_r(v[3], v[4], bits));
+}
+
+template <int MT, bool ANY, class OUT>
+__global__ void __launch_bounds__(F8_THREADS)
+    kd_gemm8_few_kernel(const int8_t* __restrict__ A, int64_t lda, const float* __restrict__ a_scale,
+                        const int8_t* __restrict__ B, int64_t ldb, const float* __restrict__ b_scale,
+                        OUT* __restrict__ C, int64_t ldc, int M, int64_t N, int K, int group) {
+  extern __shared__ uint4 tok[];  // [MT][pieces]: zeros behind K and behind the last token
+  const int pieces = (K + 15) / 16;
+  for (int i = threadIdx.x; i < MT * pieces * 16; i += F8_THREADS) {
+    const int m = i / (pieces * 16), k = i - m * pieces * 16;
+    reinterpret_cast<int8_t*>(tok)[i] = m < M && k < K ? A[m * lda + k] : int8_t(0);
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, at = lane & (group - 1);
+  const int groups = F8_THREADS / group;
+  const int64_t step = int64_t(gridDim.x) * groups * F8_ROWS;
+  for (int64_t n0 = (int64_t(blockIdx.x) * groups + threadIdx.x / group) * F8_ROWS; ; n0 += step) {
+    // a warp's groups leave together: their sums are exchanged below
+    if (!__any_sync(0xffffffffu, n0 < N)) break;
+    int acc[F8_ROWS][MT];
+#pragma unroll
+    for (int r = 0; r < F8_ROWS; ++r)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[r][m] = 0;
+    const int64_t last = N - 1;
+#pragma unroll 2
+    for (int c = at; c < pieces; c += group) {
+      uint4 w[F8_ROWS];
+#pragma unroll
+      for (int r = 0; r < F8_ROWS; ++r) {
+        const int64_t n = n0 + r < N ? n0 + r : last;  // rows behind the last: its own again, not stored
+        w[r] = load_piece<ANY>(B + n * ldb + c * 16, K - c * 16);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint4 t = tok[m * pieces + c];
+#pragma unroll
+        for (int r = 0; r < F8_ROWS; ++r) {
+          int s = acc[r][m];
+          s = __dp4a(int(w[r].x), int(t.x), s);
+          s = __dp4a(int(w[r].y), int(t.y), s);
+          s = __dp4a(int(w[r].z), int(t.z), s);
+          acc[r][m] = __dp4a(int(w[r].w), int(t.w), s);
+        }
+      }
+    }
+    for (int o = group >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < F8_ROWS; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[r][m] += __shfl_xor_sync(0xffffffffu, acc[r][m], o);
+    if (at == 0) {
+#pragma unroll
+      for (int r = 0; r < F8_ROWS; ++r) {
+        if (n0 + r >= N) break;
+        const float sb = __ldg(b_scale + n0 + r);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (m < M) store_out(C + m * ldc + n0 + r, __fmul_rn(__fmul_rn(float(acc[r][m]), __ldg(a_scale + m)), sb));
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ operands ---
 // The tokens as fp16, rows of Kp (K to the next 64, zeros behind): small beside the weights, read by every
 // tile.  A thread takes 8 elements; rows that start unaligned are read byte by byte.
@@ -461,22 +559,16 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ quantisation ---
-// A block takes a row at a time: its largest magnitude, then the row again (from cache) as integers.  x / s
-// is correctly rounded to fp32 first; where that lands on a tie, the sign of what the division left over says
-// on which side the quotient lies, so that the integer is the exact quotient's nearest.  A row that holds a
-// NaN or an infinity has scale NaN and integers 0, a row of zeros scale 0.
-template <class T>
-__device__ __forceinline__ float q_load(const T* p);
-template <>
-__device__ __forceinline__ float q_load<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float q_load<__half>(const __half* p) { return __half2float(__ldg(p)); }
-template <>
-__device__ __forceinline__ float q_load<uint16_t>(const uint16_t* p) {
-  return __uint_as_float(uint32_t(__ldg(p)) << 16);
-}
+// A row is shared by W warps of a block, each thread holding 32 elements (vectors of VE) in registers between the
+// two sweeps; what a longer row has beyond 1024 W is read twice.  Bound by HBM: an element read and a byte
+// written.  A row that holds a NaN or an infinity has scale NaN and integers 0, a row of zeros scale 0.
+//
+// x times the rounded 1 / s is within 2^-22 of the quotient, 127 at most: its nearest whole number is the
+// quotient's unless it lies within 1e-4 of a half.  Then x / s is rounded correctly to fp32, and where that lands
+// on a tie, the sign of what the division left over says on which side the quotient lies.
+constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23: whole numbers in the low bits of the sum
 
-__device__ __forceinline__ int quantized(float x, float s) {
+__device__ __noinline__ int quantized_near_half(float x, float s) {
   const float v = __fdiv_rn(x, s);
   float r = rintf(v);
   if (fabsf(v - truncf(v)) == 0.5f) {
@@ -487,40 +579,145 @@ __device__ __forceinline__ int quantized(float x, float s) {
   return int(fminf(fmaxf(r, -127.f), 127.f));
 }
 
-constexpr int Q_THREADS = 256;
+// inv 0: every element by division (a scale whose reciprocal fp32 does not hold).
+__device__ __forceinline__ uint32_t quantized(float x, float s, float inv) {
+  const float m = fmaf(x, inv, kRoundMagic);
+  const float off = fmaf(x, inv, kRoundMagic - m);
+  uint32_t q = __float_as_uint(m);
+  if (!(fabsf(off) < 0.4999f) || inv == 0.f) q = uint32_t(quantized_near_half(x, s));
+  return q & 0xFFu;
+}
 
-template <class T>
+template <class T, int VE>
+struct QVec {
+  uint32_t w[VE * sizeof(T) < 4 ? 1 : VE * sizeof(T) / 4];
+  __device__ __forceinline__ void load(const T* p) {
+    if (VE * sizeof(T) == 16) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if (sizeof(T) == 2) {
+      w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (uint32_t& x : w) x = 0;
+  }
+  __device__ __forceinline__ float get(int i) const;
+};
+template <class T, int VE>
+__device__ __forceinline__ float QVec<T, VE>::get(int i) const {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(w[i]);
+  } else {
+    const uint32_t h = (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+    if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(uint16_t(h)));
+    else return __uint_as_float(h << 16);
+  }
+}
+
+constexpr int Q_THREADS = 256, Q_EACH = 32;
+
+template <class T, int VE, int W>
 __global__ void __launch_bounds__(Q_THREADS)
     kd_quantize_kernel(const T* __restrict__ x, int64_t N, int64_t d, int64_t ld, int8_t* __restrict__ q, int64_t ldq,
                        float* __restrict__ scale) {
+  constexpr int NV = Q_EACH / VE, ROWS = Q_THREADS / 32 / W, LANES = 32 * W;
   __shared__ float part[Q_THREADS / 32];
-  __shared__ int bad[Q_THREADS / 32];
-  for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
-    const T* row = x + n * ld;
-    float most = 0.f;
-    int odd = 0;
-    for (int64_t i = threadIdx.x; i < d; i += Q_THREADS) {
-      const float v = fabsf(q_load(row + i));
-      odd |= !(v < INFINITY);
-      most = fmaxf(most, v);
+  const int warp = threadIdx.x >> 5, group = warp / W;
+  const int lane = threadIdx.x - group * LANES;
+  const int64_t nv = d / VE;  // VE > 1 only where it divides d
+  for (int64_t n0 = int64_t(blockIdx.x) * ROWS; n0 < N; n0 += int64_t(gridDim.x) * ROWS) {
+    const int64_t n = n0 + group;
+    const bool live = n < N;
+    const T* row = x + (live ? n : 0) * ld;
+    QVec<T, VE> v[NV];
+    // largest magnitude by its bits: infinities and NaNs lie above every number
+    uint32_t most = 0;
+    auto look = [&](const QVec<T, VE>& a) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) most = max(most, __float_as_uint(a.get(i)) & 0x7FFFFFFFu);
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t at = lane + j * LANES;
+      if (live && at < nv) v[j].load(row + at * VE); else v[j].zero();
     }
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    odd = __any_sync(0xffffffffu, odd);
-    if ((threadIdx.x & 31) == 0) {
-      part[threadIdx.x >> 5] = most;
-      bad[threadIdx.x >> 5] = odd;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) look(v[j]);
+    if (live) {
+      for (int64_t at = lane + NV * LANES; at < nv; at += LANES) {
+        QVec<T, VE> a;
+        a.load(row + at * VE);
+        look(a);
+      }
     }
-    __syncthreads();
-    for (int w = 0; w < Q_THREADS / 32; ++w) {
-      most = fmaxf(most, part[w]);
-      odd |= bad[w];
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (W > 1) {
+      __syncthreads();  // the last row's have been read
+      if ((threadIdx.x & 31) == 0) part[warp] = __uint_as_float(most);
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) most = max(most, __float_as_uint(part[group * W + w]));
     }
-    const float s = odd ? __int_as_float(0x7FC00000) : __fdiv_rn(most, 127.f);
-    if (threadIdx.x == 0) scale[n] = s;
-    for (int64_t i = threadIdx.x; i < d; i += Q_THREADS)
-      q[n * ldq + i] = s > 0.f ? int8_t(quantized(q_load(row + i), s)) : int8_t(0);
-    __syncthreads();
+    if (!live) continue;
+    const float s = most < 0x7F800000u ? __fdiv_rn(__uint_as_float(most), 127.f) : __int_as_float(0x7FC00000);
+    const float inv = s > 1e-37f ? 1.f / s : 0.f;
+    const bool none = !(s > 0.f);
+    if (lane == 0) scale[n] = s;
+    int8_t* out = q + n * ldq;
+    auto put = [&](const QVec<T, VE>& a, int64_t at) {
+      uint32_t o[VE / 4 > 0 ? VE / 4 : 1] = {};
+      if (!none) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) o[i / 4] |= quantized(a.get(i), s, inv) << (8 * (i & 3));
+      }
+      if constexpr (VE == 8) *reinterpret_cast<uint2*>(out + at * VE) = make_uint2(o[0], o[1]);
+      else if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(out + at * VE) = o[0];
+      else out[at] = int8_t(o[0]);
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t at = lane + j * LANES;
+      if (at < nv) put(v[j], at);
+    }
+    for (int64_t at = lane + NV * LANES; at < nv; at += LANES) {
+      QVec<T, VE> a;
+      a.load(row + at * VE);
+      put(a, at);
+    }
   }
+}
+
+template <class T, int VE, int W>
+cudaError_t launch_quantize_rows(const T* x, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq, float* scale,
+                                 cudaStream_t s) {
+  constexpr int ROWS = Q_THREADS / 32 / W;
+  const int64_t blocks = (N + ROWS - 1) / ROWS, most = int64_t(16) * gemm_max_grid();
+  kd_quantize_kernel<T, VE, W><<<unsigned(blocks < most ? blocks : most), Q_THREADS, 0, s>>>(x, N, d, ld, q, ldq, scale);
+  return cudaGetLastError();
+}
+
+// Warps to a row: as few as hold it in registers, so that short rows do not leave threads without work.
+template <class T, int VE>
+cudaError_t launch_quantize_width(const T* x, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq, float* scale,
+                                  cudaStream_t s) {
+  if (d <= 32 * Q_EACH) return launch_quantize_rows<T, VE, 1>(x, N, d, ld, q, ldq, scale, s);
+  if (d <= 64 * Q_EACH) return launch_quantize_rows<T, VE, 2>(x, N, d, ld, q, ldq, scale, s);
+  if (d <= 128 * Q_EACH) return launch_quantize_rows<T, VE, 4>(x, N, d, ld, q, ldq, scale, s);
+  return launch_quantize_rows<T, VE, 8>(x, N, d, ld, q, ldq, scale, s);
+}
+
+template <class T>
+cudaError_t launch_quantize_typed(const void* x, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq,
+                                  float* scale, cudaStream_t s) {
+  constexpr int VE = 16 / sizeof(T);
+  const T* p = static_cast<const T*>(x);
+  if (aligned(x, 16) && aligned(q, VE) && d % VE == 0 && (N == 1 || (ld % VE == 0 && ldq % VE == 0)))
+    return launch_quantize_width<T, VE>(p, N, d, ld, q, ldq, scale, s);
+  return launch_quantize_width<T, 1>(p, N, d, ld, q, ldq, scale, s);
 }
 
 // ------------------------------------------------------------------ host side ---
@@ -576,6 +773,12 @@ cudaError_t launch_t8_typed(int dtype, const T8Problem& p, const CUtensorMap& tw
 // Tokens up to which single CTAs compute a tile; a pair halves the loads of more.
 constexpr int T8_SINGLE = 64;
 
+// Whether the tokens are few, and fit into a block's shared memory.
+bool int8_few(int64_t M, int64_t K) {
+  const int64_t tokens = M <= 1 ? 1 : M <= 2 ? 2 : 4;
+  return M <= F8_TOKENS && tokens * ((K + 15) / 16 * 16) <= F8_MAX_SMEM;
+}
+
 struct I8Layout {
   size_t tokens, weights, total;
   int64_t Kp, Kw;
@@ -583,12 +786,48 @@ struct I8Layout {
 
 I8Layout int8_layout(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
   I8Layout L{};
+  L.total = sizeof(Ctrl);
+  if (int8_few(M, K)) return L;
   L.Kp = (K + 63) / 64 * 64;
   L.Kw = (K + 15) / 16 * 16;
   L.tokens = sizeof(Ctrl);
   L.weights = align_up(L.tokens + size_t(M) * size_t(L.Kp) * 2, 256);
   L.total = aligned_rows ? L.weights : align_up(L.weights + size_t(N) * size_t(L.Kw), 256);
   return L;
+}
+
+template <int MT, bool ANY, class OUT>
+cudaError_t launch_few(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
+                       const float* b_scale, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+  static PerDevice<int> attr_done;
+  const cudaError_t e = smem_attr_once(attr_done, reinterpret_cast<const void*>(kd_gemm8_few_kernel<MT, ANY, OUT>),
+                                       F8_MAX_SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t pieces = (K + 15) / 16;
+  int group = 32;
+  while (group > 1 && group / 2 >= pieces) group /= 2;
+  const int64_t per_block = int64_t(F8_THREADS / group) * F8_ROWS;
+  const int64_t blocks = (N + per_block - 1) / per_block, most = int64_t(F8_PER_SM) * gemm_max_grid();
+  kd_gemm8_few_kernel<MT, ANY, OUT><<<unsigned(blocks < most ? blocks : most), F8_THREADS, size_t(MT) * pieces * 16, s>>>(
+      A, lda, a_scale, B, ldb, b_scale, static_cast<OUT*>(C), ldc, int(M), N, int(K), group);
+  return cudaGetLastError();
+}
+
+template <int MT, bool ANY>
+cudaError_t launch_few_typed(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
+                             const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                             cudaStream_t s) {
+  if (dtype == KD_F32) return launch_few<MT, ANY, float>(A, lda, a_scale, B, ldb, b_scale, C, ldc, M, N, K, s);
+  if (dtype == KD_F16) return launch_few<MT, ANY, __half>(A, lda, a_scale, B, ldb, b_scale, C, ldc, M, N, K, s);
+  return launch_few<MT, ANY, uint16_t>(A, lda, a_scale, B, ldb, b_scale, C, ldc, M, N, K, s);
+}
+
+template <int MT>
+cudaError_t launch_few_any(bool rows16, const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B,
+                           int64_t ldb, const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N,
+                           int64_t K, cudaStream_t s) {
+  return rows16 ? launch_few_typed<MT, false>(A, lda, a_scale, B, ldb, b_scale, C, dtype, ldc, M, N, K, s)
+                : launch_few_typed<MT, true>(A, lda, a_scale, B, ldb, b_scale, C, dtype, ldc, M, N, K, s);
 }
 
 unsigned blocks_for(int64_t work, int per_sm) {
@@ -602,6 +841,15 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
                              const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N, int64_t K,
                              uint8_t* ws, uint32_t* err, cudaStream_t s) {
   const bool rows16 = aligned(B, 16) && ldb % 16 == 0;
+  if (int8_few(M, K)) {
+    prof_before("kd_gemm8_few", s);
+    const cudaError_t f =
+        M <= 1   ? launch_few_any<1>(rows16, A, lda, a_scale, B, ldb, b_scale, C, dtype, ldc, M, N, K, s)
+        : M <= 2 ? launch_few_any<2>(rows16, A, lda, a_scale, B, ldb, b_scale, C, dtype, ldc, M, N, K, s)
+                 : launch_few_any<4>(rows16, A, lda, a_scale, B, ldb, b_scale, C, dtype, ldc, M, N, K, s);
+    prof_after(s);
+    return f;
+  }
   const I8Layout L = int8_layout(M, N, K, rows16);
   uint4* tokens = reinterpret_cast<uint4*>(ws + L.tokens);
   prof_before("kd_int8_tokens", s);
@@ -653,17 +901,12 @@ size_t gemm_int8_scratch(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
 
 cudaError_t launch_quantize_int8(const void* x, int dtype, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq,
                                  float* scale, cudaStream_t s) {
-  const int64_t most = int64_t(8) * gemm_max_grid();
-  const unsigned grid = unsigned(N < most ? N : most);
   prof_before("kd_quantize_int8", s);
-  if (dtype == KD_F32)
-    kd_quantize_kernel<<<grid, Q_THREADS, 0, s>>>(static_cast<const float*>(x), N, d, ld, q, ldq, scale);
-  else if (dtype == KD_F16)
-    kd_quantize_kernel<<<grid, Q_THREADS, 0, s>>>(static_cast<const __half*>(x), N, d, ld, q, ldq, scale);
-  else
-    kd_quantize_kernel<<<grid, Q_THREADS, 0, s>>>(static_cast<const uint16_t*>(x), N, d, ld, q, ldq, scale);
+  const cudaError_t e = dtype == KD_F32   ? launch_quantize_typed<float>(x, N, d, ld, q, ldq, scale, s)
+                        : dtype == KD_F16 ? launch_quantize_typed<__half>(x, N, d, ld, q, ldq, scale, s)
+                                          : launch_quantize_typed<uint16_t>(x, N, d, ld, q, ldq, scale, s);
   prof_after(s);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace kd

@@ -49,7 +49,7 @@ def test_gemm_refuses_a_bad_workspace(lib):
         fits = int(at % 16 == 0 and ld % 16 == 0)
         need = lib.kd_gemm_int8_workspace(8, 100, 64, fits)
         assert gemm(lib, B=at, ldb=ld, wsb=need - 1) == _abi.KD_ERR_WORKSPACE
-    assert lib.kd_gemm_int8_workspace(8, 100, 64, 0) > lib.kd_gemm_int8_workspace(8, 100, 64, 1)
+    assert lib.kd_gemm_int8_workspace(80, 100, 64, 0) > lib.kd_gemm_int8_workspace(80, 100, 64, 1)
     for kw in (dict(ws=None), dict(ws=P + 64), dict(ctl=None), dict(ctl=P + 16)):
         assert gemm(lib, **kw) == _abi.KD_ERR_WORKSPACE
     assert lib.kd_gemm_int8_workspace(0, 100, 64, 1) == 0
