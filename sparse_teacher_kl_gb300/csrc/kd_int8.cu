@@ -34,8 +34,9 @@ constexpr int T8_K = 128;
 constexpr int T8_W_BYTES = T8_ROWS * T8_K;      // a stage's weights: 16 KB
 constexpr int T8_MAX_TOKENS = 256;
 constexpr int T8_TWO_ACC = 128;                 // tokens up to which there are two accumulators
+constexpr int T8_SHORT_K = 768;                 // K up to which no tile has more
 // Shared memory: two rings of stages, since a stage's weights are free as soon as they have been widened and its
-// tokens only when its MMAs are done.
+// tokens only when its MMAs are done: these go round with the widened weights, on one barrier.
 constexpr int T8_MAX_STAGES = 10;
 constexpr int T8_WIDE = 4;                      // stages of widened weights, 64 columns each
 constexpr int T8_ACC_COL = T8_WIDE * 64;
@@ -49,7 +50,7 @@ constexpr int T8_SMEM = 227 * 1024;
 
 struct __align__(16) T8Tail {
   uint64_t wgot[T8_MAX_STAGES], wempty[T8_MAX_STAGES];  // weights
-  uint64_t tgot[T8_MAX_STAGES], tdone[T8_MAX_STAGES];   // tokens
+  uint64_t tgot[T8_WIDE];                               // tokens; free with the weights widened for them
   uint64_t wide[T8_WIDE], wfree[T8_WIDE];
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
@@ -60,7 +61,7 @@ struct __align__(16) T8Tail {
 struct T8Problem {
   int M, N, K;
   int tokens;        // TN: tokens of a tile, a multiple of 16 (a pair's: of 32)
-  int token_tiles, units, w_stages, t_stages, t_bytes;
+  int token_tiles, units, w_stages, t_bytes;
   const float *a_scale, *b_scale;
   void* C;
   int64_t ldc;
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smem_t = smem + size_t(p.w_stages) * T8_W_BYTES;
-  T8Tail* tail = reinterpret_cast<T8Tail*>(smem_t + size_t(p.t_stages) * p.t_bytes);
-  const uint32_t w_stages = uint32_t(p.w_stages), t_stages = uint32_t(p.t_stages);
+  T8Tail* tail = reinterpret_cast<T8Tail*>(smem_t + size_t(T8_WIDE) * p.t_bytes);
+  const uint32_t w_stages = uint32_t(p.w_stages);
   volatile uint32_t* abort_flag = &tail->abort_flag;
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t crank = CG == 2 ? cluster_ctarank() : 0u;
@@ -124,11 +125,8 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       mbar_init(&tail->wgot[s], 1);
       mbar_init(&tail->wempty[s], 4);  // a lane of each warp of the set that widened them
     }
-    for (int s = 0; s < p.t_stages; ++s) {
-      mbar_init(&tail->tgot[s], 1);
-      mbar_init(&tail->tdone[s], 1);
-    }
     for (int t = 0; t < T8_WIDE; ++t) {
+      mbar_init(&tail->tgot[t], 1);
       mbar_init(&tail->wide[t], 4 * CG);  // a lane of each widening warp, of both CTAs
       mbar_init(&tail->wfree[t], 1);
     }
@@ -158,9 +156,9 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     // ------------------------------------------------------------ TMA producers
     if (lane == 0) {
       const bool tokens = warp == 2;
-      const uint32_t stages = tokens ? t_stages : w_stages;
+      const uint32_t stages = tokens ? uint32_t(T8_WIDE) : w_stages;
       uint64_t* got = tokens ? tail->tgot : tail->wgot;
-      uint64_t* empty = tokens ? tail->tdone : tail->wempty;
+      uint64_t* empty = tokens ? tail->wfree : tail->wempty;
       const int rows_t = p.tokens / CG;
       uint32_t it = 0;
       Turn r{0, 0};
@@ -201,7 +199,7 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       const uint64_t stage_step = uint64_t(uint32_t(p.t_bytes) >> 4);
       const uint64_t kblock = uint64_t((uint32_t(p.tokens / CG) * 128u) >> 4);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
-      Turn r{0, 0}, w{0, 0}, acc{0, 0};
+      Turn w{0, 0}, acc{0, 0};
       bool ok = true;
       for (int u = u_first; u < p.units && ok; u += u_step, acc.step(1, accs)) {
         bool go = mbar_wait_suspended(&tail->tempty[acc.at], acc.parity ^ 1u, abort_flag, p.err, 0x1200u);
@@ -216,7 +214,7 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint64_t bd = desc0 + r.at * stage_step;
+          const uint64_t bd = desc0 + w.at * stage_step;
           const uint32_t at = tm + w.at * 64u;
           const int steps = (p.K - kb * T8_K + 15) / 16;
           if (elect_one()) {
@@ -232,16 +230,13 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
             }
             if (CG == 2) {
               umma_commit_pair_mc(&tail->wfree[w.at], 0x3);
-              umma_commit_pair_mc(&tail->tdone[r.at], 0x3);
               if (kb == k_stages - 1) umma_commit_pair_mc(&tail->tfull[acc.at], 0x3);
             } else {
               umma_commit(&tail->wfree[w.at]);
-              umma_commit(&tail->tdone[r.at]);
               if (kb == k_stages - 1) umma_commit(&tail->tfull[acc.at]);
             }
           }
           __syncwarp();
-          r.step(1, t_stages);
           w.step(1, T8_WIDE);
         }
       }
@@ -261,18 +256,29 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     const int half = int(warp - 4u) >> 2;
     const int first = half == 0 ? 0 : (p.tokens / 2 + 15) / 16 * 16;
     const int end = half == 0 ? (p.tokens / 2 + 15) / 16 * 16 : p.tokens;
+    // a unit's scales are loaded while the one before is written out
+    float sb = 0.f, next_sb = 0.f, next_sa[4] = {};
+    auto load_scales = [&](int u) {
+      const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
+      const int n = (wg * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
+      const int tok0 = tt * p.tokens + first, toks = min(end - first, p.M - tok0);
+      next_sb = n < p.N ? __ldg(p.b_scale + n) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) next_sa[j] = 32 * j + int(lane) < toks ? __ldg(p.a_scale + tok0 + 32 * j + lane) : 0.f;
+    };
+    if (u_first < p.units) load_scales(u_first);
     Turn acc{0, 0};
     for (int u = u_first; u < p.units; u += u_step, acc.step(1, accs)) {
       const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
       const int n = (wg * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
       const int tok0 = tt * p.tokens + first, toks = min(end - first, p.M - tok0);  // <= 128, may be below 1
-      const float sb = n < p.N ? __ldg(p.b_scale + n) : 0.f;
       float* sa = tail->a_scale[warp - 4u];
-      __syncwarp();  // the last tile's have been read
+      __syncwarp();  // the last unit's have been read
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        sa[32 * j + lane] = 32 * j + int(lane) < toks ? __ldg(p.a_scale + tok0 + 32 * j + lane) : 0.f;
+      for (int j = 0; j < 4; ++j) sa[32 * j + lane] = next_sa[j];
+      sb = next_sb;
       __syncwarp();
+      if (u + u_step < p.units) load_scales(u + u_step);
       const bool got = mbar_wait_suspended(&tail->tfull[acc.at], acc.parity, abort_flag, p.err, 0x1500u);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
@@ -346,11 +352,10 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     const uint32_t set = (warp - 4u - T8_EPI) >> 2;
     const uint32_t total = u_first < p.units ? uint32_t((p.units - 1 - u_first) / u_step + 1) * uint32_t(k_stages) : 0;
     // a set's first stage may lie behind the ring's end: turns by steps, never by more than a ring
-    Turn r{0, 0}, b{0, 0}, w{0, 0};
+    Turn r{0, 0}, w{0, 0};
     auto step = [&](uint32_t n) {
       for (uint32_t i = 0; i < n; ++i) {
         r.step(1, w_stages);
-        b.step(1, t_stages);
         w.step(1, T8_WIDE);
       }
     };
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       tmem_st_32x32b_x32(t_lane + w.at * 64u, lo);
       tmem_st_32x32b_x32(t_lane + w.at * 64u + 32u, hi);
       // the stage's tokens, so that the MMA thread needs no barrier of the other CTA's for them
-      const bool toks = mbar_wait_suspended(&tail->tgot[b.at], b.parity, abort_flag, p.err, 0x1800u);
+      const bool toks = mbar_wait_suspended(&tail->tgot[w.at], w.parity, abort_flag, p.err, 0x1800u);
       tmem_st_wait();
       if (!__all_sync(0xffffffffu, toks)) break;
       tc_fence_before();
@@ -872,16 +877,16 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
 
   T8Problem p{};
   p.M = int(M); p.N = int(N); p.K = int(K);
-  p.token_tiles = int((M + T8_MAX_TOKENS - 1) / T8_MAX_TOKENS);
+  // Short reductions leave the draining of a large accumulator waited for too often.  us with at most 256 / 128
+  // tokens a tile: 2000 x 100000, K = 256 221 / 194, K = 512 234 / 222; 2000 x 50000, K = 1024 153 / 174, 1500
+  // 225 / 274.
+  const int most = K <= T8_SHORT_K ? T8_TWO_ACC : T8_MAX_TOKENS;
+  p.token_tiles = int((M + most - 1) / most);
   const int64_t even = (M + p.token_tiles - 1) / p.token_tiles;  // tiles of nearly the same size
   const int cg = even <= T8_SINGLE ? 1 : 2;
   p.tokens = int((even + 16 * cg - 1) / (16 * cg) * (16 * cg));
-  // tokens' stages first, up to what hides a load from L2, the rest to the weights
   p.t_bytes = p.tokens / cg * 256;
-  const int room = T8_SMEM - 1024 - int(sizeof(T8Tail));
-  p.t_stages = room * 5 / 8 / p.t_bytes;
-  if (p.t_stages > 6) p.t_stages = 6;
-  p.w_stages = (room - p.t_stages * p.t_bytes) / T8_W_BYTES;
+  p.w_stages = (T8_SMEM - 1024 - int(sizeof(T8Tail)) - T8_WIDE * p.t_bytes) / T8_W_BYTES;
   if (p.w_stages > T8_MAX_STAGES) p.w_stages = T8_MAX_STAGES;
   const int64_t channel_tiles = (N + T8_ROWS - 1) / T8_ROWS;
   p.units = int((channel_tiles + cg - 1) / cg * p.token_tiles);

@@ -58,7 +58,7 @@ int kd_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale, const int8_
   if (!ok_matrix(A, lda, a_scale, M, K) || !ok_matrix(B, ldb, b_scale, N, K)) return KD_ERR_INVALID_ARG;
   if (dtype != KD_BF16 && dtype != KD_F16 && dtype != KD_F32) return KD_ERR_INVALID_ARG;
   if (!C || !aligned(C, out_size(dtype)) || ldc < N) return KD_ERR_INVALID_ARG;
-  if (((N + 127) / 128) * ((M + 191) / 192) > kMaxInt) return KD_ERR_INVALID_ARG;
+  if (((N + 127) / 128) * ((M + 127) / 128) > kMaxInt) return KD_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256) || ws_bytes < gemm_int8_scratch(M, N, K, rows16(B, ldb)) || !control ||
       !aligned(control, 256))
     return KD_ERR_WORKSPACE;
