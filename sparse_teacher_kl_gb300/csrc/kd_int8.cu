@@ -37,12 +37,15 @@ constexpr int T8_TWO_ACC = 128;                 // tokens up to which there are 
 constexpr int T8_SHORT_K = 768;                 // K up to which no tile has more
 // Shared memory: two rings of stages, since a stage's weights are free as soon as they have been widened and its
 // tokens only when its MMAs are done: these go round with the widened weights, on one barrier.
-constexpr int T8_MAX_STAGES = 10;
+constexpr int T8_MAX_STAGES = 8;
 constexpr int T8_WIDE = 4;                      // stages of widened weights, 64 columns each
 constexpr int T8_ACC_COL = T8_WIDE * 64;
-// Sets of 4 widening warps, taking stages in turn; at most T8_WIDE, so that a set never waits for a phase two
-// ahead of the barrier's (parity cannot tell the two apart).
+// Sets of 4 widening warps, taking stages in turn (three or four leave the epilogue's and the MMA warp too few of
+// the schedulers' slots: 4096 x 2880 x 201088 2.69 ms with two, 2.73 and 2.94; 2000 x 256 x 100000 185 us, 299 and
+// 285).  The ring of weights is a multiple of the sets long, so that a place in it is always the same set's: a wait
+// by parity is only right for who has seen the barrier's last phase, and loads may land out of order.
 constexpr int T8_SETS = 2;
+static_assert(T8_MAX_STAGES % T8_SETS == 0, "places of the weights' ring belong to a set");
 constexpr int T8_EPI = 8;                       // epilogue warps, two to a quarter of the lanes
 // Warps: weights' and tokens' TMA (0, 2), MMA (1), none (3), epilogue, widening.
 constexpr int T8_THREADS = 32 * (4 + T8_EPI + 4 * T8_SETS);
@@ -57,6 +60,9 @@ struct __align__(16) T8Tail {
   uint32_t tmem_base, abort_flag;
   float a_scale[T8_EPI][128];  // of each epilogue warp's tokens
 };
+
+static_assert((T8_SMEM - 1024 - int(sizeof(T8Tail)) - T8_WIDE * (T8_MAX_TOKENS / 2 * 256)) / T8_W_BYTES >= T8_SETS,
+              "a place for every set beside the largest tiles' tokens");
 
 struct T8Problem {
   int M, N, K;
@@ -171,7 +177,11 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
             ok = false;
             break;
           }
-          if (tokens) {
+          if (tokens && CG == 2) {
+            // both CTAs' halves complete on the first CTA's barrier, where the MMAs wait
+            if (crank == 0) mbar_arrive_expect_tx(&got[r.at], 2u * uint32_t(p.t_bytes));
+            tma_load_3d_pair(smem_t + size_t(r.at) * p.t_bytes, &tmap_t, mapa_u32(&got[r.at], 0), 0, tok, kb * 2);
+          } else if (tokens) {
             mbar_arrive_expect_tx(&got[r.at], uint32_t(p.t_bytes));
             tma_load_3d(smem_t + size_t(r.at) * p.t_bytes, &tmap_t, &got[r.at], 0, tok, kb * 2);
           } else {
@@ -180,8 +190,8 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
           }
         }
       }
-      if (!ok) {
-        // let the copies already issued land before the CTA can exit
+      if (!ok && (CG == 1 || !tokens || crank == 0)) {
+        // let the copies already issued land before the CTA can exit (tokens: before the pair can)
         const uint32_t first = it > stages ? it - stages : 0;
         for (uint32_t j = first; j < it; ++j) {
           volatile uint32_t never = 0;
@@ -207,8 +217,8 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
         tc_fence_after();
         const uint32_t d_tmem = tm + T8_ACC_COL + acc.at * T8_TWO_ACC;
         for (int kb = 0; kb < k_stages; ++kb) {
-          // both CTAs' weights are in tensor memory, so their tokens are in shared memory too
-          go = mbar_wait_suspended(&tail->wide[w.at], w.parity, abort_flag, p.err, 0x1300u);
+          go = mbar_wait_suspended(&tail->tgot[w.at], w.parity, abort_flag, p.err, 0x1301u) &&
+               mbar_wait_suspended(&tail->wide[w.at], w.parity, abort_flag, p.err, 0x1300u);
           if (!__all_sync(0xffffffffu, go)) {
             ok = false;
             break;
@@ -307,24 +317,26 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
         }
       };
       if (sizeof(OUT) == 2 && accs == 1) {
-        // the accumulator is waited for: all of it to registers, in the output's type, before any store
-        uint32_t packed[64];
+        // the accumulator is waited for: it goes to registers, 64 tokens at a time in the output's type, and
+        // the last of them are stored when it has been given back
+        uint16_t* o = reinterpret_cast<uint16_t*>(out);
+#pragma unroll 1
+        for (int h = 0; h < 128; h += 64) {
+          uint32_t packed[32];
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          if (c < toks) {
-            float v[16];
-            values(c, v);
+          for (int c = 0; c < 64; c += 16) {
+            if (h + c < toks) {
+              float v[16];
+              values(h + c, v);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) packed[(c + i) / 2] = pack_out<OUT>(v[i], v[i + 1]);
+              for (int i = 0; i < 16; i += 2) packed[(c + i) / 2] = pack_out<OUT>(v[i], v[i + 1]);
+            }
           }
-        }
-        release();
-        if (n < p.N) {
-          uint16_t* o = reinterpret_cast<uint16_t*>(out);
+          if (h != 0) release();
 #pragma unroll
-          for (int c = 0; c < 128; c += 2) {
-            if (c < toks) o[0] = uint16_t(packed[c / 2] & 0xFFFFu);
-            if (c + 1 < toks) o[p.ldc] = uint16_t(packed[c / 2] >> 16);
+          for (int c = 0; c < 64; c += 2) {
+            if (h + c < toks && n < p.N) o[0] = uint16_t(packed[c / 2] & 0xFFFFu);
+            if (h + c + 1 < toks && n < p.N) o[p.ldc] = uint16_t(packed[c / 2] >> 16);
             o += 2 * p.ldc;
           }
         }
@@ -351,46 +363,40 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     const uint32_t t_lane = tmem_base + ((quarter * 32u) << 16);
     const uint32_t set = (warp - 4u - T8_EPI) >> 2;
     const uint32_t total = u_first < p.units ? uint32_t((p.units - 1 - u_first) / u_step + 1) * uint32_t(k_stages) : 0;
-    // a set's first stage may lie behind the ring's end: turns by steps, never by more than a ring
-    Turn r{0, 0}, w{0, 0};
-    auto step = [&](uint32_t n) {
-      for (uint32_t i = 0; i < n; ++i) {
-        r.step(1, w_stages);
-        w.step(1, T8_WIDE);
-      }
-    };
-    step(set);
-    for (uint32_t it = set; it < total; it += T8_SETS, step(T8_SETS)) {
-      const bool got = mbar_wait_suspended(&tail->wgot[r.at], r.parity, abort_flag, p.err, 0x1600u);
-      if (!__all_sync(0xffffffffu, got)) break;
+    Turn r{set, 0}, w{set, 0};
+    for (uint32_t it = set; it < total; it += T8_SETS) {
+      bool go = mbar_wait_suspended(&tail->wgot[r.at], r.parity, abort_flag, p.err, 0x1600u);
+      if (!__all_sync(0xffffffffu, go)) break;
       const uint8_t* src = smem + size_t(r.at) * T8_W_BYTES + row * 128u;
-      uint32_t lo[32], hi[32];
+      uint4 v[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src + ((uint32_t(c) ^ (row & 7u)) * 16u));
-        uint32_t* d = (c < 4 ? lo : hi) + (c & 3) * 8;
-        widen4(v.x, d[0], d[1]);
-        widen4(v.y, d[2], d[3]);
-        widen4(v.z, d[4], d[5]);
-        widen4(v.w, d[6], d[7]);
-      }
+      for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(src + ((uint32_t(c) ^ (row & 7u)) * 16u));
       __syncwarp();
       if (lane == 0) mbar_arrive(&tail->wempty[r.at]);
-      const bool free = mbar_wait_suspended(&tail->wfree[w.at], w.parity ^ 1u, abort_flag, p.err, 0x1700u);
-      if (!__all_sync(0xffffffffu, free)) break;
+      go = mbar_wait_suspended(&tail->wfree[w.at], w.parity ^ 1u, abort_flag, p.err, 0x1700u);
+      if (!__all_sync(0xffffffffu, go)) break;
       tc_fence_after();
-      tmem_st_32x32b_x32(t_lane + w.at * 64u, lo);
-      tmem_st_32x32b_x32(t_lane + w.at * 64u + 32u, hi);
-      // the stage's tokens, so that the MMA thread needs no barrier of the other CTA's for them
-      const bool toks = mbar_wait_suspended(&tail->tgot[w.at], w.parity, abort_flag, p.err, 0x1800u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t d[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          widen4(v[h * 4 + c].x, d[c * 8], d[c * 8 + 1]);
+          widen4(v[h * 4 + c].y, d[c * 8 + 2], d[c * 8 + 3]);
+          widen4(v[h * 4 + c].z, d[c * 8 + 4], d[c * 8 + 5]);
+          widen4(v[h * 4 + c].w, d[c * 8 + 6], d[c * 8 + 7]);
+        }
+        tmem_st_32x32b_x32(t_lane + w.at * 64u + uint32_t(h) * 32u, d);
+      }
       tmem_st_wait();
-      if (!__all_sync(0xffffffffu, toks)) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (CG == 2 && crank != 0) mbar_arrive_remote_tc(mapa_u32(&tail->wide[w.at], 0));
         else mbar_arrive(&tail->wide[w.at]);
       }
+      w.step(T8_SETS, T8_WIDE);
+      r.step(T8_SETS, w_stages);
     }
   }
 
@@ -886,7 +892,7 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
   const int cg = even <= T8_SINGLE ? 1 : 2;
   p.tokens = int((even + 16 * cg - 1) / (16 * cg) * (16 * cg));
   p.t_bytes = p.tokens / cg * 256;
-  p.w_stages = (T8_SMEM - 1024 - int(sizeof(T8Tail)) - T8_WIDE * p.t_bytes) / T8_W_BYTES;
+  p.w_stages = (T8_SMEM - 1024 - int(sizeof(T8Tail)) - T8_WIDE * p.t_bytes) / T8_W_BYTES / T8_SETS * T8_SETS;
   if (p.w_stages > T8_MAX_STAGES) p.w_stages = T8_MAX_STAGES;
   const int64_t channel_tiles = (N + T8_ROWS - 1) / T8_ROWS;
   p.units = int((channel_tiles + cg - 1) / cg * p.token_tiles);
