@@ -410,15 +410,26 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
 }
 
 // ------------------------------------------------------------------ few tokens ---
-// Up to F8_TOKENS tokens: bound by reading the weights once, which the tensor cores' tiles do at 5.0 TB/s (an
-// MMA takes about 60 cycles however few tokens it has).  Here the lanes of a group walk a weight row's 16-byte
+// Up to F8_TOKENS tokens: bound by reading the weights once.  The lanes of a group walk a weight row's 16-byte
 // pieces with the tokens' integers in shared memory, four products an instruction into exact 32-bit sums.
-// A group is as wide as a row has pieces (32 lanes at most) and takes F8_ROWS rows at a time, so that each
+// A group is as wide as a row has pieces (32 lanes at most) and takes some rows at a time, so that each
 // piece of the tokens serves all of them and their loads are in flight together.  Rows may start anywhere: a
 // piece then comes from the two aligned ones that it lies in, shifted; the second is in L1, as the next lane's.
-constexpr int F8_THREADS = 256, F8_ROWS = 4, F8_PER_SM = 3;
+// Rows at a time, blocks on an SM and pieces in flight by measurement (us, 2880 x 201088, rows / blocks / pieces):
+//   one token             8/3/1 91 (6.4 TB/s), 4/3/2 112, 4/4/2 100, 4/2/4 101, 2/4/4 100; 8/2/2 129
+//   one, rows anywhere    2/4/4 109, 4/4/2 122, 8/3/1 136, 4/3/2 149, 4/2/4 184
+//   four                  4/3/2 115, 4/2/4 129, 4/4/2 160, 8/3/1 190
+//   four, rows anywhere   4/2/4 164, 8/3/1 178, 4/4/2 194, 2/4/4 205, 4/3/2 240
+constexpr int F8_THREADS = 256;
 constexpr int F8_TOKENS = 4;
 constexpr int F8_MAX_SMEM = 64 * 1024;
+
+template <int MT, bool ANY>
+struct Few {
+  static constexpr int kRows = MT == 1 ? (ANY ? 2 : 8) : 4;
+  static constexpr int kPerSm = MT == 1 ? (ANY ? 4 : 3) : (ANY ? 2 : 3);
+  static constexpr int kUnroll = MT == 1 ? (ANY ? 4 : 1) : (ANY ? 4 : 2);
+};
 
 template <bool ANY>
 __device__ __forceinline__ uint4 load_piece(const int8_t* p, int left) {
@@ -454,6 +465,7 @@ __global__ void __launch_bounds__(F8_THREADS)
     reinterpret_cast<int8_t*>(tok)[i] = m < M && k < K ? A[m * lda + k] : int8_t(0);
   }
   __syncthreads();
+  constexpr int F8_ROWS = Few<MT, ANY>::kRows;
   const int lane = threadIdx.x & 31, at = lane & (group - 1);
   const int groups = F8_THREADS / group;
   const int64_t step = int64_t(gridDim.x) * groups * F8_ROWS;
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(F8_THREADS)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[r][m] = 0;
     const int64_t last = N - 1;
-#pragma unroll 2
+#pragma unroll (Few<MT, ANY>::kUnroll)
     for (int c = at; c < pieces; c += group) {
       uint4 w[F8_ROWS];
 #pragma unroll
@@ -784,10 +796,15 @@ cudaError_t launch_t8_typed(int dtype, const T8Problem& p, const CUtensorMap& tw
 // Tokens up to which single CTAs compute a tile; a pair halves the loads of more.
 constexpr int T8_SINGLE = 64;
 
-// Whether the tokens are few, and fit into a block's shared memory.
-bool int8_few(int64_t M, int64_t K) {
-  const int64_t tokens = M <= 1 ? 1 : M <= 2 ? 2 : 4;
-  return M <= F8_TOKENS && tokens * ((K + 15) / 16 * 16) <= F8_MAX_SMEM;
+// Whether the tokens are few, and fit into a block's shared memory.  One always; up to F8_TOKENS where the tensor
+// cores' way would copy the weights to aligned rows first (four tokens, 2880 x 201088: 164 us against 287), or
+// where the weights are few, so that its longer start counts (four tokens, this / that: 2880 x 4096 9 / 13 us,
+// 2880 x 16000 17 / 13, 2880 x 201088 115 / 97).
+constexpr int64_t F8_WEIGHTS = 24000000;
+
+bool int8_few(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
+  if (M > F8_TOKENS || (M > 1 && aligned_rows && N * K > F8_WEIGHTS)) return false;
+  return (M <= 1 ? 1 : M <= 2 ? 2 : 4) * ((K + 15) / 16 * 16) <= F8_MAX_SMEM;
 }
 
 struct I8Layout {
@@ -798,7 +815,7 @@ struct I8Layout {
 I8Layout int8_layout(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
   I8Layout L{};
   L.total = sizeof(Ctrl);
-  if (int8_few(M, K)) return L;
+  if (int8_few(M, N, K, aligned_rows)) return L;
   L.Kp = (K + 63) / 64 * 64;
   L.Kw = (K + 15) / 16 * 16;
   L.tokens = sizeof(Ctrl);
@@ -817,8 +834,8 @@ cudaError_t launch_few(const int8_t* A, int64_t lda, const float* a_scale, const
   const int64_t pieces = (K + 15) / 16;
   int group = 32;
   while (group > 1 && group / 2 >= pieces) group /= 2;
-  const int64_t per_block = int64_t(F8_THREADS / group) * F8_ROWS;
-  const int64_t blocks = (N + per_block - 1) / per_block, most = int64_t(F8_PER_SM) * gemm_max_grid();
+  const int64_t per_block = int64_t(F8_THREADS / group) * Few<MT, ANY>::kRows;
+  const int64_t blocks = (N + per_block - 1) / per_block, most = int64_t(Few<MT, ANY>::kPerSm) * gemm_max_grid();
   kd_gemm8_few_kernel<MT, ANY, OUT><<<unsigned(blocks < most ? blocks : most), F8_THREADS, size_t(MT) * pieces * 16, s>>>(
       A, lda, a_scale, B, ldb, b_scale, static_cast<OUT*>(C), ldc, int(M), N, int(K), group);
   return cudaGetLastError();
@@ -852,7 +869,7 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
                              const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N, int64_t K,
                              uint8_t* ws, uint32_t* err, cudaStream_t s) {
   const bool rows16 = aligned(B, 16) && ldb % 16 == 0;
-  if (int8_few(M, K)) {
+  if (int8_few(M, N, K, rows16)) {
     prof_before("kd_gemm8_few", s);
     const cudaError_t f =
         M <= 1   ? launch_few_any<1>(rows16, A, lda, a_scale, B, ldb, b_scale, C, dtype, ldc, M, N, K, s)
