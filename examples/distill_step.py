@@ -52,8 +52,8 @@ def dense_loss(student, x, labels, ids, vals, lse):
 
 def fused_loss(student, x, labels, ids, vals, lse):
     H, W = student.hidden(x).contiguous(), student.weight().contiguous()
-    logp, _ = kd.fused_logprobs(H, W, labels, chunk=CHUNK)
-    return ALPHA * kd.fused_kl(H, W, ids, vals, chunk=CHUNK) - (1 - ALPHA) * logp.mean()
+    hard = kd.fused_cross_entropy(H, W, labels, chunk=CHUNK)
+    return ALPHA * kd.fused_kl(H, W, ids, vals, chunk=CHUNK) + (1 - ALPHA) * hard
 
 
 def train(loss_of, data, steps):

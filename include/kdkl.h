@@ -463,7 +463,7 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
  *            all) is not 0; only those are projected, the hidden states of the others are not read.
  *            A valid position's label outside [0, V) is recorded in the error word with its position;
  *            its loss is NaN, its gradient left out.
- *   0 <= label_smoothing < 1; z_loss >= 0; softcap > 0, or 0 for none.
+ *   0 <= label_smoothing < 1; z_loss >= 0; softcap >= 1e-6, or 0 for none.
  *   loss_out: device fp32 scalar.  lse_out, loss_per_token_out: [N] fp32 (the latter may be NULL), 0 for
  *            positions that are not valid.
  * kd_fused_cross_entropy_step returns the gradients with the loss, for a grad_loss (device fp32 scalar,

@@ -69,6 +69,18 @@ def _stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _on_its_device(f):
+    """f with its first tensor's device made the current one, where it is another."""
+    @functools.wraps(f)
+    def call(*args, **kw):
+        t = args[0] if args else next((v for v in kw.values() if isinstance(v, torch.Tensor)), None)
+        if t is None or not t.is_cuda or torch.cuda.current_device() == t.device.index:
+            return f(*args, **kw)
+        with torch.cuda.device(t.device):
+            return f(*args, **kw)
+    return call
+
+
 def workspace(nbytes: int, device) -> torch.Tensor:
     """A 256-byte aligned uint8 device buffer of at least ``nbytes`` (zeroed control block)."""
     buf = torch.zeros(int(nbytes) + 256, dtype=torch.uint8, device=device)
@@ -648,6 +660,12 @@ def fused_logprobs(H, W, tokens, mask=None, chunk=4096, tau=1.0):
     return _FusedLogprobs.apply(H, W, tokens, mask, int(chunk), float(tau))
 
 
+def _ce_options(label_smoothing, z_loss, softcap, ignore_index):
+    if not -2 ** 31 <= int(ignore_index) < 2 ** 31:
+        raise ValueError("ignore_index must be an int32 number")
+    return float(label_smoothing), float(z_loss), float(softcap), int(ignore_index)
+
+
 def _ce_step(H, W, labels, mask, chunk, options, grad_loss, ws, control, loss_out=None, grad_H=None, grad_W=None,
              grad_H_fp32=False, grad_W_bf16=False):
     N, d, V, dev = _check_projection(H, W, labels, mask, "labels")
@@ -693,15 +711,17 @@ def _ce_forward(H, W, labels, mask, chunk, options, ws, control, loss_out=None):
     return loss, lse, ws
 
 
+@_on_its_device
 def fused_cross_entropy_forward(H, W, labels, mask=None, chunk=4096, label_smoothing=0.0, z_loss=0.0, softcap=0.0,
                                 ignore_index=-100, ws=None, loss_out=None):
     """kd_fused_cross_entropy_fwd: (loss [1], lse [N], ws).  Cross entropy of ``labels`` (int32 [N]) against
     softmax(H W^T), the logits never stored: the mean over the positions whose label is not ``ignore_index`` and
     whose ``mask`` is not 0; each position's own loss goes to ``loss_out`` ([N] fp32) when given."""
-    return _ce_forward(H, W, labels, mask, chunk,
-                       (float(label_smoothing), float(z_loss), float(softcap), int(ignore_index)), ws, None, loss_out)
+    return _ce_forward(H, W, labels, mask, chunk, _ce_options(label_smoothing, z_loss, softcap, ignore_index), ws, None,
+                       loss_out)
 
 
+@_on_its_device
 def fused_cross_entropy_step(H, W, labels, mask=None, chunk=4096, label_smoothing=0.0, z_loss=0.0, softcap=0.0,
                              ignore_index=-100, grad_loss=None, ws=None, loss_out=None, grad_H=None, grad_W=None,
                              grad_H_fp32=False, grad_W_bf16=False):
@@ -709,10 +729,11 @@ def fused_cross_entropy_step(H, W, labels, mask=None, chunk=4096, label_smoothin
     beforehand: (loss [1], grad_H [N, d] bf16 or fp32, grad_W [V, d]).  A ``grad_W`` of the caller's (fp32) is added
     into; without one it is a new tensor, fp32 or with ``grad_W_bf16`` (one chunk only) bf16.  Without a workspace
     errors go to the stream's control_block."""
+    options = _ce_options(label_smoothing, z_loss, softcap, ignore_index)
     _check_projection(H, W, labels, mask, "labels")
     control = _control(H.device) if ws is None else ws
-    return _ce_step(H, W, labels, mask, chunk, (float(label_smoothing), float(z_loss), float(softcap), int(ignore_index)),
-                    grad_loss, ws, control, loss_out, grad_H, grad_W, grad_H_fp32, grad_W_bf16)
+    return _ce_step(H, W, labels, mask, chunk, options, grad_loss, ws, control, loss_out, grad_H, grad_W, grad_H_fp32,
+                    grad_W_bf16)
 
 
 class _FusedCrossEntropy(torch.autograd.Function):
@@ -752,13 +773,14 @@ class _FusedCrossEntropy(torch.autograd.Function):
         return grads[0], grads[1].to(W.dtype), None, None, None, None, None
 
 
+@_on_its_device
 def fused_cross_entropy(H, W, labels, mask=None, chunk=4096, label_smoothing=0.0, z_loss=0.0, softcap=0.0,
                         ignore_index=-100):
     """Differentiable cross entropy of ``labels`` (int32 [N]) against softmax(H W^T): the mean over the positions
     whose label is not ``ignore_index`` and whose ``mask`` is not 0 (scalar tensor)."""
     wanted = torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)
-    return _FusedCrossEntropy.apply(H, W, labels, mask, int(chunk), (float(label_smoothing), float(z_loss),
-                                    float(softcap), int(ignore_index)), wanted)
+    return _FusedCrossEntropy.apply(H, W, labels, mask, int(chunk),
+                                    _ce_options(label_smoothing, z_loss, softcap, ignore_index), wanted)
 
 
 def gemm_bf16(A, B, M, N, K, a_mn_major=False, b_mn_major=False, C=None):
@@ -778,6 +800,7 @@ def gemm_bf16(A, B, M, N, K, a_mn_major=False, b_mn_major=False, C=None):
 
 # ------------------------------------------------------------------ 8 bits
 
+@_on_its_device
 def quantize_int8(x, q=None, scale=None):
     """kd_quantize_int8: (q int8 [N, d], scale fp32 [N]) of the rows of ``x`` ([N, d] bf16, fp16 or fp32, any row
     stride): scale = max |x| / 127, q = x / scale to the nearest whole number."""
@@ -813,6 +836,7 @@ def _rows_aligned(t, ld: int) -> int:
     return int(t.data_ptr() % 16 == 0 and ld % 16 == 0)
 
 
+@_on_its_device
 def gemm_int8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, ws=None):
     """kd_gemm_int8: [M, N] = (A B^T) a_scale[:, None] b_scale of int8 matrices A [M, K] (tokens) and B [N, K]
     (channels), rows of any stride, in bf16, fp16 or fp32 (``out_dtype``, or that of a given ``out``).  Weights
@@ -843,6 +867,7 @@ def gemm_int8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, ws=Non
     return out
 
 
+@_on_its_device
 def teacher_topk_int8(Ht, h_scale, Wt, w_scale, K: int, chunk: int = 1024, with_lse: bool = False,
                       with_dropped: bool = False, ws: Optional[torch.Tensor] = None):
     """Top-K cache from quantised teacher hidden states Ht [N, dt] and LM-head Wt [V, dt] (int8 with their rows'

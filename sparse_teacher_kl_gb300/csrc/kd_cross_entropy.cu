@@ -28,7 +28,7 @@ namespace kd {
 namespace {
 
 constexpr float kLog2E = 1.4426950408889634f;
-constexpr float kLn2f = 0.69314718055994531f;
+constexpr float kMinSoftcap = 1e-6f;  // its square and reciprocal are ordinary numbers
 
 __device__ __forceinline__ bool has_loss(const int32_t* labels, const uint8_t* mask, int64_t i, int ignore) {
   return labels[i] != ignore && (mask == nullptr || mask[i] != 0);
@@ -42,7 +42,8 @@ constexpr int LIST_THREADS = 1024, LIST_EACH = 8;
 __global__ void __launch_bounds__(LIST_THREADS)
     kd_ce_list_kernel(const int32_t* __restrict__ labels, const uint8_t* __restrict__ mask, int64_t N, int ignore,
                       int32_t* __restrict__ list, int32_t* __restrict__ n_valid, float* __restrict__ lse,
-                      float* __restrict__ losses) {
+                      float* __restrict__ losses, const float* __restrict__ grad_loss, float label_weight,
+                      float* __restrict__ alpha) {
   __shared__ int warp_sum[LIST_THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int base = 0;
@@ -82,7 +83,11 @@ __global__ void __launch_bounds__(LIST_THREADS)
     base += total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) *n_valid = base;
+  if (threadIdx.x == 0) {
+    *n_valid = base;
+    // the gradient's common factor, see CeCombine
+    if (alpha != nullptr) *alpha = base > 0 ? (grad_loss ? *grad_loss : 1.f) * label_weight / float(base) : 0.f;
+  }
 }
 
 __device__ __forceinline__ int chunk_rows(const int32_t* n_valid, int64_t c0, int cap) {
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(GATHER_WARPS * 32)
                         const uint8_t* __restrict__ mask, int64_t N, int64_t d, int ignore,
                         const int32_t* __restrict__ list, const int32_t* __restrict__ n_valid, int64_t c0, int cap,
                         int rows_pad, uint16_t* __restrict__ Hc, int32_t* __restrict__ labels_c,
-                        void* __restrict__ zero_H, int64_t zero_vecs) {
+                        void* __restrict__ zero_H, int64_t zero_vecs, uint32_t* err) {
   const int lane = threadIdx.x & 31;
   const int64_t w0 = int64_t(blockIdx.x) * GATHER_WARPS + (threadIdx.x >> 5), step = int64_t(gridDim.x) * GATHER_WARPS;
   const int n = chunk_rows(n_valid, c0, cap);
@@ -110,8 +115,8 @@ __global__ void __launch_bounds__(GATHER_WARPS * 32)
   const int64_t vecs = d / 8;
   for (int64_t r = w0; r < end; r += step) {
     uint4* dst = reinterpret_cast<uint4*>(Hc + r * d);
-    if (r < n) {
-      const int64_t i = list[c0 + r];
+    const int64_t i = r < n ? list[c0 + r] : 0;
+    if (r < n && KD_DCHECK(i >= 0 && i < N, err, 0x2000)) {
       const uint4* src = reinterpret_cast<const uint4*>(H + i * d);
       if (lane == 0) labels_c[r] = labels[i];
 #pragma unroll 4
@@ -130,17 +135,19 @@ __global__ void __launch_bounds__(GATHER_WARPS * 32)
 
 // ------------------------------------------------------------------ row sums ---
 // A row's tiles put together: its loss and logsumexp to the position's place and, for a step, what dZ
-// takes of it: (lse, a, b, dz_y) with dZ_v = (a p_v - b) slope_v.  32 threads share a row's tiles (as
-// the other combines: a thread's tiles are a chain of dependent exponentials).
+// takes of it: (lse, a, b, dz_y) with dZ_v = (a p_v - b) slope_v.  dZ leaves out alpha = G (1 - e), which is every
+// entry's and joins the fp32 products: the label's entry is then 1 - p_y / (1 - e) and not G times that, whose
+// rounding to bf16 would be the same in every row that the model has not learnt (p_y near 0), up to 2^-8 of the
+// gradients.  32 threads share a row's tiles (as the other combines: a thread's tiles are a chain of dependent
+// exponentials).
 constexpr int CC_ROWS = 32, CC_PHASES = 32;
 
 struct CeCombine {
   const float4* partials;
   int tiles, rows_pad, cap;
-  int64_t c0, V;
+  int64_t c0, N, V;
   const int32_t *list, *n_valid, *labels_c;
   float smooth, z_loss, softcap;
-  const float* grad_loss;
   float *lse, *losses;
   float4* row_stats;
   uint32_t* err;
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(CC_ROWS * CC_PHASES) kd_ce_combine_kernel(cons
     Z += q.w;
   }
   const int64_t pos = a.list[a.c0 + r];
+  if (!KD_DCHECK(pos >= 0 && pos < a.N, a.err, 0x2001)) return;
   const int32_t label = a.labels_c[r];
   const bool bad = label < 0 || int64_t(label) >= a.V;
   if (bad) raise_error(a.err, KD_DEVERR_BAD_ID, uint32_t(pos));
@@ -193,11 +201,11 @@ __global__ void __launch_bounds__(CC_ROWS * CC_PHASES) kd_ce_combine_kernel(cons
   if (a.row_stats == nullptr) return;
   float4 st = make_float4(lse, 0.f, 0.f, 0.f);
   if (!bad) {
-    const float G = (a.grad_loss ? *a.grad_loss : 1.f) / float(*a.n_valid);
-    st.y = G * fmaf(2.f * a.z_loss, lse, 1.f);
-    st.z = G * (a.smooth / float(a.V));
+    const float scale = 1.f / (1.f - a.smooth);
+    st.y = scale * fmaf(2.f * a.z_loss, lse, 1.f);
+    st.z = scale * (a.smooth / float(a.V));
     const float t = a.softcap > 0.f ? Y / a.softcap : 0.f;
-    st.w = (st.y * exp2f(-nll * kLog2E) - st.z - G * (1.f - a.smooth)) * fmaf(-t, t, 1.f);
+    st.w = (st.y * exp2f(-nll * kLog2E) - st.z - 1.f) * fmaf(-t, t, 1.f);
   }
   a.row_stats[r] = st;
 }
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(256) kd_ce_scale_kernel(T* __restrict__ x, int
 // ------------------------------------------------------------------ host side ---
 
 struct CeLayout {
-  size_t list, losses, labels, stats, partials, hidden, dz, gh_part, total;
+  size_t alpha, list, losses, labels, stats, partials, hidden, dz, gh_part, total;
   int64_t rows_pad, nvb;
   int tiles;
 };
@@ -323,6 +331,7 @@ CeLayout ce_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool step) {
     off = align_up(off + bytes, 256);
     return at;
   };
+  L.alpha = take(4);
   L.list = take(size_t(N) * 4);
   L.losses = take(size_t(N) * 4);
   L.labels = take(size_t(L.rows_pad) * 4);
@@ -385,6 +394,7 @@ int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int
   Ctrl* ctrl = static_cast<Ctrl*>(a.ws);
   uint32_t* err = &static_cast<Ctrl*>(a.control)->err;
   const int32_t* list = reinterpret_cast<const int32_t*>(w8 + L.list);
+  const float* alpha = reinterpret_cast<const float*>(w8 + L.alpha);
   const uint16_t* Hc = reinterpret_cast<const uint16_t*>(w8 + L.hidden);
   const void* dz = w8 + L.dz;
   const uint64_t d = uint64_t(a.d), V = uint64_t(a.V), row_bytes = d * 2;
@@ -404,11 +414,13 @@ int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int
   q.n_units = ((q.m_tiles + q.cluster - 1) / q.cluster) * q.n_tiles * q.k_splits;
   q.rows = n; q.rows_dev = &ctrl->n_valid; q.row_first = int(c0);
   q.err = err;
+  q.alpha = alpha;
   q.ldc = a.d;
   if (q.k_splits == 1) {
     q.C = a.grad_H;
     q.c_bf16 = a.grad_H_f32 ? 0 : 1;
     q.row_map = list + c0;
+    q.map_rows = a.N;
   } else {
     q.C = w8 + L.gh_part;  // fp32 partial per split, summed in split order below
     q.split_stride = L.rows_pad * a.d;
@@ -443,6 +455,7 @@ int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int
   r.n_units = ((r.m_tiles + r.cluster - 1) / r.cluster) * r.n_tiles;
   r.rows = n; r.rows_dev = &ctrl->n_valid; r.row_first = int(c0);
   r.C = a.grad_W; r.ldc = a.d; r.err = err;
+  r.alpha = alpha;
   r.c_bf16 = r.c_tma = a.w_kind == KD_GRAD_STORE_BF16;
   r.b_box2 = r.cta_pair && d64;
   const int kr = r.cta_pair ? pair_kblocks(1, 1) : 1;
@@ -464,7 +477,7 @@ int ce_run(const CeCall& a, bool step) {
   kd_status st = check_proj_args(a.H, a.W, a.N, a.d, a.V, a.chunk, 1.f);
   if (st != KD_OK) return st;
   if (!(a.smooth >= 0.f && a.smooth < 1.f) || !(a.z_loss >= 0.f && isfinite(a.z_loss)) ||
-      !(a.softcap >= 0.f && isfinite(a.softcap)))
+      !(a.softcap == 0.f || (a.softcap >= kMinSoftcap && isfinite(a.softcap))))
     return KD_ERR_INVALID_ARG;
   if (!ok4(a.labels) || !ok4(a.loss) || !ok4(a.lse) || !aligned(a.losses, 4)) return KD_ERR_INVALID_ARG;
   if (step) {
@@ -493,7 +506,9 @@ int ce_run(const CeCall& a, bool step) {
   const int grid = gemm_max_grid();
 
   prof_before("kd_ce_list", s);
-  kd_ce_list_kernel<<<1, LIST_THREADS, 0, s>>>(a.labels, a.mask, a.N, a.ignore, list, &ctrl->n_valid, a.lse, losses);
+  kd_ce_list_kernel<<<1, LIST_THREADS, 0, s>>>(a.labels, a.mask, a.N, a.ignore, list, &ctrl->n_valid, a.lse, losses,
+                                             a.grad_loss, 1.f - a.smooth,
+                                             step ? reinterpret_cast<float*>(w8 + L.alpha) : nullptr);
   prof_after(s);
   KD_TRY(cudaGetLastError());
 
@@ -505,7 +520,7 @@ int ce_run(const CeCall& a, bool step) {
     prof_before("kd_ce_gather", s);
     kd_ce_gather_kernel<<<unsigned(blocks < 8 * grid ? blocks : 8 * grid), GATHER_WARPS * 32, 0, s>>>(
         static_cast<const uint16_t*>(a.H), a.labels, a.mask, a.N, a.d, a.ignore, list, &ctrl->n_valid, c0, n,
-        int(L.rows_pad), Hc, labels_c, zero ? a.grad_H : nullptr, a.d * (a.grad_H_f32 ? 4 : 2) / 16);
+        int(L.rows_pad), Hc, labels_c, zero ? a.grad_H : nullptr, a.d * (a.grad_H_f32 ? 4 : 2) / 16, err);
     prof_after(s);
     KD_TRY(cudaGetLastError());
 
@@ -539,10 +554,9 @@ int ce_run(const CeCall& a, bool step) {
     CeCombine c{};
     c.partials = partials;
     c.tiles = L.tiles; c.rows_pad = int((n + BM - 1) / BM * BM); c.cap = n;
-    c.c0 = c0; c.V = a.V;
+    c.c0 = c0; c.N = a.N; c.V = a.V;
     c.list = list; c.n_valid = &ctrl->n_valid; c.labels_c = labels_c;
     c.smooth = a.smooth; c.z_loss = a.z_loss; c.softcap = a.softcap;
-    c.grad_loss = a.grad_loss;
     c.lse = a.lse; c.losses = losses;
     c.row_stats = step ? row_stats : nullptr;
     c.err = err;

@@ -480,9 +480,19 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// c tanh(z / c) = c - 2 c / (e^(2 z / c) + 1), k = 2 log2(e) / c: within a few roundings of c at any z.
+// c tanh(z / c), k = 2 log2(e) / c.  c - 2 c / (e^(2 z / c) + 1) is within a few roundings of c at any z, 1e-5 for
+// c up to CE_CAP_NEAR.  Beyond, where z / c is small, that would be many roundings of z: below 1/4 the series
+// z (1 - x^2 / 3 + 2 x^4 / 15 - 17 x^6 / 315 + 62 x^8 / 2835), x = z / c, is taken (the next term is 1e-8 of it).
+constexpr float CE_CAP_NEAR = 64.f;
+
 __device__ __forceinline__ float ce_capped(float z, float c, float k) {
   return fmaf(-2.f * c, rcp_approx(ex2_approx(z * k) + 1.f), c);
+}
+
+__device__ __forceinline__ float ce_capped_far(float z, float c, float k) {
+  const float x = z * (k * 0.34657359027997264f), x2 = x * x;  // k ln(2) / 2 = 1 / c
+  const float p = fmaf(fmaf(fmaf(62.f / 2835.f, x2, -17.f / 315.f), x2, 2.f / 15.f), x2, -1.f / 3.f);
+  return fabsf(x) < 0.25f ? fmaf(z * x2, p, z) : ce_capped(z, c, k);
 }
 
 // Value of r[i] for a run-time i in [0, 32), by a tree of selects so that the

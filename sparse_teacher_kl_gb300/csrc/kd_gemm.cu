@@ -147,70 +147,67 @@ __device__ __forceinline__ void unit_coords(const GemmProblem& p, const Extent& 
 
 // Warps that drain finished accumulators.  The cross entropy's take two sweeps and, with a softcap, three
 // special-function results for each logit: two warps on each of the SM's four schedulers, each with half of
-// the columns, hide their latency (509 x 50257, d = 1000, capped: EPI_CE_MEASURED).
+// the columns, hide their latency (509 x 50257, d = 1000, capped: 62 us, with four warps 78).
 template <int EPI>
 constexpr int kEpiWarps = EPI == EPI_CE ? 8 : 4;
 template <int EPI>
 constexpr int kThreads = 64 + 32 * kEpiWarps<EPI>;
 static_assert(kThreads<EPI_STORE> == GEMM_THREADS, "TMA warp, MMA warp, 4 epilogue warps");
 
-// A warp's half of a tile of EPI_CE (CE_COLS columns from `first`), for the row of this thread: two sweeps
-// over the accumulator, the first for the largest logit, so that the sum needs no rescaling and the
-// distances have their final reference.
-__device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap& tmap_c, uint32_t t_acc, int first,
+// A warp's half of a tile of EPI_CE: the CE_COLS logits z from column `first` on of the row of this thread.  The
+// largest first, so that the sum needs no rescaling and the distances have their final reference.
+//
+// The tensor cores cut each addition to an accumulator off where it should be rounded, so that a sum of n
+// steps of 16 is about n 2^-26 of itself too near to 0: 2e-6 of a label's logit at d = 2048, and of the losses.
+// EPI_CE therefore takes the reduction CE_CHUNK_K deep at a time and adds the parts in registers (losses at
+// d = 3320 within CE_LOSS_ERR of float64, 2.6e-6 in one piece), in the time of the next part's MMAs.
+__device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap& tmap_c, float (&z)[CE_COLS], int first,
                                         int m_blk, int row, int rows, int nid, uint8_t* box, uint32_t lane,
                                         uint32_t quarter) {
   constexpr float kL2E = 1.4426950408889634f;
   const bool last = first + CE_COLS > p.N;  // columns past the vocabulary: weight 0
-  float m = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < CE_COLS / 32; ++c) {
-    uint32_t raw[32];
-    tmem_ld_32x32b_x32(t_acc + c * 32, raw);
-    tmem_ld_wait();
-    if (last) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (first + c * 32 + i < p.N) m = fmaxf(m, __uint_as_float(raw[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(raw[i]));
-    }
-  }
   const float cap = p.ce_cap, cap_k = cap > 0.f ? 2.f * kL2E / cap : 0.f;
-  if (cap > 0.f) m = ce_capped(m, cap, cap_k);
+  if (cap > CE_CAP_NEAR) {
+#pragma unroll
+    for (int i = 0; i < CE_COLS; ++i) z[i] = ce_capped_far(z[i], cap, cap_k);
+  } else if (cap > 0.f) {
+#pragma unroll
+    for (int i = 0; i < CE_COLS; ++i) z[i] = ce_capped(z[i], cap, cap_k);
+  }
+  float zs = 0.f;
+  if (p.ce_sum) {
+    float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < CE_COLS; i += 2) {
+      z0 += !last || first + i < p.N ? z[i] : 0.f;
+      z1 += !last || first + i + 1 < p.N ? z[i + 1] : 0.f;
+    }
+    zs = z0 + z1;
+  }
+  if (last) {
+#pragma unroll
+    for (int i = 0; i < CE_COLS; ++i)
+      if (first + i >= p.N) z[i] = -INFINITY;
+  }
+  float zy = 0.f;
+  if (uint32_t(nid - first) < uint32_t(CE_COLS)) {
+#pragma unroll
+    for (int i = 0; i < CE_COLS; ++i) zy = nid - first == i ? z[i] : zy;
+  }
+  float m = z[0], m1 = z[1];
+#pragma unroll
+  for (int i = 2; i < CE_COLS; i += 2) {
+    m = fmaxf(m, z[i]);
+    m1 = fmaxf(m1, z[i + 1]);
+  }
+  m = fmaxf(m, m1);
   const float ref = m == -INFINITY ? 0.f : m;  // nothing but -inf: distances stay infinite, not NaN
-  float s0 = 0.f, s1 = 0.f, zs = 0.f, zy = 0.f;
-#pragma unroll 1
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
   for (int c = 0; c < CE_COLS / 32; ++c) {
-    const int col0 = first + c * 32;
-    uint32_t raw[32];
-    tmem_ld_32x32b_x32(t_acc + c * 32, raw);
-    tmem_ld_wait();
-    float x[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
-    if (cap > 0.f) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = ce_capped(x[i], cap, cap_k);
-    }
-    if (p.ce_sum) {
-      float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        z0 += !last || col0 + i < p.N ? x[i] : 0.f;
-        z1 += !last || col0 + i + 1 < p.N ? x[i + 1] : 0.f;
-      }
-      zs += z0 + z1;
-    }
-    if (uint32_t(nid - col0) < 32u) zy = select32(x, uint32_t(nid - col0));
+    float* x = z + c * 32;
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = ref - x[i];
-    if (last) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col0 + i >= p.N) x[i] = INFINITY;
-    }
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       s0 += ex2_approx(x[i] * -kL2E);
@@ -222,17 +219,16 @@ __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap&
         __syncwarp();
       }
       // 2^23 added: the distance in whole steps, rounded, in the low bits of the sum
-      uint32_t q[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        q[i] = __float_as_uint(fminf(fmaxf(fmaf(x[i], CE_STEPS, 8388608.f), 8388608.f), 8388608.f + 65535.f));
+      auto steps = [&](int i) {
+        return __float_as_uint(fminf(fmaxf(fmaf(x[i], CE_STEPS, 8388608.f), 8388608.f), 8388608.f + 65535.f));
+      };
 #pragma unroll
       for (int g8 = 0; g8 < 4; ++g8) {
         uint4 v;
-        v.x = __byte_perm(q[g8 * 8 + 0], q[g8 * 8 + 1], 0x5410);
-        v.y = __byte_perm(q[g8 * 8 + 2], q[g8 * 8 + 3], 0x5410);
-        v.z = __byte_perm(q[g8 * 8 + 4], q[g8 * 8 + 5], 0x5410);
-        v.w = __byte_perm(q[g8 * 8 + 6], q[g8 * 8 + 7], 0x5410);
+        v.x = __byte_perm(steps(g8 * 8 + 0), steps(g8 * 8 + 1), 0x5410);
+        v.y = __byte_perm(steps(g8 * 8 + 2), steps(g8 * 8 + 3), 0x5410);
+        v.z = __byte_perm(steps(g8 * 8 + 4), steps(g8 * 8 + 5), 0x5410);
+        v.w = __byte_perm(steps(g8 * 8 + 6), steps(g8 * 8 + 7), 0x5410);
         const uint32_t j = uint32_t((c & 1) * 4 + g8);
         *reinterpret_cast<uint4*>(box + lane * 128u + ((j ^ (lane & 7u)) * 16u)) = v;
       }
@@ -240,7 +236,7 @@ __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap&
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&tmap_c, box, 0, m_blk * BM + int(quarter) * 32, (col0 - 32) / 64);
+          tma_store_3d(&tmap_c, box, 0, m_blk * BM + int(quarter) * 32, (first + c * 32 - 32) / 64);
           bulk_commit();
         }
       }
@@ -413,7 +409,10 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
       for (int u = u_first; u < ext.n_units && ok; u += u_step) {
         int m_blk, n_first, n_count, kb_lo, kb_hi, split;
         unit_coords(p, ext, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
-        for (int nb = n_first; nb < n_first + n_count && ok; ++nb, ++acc_it) {
+        const int k_step = EPI == EPI_CE ? CE_CHUNK_K / (BK * G::kKB) : kb_hi - kb_lo;
+        for (int nb = n_first; nb < n_first + n_count && ok; ++nb) {
+         // an accumulator for each k_step stages of the reduction: all of them but for EPI_CE
+         for (int kc = kb_lo; kc < kb_hi && ok; kc += k_step, ++acc_it) {
           const uint32_t a = acc_it & 1u;
           const uint32_t aph = (acc_it >> 1) & 1u;
           if (!mbar_wait(&tail->tempty[a], aph ^ 1u, abort_flag, p.err, 0x200u)) {
@@ -422,7 +421,8 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
           }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + a * BN;
-          for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+          const int kb_end = min(kb_hi, kc + k_step);
+          for (int kb = kc; kb < kb_end; ++kb, ++it) {
             const uint32_t s = it % G::kStages;
             const uint32_t ph = (it / G::kStages) & 1u;
             if (!mbar_wait(&tail->full[s], ph, abort_flag, p.err, 0x300u)) {
@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
               const uint32_t b_off = p.b_mn ? uint32_t(k) * 2048u : uint32_t(k >> 2) * (G::kB / G::kKB) + (k & 3) * 32u;
               const uint64_t ad = sdesc_sw128(sa + a_off, a_lbo);
               const uint64_t bd = sdesc_sw128(sb + b_off, b_lbo);
-              if (CG == 2) umma_bf16_pair(d_tmem, ad, bd, idesc, (kb != kb_lo || k != 0) ? 1u : 0u);
-              else umma_bf16(d_tmem, ad, bd, idesc, (kb != kb_lo || k != 0) ? 1u : 0u);
+              if (CG == 2) umma_bf16_pair(d_tmem, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
+              else umma_bf16(d_tmem, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
             }
             if (CG == 2) umma_commit_pair_mc(&tail->empty[s], 0x3);
             else umma_commit(&tail->empty[s]);
@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
           if (ok) {
             if (CG == 2) umma_commit_pair_mc(&tail->tfull[a], 0x3); else umma_commit(&tail->tfull[a]);
           }
+         }
         }
       }
       // Drain: every MMA issued above has completed once this arrives.
@@ -531,6 +532,39 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
         }
       }
 
+      if (EPI == EPI_CE) {
+        const int half = int(warp - 2u) >> 2, k_step = CE_CHUNK_K / (BK * G::kKB);
+        for (int nb = n_first; nb < n_first + n_count && ok; ++nb) {
+          float x[CE_COLS];
+#pragma unroll
+          for (int i = 0; i < CE_COLS; ++i) x[i] = 0.f;
+          for (int kc = kb_lo; kc < kb_hi; kc += k_step, ++acc_it) {
+            const uint32_t a = acc_it & 1u;
+            const bool got = mbar_wait(&tail->tfull[a], (acc_it >> 1) & 1u, abort_flag, p.err, 0x500u);
+            if (!__all_sync(0xffffffffu, got)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < CE_COLS / 16; ++c) {
+              uint32_t raw[16];
+              tmem_ld_32x32b_x16(t_lane + a * BN + half * CE_COLS + c * 16, raw);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[c * 16 + i] += __uint_as_float(raw[i]);
+            }
+            tc_fence_before();
+            if (CG == 2 && crank != 0) mbar_arrive_remote_tc(mapa_u32(&tail->tempty[a], 0));
+            else mbar_arrive(&tail->tempty[a]);
+          }
+          if (ok)
+            ce_half(p, tmap_c, x, nb * BN + half * CE_COLS, m_blk, row, ext.rows, nid, staging + (warp - 2u) * 4096u,
+                    lane, quarter);
+        }
+        continue;
+      }
+
       for (int nb = n_first; nb < n_first + n_count; ++nb, ++acc_it) {
         const uint32_t a = acc_it & 1u;
         const uint32_t aph = (acc_it >> 1) & 1u;
@@ -545,14 +579,8 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
         tc_fence_after();
         const uint32_t t_acc = t_lane + a * BN;
 
-        if (EPI == EPI_CE) {
-          const int half = int(warp - 2u) >> 2;
-          ce_half(p, tmap_c, t_acc + half * CE_COLS, nb * BN + half * CE_COLS, m_blk, row, ext.rows, nid,
-                  staging + (warp - 2u) * 4096u, lane, quarter);
-        }
-
 #pragma unroll 1
-        for (int c = 0; c < (EPI == EPI_CE ? 0 : BN / 32); ++c) {
+        for (int c = 0; c < BN / 32; ++c) {
           uint32_t raw[32];
           tmem_ld_32x32b_x32(t_acc + c * 32, raw);
           tmem_ld_wait();
@@ -560,6 +588,11 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
           const int col0 = nb * BN + c * 32;
+          if ((EPI == EPI_STORE || EPI == EPI_ACCUM) && p.alpha != nullptr) {
+            const float alpha = __ldg(p.alpha);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] *= alpha;
+          }
 
           if (EPI == EPI_LSE_Z) {
             // forward-chunked: keep this tile's raw logits (bf16) for the backward pass
@@ -837,8 +870,8 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
             }
           } else {
             // EPI_STORE: C[row, col0 + i]
-            if (row < ext.M) {
-              const int crow = p.row_map ? __ldg(p.row_map + row) : row;
+            const int crow = p.row_map && row < ext.M ? __ldg(p.row_map + row) : row;
+            if (row < ext.M && KD_DCHECK(!p.row_map || (crow >= 0 && crow < p.map_rows), p.err, 0x2002)) {
               if (p.c_bf16) {
                 uint16_t* dst =
                     reinterpret_cast<uint16_t*>(p.C) + size_t(split) * p.split_stride + size_t(crow) * p.ldc + col0;

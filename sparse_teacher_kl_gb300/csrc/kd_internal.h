@@ -144,7 +144,9 @@ struct GemmProblem {
   // (there an EPI_STORE takes one k-block of zeros when none exists).
   const int32_t* rows_dev;
   int row_first;
-  const int32_t* row_map;     // EPI_STORE without c_tma and splits (NULL: none): row of C that row i goes to
+  const int32_t* row_map;     // EPI_STORE without c_tma and splits (NULL: none): row of C that row i goes to, below
+  int64_t map_rows;           // map_rows
+  const float* alpha;         // EPI_STORE / EPI_ACCUM (NULL: 1): device scalar, a factor of the product
   // EPI_CE: tokens as above; logits capped to ce_cap tanh(z / ce_cap) (0: not); ce_sum: the sum of
   // logits is wanted; ce_q: the 16-bit logits go out through tmap_c
   float ce_cap;
@@ -157,6 +159,7 @@ struct GemmProblem {
 // anything 32 and further below (e^-32 of the largest, 1.3e-14).  Half a step makes 2.4e-4 of a
 // probability, an eighth of the rounding of bf16 dZ; bf16 logits would make 2^-8 of every unit of |z|.
 constexpr int CE_COLS = BN / 2;
+constexpr int CE_CHUNK_K = 1024;  // depth of EPI_CE's partial sums
 constexpr float CE_STEPS = 2048.f;
 
 

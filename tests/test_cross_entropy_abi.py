@@ -35,7 +35,7 @@ NAN, INF = float("nan"), float("inf")
     dict(N=0), dict(N=1 << 31), dict(d=0), dict(d=60), dict(V=0), dict(V=1 << 31), dict(chunk=0), dict(chunk=100),
     dict(H=None), dict(W=None), dict(H=P + 8), dict(W=P + 2), dict(y=None), dict(y=P + 1), dict(loss=None),
     dict(loss=P + 2), dict(lse=None), dict(lse=P + 1), dict(each=P + 2), dict(smooth=-0.1), dict(smooth=1.0),
-    dict(smooth=NAN), dict(z=-1.0), dict(z=INF), dict(z=NAN), dict(cap=-1.0), dict(cap=INF), dict(cap=NAN))]
+    dict(smooth=NAN), dict(z=-1.0), dict(z=INF), dict(z=NAN), dict(cap=-1.0), dict(cap=INF), dict(cap=NAN), dict(cap=1e-30), dict(cap=9e-7))]
     + [(True, k) for k in (dict(g=P + 1), dict(gH=None), dict(gH=P + 8), dict(gW=None), dict(gW=P + 4), dict(kind=3),
                            dict(kind=-1), dict(kind=2))])
 def test_refuses(lib, step, kw):
@@ -62,3 +62,10 @@ def test_wrappers_refuse_wrong_tensors():
     for f in (kd.fused_cross_entropy, kd.fused_cross_entropy_forward, kd.fused_cross_entropy_step):
         with pytest.raises(ValueError):
             f(H, H, y)              # not CUDA tensors
+
+
+def test_ignore_index_is_an_int32():
+    H = torch.zeros((2, 8), dtype=torch.bfloat16)
+    for f in (kd.fused_cross_entropy, kd.fused_cross_entropy_forward, kd.fused_cross_entropy_step):
+        with pytest.raises(ValueError, match="ignore_index"):
+            f(H, H, torch.zeros((2,), dtype=torch.int32), ignore_index=2 ** 32 - 100)

@@ -283,3 +283,24 @@ def test_two_streams(kd, cuda_device):
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert all(torch.equal(p, q) for p, q in zip(x, y))
+
+
+@pytest.mark.parametrize("cap", [64.0, 65.0, 1e3, 1e5, 1e30])
+def test_wide_softcaps(kd, cuda_device, cap):
+    """Logits of +-70 under caps from near to far: the wider, the nearer to no cap at all."""
+    H, W, labels = case(130, 64, 600, 0.9, seed=6)
+    H = (H.float() * 8).to(torch.bfloat16)
+    loss_r, each_r, lse_r, gH_r, gW_r, bH, bW = reference(H, W, labels, cap=cap)
+    each = torch.empty((130,), device="cuda")
+    loss, gH, gW = kd.fused_cross_entropy_step(H, W, labels, softcap=cap, loss_out=each, grad_H_fp32=True)
+    # logits, and so their errors, 8 times those of the other cases: 1.6e-3 of a probability beside 2^-8 and 2^-12
+    assert ((each.double() - each_r).abs() <= 8 * 2.5e-4).all()
+    near(gH, gH_r, 1.25 * bH, False)
+    near(gW, gW_r, 1.25 * bW, False)
+
+
+def test_called_by_keyword(kd, cuda_device):
+    H, W, labels = case(64, 64, 200)
+    a = kd.fused_cross_entropy(H, W, labels)
+    assert torch.equal(kd.fused_cross_entropy(labels=labels, W=W, H=H), a)
+    assert torch.equal(kd.fused_cross_entropy_forward(H=H, W=W, labels=labels)[0][0], a)
