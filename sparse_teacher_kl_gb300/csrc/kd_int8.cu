@@ -9,6 +9,10 @@
 // a hundred times below it), and beyond that sums rounded to fp32.  So the operations cannot go
 // faster than the 16-bit rate, but the weights keep their single byte all the way from HBM to the SM:
 // they are widened on their way from shared to tensor memory, where tcgen05.mma takes its A operand from.
+//
+// Measured, K = 2880, N = 201088, bf16 out (us; TB/s of what must move, or PFLOP/s): 1 token 92 (6.2 TB/s, 93 % of the
+// copy), 5 98 (5.9), 64 109 (5.5), 128 118, 256 180 (1.65 PFLOP/s), 512 325 (1.82), 4096 2690 (1.76 in a row, 1.95 alone,
+// 91 % and 101 % of the bf16 rate); quantising 8192 x 4096 bf16 26 us (3.9 TB/s), fp32 29 (5.8), 1 x 2880 2.6.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -582,13 +586,14 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ quantisation ---
-// A row is shared by W warps of a block, each thread holding 32 elements (vectors of VE) in registers between the
-// two sweeps; what a longer row has beyond 1024 W is read twice.  Bound by HBM: an element read and a byte
+// A row is shared by W warps of a block, each thread holding 64 bytes of it (vectors of VE elements) in registers
+// between the two sweeps (128: 8192 x 4096 bf16 32 us against 27); what a longer row has beyond that is read twice.  Bound by HBM: an element read and a byte
 // written.  A row that holds a NaN or an infinity has scale NaN and integers 0, a row of zeros scale 0.
 //
-// x times the rounded 1 / s is within 2^-22 of the quotient, 127 at most: its nearest whole number is the
-// quotient's unless it lies within 1e-4 of a half.  Then x / s is rounded correctly to fp32, and where that lands
+// x times the rounded 1 / s is within 2^-23 of the quotient, 127 at most: its nearest whole number is the
+// quotient's unless it lies within 1.6e-5 of a half.  Then x / s is rounded correctly to fp32, and where that lands
 // on a tie, the sign of what the division left over says on which side the quotient lies.
+constexpr float kSureOff = 0.49998f;
 constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23: whole numbers in the low bits of the sum
 
 __device__ __noinline__ int quantized_near_half(float x, float s) {
@@ -602,13 +607,29 @@ __device__ __noinline__ int quantized_near_half(float x, float s) {
   return int(fminf(fmaxf(r, -127.f), 127.f));
 }
 
-// inv 0: every element by division (a scale whose reciprocal fp32 does not hold).
-__device__ __forceinline__ uint32_t quantized(float x, float s, float inv) {
-  const float m = fmaf(x, inv, kRoundMagic);
-  const float off = fmaf(x, inv, kRoundMagic - m);
-  uint32_t q = __float_as_uint(m);
-  if (!(fabsf(off) < 0.4999f) || inv == 0.f) q = uint32_t(quantized_near_half(x, s));
-  return q & 0xFFu;
+// N elements' integers, four to a word.  inv 0: every element by division (a scale whose reciprocal fp32 does not
+// hold).  One test for all of them first, as few lie near a half.
+template <int N, class X>
+__device__ __forceinline__ void quantize_vec(const X& x, float s, float inv, uint32_t* out) {
+  float m[N], far = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float v = x.get(i);
+    m[i] = fmaf(v, inv, kRoundMagic);
+    far = fmaxf(far, fabsf(fmaf(v, inv, kRoundMagic - m[i])));
+  }
+  if (!(far < kSureOff) || inv == 0.f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(fabsf(fmaf(x.get(i), inv, kRoundMagic - m[i])) < kSureOff) || inv == 0.f)
+        m[i] = __int_as_float(quantized_near_half(x.get(i), s));
+  }
+  uint32_t q[(N + 3) / 4 * 4];
+#pragma unroll
+  for (int i = 0; i < (N + 3) / 4 * 4; ++i) q[i] = i < N ? __float_as_uint(m[i < N ? i : 0]) : 0u;
+#pragma unroll
+  for (int i = 0; i < (N + 3) / 4; ++i)
+    out[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
 }
 
 template <class T, int VE>
@@ -618,6 +639,9 @@ struct QVec {
     if (VE * sizeof(T) == 16) {
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
       w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if (VE * sizeof(T) == 8) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x; w[1] = v.y;
     } else if (sizeof(T) == 2) {
       w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
     } else {
@@ -629,6 +653,19 @@ struct QVec {
     for (uint32_t& x : w) x = 0;
   }
   __device__ __forceinline__ float get(int i) const;
+  // the largest magnitude so far, as bits (of one element, or of two 16-bit ones side by side): infinities and
+  // NaNs lie above every number
+  __device__ __forceinline__ uint32_t largest(uint32_t most) const {
+#pragma unroll
+    for (uint32_t x : w) most = sizeof(T) == 4 ? max(most, x & 0x7FFFFFFFu) : __vmaxu2(most, x & 0x7FFF7FFFu);
+    return most;
+  }
+  // those bits as fp32's
+  __device__ __forceinline__ static uint32_t as_f32(uint32_t most) {
+    if (sizeof(T) == 4) return most;
+    const uint32_t h = max(most & 0xFFFFu, most >> 16);
+    return std::is_same<T, __half>::value ? __float_as_uint(__half2float(__ushort_as_half(uint16_t(h)))) : h << 16;
+  }
 };
 template <class T, int VE>
 __device__ __forceinline__ float QVec<T, VE>::get(int i) const {
@@ -641,72 +678,63 @@ __device__ __forceinline__ float QVec<T, VE>::get(int i) const {
   }
 }
 
-constexpr int Q_THREADS = 256, Q_EACH = 32;
+constexpr int Q_THREADS = 256;
+template <class T>
+constexpr int kQEach = 64 / sizeof(T);  // elements that a thread holds
 
 template <class T, int VE, int W>
 __global__ void __launch_bounds__(Q_THREADS)
     kd_quantize_kernel(const T* __restrict__ x, int64_t N, int64_t d, int64_t ld, int8_t* __restrict__ q, int64_t ldq,
                        float* __restrict__ scale) {
-  constexpr int NV = Q_EACH / VE, ROWS = Q_THREADS / 32 / W, LANES = 32 * W;
-  __shared__ float part[Q_THREADS / 32];
+  constexpr int NV = kQEach<T> / VE, ROWS = Q_THREADS / 32 / W, LANES = 32 * W;
+  __shared__ uint32_t part[2][Q_THREADS / 32];
   const int warp = threadIdx.x >> 5, group = warp / W;
   const int lane = threadIdx.x - group * LANES;
-  const int64_t nv = d / VE;  // VE > 1 only where it divides d
-  for (int64_t n0 = int64_t(blockIdx.x) * ROWS; n0 < N; n0 += int64_t(gridDim.x) * ROWS) {
-    const int64_t n = n0 + group;
-    const bool live = n < N;
-    const T* row = x + (live ? n : 0) * ld;
+  const int nv = int(d / VE);  // VE > 1 only where it divides d
+  int turn = 0;
+  // a row's warps go through the loop together, and wait for nobody else
+  for (int64_t n = int64_t(blockIdx.x) * ROWS + group; n < N; n += int64_t(gridDim.x) * ROWS, turn ^= 1) {
+    const T* row = x + n * ld;
     QVec<T, VE> v[NV];
-    // largest magnitude by its bits: infinities and NaNs lie above every number
     uint32_t most = 0;
-    auto look = [&](const QVec<T, VE>& a) {
-#pragma unroll
-      for (int i = 0; i < VE; ++i) most = max(most, __float_as_uint(a.get(i)) & 0x7FFFFFFFu);
-    };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t at = lane + j * LANES;
-      if (live && at < nv) v[j].load(row + at * VE); else v[j].zero();
+      const int at = lane + j * LANES;
+      if (at < nv) v[j].load(row + at * VE); else v[j].zero();
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) look(v[j]);
-    if (live) {
-      for (int64_t at = lane + NV * LANES; at < nv; at += LANES) {
-        QVec<T, VE> a;
-        a.load(row + at * VE);
-        look(a);
-      }
+    for (int j = 0; j < NV; ++j) most = v[j].largest(most);
+    for (int at = lane + NV * LANES; at < nv; at += LANES) {
+      QVec<T, VE> a;
+      a.load(row + at * VE);
+      most = a.largest(most);
     }
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    most = __reduce_max_sync(0xffffffffu, QVec<T, VE>::as_f32(most));
     if (W > 1) {
-      __syncthreads();  // the last row's have been read
-      if ((threadIdx.x & 31) == 0) part[warp] = __uint_as_float(most);
-      __syncthreads();
+      if ((threadIdx.x & 31) == 0) part[turn][warp] = most;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(LANES) : "memory");
 #pragma unroll
-      for (int w = 0; w < W; ++w) most = max(most, __float_as_uint(part[group * W + w]));
+      for (int w = 0; w < W; ++w) most = max(most, part[turn][group * W + w]);
     }
-    if (!live) continue;
     const float s = most < 0x7F800000u ? __fdiv_rn(__uint_as_float(most), 127.f) : __int_as_float(0x7FC00000);
     const float inv = s > 1e-37f ? 1.f / s : 0.f;
     const bool none = !(s > 0.f);
     if (lane == 0) scale[n] = s;
     int8_t* out = q + n * ldq;
-    auto put = [&](const QVec<T, VE>& a, int64_t at) {
-      uint32_t o[VE / 4 > 0 ? VE / 4 : 1] = {};
-      if (!none) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) o[i / 4] |= quantized(a.get(i), s, inv) << (8 * (i & 3));
-      }
+    auto put = [&](const QVec<T, VE>& a, int at) {
+      uint32_t o[(VE + 3) / 4] = {};
+      if (!none) quantize_vec<VE>(a, s, inv, o);
       if constexpr (VE == 8) *reinterpret_cast<uint2*>(out + at * VE) = make_uint2(o[0], o[1]);
       else if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(out + at * VE) = o[0];
+      else if constexpr (VE == 2) *reinterpret_cast<uint16_t*>(out + at * VE) = uint16_t(o[0]);
       else out[at] = int8_t(o[0]);
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t at = lane + j * LANES;
+      const int at = lane + j * LANES;
       if (at < nv) put(v[j], at);
     }
-    for (int64_t at = lane + NV * LANES; at < nv; at += LANES) {
+    for (int at = lane + NV * LANES; at < nv; at += LANES) {
       QVec<T, VE> a;
       a.load(row + at * VE);
       put(a, at);
@@ -727,19 +755,24 @@ cudaError_t launch_quantize_rows(const T* x, int64_t N, int64_t d, int64_t ld, i
 template <class T, int VE>
 cudaError_t launch_quantize_width(const T* x, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq, float* scale,
                                   cudaStream_t s) {
-  if (d <= 32 * Q_EACH) return launch_quantize_rows<T, VE, 1>(x, N, d, ld, q, ldq, scale, s);
-  if (d <= 64 * Q_EACH) return launch_quantize_rows<T, VE, 2>(x, N, d, ld, q, ldq, scale, s);
-  if (d <= 128 * Q_EACH) return launch_quantize_rows<T, VE, 4>(x, N, d, ld, q, ldq, scale, s);
+  if (d <= 32 * kQEach<T>) return launch_quantize_rows<T, VE, 1>(x, N, d, ld, q, ldq, scale, s);
+  if (d <= 64 * kQEach<T>) return launch_quantize_rows<T, VE, 2>(x, N, d, ld, q, ldq, scale, s);
+  if (d <= 128 * kQEach<T>) return launch_quantize_rows<T, VE, 4>(x, N, d, ld, q, ldq, scale, s);
   return launch_quantize_rows<T, VE, 8>(x, N, d, ld, q, ldq, scale, s);
 }
 
 template <class T>
 cudaError_t launch_quantize_typed(const void* x, int64_t N, int64_t d, int64_t ld, int8_t* q, int64_t ldq,
                                   float* scale, cudaStream_t s) {
-  constexpr int VE = 16 / sizeof(T);
+  // vectors of 16 or 8 bytes where every row allows them
+  constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T);
   const T* p = static_cast<const T*>(x);
-  if (aligned(x, 16) && aligned(q, VE) && d % VE == 0 && (N == 1 || (ld % VE == 0 && ldq % VE == 0)))
-    return launch_quantize_width<T, VE>(p, N, d, ld, q, ldq, scale, s);
+  auto fits = [&](int ve) {
+    return aligned(x, ve * sizeof(T)) && aligned(q, size_t(ve)) && d % ve == 0 &&
+           (N == 1 || (ld % ve == 0 && ldq % ve == 0));
+  };
+  if (fits(V16)) return launch_quantize_width<T, V16>(p, N, d, ld, q, ldq, scale, s);
+  if (fits(V8)) return launch_quantize_width<T, V8>(p, N, d, ld, q, ldq, scale, s);
   return launch_quantize_width<T, 1>(p, N, d, ld, q, ldq, scale, s);
 }
 
