@@ -76,6 +76,16 @@ def test_rows_anywhere(kd, cuda_device, M, N, K, pad_a, pad_b, start):
 def test_short_rows_end_where_they_should(kd, cuda_device, K):
     for start in range(4):
         check(kd, 4, 37, K, torch.float32, 0, 0, start, seed=K)
+        check(kd, 6, 137, K, torch.float32, 0, 0, start, seed=K)
+        check(kd, 70, 300, K, torch.bfloat16, 0, 1, start, seed=K)
+
+
+@pytest.mark.parametrize("M", [1, 3, 7, 70, 300])
+def test_every_start_of_a_row(kd, cuda_device, M):
+    """Rows that start at each of the 16 places of a piece, at every row of a tile."""
+    for start in range(16):
+        check(kd, M, 150, 300, torch.float32, 0, 0, start, seed=start)
+        check(kd, M, 150, 272, torch.float32, 0, start, 0, seed=start)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
