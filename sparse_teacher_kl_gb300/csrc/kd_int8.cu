@@ -105,6 +105,23 @@ struct Turn {
   }
 };
 
+// A CTA's (pair's) units in turn: unit u is channel group u / token_tiles, token tile u % token_tiles.
+struct Walk {
+  int u, group, tile;
+  __device__ __forceinline__ Walk(const T8Problem& p, int first) : u(first), group(first / p.token_tiles) {
+    tile = first - group * p.token_tiles;
+  }
+  __device__ __forceinline__ void step(const T8Problem& p, int by, int by_groups, int by_tiles) {
+    u += by;
+    group += by_groups;
+    tile += by_tiles;
+    if (tile >= p.token_tiles) {
+      tile -= p.token_tiles;
+      ++group;
+    }
+  }
+};
+
 template <class OUT>
 __device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
   return pack_bf16x2(lo, hi);
@@ -113,6 +130,19 @@ template <>
 __device__ __forceinline__ uint32_t pack_out<__half>(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two tokens' values of a channel.
+template <class OUT>
+__device__ __forceinline__ void store_pair(OUT* a, OUT* b, float x, float y) {
+  if constexpr (sizeof(OUT) == 4) {
+    *a = x;
+    *b = y;
+  } else {
+    const uint32_t w = pack_out<OUT>(x, y);
+    *reinterpret_cast<uint16_t*>(a) = uint16_t(w & 0xFFFFu);
+    *reinterpret_cast<uint16_t*>(b) = uint16_t(w >> 16);
+  }
 }
 
 template <int CG, class OUT>
@@ -129,6 +159,7 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
   const uint32_t crank = CG == 2 ? cluster_ctarank() : 0u;
   const int u_first = int(blockIdx.x) / CG, u_step = int(gridDim.x) / CG;
   const int k_stages = (p.K + T8_K - 1) / T8_K;
+  const int step_groups = u_step / p.token_tiles, step_tiles = u_step - step_groups * p.token_tiles;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.w_stages; ++s) {
@@ -173,9 +204,8 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
       uint32_t it = 0;
       Turn r{0, 0};
       bool ok = true;
-      for (int u = u_first; u < p.units && ok; u += u_step) {
-        const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
-        const int row = (wg * CG + int(crank)) * T8_ROWS, tok = tt * p.tokens + int(crank) * rows_t;
+      for (Walk at(p, u_first); at.u < p.units && ok; at.step(p, u_step, step_groups, step_tiles)) {
+        const int row = (at.group * CG + int(crank)) * T8_ROWS, tok = at.tile * p.tokens + int(crank) * rows_t;
         for (int kb = 0; kb < k_stages; ++kb, ++it, r.step(1, stages)) {
           if (!mbar_wait_suspended(&empty[r.at], r.parity ^ 1u, abort_flag, p.err, 0x1100u + warp)) {
             ok = false;
@@ -272,27 +302,28 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
     const int end = half == 0 ? (p.tokens / 2 + 15) / 16 * 16 : p.tokens;
     // a unit's scales are loaded while the one before is written out
     float sb = 0.f, next_sb = 0.f, next_sa[4] = {};
-    auto load_scales = [&](int u) {
-      const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
-      const int n = (wg * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
-      const int tok0 = tt * p.tokens + first, toks = min(end - first, p.M - tok0);
+    auto load_scales = [&](const Walk& at) {
+      const int n = (at.group * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
+      const int tok0 = at.tile * p.tokens + first, toks = min(end - first, p.M - tok0);
       next_sb = n < p.N ? __ldg(p.b_scale + n) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) next_sa[j] = 32 * j + int(lane) < toks ? __ldg(p.a_scale + tok0 + 32 * j + lane) : 0.f;
+      for (int j = 0; j < 4; ++j)
+        next_sa[j] = 32 * j + int(lane) < toks ? __ldg(p.a_scale + tok0 + 32 * j + lane) : 0.f;
     };
-    if (u_first < p.units) load_scales(u_first);
+    Walk next(p, u_first);
+    if (next.u < p.units) load_scales(next);
     Turn acc{0, 0};
-    for (int u = u_first; u < p.units; u += u_step, acc.step(1, accs)) {
-      const int wg = u / p.token_tiles, tt = u - wg * p.token_tiles;
-      const int n = (wg * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
-      const int tok0 = tt * p.tokens + first, toks = min(end - first, p.M - tok0);  // <= 128, may be below 1
+    for (Walk at = next; at.u < p.units; at = next, acc.step(1, accs)) {
+      const int n = (at.group * CG + int(crank)) * T8_ROWS + int(quarter * 32u + lane);
+      const int tok0 = at.tile * p.tokens + first, toks = min(end - first, p.M - tok0);  // <= 128, may be below 1
       float* sa = tail->a_scale[warp - 4u];
       __syncwarp();  // the last unit's have been read
 #pragma unroll
       for (int j = 0; j < 4; ++j) sa[32 * j + lane] = next_sa[j];
       sb = next_sb;
       __syncwarp();
-      if (u + u_step < p.units) load_scales(u + u_step);
+      next.step(p, u_step, step_groups, step_tiles);
+      if (next.u < p.units) load_scales(next);
       const bool got = mbar_wait_suspended(&tail->tfull[acc.at], acc.parity, abort_flag, p.err, 0x1500u);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
@@ -306,6 +337,7 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
         }
       };
       OUT* out = reinterpret_cast<OUT*>(p.C) + int64_t(tok0) * p.ldc + n;
+      const bool whole = __all_sync(0xffffffffu, n < p.N);
       // 16 tokens' values: (sum a_scale) b_scale, each product rounded once
       auto values = [&](int c, float (&v)[16]) {
         uint32_t raw[16];
@@ -337,11 +369,20 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
             }
           }
           if (h != 0) release();
+          if (h + 64 <= toks && whole) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            if (h + c < toks && n < p.N) o[0] = uint16_t(packed[c / 2] & 0xFFFFu);
-            if (h + c + 1 < toks && n < p.N) o[p.ldc] = uint16_t(packed[c / 2] >> 16);
-            o += 2 * p.ldc;
+            for (int c = 0; c < 64; c += 2) {
+              o[0] = uint16_t(packed[c / 2] & 0xFFFFu);
+              o[p.ldc] = uint16_t(packed[c / 2] >> 16);
+              o += 2 * p.ldc;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              if (h + c < toks && n < p.N) o[0] = uint16_t(packed[c / 2] & 0xFFFFu);
+              if (h + c + 1 < toks && n < p.N) o[p.ldc] = uint16_t(packed[c / 2] >> 16);
+              o += 2 * p.ldc;
+            }
           }
         }
       } else {
@@ -351,10 +392,18 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
           float v[16];
           values(c, v);
           if (c + 16 >= toks) release();
+          if (c + 16 <= toks && whole) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (c + i < toks && n < p.N) store_out(out, v[i]);
-            out += p.ldc;
+            for (int i = 0; i < 16; i += 2) {
+              store_pair(out, out + p.ldc, v[i], v[i + 1]);
+              out += 2 * p.ldc;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (c + i < toks && n < p.N) store_out(out, v[i]);
+              out += p.ldc;
+            }
           }
         }
       }
