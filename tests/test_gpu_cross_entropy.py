@@ -304,3 +304,39 @@ def test_called_by_keyword(kd, cuda_device):
     a = kd.fused_cross_entropy(H, W, labels)
     assert torch.equal(kd.fused_cross_entropy(labels=labels, W=W, H=H), a)
     assert torch.equal(kd.fused_cross_entropy_forward(H=H, W=W, labels=labels)[0][0], a)
+
+
+def test_autograd_captured_and_replayed(kd, cuda_device):
+    H, W, labels = case(200, 128, 700, 0.8)
+    h, w = H.clone().requires_grad_(), W.clone().requires_grad_()
+    def step():
+        return torch.autograd.grad(0.5 * kd.fused_cross_entropy(h, w, labels), (h, w))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    H2, W2, l2 = case(200, 128, 700, 0.3, seed=9)
+    with torch.no_grad():
+        h.copy_(H2), w.copy_(W2), labels.copy_(l2)
+    graph.replay()
+    torch.cuda.synchronize()
+    _, gH, gW = kd.fused_cross_entropy_step(H2, W2, l2, grad_W_bf16=True)
+    assert torch.equal(got[0], gH * 0.5) and torch.equal(got[1], gW * 0.5)
+
+
+def test_without_gradients(kd, cuda_device):
+    H, W, labels = case(100, 64, 300)
+    want = kd.fused_cross_entropy_forward(H, W, labels)[0][0]
+    with torch.inference_mode():
+        assert torch.equal(kd.fused_cross_entropy(H, W, labels), want)
+    w = W.clone().requires_grad_()
+    loss = kd.fused_cross_entropy(H, w, labels)
+    loss.backward()
+    assert torch.equal(loss.detach(), want) and torch.isfinite(w.grad).all()
+    first = w.grad.clone()
+    kd.fused_cross_entropy(H, w, labels).backward()     # added to, as any gradient
+    assert torch.equal(w.grad, first + first)
