@@ -507,8 +507,9 @@ KD_API int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* facto
  * integer sum is exact below 2^24 (always for K <= 1024) and rounded to fp32 from there on; each of the two
  * products with a scale rounds once to fp32, and the result once to C's type.  Weights whose rows start on
  * 16-byte boundaries (B and ldb multiples of 16) are read in place, others are copied to such rows
- * in the workspace by every call.  Workspace: `b_rows_aligned` as B's rows are; memory of any content,
- * the error word in `control` (see kd_logits_kl_fwd_ctl).
+ * in the workspace by every call (kd_teacher_topk_int8: once for all its chunks).  Workspace:
+ * `b_rows_aligned` as B's rows are; memory of any content, the error word in `control` (see
+ * kd_logits_kl_fwd_ctl).
  *
  * kd_teacher_topk_int8: kd_teacher_topk from quantised hidden states Ht [N, dt] and head Wt [V, dt]; any
  * chunk >= 1.

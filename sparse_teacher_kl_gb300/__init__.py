@@ -807,13 +807,15 @@ def quantize_int8(x, q=None, scale=None):
     dt, N, d, ld = _check_logits(x, "x")
     given = q, scale
     if q is None:
-        q = torch.empty((N, d), dtype=torch.int8, device=x.device)
+        q, ldq = torch.empty((N, d), dtype=torch.int8, device=x.device), d
+    else:
+        ldq = _check_int8(q, "q", x.device)
+        if q.shape != x.shape:
+            raise ValueError("q must have the shape of x")
     if scale is None:
         scale = torch.empty((N,), dtype=torch.float32, device=x.device)
-    ldq = _check_int8(q, "q", x.device)
-    if q.shape != x.shape:
-        raise ValueError("q must have the shape of x")
-    _check(scale, "scale", torch.float32, (N,), x.device)
+    else:
+        _check(scale, "scale", torch.float32, (N,), x.device)
     st = _abi.kd_quantize_int8(_ptr(x), dt, N, d, ld, _ptr(q), ldq, _ptr(scale), _stream(x.device))
     _abi.check(st, "kd_quantize_int8")
     _written(*given)
@@ -852,14 +854,17 @@ def gemm_int8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, ws=Non
     if out is None:
         if out_dtype not in _DTYPES:
             raise ValueError("out_dtype must be bf16, fp16 or fp32")
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    if out.device != dev or out.shape != (M, N):
-        raise ValueError(f"out must be [{M}, {N}] on {dev}")
-    dt, _, _, ldc = _check_logits(out, "out")
+        out, dt, ldc = torch.empty((M, N), dtype=out_dtype, device=dev), _DTYPES[out_dtype], N
+    else:
+        if out.device != dev or out.shape != (M, N):
+            raise ValueError(f"out must be [{M}, {N}] on {dev}")
+        dt, _, _, ldc = _check_logits(out, "out")
     control = ws
     if ws is None:
-        control = _control(dev)
-        ws = _scratch(_abi.kd_gemm_int8_workspace(M, N, K, _rows_aligned(B, ldb)), dev)
+        ws = control = _control(dev)
+        need = _abi.kd_gemm_int8_workspace(M, N, K, _rows_aligned(B, ldb))
+        if need > ws.numel():  # few tokens need the control block alone
+            ws = _scratch(need, dev)
     st = _abi.kd_gemm_int8(_ptr(A), lda, _ptr(a_scale), _ptr(B), ldb, _ptr(b_scale), _ptr(out), dt, ldc, M, N, K,
                            _ptr(ws), ws.numel(), _ptr(control), _stream(dev))
     _abi.check(st, "kd_gemm_int8")

@@ -31,8 +31,9 @@ namespace {
 // deep a stage.  Tensor memory's 512 columns: four stages of widened weights, which cover the way from an
 // MMA's end over the barriers to the next weights' arrival (about 1300 cycles; two stages left the tensor
 // cores waiting a third of the time), and one accumulator of up to 256 tokens, or two of up to 128.  One large
-// accumulator, whose draining the next tile waits for, beats two of 192: the thread that issues the MMAs
-// needs about 60 cycles for each, so short ones (96 cycles for 192 tokens) leave it none for its barriers.
+// accumulator, whose draining the next tile waits for, beats two of 192 (4096 x 2880 x 201088 3.5 ms against 3.95,
+// before the later steps): an MMA takes 40 to 60 cycles to issue, and short ones (96 cycles for 192 tokens)
+// leave the issuing warp little for its barriers.
 constexpr int T8_ROWS = 128;
 constexpr int T8_K = 128;
 constexpr int T8_W_BYTES = T8_ROWS * T8_K;      // a stage's weights: 16 KB
@@ -971,11 +972,7 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
   const void* weights = B;
   uint64_t w_stride = uint64_t(ldb);
   if (!rows16) {
-    prof_before("kd_int8_rows", s);
-    kd_int8_rows_kernel<<<blocks_for(N * (L.Kw / 16), 16), 256, 0, s>>>(B, ldb, N, int(K), int(L.Kw),
-                                                                       reinterpret_cast<uint4*>(ws + L.weights));
-    prof_after(s);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_int8_rows(B, ldb, N, K, L.Kw, ws + L.weights, s)) != cudaSuccess) return e;
     weights = ws + L.weights;
     w_stride = uint64_t(L.Kw);
   }
@@ -1004,6 +1001,16 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
     return cudaErrorInvalidValue;
   return cg == 1 ? launch_t8_typed<1>(dtype, p, tw, tt, s) : launch_t8_typed<2>(dtype, p, tw, tt, s);
 }
+
+cudaError_t launch_int8_rows(const int8_t* B, int64_t ldb, int64_t N, int64_t K, int64_t Kw, void* out,
+                             cudaStream_t s) {
+  prof_before("kd_int8_rows", s);
+  kd_int8_rows_kernel<<<blocks_for(N * (Kw / 16), 16), 256, 0, s>>>(B, ldb, N, int(K), int(Kw), static_cast<uint4*>(out));
+  prof_after(s);
+  return cudaGetLastError();
+}
+
+bool gemm_int8_copies_rows(int64_t M, int64_t N, int64_t K) { return !int8_few(M, N, K, false); }
 
 size_t gemm_int8_scratch(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
   return int8_layout(M, N, K, aligned_rows).total;

@@ -6,7 +6,7 @@ using namespace kd;
 
 namespace {
 
-constexpr int64_t kMaxInt = 0x7fffffffLL;
+constexpr int64_t kMaxInt = 0x7fffffffLL, kMaxRows = kMaxInt - 1023;  // a tile behind the last row still counts
 
 size_t out_size(int dtype) { return dtype == KD_F32 ? 4 : 2; }
 bool rows16(const void* B, int64_t ldb) { return aligned(B, 16) && ldb % 16 == 0; }
@@ -14,12 +14,12 @@ bool ok4(const void* p) { return p != nullptr && aligned(p, 4); }
 
 // An integer matrix [rows, K] with row stride ld and its scales.
 bool ok_matrix(const void* q, int64_t ld, const void* scale, int64_t rows, int64_t K) {
-  return q && rows >= 1 && rows <= kMaxInt && K >= 1 && K <= KD_MAX_INT8_K && ld >= K && ok4(scale);
+  return q && rows >= 1 && rows <= kMaxRows && K >= 1 && K <= KD_MAX_INT8_K && ld >= K && ok4(scale);
 }
 
 struct TopkLayout {
-  size_t logits, gemm, scratch, total;
-  int64_t ldz;
+  size_t logits, gemm, weights, scratch, total;
+  int64_t ldz, ldw;  // ldw: row stride of the copied weights, 0 where they are read in place
 };
 
 TopkLayout topk_layout(int64_t N, int64_t dt, int64_t V, int K, int64_t chunk, bool aligned_rows) {
@@ -27,8 +27,15 @@ TopkLayout topk_layout(int64_t N, int64_t dt, int64_t V, int K, int64_t chunk, b
   const int64_t c = chunk < N ? chunk : N;
   L.ldz = (V + 7) / 8 * 8;
   L.logits = sizeof(Ctrl);
+  // weights whose rows do not start on 16-byte boundaries: copied once for all chunks
+  L.ldw = !aligned_rows && gemm_int8_copies_rows(c, V, dt) ? (dt + 15) / 16 * 16 : 0;
   L.gemm = align_up(L.logits + size_t(c) * size_t(L.ldz) * 2, 256);
-  L.scratch = align_up(L.gemm + gemm_int8_scratch(c, V, dt, aligned_rows), 256);
+  // the last chunk is shorter, and may take the other way
+  const int64_t last = (N - 1) % c + 1;
+  const bool in_place = aligned_rows || L.ldw;
+  const size_t one = gemm_int8_scratch(c, V, dt, in_place), two = gemm_int8_scratch(last, V, dt, in_place);
+  L.weights = align_up(L.gemm + (one > two ? one : two), 256);
+  L.scratch = align_up(L.weights + size_t(V) * size_t(L.ldw), 256);
   L.total = L.scratch + align_up(topk_scratch_bytes(c, K), 256);
   return L;
 }
@@ -88,6 +95,11 @@ int kd_teacher_topk_int8(const int8_t* Ht, int64_t ld_h, const float* h_scale, c
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   uint16_t* logits = reinterpret_cast<uint16_t*>(w8 + L.logits);
   uint32_t* err = &static_cast<Ctrl*>(control)->err;
+  if (L.ldw) {
+    if (launch_int8_rows(Wt, ld_w, V, dt, L.ldw, w8 + L.weights, s) != cudaSuccess) return KD_ERR_CUDA;
+    Wt = reinterpret_cast<const int8_t*>(w8 + L.weights);
+    ld_w = L.ldw;
+  }
   for (int64_t c0 = 0; c0 < N; c0 += chunk) {
     const int64_t n = (N - c0) < chunk ? (N - c0) : chunk;
     // the chunk's logits, rounded once to bf16, then their exact top-K

@@ -300,6 +300,10 @@ cudaError_t launch_masked_mean(const float* kl, const uint8_t* mask, int64_t N, 
 
 // 8-bit integers (kd_int8.cu).  ws: gemm_int8_scratch bytes, its first 256 left alone; aligned_rows: the rows of
 // B start on 16-byte boundaries.
+// Rows that do not are copied (to rows of Kw, a multiple of 16) where gemm_int8_copies_rows says so.
+bool gemm_int8_copies_rows(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_int8_rows(const int8_t* B, int64_t ldb, int64_t N, int64_t K, int64_t Kw, void* out,
+                             cudaStream_t s);
 size_t gemm_int8_scratch(int64_t M, int64_t N, int64_t K, bool aligned_rows);
 cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
                              const float* b_scale, void* C, int dtype, int64_t ldc, int64_t M, int64_t N, int64_t K,

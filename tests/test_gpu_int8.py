@@ -188,7 +188,8 @@ def test_quantize_into_the_callers(kd, cuda_device):
     assert s is scale and torch.equal(q, rq) and torch.equal(scale, rs) and (room[:, 100:] == 5).all()
 
 
-@pytest.mark.parametrize("N,d,V,K,chunk", [(1, 64, 1000, 10, 1024), (70, 96, 3000, 100, 32), (130, 200, 1111, 33, 1024)])
+@pytest.mark.parametrize("N,d,V,K,chunk", [(1, 64, 1000, 10, 1024), (70, 96, 3000, 100, 32), (130, 200, 1111, 33, 1024),
+                                           (67, 101, 700, 20, 32), (9, 64, 500, 7, 4), (5, 33, 400, 5, 2)])
 @pytest.mark.parametrize("pad", [0, 3])
 def test_teacher(kd, cuda_device, N, d, V, K, chunk, pad):
     """Quantised states and head to a cache: the top-K of the bf16 logits that the product's definition gives."""

@@ -37,7 +37,7 @@ def gemm(lib, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(A=None), dict(B=None), dict(C=None), dict(sa=None), dict(sb=None), dict(sa=P + 1), dict(sb=P + 2),
-    dict(lda=63), dict(ldb=63), dict(ldc=99), dict(M=0), dict(N=0), dict(K=0), dict(M=1 << 31), dict(N=1 << 31),
+    dict(lda=63), dict(ldb=63), dict(ldc=99), dict(M=0), dict(N=0), dict(K=0), dict(M=1 << 31), dict(N=1 << 31), dict(M=(1 << 31) - 512), dict(N=(1 << 31) - 1, ldc=1 << 31),
     dict(K=65537, lda=65537, ldb=65537), dict(dt=3), dict(dt=-1), dict(C=P + 1), dict(dt=2, C=P + 2),
     dict(M=(1 << 31) - 1, N=(1 << 31) - 1, ldc=1 << 31)])
 def test_gemm_refuses(lib, kw):
