@@ -412,47 +412,47 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
         unit_coords(p, ext, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
         const int k_step = EPI == EPI_CE ? CE_CHUNK_K / (BK * G::kKB) : kb_hi - kb_lo;
         for (int nb = n_first; nb < n_first + n_count && ok; ++nb) {
-         // an accumulator for each k_step stages of the reduction: all of them but for EPI_CE
-         for (int kc = kb_lo; kc < kb_hi && ok; kc += k_step, ++acc_it) {
-          const uint32_t a = acc_it & 1u;
-          const uint32_t aph = (acc_it >> 1) & 1u;
-          if (!mbar_wait(&tail->tempty[a], aph ^ 1u, abort_flag, p.err, 0x200u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d_tmem = tmem_base + a * BN;
-          const int kb_end = min(kb_hi, kc + k_step);
-          for (int kb = kc; kb < kb_end; ++kb, ++it) {
-            const uint32_t s = it % G::kStages;
-            const uint32_t ph = (it / G::kStages) & 1u;
-            if (!mbar_wait(&tail->full[s], ph, abort_flag, p.err, 0x300u)) {
+          // an accumulator for each k_step stages of the reduction: all of them but for EPI_CE
+          for (int kc = kb_lo; kc < kb_hi && ok; kc += k_step, ++acc_it) {
+            const uint32_t a = acc_it & 1u;
+            const uint32_t aph = (acc_it >> 1) & 1u;
+            if (!mbar_wait(&tail->tempty[a], aph ^ 1u, abort_flag, p.err, 0x200u)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = smem_u32(stage_base + size_t(s) * G::kStage);
-            const uint32_t sb = sa + G::kA;
-            // 16-deep steps of this stage inside K (a pair's last stage may hold one
-            // k-block of zeros past the end of K: skip its MMAs)
-            const int ksteps = (ext.K - kb * BK * G::kKB + 15) / 16;
+            const uint32_t d_tmem = tmem_base + a * BN;
+            const int kb_end = min(kb_hi, kc + k_step);
+            for (int kb = kc; kb < kb_end; ++kb, ++it) {
+              const uint32_t s = it % G::kStages;
+              const uint32_t ph = (it / G::kStages) & 1u;
+              if (!mbar_wait(&tail->full[s], ph, abort_flag, p.err, 0x300u)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(stage_base + size_t(s) * G::kStage);
+              const uint32_t sb = sa + G::kA;
+              // 16-deep steps of this stage inside K (a pair's last stage may hold one
+              // k-block of zeros past the end of K: skip its MMAs)
+              const int ksteps = (ext.K - kb * BK * G::kKB + 15) / 16;
 #pragma unroll
-            for (int k = 0; k < G::kKB * (BK / 16); ++k) {
-              if (CG == 2 && k >= BK / 16 && k >= ksteps) break;
-              const uint32_t a_off = p.a_mn ? uint32_t(k) * 2048u : uint32_t(k >> 2) * (G::kA / G::kKB) + (k & 3) * 32u;
-              const uint32_t b_off = p.b_mn ? uint32_t(k) * 2048u : uint32_t(k >> 2) * (G::kB / G::kKB) + (k & 3) * 32u;
-              const uint64_t ad = sdesc_sw128(sa + a_off, a_lbo);
-              const uint64_t bd = sdesc_sw128(sb + b_off, b_lbo);
-              if (CG == 2) umma_bf16_pair(d_tmem, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
-              else umma_bf16(d_tmem, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
+              for (int k = 0; k < G::kKB * (BK / 16); ++k) {
+                if (CG == 2 && k >= BK / 16 && k >= ksteps) break;
+                const uint32_t a_off = p.a_mn ? uint32_t(k) * 2048u : uint32_t(k >> 2) * (G::kA / G::kKB) + (k & 3) * 32u;
+                const uint32_t b_off = p.b_mn ? uint32_t(k) * 2048u : uint32_t(k >> 2) * (G::kB / G::kKB) + (k & 3) * 32u;
+                const uint64_t ad = sdesc_sw128(sa + a_off, a_lbo);
+                const uint64_t bd = sdesc_sw128(sb + b_off, b_lbo);
+                if (CG == 2) umma_bf16_pair(d_tmem, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
+                else umma_bf16(d_tmem, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
+              }
+              if (CG == 2) umma_commit_pair_mc(&tail->empty[s], 0x3);
+              else umma_commit(&tail->empty[s]);
             }
-            if (CG == 2) umma_commit_pair_mc(&tail->empty[s], 0x3);
-            else umma_commit(&tail->empty[s]);
+            if (ok) {
+              if (CG == 2) umma_commit_pair_mc(&tail->tfull[a], 0x3); else umma_commit(&tail->tfull[a]);
+            }
           }
-          if (ok) {
-            if (CG == 2) umma_commit_pair_mc(&tail->tfull[a], 0x3); else umma_commit(&tail->tfull[a]);
-          }
-         }
         }
       }
       // Drain: every MMA issued above has completed once this arrives.
