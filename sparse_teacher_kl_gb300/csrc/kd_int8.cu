@@ -980,8 +980,8 @@ cudaError_t launch_gemm_int8(const int8_t* A, int64_t lda, const float* a_scale,
   T8Problem p{};
   p.M = int(M); p.N = int(N); p.K = int(K);
   // Short reductions leave the draining of a large accumulator waited for too often.  us with at most 256 / 128
-  // tokens a tile: 2000 x 100000, K = 256 221 / 194, K = 512 234 / 222; 2000 x 50000, K = 1024 153 / 174, 1500
-  // 225 / 274.
+  // tokens a tile: 2000 x 100000, K = 256 158 / 146, K = 512 205 / 176, K = 768 250 / 240; 2000 x 50000, K = 1024
+  // 154 / 159, K = 1536 201 / 224.
   const int most = K <= T8_SHORT_K ? T8_TWO_ACC : T8_MAX_TOKENS;
   p.token_tiles = int((M + most - 1) / most);
   const int64_t even = (M + p.token_tiles - 1) / p.token_tiles;  // tiles of nearly the same size
