@@ -160,8 +160,8 @@ static_assert(kThreads<EPI_STORE> == GEMM_THREADS, "TMA warp, MMA warp, 4 epilog
 // The tensor cores cut each addition to an accumulator off where it should be rounded, so that a sum of n
 // steps of 16 is about n 2^-26 of itself too near to 0: 2e-6 of a label's logit at d = 2048, and of the losses.
 // EPI_CE therefore takes the reduction CE_CHUNK_K deep at a time and adds the parts in registers, in the time of
-// the next part's MMAs: losses at d = 3320 within 6.5e-7 of float64 (in one piece 2.6e-6), for 4 % of the projection
-// (4096 x 2880 x 201088 2.69 ms; 512 deep 2.73).
+// the next part's MMAs.  512 deep: the losses of 3 positions that lean towards their labels, d = 2328, are within
+// 5.3e-7 of float64 (1024 deep 1.4e-6), for 6 % of the projection (4096 x 2880 x 201088 2.73 ms; 1024 deep 2.69).
 __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap& tmap_c, float (&z)[CE_COLS], int first,
                                         int m_blk, int row, int rows, int nid, uint8_t* box, uint32_t lane,
                                         uint32_t quarter) {

@@ -159,7 +159,7 @@ struct GemmProblem {
 // anything 32 and further below (e^-32 of the largest, 1.3e-14).  Half a step makes 2.4e-4 of a
 // probability, an eighth of the rounding of bf16 dZ; bf16 logits would make 2^-8 of every unit of |z|.
 constexpr int CE_COLS = BN / 2;
-constexpr int CE_CHUNK_K = 1024;  // depth of EPI_CE's partial sums
+constexpr int CE_CHUNK_K = 512;   // depth of EPI_CE's partial sums
 constexpr float CE_STEPS = 2048.f;
 
 
