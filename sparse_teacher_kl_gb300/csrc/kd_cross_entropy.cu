@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(GATHER_WARPS * 32)
 
 // ------------------------------------------------------------------ row sums ---
 // A row's tiles put together: its loss and logsumexp to the position's place and, for a step, what dZ
-// takes of it: (lse, a, b, dz_y) with dZ_v = (a p_v - b) slope_v.  dZ leaves out alpha = G (1 - e), which is every
+// takes of it: (M, a, b, dz_y) with dZ_v = (a e^(z'_v - M) - b) slope_v, M the largest logit: 1 / S is in a, since
+// M + ln S would be rounded at its own size (logits of 1e6: to 1/16).  dZ leaves out alpha = G (1 - e), which is every
 // entry's and joins the fp32 products: the label's entry is then 1 - p_y / (1 - e) and not G times that, whose
 // rounding to bf16 would be the same in every row that the model has not learnt (p_y near 0), up to 2^-8 of the
 // gradients.  32 threads share a row's tiles (as the other combines: a thread's tiles are a chain of dependent
@@ -203,13 +204,13 @@ __global__ void __launch_bounds__(CC_ROWS * CC_PHASES) kd_ce_combine_kernel(cons
   a.lse[pos] = lse;
   a.losses[pos] = bad ? __int_as_float(0x7FC00000) : nll + a.smooth * mean_off + a.z_loss * lse * lse;
   if (a.row_stats == nullptr) return;
-  float4 st = make_float4(lse, 0.f, 0.f, 0.f);
+  float4 st = make_float4(M, 0.f, 0.f, 0.f);
   if (!bad) {
-    const float scale = 1.f / (1.f - a.smooth);
-    st.y = scale * fmaf(2.f * a.z_loss, lse, 1.f);
+    const float scale = 1.f / (1.f - a.smooth), of_p = scale * fmaf(2.f * a.z_loss, lse, 1.f);
+    st.y = of_p / S;
     st.z = scale * (a.smooth / float(a.V));
     const float t = a.softcap > 0.f ? Y / a.softcap : 0.f;
-    st.w = (st.y * exp2f(-nll * kLog2E) - st.z - 1.f) * fmaf(-t, t, 1.f);
+    st.w = (of_p * exp2f(-nll * kLog2E) - st.z - 1.f) * fmaf(-t, t, 1.f);
   }
   a.row_stats[r] = st;
 }
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(256)
     const float4 st = row_stats[r];
     const float m = partials[size_t(tile) * ld_part + r].x;
     const int label = labels_c[r];
-    // columns of nothing but -inf have no probability, whatever their distances (then m - lse is -inf)
+    // columns of nothing but -inf have no probability, whatever their distances (then m - M is -inf)
     const float shift = (m - st.x) * kLog2E;
 #pragma unroll
     for (int b = 0; b < DQ_BLOCKS; ++b) {

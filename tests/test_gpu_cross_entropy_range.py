@@ -1,0 +1,48 @@
+"""fused_cross_entropy where its numbers end: logits far from zero and beyond 2^64, columns and labels at -inf.
+
+One position a coordinate: H has a single 1 (or one power of two) in each row, so a row's logits are a column of W
+times it, exact bf16 numbers, and grad_W holds dZ itself.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def kd(cuda_device):
+    from sparse_teacher_kl_gb300.build import build_library
+    build_library()
+    import sparse_teacher_kl_gb300 as kd
+    return kd
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def close(got, want, each):
+    """dZ: rounded to bf16 once (2^-8 of the entry), 2^-11 of a probability for its 16-bit distance, 1e-6 the rest."""
+    assert torch.isfinite(got).all()
+    assert ((got.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want.abs() + each).all()
+
+
+@pytest.mark.parametrize("size", [1e4, 1e5, 1e6, 1e9, 1e15])
+@pytest.mark.parametrize("smooth", [0.0, 0.1])
+def test_equal_logits_far_from_zero(kd, cuda_device, size, smooth):
+    """Row n has n + 2 logits at its largest, so far from zero that lse = size + ln(n + 2) is not an fp32 number:
+    each of them has a probability of 1 / (n + 2)."""
+    N, V = 8, 1000
+    H = torch.eye(N, device="cuda").to(torch.bfloat16)
+    W = (torch.randn((V, N), generator=gen(3), device="cuda") * 0.1 * size).clamp(max=0.5 * size)
+    for n in range(N):
+        W[torch.arange(n + 2) * 90 + 3 * n, n] = size
+    W = W.to(torch.bfloat16)
+    labels = torch.arange(N, device="cuda", dtype=torch.int32) * 3
+    labels[::2] += 1                            # half of the labels among them
+    _, _, gW = kd.fused_cross_entropy_step(H, W, labels, label_smoothing=smooth)
+    want = W.double().T.softmax(1) - smooth / V
+    want[torch.arange(N), labels.long()] -= 1 - smooth
+    close(gW.T, want / N, 1e-6)
