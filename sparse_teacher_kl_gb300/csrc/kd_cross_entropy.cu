@@ -225,7 +225,8 @@ __device__ __forceinline__ float dz_of(uint32_t q, float shift, float m, const f
   const float far = float(q);
   const float p = ex2_approx(fmaf(far, -kLog2E / CE_STEPS, shift));
   const float z = fmaf(far, -1.f / CE_STEPS, m);
-  return fmaf(st.y, p, -st.z) * fmaf(-z * z, cap2, 1.f);
+  const float d = fmaf(st.y, p, -st.z);
+  return cap2 > 0.f ? d * fmaf(-z * z, cap2, 1.f) : d;  // without a cap z may be infinite, or its square
 }
 
 __global__ void __launch_bounds__(256)

@@ -46,3 +46,47 @@ def test_equal_logits_far_from_zero(kd, cuda_device, size, smooth):
     want = W.double().T.softmax(1) - smooth / V
     want[torch.arange(N), labels.long()] -= 1 - smooth
     close(gW.T, want / N, 1e-6)
+
+
+@pytest.mark.parametrize("size", [1e18, 3e19, 1e25, 1e37])
+def test_logits_whose_squares_overflow(kd, cuda_device, size):
+    N, V = 8, 1000
+    H = torch.eye(N, device="cuda").to(torch.bfloat16)
+    W = (torch.randn((V, N), generator=gen(1), device="cuda") * size).to(torch.bfloat16)
+    labels = torch.arange(0, 8 * N, 8, device="cuda", dtype=torch.int32)
+    each = torch.empty((N,), device="cuda")
+    _, gH, gW = kd.fused_cross_entropy_step(H, W, labels, loss_out=each, grad_H_fp32=True)
+    z = W.double().T
+    want = z.softmax(1)
+    want[torch.arange(N), labels.long()] -= 1
+    losses = z.logsumexp(1) - z.gather(1, labels.long()[:, None])[:, 0]
+    assert ((each.double() - losses).abs() <= 1e-6 * z.abs().amax(1)).all()
+    close(gW.T, want / N, 1e-6)
+    full = want / N @ W.double()
+    assert torch.isfinite(gH).all() and ((gH.double() - full).abs() <= 2 * 2.0 ** -8 * (want.abs() / N @ W.double().abs())).all()
+
+
+@pytest.mark.parametrize("V", [300, 1000])
+def test_columns_of_nothing_but_minus_infinity(kd, cuda_device, V):
+    """Columns 128 .. 255 overflow to -inf for every position: no probability, no gradient, the others as ever."""
+    N, d = 6, 16
+    H = torch.zeros((N, d), device="cuda")
+    H[:, :N] = torch.eye(N)
+    H[:, 8] = 1e20
+    W = torch.randn((V, d), generator=gen(2), device="cuda") * 2
+    W[:, 8] = 0
+    W[128:256, 8] = -1e20
+    H, W = H.to(torch.bfloat16), W.to(torch.bfloat16)
+    labels = torch.tensor([0, 5, 127, 256, 270, 299], device="cuda", dtype=torch.int32)
+    loss, gH, gW = kd.fused_cross_entropy_step(H, W, labels, grad_H_fp32=True)
+    z = H.double() @ W.double().T
+    lp = z.log_softmax(1)
+    dz = lp.exp()
+    dz[torch.arange(N), labels.long()] -= 1
+    dz /= N
+    assert abs(float(loss) + float(lp.gather(1, labels.long()[:, None]).mean())) < 1e-5
+    assert not gW[128:256].any()
+    close(gW[:, :N].T, dz, 1e-6)
+    keep = [i for i in range(d) if i != 8]
+    bound = 2 * 2.0 ** -8 * (dz.abs() @ W.double().abs())
+    assert torch.isfinite(gH).all() and ((gH.double() - dz @ W.double()).abs() <= bound + 1e-6)[:, keep].all()
