@@ -470,8 +470,10 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
  * NULL: 1) known beforehand: one projection and two products in place of the two and two that a
  * separate backward pass needs.
  *   grad_H : [N, d] bf16 or fp32, zero rows where not valid.  grad_W, grad_W_kind as for
- *            kd_fused_logprobs_bwd.  dZ is rounded to bf16; probabilities below e^-32 of the
- *            largest of their 128 columns are taken as that.
+ *            kd_fused_logprobs_bwd.  dZ is rounded to bf16, from logits kept in 16 bits: a probability
+ *            is off by 2.4e-4 of itself at most (with a softcap c below 16: 3.1e-5 c), a cap's slope by 6e-5 (3e-5
+ *            from c = 16 on), and by 0.04 % of a slope of 0.01 up to c = 16; probabilities below e^-32 (with a
+ *            softcap above 16: e^-28) of the largest of their 128 columns are known to be that small only.
  * Workspace: `step` != 0 asks for the step's (it grows with chunk * V), 0 for the forward pass's
  * (chunk * (V / 16 + 2 d) bytes).  `ws` may be memory of any content; the error word is in `control`
  * (see kd_logits_kl_fwd_ctl), which may be `ws` itself once kd_workspace_clear has cleared it.

@@ -9,8 +9,8 @@
 //
 // What a step cannot do without is 6 N d V operations (one projection, two gradient products); what it
 // must move is H, W and the two gradients.  The usual way to keep no logits is to project twice (8 N d V).
-// Here the projection's epilogue leaves each chunk's logits as 16-bit distances from the largest of
-// their CE_COLS columns (CE_STEPS; 2 bytes each, in the buffer that dZ needs anyway), and once a row's sum is
+// Here the projection's epilogue leaves each chunk's logits in 16 bits (CeCode: distances from the largest of
+// their CE_COLS columns, with a softcap a code that keeps its slope; in the buffer that dZ needs anyway), and once a row's sum is
 // known one pass over that buffer turns them into bf16 dZ where they lie: 6 bytes moved for each logit
 // against 2 d operations, 0.9 ns against 3.3 ns per thousand at d = 2880.  The label's own entry, where
 // p_y - 1 would cancel, comes from its fp32 logit.
@@ -209,26 +209,48 @@ __global__ void __launch_bounds__(CC_ROWS * CC_PHASES) kd_ce_combine_kernel(cons
     const float scale = 1.f / (1.f - a.smooth), of_p = scale * fmaf(2.f * a.z_loss, lse, 1.f);
     st.y = of_p / S;
     st.z = scale * (a.smooth / float(a.V));
-    const float t = a.softcap > 0.f ? Y / a.softcap : 0.f;
-    st.w = (of_p * exp2f(-nll * kLog2E) - st.z - 1.f) * fmaf(-t, t, 1.f);
+    st.w = of_p * exp2f(-nll * kLog2E) - st.z - 1.f;
+    if (a.softcap > 0.f) {
+      const float e = fmaxf(a.softcap - fabsf(Y), 0.f) / a.softcap;
+      st.w *= e * (2.f - e);
+    }
   }
   a.row_stats[r] = st;
 }
 
 // ------------------------------------------------------------------ dZ ---
-// The chunk's 16-bit distances to bf16 dZ, in place ([V / 64][row][64], both).  A block takes 128 rows of
+// The chunk's 16-bit codes to bf16 dZ, in place ([V / 64][row][64], both).  A block takes 128 rows of
 // CE_COLS columns: 8 lanes to a 128-byte row of a 64-column block, 8 vectors of 16 bytes in flight a thread.
 // Bound by HBM: 4 bytes a logit.
 constexpr int DQ_ROWS = 128, DQ_BLOCKS = CE_COLS / 64;
 
-__device__ __forceinline__ float dz_of(uint32_t q, float shift, float m, const float4& st, float cap2) {
-  const float far = float(q);
-  const float p = ex2_approx(fmaf(far, -kLog2E / CE_STEPS, shift));
-  const float z = fmaf(far, -1.f / CE_STEPS, m);
-  const float d = fmaf(st.y, p, -st.z);
-  return cap2 > 0.f ? d * fmaf(-z * z, cap2, 1.f) : d;  // without a cap z may be infinite, or its square
+// What the entries of a row's CE_COLS columns take of it: dZ = (a e^(z' - M) - b) slope.
+struct DzRow {
+  float a, b, m, M, shift, cap, cap_inv;
+};
+
+// An entry from its code (CeCode).  Where no column of the CE_COLS is above -inf, m - M is -inf and p is 0.
+template <CeCode CODE>
+__device__ __forceinline__ float dz_of(uint32_t q, const DzRow& r) {
+  if (CODE == CE_CODE_EDGE) {
+    const float w = float(q & 0x7FFFu) * (1.f / CE_EDGE_STEPS), e = w * w;  // e = 1 - |z'| / c
+    const float z = __uint_as_float(__float_as_uint(fmaf(-r.cap, e, r.cap)) | (q & 0x8000u) << 16);
+    return fmaf(r.a, ex2_approx((z - r.M) * kLog2E), -r.b) * (e * (2.f - e));
+  }
+  float shift = fmaf(float(q), -kLog2E / CE_STEPS, r.shift);
+  if (CODE == CE_CODE_DIST) return fmaf(r.a, ex2_approx(shift), -r.b);
+  const float z = fmaf(float(q), -1.f / CE_STEPS, r.m);
+  float e = fmaxf(r.cap - fabsf(z), 0.f) * r.cap_inv, slope = e * (2.f - e);
+  if (q >= CE_SPLIT_CODE) {
+    const float w = float(q - CE_SPLIT_CODE) * (1.f / CE_FAR_STEPS);
+    e = w * w;  // (z' + c) / 2 c, whose step may be wide (c / 4096): the distance is known to be CE_SPLIT at least
+    shift = fmaf(fminf(r.cap * fmaf(2.f, e, -1.f) - r.m, -CE_SPLIT), kLog2E, r.shift);
+    slope = 4.f * e * (1.f - e);
+  }
+  return fmaf(r.a, ex2_approx(shift), -r.b) * slope;
 }
 
+template <CeCode CODE>
 __global__ void __launch_bounds__(256)
     kd_ce_dz_kernel(uint4* __restrict__ dz, int rows_pad, int64_t nvb, const float4* __restrict__ partials, int ld_part,
                     const float4* __restrict__ row_stats, const int32_t* __restrict__ labels_c,
@@ -238,7 +260,6 @@ __global__ void __launch_bounds__(256)
   const uint32_t row_blocks = uint32_t(cap + DQ_ROWS - 1) / DQ_ROWS;
   const int tile = int(blockIdx.x / row_blocks), lane8 = threadIdx.x & 7;
   const int first = int(blockIdx.x - uint32_t(tile) * row_blocks) * DQ_ROWS, r0 = first + (threadIdx.x >> 3);
-  const float cap2 = softcap > 0.f ? 1.f / (softcap * softcap) : 0.f;
   if (first >= end) return;
   const int vb0 = tile * DQ_BLOCKS;
   uint4 v[DQ_ROWS / 32][DQ_BLOCKS];
@@ -258,10 +279,15 @@ __global__ void __launch_bounds__(256)
       continue;
     }
     const float4 st = row_stats[r];
-    const float m = partials[size_t(tile) * ld_part + r].x;
+    DzRow row{};
+    row.a = st.y; row.b = st.z; row.M = st.x;
+    row.m = partials[size_t(tile) * ld_part + r].x;
+    row.shift = (row.m - row.M) * kLog2E;
+    if (CODE != CE_CODE_DIST) {
+      row.cap = softcap;
+      row.cap_inv = 1.f / softcap;
+    }
     const int label = labels_c[r];
-    // columns of nothing but -inf have no probability, whatever their distances (then m - M is -inf)
-    const float shift = (m - st.x) * kLog2E;
 #pragma unroll
     for (int b = 0; b < DQ_BLOCKS; ++b) {
       if (vb0 + b >= nvb) break;
@@ -270,7 +296,7 @@ __global__ void __launch_bounds__(256)
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float lo = dz_of(w[i] & 0xFFFFu, shift, m, st, cap2), hi = dz_of(w[i] >> 16, shift, m, st, cap2);
+        float lo = dz_of<CODE>(w[i] & 0xFFFFu, row), hi = dz_of<CODE>(w[i] >> 16, row);
         lo = off == 2 * i ? st.w : lo;
         hi = off == 2 * i + 1 ? st.w : hi;
         o[i] = pack_bf16x2(lo, hi);
@@ -278,6 +304,19 @@ __global__ void __launch_bounds__(256)
       dz[(size_t(vb0 + b) * rows_pad + r) * 8 + lane8] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+}
+
+cudaError_t launch_ce_dz(unsigned blocks, cudaStream_t s, uint4* dz, int rows_pad, int64_t nvb, const float4* partials,
+                         int ld_part, const float4* row_stats, const int32_t* labels_c, const int32_t* n_valid,
+                         int64_t c0, int cap, float softcap) {
+  const CeCode code = ce_code(softcap);
+  auto* k = code == CE_CODE_DIST   ? kd_ce_dz_kernel<CE_CODE_DIST>
+            : code == CE_CODE_EDGE ? kd_ce_dz_kernel<CE_CODE_EDGE>
+                                   : kd_ce_dz_kernel<CE_CODE_SPLIT>;
+  prof_before("kd_ce_dz", s);
+  k<<<blocks, 256, 0, s>>>(dz, rows_pad, nvb, partials, ld_part, row_stats, labels_c, n_valid, c0, cap, softcap);
+  prof_after(s);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ split sums ---
@@ -572,12 +611,9 @@ int ce_run(const CeCall& a, bool step) {
     KD_TRY(cudaGetLastError());
     if (!step) continue;
 
-    prof_before("kd_ce_dz", s);
-    kd_ce_dz_kernel<<<unsigned((n + DQ_ROWS - 1) / DQ_ROWS) * unsigned(L.tiles), 256, 0, s>>>(
-        reinterpret_cast<uint4*>(w8 + L.dz), int(L.rows_pad), L.nvb, partials, c.rows_pad, row_stats, labels_c,
-        &ctrl->n_valid, c0, n, a.softcap);
-    prof_after(s);
-    KD_TRY(cudaGetLastError());
+    KD_TRY(launch_ce_dz(unsigned((n + DQ_ROWS - 1) / DQ_ROWS) * unsigned(L.tiles), s,
+                        reinterpret_cast<uint4*>(w8 + L.dz), int(L.rows_pad), L.nvb, partials, c.rows_pad, row_stats,
+                        labels_c, &ctrl->n_valid, c0, n, a.softcap));
     if ((st = kd_status(ce_products(a, L, w8, c0, n, s))) != KD_OK) return st;
   }
   return map_cuda(launch_loss_reduce(losses, nullptr, a.N, &ctrl->n_valid, a.loss, s));

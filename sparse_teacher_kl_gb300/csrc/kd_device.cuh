@@ -480,6 +480,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// The square root on the special-function unit (approximate; 0 for 0).
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // c tanh(z / c), k = 2 log2(e) / c.  c - 2 c / (e^(2 z / c) + 1) is within a few roundings of c at any z, 1e-5 for
 // c up to CE_CAP_NEAR.  Beyond, where z / c is small, that would be many roundings of z: below 1/4 the series
 // z (1 - x^2 / 3 + 2 x^4 / 15 - 17 x^6 / 315 + 62 x^8 / 2835), x = z / c, is taken (the next term is 1e-8 of it).

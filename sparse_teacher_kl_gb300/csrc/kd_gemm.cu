@@ -29,7 +29,7 @@
 //             rounding of bf16 outputs; a second bf16 term of dZ would run the products twice.
 //   EPI_CE    cross entropy: per row and half tile the largest (capped) logit, the sum of exponentials
 //             against it, the label's logit and the sum of logits; for a training step also every
-//             logit as a 16-bit distance from that largest, which kd_cross_entropy.cu turns
+//             logit in 16 bits (CeCode), which kd_cross_entropy.cu turns
 //             into dZ where it lies once the rows' sums are known (no second projection).
 //   EPI_STORE / EPI_ACCUM  plain C = acc / C += acc for the gradient products.
 #include <math.h>
@@ -154,6 +154,38 @@ template <int EPI>
 constexpr int kThreads = 64 + 32 * kEpiWarps<EPI>;
 static_assert(kThreads<EPI_STORE> == GEMM_THREADS, "TMA warp, MMA warp, 4 epilogue warps");
 
+// 32 logits' 16-bit codes (CeCode) into half of a row of a box: its 16-byte chunks j0 .. j0 + 3, swizzled.  2^23 added
+// to a number of steps leaves it, rounded, in the low bits of the sum.
+template <CeCode CODE>
+__device__ __forceinline__ void ce_codes(const float* z, float ref, float cap, float cap_inv, uint8_t* box, uint32_t lane,
+                                         uint32_t j0) {
+  constexpr float kMagic = 8388608.f;
+  auto steps = [&](float v) {
+    if (CODE == CE_CODE_EDGE)
+      return __float_as_uint(fmaf(sqrt_approx(fmaxf(cap - fabsf(v), 0.f) * cap_inv), CE_EDGE_STEPS, kMagic));
+    constexpr float most = kMagic + (CODE == CE_CODE_DIST ? 65535.f : float(CE_SPLIT_CODE - 1));
+    const float dist = ref - v;
+    float code = fminf(fmaxf(fmaf(dist, CE_STEPS, kMagic), kMagic), most);
+    if (CODE == CE_CODE_SPLIT) {
+      const float w = fminf(sqrt_approx(fmaxf(v + cap, 0.f) * (0.5f * cap_inv)), 1.f);
+      code = dist >= CE_SPLIT ? fmaf(w, CE_FAR_STEPS, kMagic + float(CE_SPLIT_CODE)) : code;
+    }
+    return __float_as_uint(code);
+  };
+#pragma unroll
+  for (int g8 = 0; g8 < 4; ++g8) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = z[g8 * 8 + 2 * i], hi = z[g8 * 8 + 2 * i + 1];
+      o[i] = __byte_perm(steps(lo), steps(hi), 0x5410);
+      if (CODE == CE_CODE_EDGE)
+        o[i] |= __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632) & 0x80008000u;
+    }
+    *reinterpret_cast<uint4*>(box + lane * 128u + (((j0 + g8) ^ (lane & 7u)) * 16u)) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
 // A warp's half of a tile of EPI_CE: the CE_COLS logits z from column `first` on of the row of this thread.  The
 // largest first, so that the sum needs no rescaling and the distances have their final reference.
 //
@@ -167,7 +199,8 @@ __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap&
                                         uint32_t quarter) {
   constexpr float kL2E = 1.4426950408889634f;
   const bool last = first + CE_COLS > p.N;  // columns past the vocabulary: weight 0
-  const float cap = p.ce_cap, cap_k = cap > 0.f ? 2.f * kL2E / cap : 0.f;
+  const float cap = p.ce_cap, cap_inv = cap > 0.f ? 1.f / cap : 0.f, cap_k = cap > 0.f ? 2.f * kL2E / cap : 0.f;
+  const CeCode code = ce_code(cap);
   if (cap > CE_CAP_NEAR) {
 #pragma unroll
     for (int i = 0; i < CE_COLS; ++i) z[i] = ce_capped_far(z[i], cap, cap_k);
@@ -207,32 +240,15 @@ __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap&
 #pragma unroll
   for (int c = 0; c < CE_COLS / 32; ++c) {
     float* x = z + c * 32;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = ref - x[i];
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      s0 += ex2_approx(x[i] * -kL2E);
-      s1 += ex2_approx(x[i + 1] * -kL2E);
-    }
     if (p.ce_q) {
       if ((c & 1) == 0) {
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
       }
-      // 2^23 added: the distance in whole steps, rounded, in the low bits of the sum
-      auto steps = [&](int i) {
-        return __float_as_uint(fminf(fmaxf(fmaf(x[i], CE_STEPS, 8388608.f), 8388608.f), 8388608.f + 65535.f));
-      };
-#pragma unroll
-      for (int g8 = 0; g8 < 4; ++g8) {
-        uint4 v;
-        v.x = __byte_perm(steps(g8 * 8 + 0), steps(g8 * 8 + 1), 0x5410);
-        v.y = __byte_perm(steps(g8 * 8 + 2), steps(g8 * 8 + 3), 0x5410);
-        v.z = __byte_perm(steps(g8 * 8 + 4), steps(g8 * 8 + 5), 0x5410);
-        v.w = __byte_perm(steps(g8 * 8 + 6), steps(g8 * 8 + 7), 0x5410);
-        const uint32_t j = uint32_t((c & 1) * 4 + g8);
-        *reinterpret_cast<uint4*>(box + lane * 128u + ((j ^ (lane & 7u)) * 16u)) = v;
-      }
+      const uint32_t j0 = uint32_t(c & 1) * 4;
+      if (code == CE_CODE_DIST) ce_codes<CE_CODE_DIST>(x, ref, cap, cap_inv, box, lane, j0);
+      else if (code == CE_CODE_EDGE) ce_codes<CE_CODE_EDGE>(x, ref, cap, cap_inv, box, lane, j0);
+      else ce_codes<CE_CODE_SPLIT>(x, ref, cap, cap_inv, box, lane, j0);
       if (c & 1) {
         fence_proxy_async_smem();
         __syncwarp();
@@ -241,6 +257,11 @@ __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap&
           bulk_commit();
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      s0 += ex2_approx((ref - x[i]) * -kL2E);
+      s1 += ex2_approx((ref - x[i + 1]) * -kL2E);
     }
   }
   if (row < rows && first < p.N)

@@ -57,7 +57,7 @@ enum EpiKind : int {
   EPI_LSE_H = 5,  // log probabilities: online logsumexp and entropy sum, the token's logit -> partials
   EPI_DZ_LP = 6,  // their gradient: dZ = p (c0 + c1 log2 p) + [v = token] g / tau -> bf16, blocked
   EPI_CE = 7,     // cross entropy: a tile's (max, sum, label's logit, sum of logits) -> partials; with ce_q the
-                  // logits as 16-bit distances from the tile's largest, blocked as dZ
+                  // logits in 16 bits (CeCode), blocked as dZ
 };
 
 // 64-deep k-blocks per ring stage of a CTA-pair launch: two when both operands are
@@ -154,14 +154,31 @@ struct GemmProblem {
   uint32_t* err;
 };
 
-// EPI_CE's partials and 16-bit logits belong to CE_COLS columns (half a tile).  The latter are the distance
-// from the largest of those columns in steps of 1 / CE_STEPS, 65535 for
-// anything 32 and further below (e^-32 of the largest, 1.3e-14).  Half a step makes 2.4e-4 of a
-// probability, an eighth of the rounding of bf16 dZ; bf16 logits would make 2^-8 of every unit of |z|.
+// EPI_CE's partials and 16-bit logits belong to CE_COLS columns (half a tile).  What the 16 bits hold depends on the
+// softcap c, since dZ takes the cap's slope 1 - (z'/c)^2 from them as well as the probability:
+//   CE_CODE_DIST   no cap: the distance from the largest of those columns in steps of 1 / CE_STEPS, 65535 for
+//                  anything 32 and further below (e^-32 of the largest, 1.3e-14).  Half a step makes 2.4e-4 of a
+//                  probability, an eighth of the rounding of bf16 dZ; bf16 logits would make 2^-8 of every unit of |z|.
+//   CE_CODE_EDGE   c up to CE_CAP_EDGE: the sign of z' and w = sqrt(1 - |z'| / c) in steps of 1 / CE_EDGE_STEPS, so
+//                  z' = +-c (1 - w^2) and the slope w^2 (2 - w^2).  Half a step is at most 3.1e-5 c of z' (4.9e-4
+//                  of a probability at c = 16, 2.4e-4 at 8), and of the slope 6.2e-5 or 3.1e-5 / w of itself, so that
+//                  logits near the cap keep theirs: 0.04 % of a slope of 0.01, 0.4 % of 1e-4, 0 at the cap.
+//   CE_CODE_SPLIT  wider caps: the distance as above where it is below CE_SPLIT, and beyond, where the probability is
+//                  below e^-28 of the largest (7e-13; it is taken as at most that) and only the slope counts,
+//                  w = sqrt((z' + c) / 2 c) in steps of 1 / CE_FAR_STEPS, the slope 4 w^2 (1 - w^2).  A distance's half
+//                  step is 2.4e-4 / c of z' / c: 3e-5 of a slope at c = 16.
 constexpr int CE_COLS = BN / 2;
 constexpr int CE_CHUNK_K = 512;   // depth of EPI_CE's partial sums
 constexpr float CE_STEPS = 2048.f;
-
+enum CeCode : int { CE_CODE_DIST = 0, CE_CODE_EDGE = 1, CE_CODE_SPLIT = 2 };
+constexpr float CE_CAP_EDGE = 16.f;
+constexpr float CE_EDGE_STEPS = 32767.f;
+constexpr float CE_SPLIT = 28.f;
+constexpr uint32_t CE_SPLIT_CODE = uint32_t(CE_SPLIT * CE_STEPS);
+constexpr float CE_FAR_STEPS = float(65535 - CE_SPLIT_CODE);
+__host__ __device__ inline CeCode ce_code(float cap) {
+  return !(cap > 0.f) ? CE_CODE_DIST : cap <= CE_CAP_EDGE ? CE_CODE_EDGE : CE_CODE_SPLIT;
+}
 
 // Host helpers of the C ABI.
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
