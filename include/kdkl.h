@@ -458,7 +458,8 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
  * c tanh(h W^T / c) for a softcap c, and lse = logsumexp(z'),
  *   loss_n = lse - (1 - e) z'_y - (e / V) sum_v z'_v + l lse^2     e label_smoothing, l z_loss
  *   loss   = sum over valid n of loss_n / n_valid                  (0 when none is)
- *   H_bf16, W_bf16, chunk : as for kd_fused_kl_fwd.
+ *   H_bf16, W_bf16, chunk : as for kd_fused_kl_fwd; N, d and V at most 2^31 - 1024, as in every call on
+ *            hidden states and a head.
  *   labels : [N] int32.  A position is valid if its label is not ignore_index and mask ([N] uint8, NULL:
  *            all) is not 0; only those are projected, the hidden states of the others are not read.
  *            A valid position's label outside [0, V) is recorded in the error word with its position;
@@ -502,10 +503,10 @@ KD_API int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* facto
  * kd_quantize_int8: rows of x [N, d] (bf16, fp16 or fp32, kd_dtype, any row stride ld >= d) to integers,
  *   scale_n = max |x_n| / 127 (fp32),   q_nk = the whole number nearest to x_nk / scale_n, ties to even,
  * the quotient taken exactly.  A row of zeros has scale 0; one that holds a NaN or an infinity has
- * scale NaN and integers 0.  q_out: [N, d] with row stride ld_q >= d.
+ * scale NaN and integers 0.  q_out: [N, d] with row stride ld_q >= d; d at most 2^31 - 1024.
  *
  * kd_gemm_int8: C_mn = (sum_k A_mk B_nk) a_scale_m b_scale_n, A [M, K] the tokens and B [N, K] the channels,
- * 1 <= K <= KD_MAX_INT8_K, any row strides lda, ldb >= K, ldc >= N; C bf16, fp16 or fp32 (kd_dtype).  The
+ * 1 <= K <= KD_MAX_INT8_K, M and N at most 2^31 - 1024, any row strides lda, ldb >= K, ldc >= N; C bf16, fp16 or fp32 (kd_dtype).  The
  * integer sum is exact while it stays below 2^24 (always for K <= 1024); from there on the tensor cores add in
  * fp32 and cut off, up to a step of the sum for each 16 products.  Each of the two products with a scale rounds
  * once to fp32, and the result once to C's type.  Weights whose rows start on

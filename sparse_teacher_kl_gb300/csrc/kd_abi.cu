@@ -202,7 +202,7 @@ kd_status check_proj_args(const void* H, const void* W, int64_t N, int64_t d, in
                                  float tau) {
   if (N < 1 || d < 8 || V < 1 || chunk < BM) return KD_ERR_INVALID_ARG;
   if (d % 8 != 0 || chunk % BM != 0) return KD_ERR_INVALID_ARG;
-  if (V > 0x7fffffffLL || N > 0x7fffffffLL || d > 0x7fffffffLL) return KD_ERR_INVALID_ARG;
+  if (V > KD_MAX_EXTENT || N > KD_MAX_EXTENT || d > KD_MAX_EXTENT) return KD_ERR_INVALID_ARG;
   if (!(tau > 0.f) || !isfinite(tau)) return KD_ERR_INVALID_ARG;
   if (!H || !W || !aligned(H, 16) || !aligned(W, 16)) return KD_ERR_INVALID_ARG;
   return KD_OK;
@@ -291,7 +291,7 @@ int kd_teacher_topk(const void* Ht_bf16, const void* Wt_bf16, int64_t N, int64_t
                     int64_t chunk, int32_t* ids_out, float* vals_out, float* lse_out, float* dropped_out, void* ws,
                     size_t ws_bytes, void* stream) {
   if (N < 1 || dt < 8 || dt % 8 != 0 || V < 1 || K < 1 || K > KD_MAX_K || int64_t(K) > V) return KD_ERR_INVALID_ARG;
-  if (chunk < BM || chunk % BM != 0 || V > 0x7fffffffLL || N > 0x7fffffffLL || dt > 0x7fffffffLL)
+  if (chunk < BM || chunk % BM != 0 || V > KD_MAX_EXTENT || N > KD_MAX_EXTENT || dt > KD_MAX_EXTENT)
     return KD_ERR_INVALID_ARG;
   if (!Ht_bf16 || !Wt_bf16 || !ids_out || !vals_out) return KD_ERR_INVALID_ARG;
   if (!aligned(Ht_bf16, 16) || !aligned(Wt_bf16, 16) || !aligned(ids_out, 4) || !aligned(vals_out, 4))
@@ -811,7 +811,7 @@ int kd_check_wait_timeout(void* ws, size_t ws_bytes, int64_t limit_ns, void* str
 
 int kd_gemm_bf16(const void* A, const void* B, float* C, int64_t M, int64_t N, int64_t K, int a_mn, int b_mn,
                  int accumulate, void* ws, size_t ws_bytes, void* stream) {
-  if (M < 1 || N < 1 || K < 1 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
+  if (M < 1 || N < 1 || K < 1 || M > KD_MAX_EXTENT || N > KD_MAX_EXTENT || K > KD_MAX_EXTENT)
     return KD_ERR_INVALID_ARG;
   if (!A || !B || !C || !aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16)) return KD_ERR_INVALID_ARG;
   if (N % 4 != 0) return KD_ERR_INVALID_ARG;

@@ -6,7 +6,7 @@ using namespace kd;
 
 namespace {
 
-constexpr int64_t kMaxInt = 0x7fffffffLL, kMaxRows = kMaxInt - 1023;  // a tile behind the last row still counts
+constexpr int64_t kMaxInt = 0x7fffffffLL;
 
 size_t out_size(int dtype) { return dtype == KD_F32 ? 4 : 2; }
 bool rows16(const void* B, int64_t ldb) { return aligned(B, 16) && ldb % 16 == 0; }
@@ -14,7 +14,7 @@ bool ok4(const void* p) { return p != nullptr && aligned(p, 4); }
 
 // An integer matrix [rows, K] with row stride ld and its scales.
 bool ok_matrix(const void* q, int64_t ld, const void* scale, int64_t rows, int64_t K) {
-  return q && rows >= 1 && rows <= kMaxRows && K >= 1 && K <= KD_MAX_INT8_K && ld >= K && ok4(scale);
+  return q && rows >= 1 && rows <= KD_MAX_EXTENT && K >= 1 && K <= KD_MAX_INT8_K && ld >= K && ok4(scale);
 }
 
 struct TopkLayout {
@@ -46,7 +46,7 @@ extern "C" {
 
 int kd_quantize_int8(const void* x, int dtype, int64_t N, int64_t d, int64_t ld, int8_t* q_out, int64_t ld_q,
                      float* scale_out, void* stream) {
-  if (N < 1 || N > kMaxInt || d < 1 || d > kMaxInt || ld < d || ld_q < d) return KD_ERR_INVALID_ARG;
+  if (N < 1 || N > kMaxInt || d < 1 || d > KD_MAX_EXTENT || ld < d || ld_q < d) return KD_ERR_INVALID_ARG;
   if (dtype != KD_BF16 && dtype != KD_F16 && dtype != KD_F32) return KD_ERR_INVALID_ARG;
   if (!x || !aligned(x, out_size(dtype)) || !q_out || !ok4(scale_out)) return KD_ERR_INVALID_ARG;
   kd_status st = check_device();

@@ -191,6 +191,8 @@ inline float log2e_over_tau(float tau) {
   const double k = 1.4426950408889634 / double(tau);
   return k <= double(FLT_MAX) ? float(k) : FLT_MAX;
 }
+// Rows, columns and depths are counted in 32 bits, up to a tile (or a block's step) behind the last one.
+constexpr int64_t KD_MAX_EXTENT = 0x7fffffffLL - 1023;
 // What every call on hidden states and a head checks: sizes, chunk, alignment, temperature.
 kd_status check_proj_args(const void* H, const void* W, int64_t N, int64_t d, int64_t V, int64_t chunk, float tau);
 // KD_OK if the current device is an sm_103 GPU.
