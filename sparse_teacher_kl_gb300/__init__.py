@@ -561,9 +561,9 @@ def logits_kl(logits, ids, tlog, mask=None, tau=1.0, t_lse=None):
 
 
 def _check_projection(H, W, tokens, mask, name="tokens"):
-    for t, name in ((H, "H"), (W, "W")):
+    for t, which in ((H, "H"), (W, "W")):
         if not t.is_cuda or t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 2-D bf16 CUDA tensor")
+            raise ValueError(f"{which} must be a contiguous 2-D bf16 CUDA tensor")
     N, d = H.shape
     if W.shape[1] != d or W.device != H.device:
         raise ValueError("W must be [V, d] on the device of H [N, d]")
