@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(CC_ROWS * CC_PHASES) kd_ce_combine_kernel(cons
   const float ln_s = logf(S), lse = M + ln_s;
   // as a difference of logits: lse and z_y would each be rounded at their own size
   const float nll = ln_s - (Y - M);
-  const float mean_off = a.smooth > 0.f ? Y - Z / float(a.V) : 0.f;
+  // (a label at -inf: nll is +inf, and so is the loss, though the mean is at -inf with it)
+  const float mean_off = a.smooth > 0.f && Y != -INFINITY ? Y - Z / float(a.V) : 0.f;
   a.lse[pos] = lse;
   a.losses[pos] = bad ? __int_as_float(0x7FC00000) : nll + a.smooth * mean_off + a.z_loss * lse * lse;
   if (a.row_stats == nullptr) return;

@@ -90,3 +90,26 @@ def test_columns_of_nothing_but_minus_infinity(kd, cuda_device, V):
     keep = [i for i in range(d) if i != 8]
     bound = 2 * 2.0 ** -8 * (dz.abs() @ W.double().abs())
     assert torch.isfinite(gH).all() and ((gH.double() - dz @ W.double()).abs() <= bound + 1e-6)[:, keep].all()
+
+
+@pytest.mark.parametrize("smooth", [0.0, 0.1])
+def test_label_at_minus_infinity(kd, cuda_device, smooth):
+    """A logit that overflows to -inf has no probability: as a label its loss is +inf, the gradients stay finite."""
+    N, V, d = 4, 500, 16
+    H = torch.zeros((N, d), device="cuda")
+    H[:, :N] = torch.eye(N)
+    H[:2, 8] = 1e20
+    W = torch.randn((V, d), generator=gen(4), device="cuda")
+    W[:, 8] = 0
+    W[300, 8] = -1e20
+    H, W = H.to(torch.bfloat16), W.to(torch.bfloat16)
+    labels = torch.tensor([300, 7, 300, 8], device="cuda", dtype=torch.int32)
+    each = torch.empty((N,), device="cuda")
+    loss, gH, gW = kd.fused_cross_entropy_step(H, W, labels, label_smoothing=smooth, loss_out=each)
+    # with smoothing a logit of -inf is in every loss of its row, by e / V
+    assert each[0] == INF and loss[0] == INF and torch.isfinite(each[2:]).all()
+    assert torch.isfinite(each[1]) if smooth == 0 else each[1] == INF
+    z = H.double() @ W.double().T
+    dz = z.softmax(1) - smooth / V
+    dz[torch.arange(N), labels.long()] -= 1 - smooth
+    close(gW[:, :N].T, dz / N, 1e-6)
