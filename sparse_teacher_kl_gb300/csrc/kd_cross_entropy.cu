@@ -24,6 +24,8 @@
 // its gradient, which projects twice: 2.7); 4096 x 4096 x 151936 with 65 % ignored 3.7 ms, none ignored 9.0.
 #include <math.h>
 
+#include <type_traits>
+
 #include "kd_device.cuh"
 #include "kd_internal.h"
 
@@ -230,8 +232,9 @@ struct DzRow {
   float a, b, m, M, shift, cap, cap_inv;
 };
 
-// An entry from its code (CeCode).  Where no column of the CE_COLS is above -inf, m - M is -inf and p is 0.
-template <CeCode CODE>
+// An entry from its code (CeCode; FAR as for ce_codes).  Where no column of the CE_COLS is above -inf, m - M is -inf
+// and p is 0.
+template <CeCode CODE, bool FAR = true>
 __device__ __forceinline__ float dz_of(uint32_t q, const DzRow& r) {
   if (CODE == CE_CODE_EDGE) {
     const float w = float(q & 0x7FFFu) * (1.f / CE_EDGE_STEPS), e = w * w;  // e = 1 - |z'| / c
@@ -242,7 +245,7 @@ __device__ __forceinline__ float dz_of(uint32_t q, const DzRow& r) {
   if (CODE == CE_CODE_DIST) return fmaf(r.a, ex2_approx(shift), -r.b);
   const float z = fmaf(float(q), -1.f / CE_STEPS, r.m);
   float e = fmaxf(r.cap - fabsf(z), 0.f) * r.cap_inv, slope = e * (2.f - e);
-  if (q >= CE_SPLIT_CODE) {
+  if (FAR && q >= CE_SPLIT_CODE) {
     const float w = float(q - CE_SPLIT_CODE) * (1.f / CE_FAR_STEPS);
     e = w * w;  // (z' + c) / 2 c, whose step may be wide (c / 4096): the distance is known to be CE_SPLIT at least
     shift = fmaf(fminf(r.cap * fmaf(2.f, e, -1.f) - r.m, -CE_SPLIT), kLog2E, r.shift);
@@ -295,12 +298,21 @@ __global__ void __launch_bounds__(256)
       const uint32_t w[4] = {v[h][b].x, v[h][b].y, v[h][b].z, v[h][b].w};
       const int off = label - (vb0 + b) * 64 - lane8 * 8;
       uint32_t o[4];
+      auto entries = [&](auto far) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float lo = dz_of<CODE>(w[i] & 0xFFFFu, row), hi = dz_of<CODE>(w[i] >> 16, row);
-        lo = off == 2 * i ? st.w : lo;
-        hi = off == 2 * i + 1 ? st.w : hi;
-        o[i] = pack_bf16x2(lo, hi);
+        for (int i = 0; i < 4; ++i) {
+          float lo = dz_of<CODE, decltype(far)::value>(w[i] & 0xFFFFu, row);
+          float hi = dz_of<CODE, decltype(far)::value>(w[i] >> 16, row);
+          lo = off == 2 * i ? st.w : lo;
+          hi = off == 2 * i + 1 ? st.w : hi;
+          o[i] = pack_bf16x2(lo, hi);
+        }
+      };
+      if constexpr (CODE == CE_CODE_SPLIT) {
+        const uint32_t most = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+        if (max(most & 0xFFFFu, most >> 16) >= CE_SPLIT_CODE) entries(std::true_type{}); else entries(std::false_type{});
+      } else {
+        entries(std::true_type{});
       }
       dz[(size_t(vb0 + b) * rows_pad + r) * 8 + lane8] = make_uint4(o[0], o[1], o[2], o[3]);
     }
