@@ -475,6 +475,10 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
  *            is off by 2.4e-4 of itself at most (with a softcap c below 16: 3.1e-5 c), a cap's slope by 6e-5 (3e-5
  *            from c = 16 on), and by 0.04 % of a slope of 0.01 up to c = 16; probabilities below e^-32 (with a
  *            softcap above 16: e^-28) of the largest of their 128 columns are known to be that small only.
+ * kd_fused_cross_entropy_keep and _bwd are the step in two calls, for a grad_loss that is known only after the
+ * loss (autograd's), all positions in one chunk: the first is the forward pass and leaves in `kept`
+ * (kd_fused_cross_entropy_kept bytes, of any content before) what the second, given the same W, sizes and
+ * options, makes the gradients of, once: it writes dZ where the logits lay.
  * Workspace: `step` != 0 asks for the step's (it grows with chunk * V), 0 for the forward pass's
  * (chunk * (V / 16 + 2 d) bytes).  `ws` may be memory of any content; the error word is in `control`
  * (see kd_logits_kl_fwd_ctl), which may be `ws` itself once kd_workspace_clear has cleared it.
@@ -493,8 +497,23 @@ KD_API int kd_fused_cross_entropy_step(const void* H_bf16, const void* W_bf16, c
                     float* lse_out, float* loss_per_token_out, void* grad_H, int grad_H_is_fp32, void* grad_W,
                     int grad_W_kind, void* ws, size_t ws_bytes, void* control, void* stream);
 
+KD_API size_t kd_fused_cross_entropy_kept(int64_t N, int64_t d, int64_t V);
+
+KD_API int kd_fused_cross_entropy_keep(const void* H_bf16, const void* W_bf16, const int32_t* labels,
+                    const uint8_t* mask, int64_t N, int64_t d, int64_t V, float label_smoothing, float z_loss,
+                    float softcap, int ignore_index, float* loss_out, float* lse_out, float* loss_per_token_out,
+                    void* kept, size_t kept_bytes, void* control, void* stream);
+
+KD_API size_t kd_fused_cross_entropy_bwd_workspace(int64_t N, int64_t d, int64_t V);
+
+KD_API int kd_fused_cross_entropy_bwd(const void* W_bf16, int64_t N, int64_t d, int64_t V, float label_smoothing,
+                    float softcap, const float* grad_loss, void* grad_H, int grad_H_is_fp32, void* grad_W,
+                    int grad_W_kind, void* kept, size_t kept_bytes, void* ws, size_t ws_bytes, void* control,
+                    void* stream);
+
 /* x[0 .. n) *= *factor (device fp32 scalar), bf16 or fp32, n a multiple of 8; nothing is read or
- * written where the factor is 1.  What a backward pass does to a step's gradients. */
+ * written where the factor is 1.  What a backward pass does to a step's fp32 gradients before they are
+ * rounded (bf16 ones are rounded a second time by it). */
 KD_API int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* factor, void* stream);
 
 /* ------------------------------------------------------------------------ *

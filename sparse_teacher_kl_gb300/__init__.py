@@ -737,47 +737,63 @@ def fused_cross_entropy_step(H, W, labels, mask=None, chunk=4096, label_smoothin
 
 
 class _FusedCrossEntropy(torch.autograd.Function):
-    """The forward pass takes the gradients of a factor 1 with the loss (one projection in place of two); the
-    backward pass multiplies them by the factor that arrives, which costs nothing where that is 1."""
+    """The factor that arrives joins the gradients before they are rounded to their type.  Positions of one chunk: the
+    forward pass keeps the logits in 16 bits and the backward pass takes both gradients from them (one projection in
+    place of two).  Of more chunks: the forward pass takes the gradients of a factor 1 in fp32, the backward pass
+    multiplies and rounds them."""
 
     @staticmethod
     def forward(ctx, H, W, labels, mask, chunk, options, wanted):
-        _check_projection(H, W, labels, mask, "labels")
-        ctx.control = _control(H.device)
-        ctx.chunk, ctx.options, ctx.grads = chunk, options, None
-        ctx.save_for_backward(H, W, labels, mask)
+        N, d, V, dev = _check_projection(H, W, labels, mask, "labels")
+        ctx.control = _control(dev)
+        ctx.chunk, ctx.options, ctx.spent = chunk, options, False
         if not wanted:
             return _ce_forward(H, W, labels, mask, chunk, options, None, ctx.control)[0][0]
-        loss, grads = _FusedCrossEntropy.step(ctx, H, W, labels, mask)
-        ctx.grads = grads
+        if N <= chunk:
+            kept = (_scratch(_abi.kd_fused_cross_entropy_kept(N, d, V), dev),)
+            loss = torch.empty((1,), dtype=torch.float32, device=dev)
+            lse = torch.empty((N,), dtype=torch.float32, device=dev)
+            st = _abi.kd_fused_cross_entropy_keep(_ptr(H), _ptr(W), _ptr(labels), _ptr(mask), N, d, V, *options,
+                                                  _ptr(loss), _ptr(lse), None, _ptr(kept[0]), kept[0].numel(),
+                                                  _ptr(ctx.control), _stream(dev))
+            _abi.check(st, "kd_fused_cross_entropy_keep")
+        else:
+            loss, *kept = _ce_step(H, W, labels, mask, chunk, options, None, None, ctx.control, grad_H_fp32=True)
+        ctx.save_for_backward(H, W, labels, mask, *kept)
         return loss[0]
-
-    @staticmethod
-    def step(ctx, H, W, labels, mask):
-        loss, *grads = _ce_step(H, W, labels, mask, ctx.chunk, ctx.options, None, None, ctx.control,
-                                grad_W_bf16=H.shape[0] <= ctx.chunk)
-        return loss, grads
 
     @staticmethod
     @_once_differentiable
     def backward(ctx, grad_out):
-        H, W, labels, mask = ctx.saved_tensors
-        # handed out once: what becomes of them is the caller's, so a second pass takes them anew
-        grads, ctx.grads = ctx.grads, None
-        if grads is None:
-            grads = _FusedCrossEntropy.step(ctx, H, W, labels, mask)[1]
-        g = _f32c(grad_out.reshape(1))
-        for t in grads:
-            _abi.check(_abi.kd_scale_gradient(_ptr(t), t.numel(), int(t.dtype == torch.float32), _ptr(g),
-                                              _stream(H.device)), "kd_scale_gradient")
-        return grads[0], grads[1].to(W.dtype), None, None, None, None, None
+        H, W, labels, mask, *kept = ctx.saved_tensors
+        (N, d), V, dev = H.shape, W.shape[0], H.device
+        one, g = N <= ctx.chunk, _f32c(grad_out.reshape(1))
+        if ctx.spent:
+            # what was kept has become the first pass's gradients: a second one takes them anew
+            _, gH, gW = _ce_step(H, W, labels, mask, ctx.chunk, ctx.options, g, None, ctx.control, grad_H_fp32=not one,
+                                 grad_W_bf16=one)
+            return gH.to(H.dtype), gW.to(W.dtype), None, None, None, None, None
+        ctx.spent = True
+        if one:
+            gH, gW = torch.empty_like(H), torch.empty_like(W)
+            ws = _scratch(_abi.kd_fused_cross_entropy_bwd_workspace(N, d, V), dev)
+            st = _abi.kd_fused_cross_entropy_bwd(_ptr(W), N, d, V, ctx.options[0], ctx.options[2], _ptr(g), _ptr(gH), 0,
+                                                 _ptr(gW), _abi.KD_GRAD_STORE_BF16, _ptr(kept[0]), kept[0].numel(),
+                                                 _ptr(ws), ws.numel(), _ptr(ctx.control), _stream(dev))
+            _abi.check(st, "kd_fused_cross_entropy_bwd")
+            return gH, gW, None, None, None, None, None
+        for t in kept:
+            _abi.check(_abi.kd_scale_gradient(_ptr(t), t.numel(), 1, _ptr(g), _stream(dev)), "kd_scale_gradient")
+        return kept[0].to(H.dtype), kept[1].to(W.dtype), None, None, None, None, None
 
 
 @_on_its_device
 def fused_cross_entropy(H, W, labels, mask=None, chunk=4096, label_smoothing=0.0, z_loss=0.0, softcap=0.0,
                         ignore_index=-100):
     """Differentiable cross entropy of ``labels`` (int32 [N]) against softmax(H W^T): the mean over the positions
-    whose label is not ``ignore_index`` and whose ``mask`` is not 0 (scalar tensor)."""
+    whose label is not ``ignore_index`` and whose ``mask`` is not 0 (scalar tensor).  Up to ``chunk`` positions the
+    graph keeps their logits in 16 bits until the backward pass (2 N V bytes); of more, the forward pass takes both
+    gradients already, in fp32 (4 V d bytes), so a loss that is not differentiated belongs under ``no_grad``."""
     wanted = torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)
     return _FusedCrossEntropy.apply(H, W, labels, mask, int(chunk),
                                     _ce_options(label_smoothing, z_loss, softcap, ignore_index), wanted)

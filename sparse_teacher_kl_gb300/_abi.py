@@ -87,6 +87,13 @@ _SIGNATURES = {
     "kd_fused_cross_entropy_step": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_float,
                                              _c_float, _c_float, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
                                              _c_int, _c_ptr, _c_int, _c_ptr, _c_size, _c_ptr, _c_ptr]),
+    "kd_fused_cross_entropy_kept": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "kd_fused_cross_entropy_keep": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_float, _c_float,
+                                             _c_float, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr,
+                                             _c_ptr]),
+    "kd_fused_cross_entropy_bwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "kd_fused_cross_entropy_bwd": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_i64, _c_float, _c_float, _c_ptr, _c_ptr, _c_int,
+                                            _c_ptr, _c_int, _c_ptr, _c_size, _c_ptr, _c_size, _c_ptr, _c_ptr]),
     "kd_scale_gradient": (_c_int, [_c_ptr, _c_i64, _c_int, _c_ptr, _c_ptr]),
     "kd_quantize_int8": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr]),
     "kd_gemm_int8_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int]),
@@ -198,6 +205,10 @@ kd_fused_logprobs_bwd_ctl = _wrap("kd_fused_logprobs_bwd_ctl")
 kd_fused_cross_entropy_workspace = _wrap("kd_fused_cross_entropy_workspace")
 kd_fused_cross_entropy_fwd = _wrap("kd_fused_cross_entropy_fwd")
 kd_fused_cross_entropy_step = _wrap("kd_fused_cross_entropy_step")
+kd_fused_cross_entropy_kept = _wrap("kd_fused_cross_entropy_kept")
+kd_fused_cross_entropy_keep = _wrap("kd_fused_cross_entropy_keep")
+kd_fused_cross_entropy_bwd_workspace = _wrap("kd_fused_cross_entropy_bwd_workspace")
+kd_fused_cross_entropy_bwd = _wrap("kd_fused_cross_entropy_bwd")
 kd_scale_gradient = _wrap("kd_scale_gradient")
 kd_quantize_int8 = _wrap("kd_quantize_int8")
 kd_gemm_int8_workspace = _wrap("kd_gemm_int8_workspace")

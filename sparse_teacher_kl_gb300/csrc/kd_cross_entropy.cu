@@ -48,8 +48,7 @@ constexpr int LIST_THREADS = 1024, LIST_EACH = 8;
 __global__ void __launch_bounds__(LIST_THREADS)
     kd_ce_list_kernel(const int32_t* __restrict__ labels, const uint8_t* __restrict__ mask, int64_t N, int ignore,
                       int32_t* __restrict__ list, int32_t* __restrict__ n_valid, float* __restrict__ lse,
-                      float* __restrict__ losses, const float* __restrict__ grad_loss, float label_weight,
-                      float* __restrict__ alpha) {
+                      float* __restrict__ losses) {
   __shared__ int warp_sum[LIST_THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int base = 0;
@@ -89,11 +88,7 @@ __global__ void __launch_bounds__(LIST_THREADS)
     base += total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    *n_valid = base;
-    // the gradient's common factor, see CeCombine
-    if (alpha != nullptr) *alpha = base > 0 ? (grad_loss ? *grad_loss : 1.f) * label_weight / float(base) : 0.f;
-  }
+  if (threadIdx.x == 0) *n_valid = base;
 }
 
 __device__ __forceinline__ int chunk_rows(const int32_t* n_valid, int64_t c0, int cap) {
@@ -258,9 +253,12 @@ template <CeCode CODE>
 __global__ void __launch_bounds__(256)
     kd_ce_dz_kernel(uint4* __restrict__ dz, int rows_pad, int64_t nvb, const float4* __restrict__ partials, int ld_part,
                     const float4* __restrict__ row_stats, const int32_t* __restrict__ labels_c,
-                    const int32_t* __restrict__ n_valid, int64_t c0, int cap, float softcap) {
+                    const int32_t* __restrict__ n_valid, int64_t c0, int cap, float softcap,
+                    const float* __restrict__ grad_loss, float label_weight, float* __restrict__ alpha) {
   const int n = chunk_rows(n_valid, c0, cap);
   const int end = min(read_rows(n), rows_pad);
+  if (blockIdx.x == 0 && threadIdx.x == 0)  // the gradients' common factor, see CeCombine
+    *alpha = *n_valid > 0 ? (grad_loss ? *grad_loss : 1.f) * label_weight / float(*n_valid) : 0.f;
   const uint32_t row_blocks = uint32_t(cap + DQ_ROWS - 1) / DQ_ROWS;
   const int tile = int(blockIdx.x / row_blocks), lane8 = threadIdx.x & 7;
   const int first = int(blockIdx.x - uint32_t(tile) * row_blocks) * DQ_ROWS, r0 = first + (threadIdx.x >> 3);
@@ -319,19 +317,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-cudaError_t launch_ce_dz(unsigned blocks, cudaStream_t s, uint4* dz, int rows_pad, int64_t nvb, const float4* partials,
-                         int ld_part, const float4* row_stats, const int32_t* labels_c, const int32_t* n_valid,
-                         int64_t c0, int cap, float softcap) {
-  const CeCode code = ce_code(softcap);
-  auto* k = code == CE_CODE_DIST   ? kd_ce_dz_kernel<CE_CODE_DIST>
-            : code == CE_CODE_EDGE ? kd_ce_dz_kernel<CE_CODE_EDGE>
-                                   : kd_ce_dz_kernel<CE_CODE_SPLIT>;
-  prof_before("kd_ce_dz", s);
-  k<<<blocks, 256, 0, s>>>(dz, rows_pad, nvb, partials, ld_part, row_stats, labels_c, n_valid, c0, cap, softcap);
-  prof_after(s);
-  return cudaGetLastError();
-}
-
 // ------------------------------------------------------------------ split sums ---
 // grad_H of a chunk from its fp32 partials, summed in split order, each row to its position.
 __global__ void __launch_bounds__(256)
@@ -371,12 +356,16 @@ __global__ void __launch_bounds__(256) kd_ce_scale_kernel(T* __restrict__ x, int
 
 // ------------------------------------------------------------------ host side ---
 
+// The fp32 partials of grad_H's splits.
+size_t ce_split_bytes(int64_t rows_pad, int64_t d) { return align_up(size_t(KD_MAX_SPLITS) * rows_pad * size_t(d) * 4, 256); }
+
 struct CeLayout {
-  size_t alpha, list, losses, labels, stats, partials, hidden, dz, gh_part, total;
+  size_t alpha, list, losses, labels, stats, partials, hidden, dz, kept, gh_part, total;
   int64_t rows_pad, nvb;
   int tiles;
 };
 
+// Up to `kept`: what a forward pass that keeps its logits leaves for the gradients; behind it, what they need besides.
 CeLayout ce_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool step) {
   CeLayout L{};
   const int64_t c = chunk < N ? chunk : N;
@@ -398,7 +387,8 @@ CeLayout ce_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool step) {
   L.hidden = take(size_t(L.rows_pad) * size_t(d) * 2);
   if (step) {
     L.dz = take(size_t(L.nvb) * L.rows_pad * 128);
-    L.gh_part = take(size_t(KD_MAX_SPLITS) * L.rows_pad * size_t(d) * 4);
+    L.kept = off;
+    L.gh_part = take(ce_split_bytes(L.rows_pad, d));
   }
   L.total = off;
   return L;
@@ -419,7 +409,14 @@ struct CeCall {
   int w_kind;
   void* ws;
   size_t ws_bytes;
+  void* split;  // the partials of grad_H's splits
   void *control, *stream;
+};
+
+enum CeWhat : int {
+  CE_LOSS,   // the loss
+  CE_KEEP,   // the loss, the workspace kept as the gradients need it
+  CE_STEP,   // the loss and the gradients
 };
 
 #define KD_TRY(call)                      \
@@ -447,12 +444,24 @@ int ce_splits(const GemmProblem& q, int slots, int k_blocks) {
   return best;
 }
 
-// The two gradient products of a chunk, from dZ and the gathered hidden states.
-int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int n, cudaStream_t s) {
+// A chunk's gradients: dZ from its kept logits, where they lie, and the two products of dZ and the gathered hidden states.
+int ce_gradients(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int n, cudaStream_t s) {
   Ctrl* ctrl = static_cast<Ctrl*>(a.ws);
   uint32_t* err = &static_cast<Ctrl*>(a.control)->err;
   const int32_t* list = reinterpret_cast<const int32_t*>(w8 + L.list);
-  const float* alpha = reinterpret_cast<const float*>(w8 + L.alpha);
+  float* alpha = reinterpret_cast<float*>(w8 + L.alpha);
+  const CeCode code = ce_code(a.softcap);
+  auto* dz_kernel = code == CE_CODE_DIST   ? kd_ce_dz_kernel<CE_CODE_DIST>
+                    : code == CE_CODE_EDGE ? kd_ce_dz_kernel<CE_CODE_EDGE>
+                                           : kd_ce_dz_kernel<CE_CODE_SPLIT>;
+  prof_before("kd_ce_dz", s);
+  dz_kernel<<<unsigned((n + DQ_ROWS - 1) / DQ_ROWS) * unsigned(L.tiles), 256, 0, s>>>(
+      reinterpret_cast<uint4*>(w8 + L.dz), int(L.rows_pad), L.nvb, reinterpret_cast<const float4*>(w8 + L.partials),
+      int((n + BM - 1) / BM * BM), reinterpret_cast<const float4*>(w8 + L.stats),
+      reinterpret_cast<const int32_t*>(w8 + L.labels), &ctrl->n_valid, c0, n, a.softcap, a.grad_loss, 1.f - a.smooth, alpha);
+  prof_after(s);
+  KD_TRY(cudaGetLastError());
+
   const uint16_t* Hc = reinterpret_cast<const uint16_t*>(w8 + L.hidden);
   const void* dz = w8 + L.dz;
   const uint64_t d = uint64_t(a.d), V = uint64_t(a.V), row_bytes = d * 2;
@@ -480,7 +489,7 @@ int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int
     q.row_map = list + c0;
     q.map_rows = a.N;
   } else {
-    q.C = w8 + L.gh_part;  // fp32 partial per split, summed in split order below
+    q.C = a.split;  // fp32 partial per split, summed in split order below
     q.split_stride = L.rows_pad * a.d;
   }
   q.b_box2 = q.cta_pair && d64;
@@ -494,7 +503,7 @@ int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int
     const int64_t work = (int64_t(n) * (a.d / 4) + 255) / 256;
     prof_before("kd_ce_split", s);
     kd_ce_split_kernel<<<unsigned(work < 4 * grid ? work : 4 * grid), 256, 0, s>>>(
-        reinterpret_cast<const float4*>(w8 + L.gh_part), q.k_splits, L.rows_pad * a.d / 4, a.d / 4, list,
+        static_cast<const float4*>(a.split), q.k_splits, L.rows_pad * a.d / 4, a.d / 4, list,
         &ctrl->n_valid, c0, n, a.grad_H, a.grad_H_f32 ? 0 : 1);
     prof_after(s);
     KD_TRY(cudaGetLastError());
@@ -531,32 +540,44 @@ int ce_products(const CeCall& a, const CeLayout& L, uint8_t* w8, int64_t c0, int
 
 bool ok4(const void* p) { return p != nullptr && aligned(p, 4); }
 
-int ce_run(const CeCall& a, bool step) {
-  kd_status st = check_proj_args(a.H, a.W, a.N, a.d, a.V, a.chunk, 1.f);
-  if (st != KD_OK) return st;
+kd_status ce_check_options(const CeCall& a) {
   if (!(a.smooth >= 0.f && a.smooth < 1.f) || !(a.z_loss >= 0.f && isfinite(a.z_loss)) ||
       !(a.softcap == 0.f || (a.softcap >= kMinSoftcap && isfinite(a.softcap))))
     return KD_ERR_INVALID_ARG;
+  return KD_OK;
+}
+
+kd_status ce_check_gradients(const CeCall& a) {
+  if (!aligned(a.grad_loss, 4) || !a.grad_H || !aligned(a.grad_H, 16) || !a.grad_W || !aligned(a.grad_W, 16))
+    return KD_ERR_INVALID_ARG;
+  if (a.w_kind < KD_GRAD_ADD_F32 || a.w_kind > KD_GRAD_STORE_BF16) return KD_ERR_INVALID_ARG;
+  if (a.w_kind == KD_GRAD_STORE_BF16 && a.N > a.chunk) return KD_ERR_INVALID_ARG;
+  return KD_OK;
+}
+
+// A single chunk for all N positions.
+int64_t one_chunk(int64_t N) { return N <= KD_MAX_EXTENT ? (N + BM - 1) / BM * BM : BM; }
+
+int ce_run(CeCall a, CeWhat what) {
+  kd_status st = check_proj_args(a.H, a.W, a.N, a.d, a.V, a.chunk, 1.f);
+  if (st == KD_OK) st = ce_check_options(a);
+  if (st != KD_OK) return st;
   if (!ok4(a.labels) || !ok4(a.loss) || !ok4(a.lse) || !aligned(a.losses, 4)) return KD_ERR_INVALID_ARG;
-  if (step) {
-    if (!aligned(a.grad_loss, 4) || !a.grad_H || !aligned(a.grad_H, 16) || !a.grad_W || !aligned(a.grad_W, 16))
-      return KD_ERR_INVALID_ARG;
-    if (a.w_kind < KD_GRAD_ADD_F32 || a.w_kind > KD_GRAD_STORE_BF16) return KD_ERR_INVALID_ARG;
-    if (a.w_kind == KD_GRAD_STORE_BF16 && a.N > a.chunk) return KD_ERR_INVALID_ARG;
-  }
-  const CeLayout L = ce_layout(a.N, a.d, a.V, a.chunk, step);
-  if (!a.ws || !aligned(a.ws, 256) || a.ws_bytes < L.total || !a.control || !aligned(a.control, 256))
+  if (what == CE_STEP && (st = ce_check_gradients(a)) != KD_OK) return st;
+  const CeLayout L = ce_layout(a.N, a.d, a.V, a.chunk, what != CE_LOSS);
+  if (!a.ws || !aligned(a.ws, 256) || a.ws_bytes < (what == CE_KEEP ? L.kept : L.total) || !a.control ||
+      !aligned(a.control, 256))
     return KD_ERR_WORKSPACE;
   if ((st = check_device()) != KD_OK) return st;
 
   cudaStream_t s = static_cast<cudaStream_t>(a.stream);
   uint8_t* w8 = static_cast<uint8_t*>(a.ws);
+  a.split = w8 + L.gh_part;
   Ctrl* ctrl = static_cast<Ctrl*>(a.ws);
   uint32_t* err = &static_cast<Ctrl*>(a.control)->err;
   int32_t* list = reinterpret_cast<int32_t*>(w8 + L.list);
   float* losses = a.losses ? a.losses : reinterpret_cast<float*>(w8 + L.losses);
   int32_t* labels_c = reinterpret_cast<int32_t*>(w8 + L.labels);
-  float4* row_stats = reinterpret_cast<float4*>(w8 + L.stats);
   float4* partials = reinterpret_cast<float4*>(w8 + L.partials);
   uint16_t* Hc = reinterpret_cast<uint16_t*>(w8 + L.hidden);
   const uint64_t d = uint64_t(a.d), V = uint64_t(a.V), row_bytes = d * 2;
@@ -564,15 +585,13 @@ int ce_run(const CeCall& a, bool step) {
   const int grid = gemm_max_grid();
 
   prof_before("kd_ce_list", s);
-  kd_ce_list_kernel<<<1, LIST_THREADS, 0, s>>>(a.labels, a.mask, a.N, a.ignore, list, &ctrl->n_valid, a.lse, losses,
-                                             a.grad_loss, 1.f - a.smooth,
-                                             step ? reinterpret_cast<float*>(w8 + L.alpha) : nullptr);
+  kd_ce_list_kernel<<<1, LIST_THREADS, 0, s>>>(a.labels, a.mask, a.N, a.ignore, list, &ctrl->n_valid, a.lse, losses);
   prof_after(s);
   KD_TRY(cudaGetLastError());
 
   for (int64_t c0 = 0; c0 < a.N; c0 += a.chunk) {
     const int n = int((a.N - c0) < a.chunk ? (a.N - c0) : a.chunk);  // at most
-    const bool zero = step && c0 == 0;
+    const bool zero = what == CE_STEP && c0 == 0;
     const int64_t warps = (zero && a.N > L.rows_pad ? a.N : L.rows_pad);
     const int64_t blocks = (warps + GATHER_WARPS - 1) / GATHER_WARPS;
     prof_before("kd_ce_gather", s);
@@ -597,7 +616,7 @@ int ce_run(const CeCall& a, bool step) {
     p.tokens = labels_c;
     p.ce_cap = a.softcap;
     p.ce_sum = a.smooth > 0.f;
-    p.ce_q = step;
+    p.ce_q = what != CE_LOSS;
     p.err = err;
     p.a_k3d = p.b_k3d = p.cta_pair && d64;
     if (!(p.a_k3d ? make_tmap_mn2_bf16(&th, Hc, d, uint64_t(n), row_bytes, BM)
@@ -605,9 +624,9 @@ int ce_run(const CeCall& a, bool step) {
         !(p.b_k3d ? make_tmap_mn2_bf16(&tw, a.W, d, V, row_bytes, BN / 2)
                   : make_tmap_2d_bf16(&tw, a.W, d, V, row_bytes, BK, p.cta_pair ? BN / 2 : BN)))
       return KD_ERR_CUDA;
-    if (step && !make_tmap_dz_blocked(&tq, w8 + L.dz, uint64_t(n), uint64_t(L.rows_pad), uint64_t(L.nvb), 32))
+    if (p.ce_q && !make_tmap_dz_blocked(&tq, w8 + L.dz, uint64_t(n), uint64_t(L.rows_pad), uint64_t(L.nvb), 32))
       return KD_ERR_CUDA;
-    KD_TRY(launch_gemm(p, th, tw, step ? tq : tw, grid, s));
+    KD_TRY(launch_gemm(p, th, tw, p.ce_q ? tq : tw, grid, s));
 
     CeCombine c{};
     c.partials = partials;
@@ -616,20 +635,32 @@ int ce_run(const CeCall& a, bool step) {
     c.list = list; c.n_valid = &ctrl->n_valid; c.labels_c = labels_c;
     c.smooth = a.smooth; c.z_loss = a.z_loss; c.softcap = a.softcap;
     c.lse = a.lse; c.losses = losses;
-    c.row_stats = step ? row_stats : nullptr;
+    c.row_stats = what != CE_LOSS ? reinterpret_cast<float4*>(w8 + L.stats) : nullptr;
     c.err = err;
     prof_before("kd_ce_combine", s);
     kd_ce_combine_kernel<<<unsigned((n + CC_ROWS - 1) / CC_ROWS), dim3(CC_ROWS, CC_PHASES), 0, s>>>(c);
     prof_after(s);
     KD_TRY(cudaGetLastError());
-    if (!step) continue;
-
-    KD_TRY(launch_ce_dz(unsigned((n + DQ_ROWS - 1) / DQ_ROWS) * unsigned(L.tiles), s,
-                        reinterpret_cast<uint4*>(w8 + L.dz), int(L.rows_pad), L.nvb, partials, c.rows_pad, row_stats,
-                        labels_c, &ctrl->n_valid, c0, n, a.softcap));
-    if ((st = kd_status(ce_products(a, L, w8, c0, n, s))) != KD_OK) return st;
+    if (what == CE_STEP && (st = kd_status(ce_gradients(a, L, w8, c0, n, s))) != KD_OK) return st;
   }
   return map_cuda(launch_loss_reduce(losses, nullptr, a.N, &ctrl->n_valid, a.loss, s));
+}
+
+// The gradients of a forward pass (CE_KEEP) from its workspace.
+int ce_from_kept(CeCall a) {
+  kd_status st = check_proj_args(a.W, a.W, a.N, a.d, a.V, a.chunk, 1.f);  // the hidden states are among what was kept
+  if (st == KD_OK) st = ce_check_options(a);
+  if (st == KD_OK) st = ce_check_gradients(a);
+  if (st != KD_OK) return st;
+  const CeLayout L = ce_layout(a.N, a.d, a.V, a.chunk, true);
+  if (!a.ws || !aligned(a.ws, 256) || a.ws_bytes < L.kept || !a.split || !aligned(a.split, 256) || !a.control ||
+      !aligned(a.control, 256))
+    return KD_ERR_WORKSPACE;
+  if ((st = check_device()) != KD_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(a.stream);
+  // the rows of positions without a loss stay zero
+  KD_TRY(cudaMemsetAsync(a.grad_H, 0, size_t(a.N) * size_t(a.d) * (a.grad_H_f32 ? 4 : 2), s));
+  return ce_gradients(a, L, static_cast<uint8_t*>(a.ws), 0, int(a.N), s);
 }
 
 }  // namespace
@@ -655,7 +686,7 @@ int kd_fused_cross_entropy_fwd(const void* H_bf16, const void* W_bf16, const int
   a.smooth = label_smoothing; a.z_loss = z_loss; a.softcap = softcap; a.ignore = ignore_index;
   a.loss = loss_out; a.lse = lse_out; a.losses = loss_per_token_out;
   a.ws = ws; a.ws_bytes = ws_bytes; a.control = control; a.stream = stream;
-  return ce_run(a, false);
+  return ce_run(a, CE_LOSS);
 }
 
 int kd_fused_cross_entropy_step(const void* H_bf16, const void* W_bf16, const int32_t* labels, const uint8_t* mask,
@@ -672,7 +703,44 @@ int kd_fused_cross_entropy_step(const void* H_bf16, const void* W_bf16, const in
   a.loss = loss_out; a.lse = lse_out; a.losses = loss_per_token_out;
   a.grad_H = grad_H; a.grad_H_f32 = grad_H_is_fp32; a.grad_W = grad_W; a.w_kind = grad_W_kind;
   a.ws = ws; a.ws_bytes = ws_bytes; a.control = control; a.stream = stream;
-  return ce_run(a, true);
+  return ce_run(a, CE_STEP);
+}
+
+size_t kd_fused_cross_entropy_kept(int64_t N, int64_t d, int64_t V) {
+  if (N < 1 || d < 1 || V < 1) return 0;
+  return ce_layout(N, d, V, one_chunk(N), true).kept;
+}
+
+int kd_fused_cross_entropy_keep(const void* H_bf16, const void* W_bf16, const int32_t* labels, const uint8_t* mask,
+                                int64_t N, int64_t d, int64_t V, float label_smoothing, float z_loss, float softcap,
+                                int ignore_index, float* loss_out, float* lse_out, float* loss_per_token_out,
+                                void* kept, size_t kept_bytes, void* control, void* stream) {
+  CeCall a{};
+  a.H = H_bf16; a.W = W_bf16; a.labels = labels; a.mask = mask;
+  a.N = N; a.d = d; a.V = V; a.chunk = one_chunk(N);
+  a.smooth = label_smoothing; a.z_loss = z_loss; a.softcap = softcap; a.ignore = ignore_index;
+  a.loss = loss_out; a.lse = lse_out; a.losses = loss_per_token_out;
+  a.ws = kept; a.ws_bytes = kept_bytes; a.control = control; a.stream = stream;
+  return ce_run(a, CE_KEEP);
+}
+
+size_t kd_fused_cross_entropy_bwd_workspace(int64_t N, int64_t d, int64_t V) {
+  if (N < 1 || d < 1 || V < 1) return 0;
+  return ce_split_bytes(one_chunk(N), d);
+}
+
+int kd_fused_cross_entropy_bwd(const void* W_bf16, int64_t N, int64_t d, int64_t V, float label_smoothing,
+                               float softcap, const float* grad_loss, void* grad_H, int grad_H_is_fp32, void* grad_W,
+                               int grad_W_kind, void* kept, size_t kept_bytes, void* ws, size_t ws_bytes, void* control,
+                               void* stream) {
+  CeCall a{};
+  a.W = W_bf16;
+  a.N = N; a.d = d; a.V = V; a.chunk = one_chunk(N);
+  a.smooth = label_smoothing; a.softcap = softcap; a.grad_loss = grad_loss;
+  a.grad_H = grad_H; a.grad_H_f32 = grad_H_is_fp32; a.grad_W = grad_W; a.w_kind = grad_W_kind;
+  a.ws = kept; a.ws_bytes = kept_bytes; a.control = control; a.stream = stream;
+  a.split = ws_bytes >= kd_fused_cross_entropy_bwd_workspace(N, d, V) ? ws : nullptr;
+  return ce_from_kept(a);
 }
 
 int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* factor, void* stream) {
