@@ -479,8 +479,9 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
  * loss (autograd's), all positions in one chunk: the first is the forward pass and leaves in `kept`
  * (kd_fused_cross_entropy_kept bytes, of any content before) what the second, given the same W, sizes and
  * options, makes the gradients of, once: it writes dZ where the logits lay.
- * Workspace: `step` != 0 asks for the step's (it grows with chunk * V), 0 for the forward pass's
- * (chunk * (V / 16 + 2 d) bytes).  `ws` may be memory of any content; the error word is in `control`
+ * Workspace, in bytes, for chunk positions or N where that is less, to whole tiles: 0 for `step` asks for the forward
+ * pass's, chunk * (V / 8 + 2 d + 20) + 8 N; anything else for the step's, chunk * (2 V + 32 d) more, for the 16-bit
+ * logits and for up to eight fp32 parts of grad_H.  `ws` may be memory of any content; the error word is in `control`
  * (see kd_logits_kl_fwd_ctl), which may be `ws` itself once kd_workspace_clear has cleared it.
  * ------------------------------------------------------------------------ */
 

@@ -57,3 +57,17 @@ def test_bad_workspaces(lib):
                dict(ctl=None), dict(ctl=P + 16)):
         assert bwd(lib, **kw) == _abi.KD_ERR_WORKSPACE
     assert lib.kd_fused_cross_entropy_kept(0, 64, 1000) == lib.kd_fused_cross_entropy_bwd_workspace(0, 64, 1000) == 0
+
+
+@pytest.mark.parametrize("N,d,V,chunk", [(1, 8, 1, 128), (4096, 2880, 201088, 4096), (8192, 2048, 32000, 4096),
+                                         (509, 1000, 50257, 8192)])
+def test_workspaces_are_as_documented(lib, N, d, V, chunk):
+    """The header's sums, sizes to whole tiles (128 positions, 128 columns; 64 of the 16-bit logits), nine parts each
+    to 256 bytes."""
+    up = lambda x, to: -(-x // to) * to
+    c, room = up(min(N, chunk), 128), 9 * 256
+    forward = c * (up(V, 128) // 8 + 2 * d + 20) + 8 * N
+    more = c * (2 * up(V, 64) + 32 * d)
+    for step, most in ((0, forward), (1, forward + more)):
+        need = lib.kd_fused_cross_entropy_workspace(N, d, V, chunk, step)
+        assert most - 256 <= need <= most + room + 256
