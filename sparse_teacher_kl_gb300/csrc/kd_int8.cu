@@ -5,8 +5,9 @@
 //
 // sm_103a's fast tensor path takes no 8-bit integers, but every one of them is a 16-bit floating-point
 // number, and so is their product a sum of exact terms: fp16 operands and fp32 accumulators give the integer
-// sums themselves as long as those stay below 2^24 (always for K <= 1024; K = 4096 of random integers stays
-// a hundred times below it), and beyond that sums rounded to fp32.  So the operations cannot go
+// sums themselves as long as those stay within 2^24 (always for K <= 1024; at K = 4096 a standard deviation of the
+// sum of uniform integers is 2^24 / 48, and the largest of 5 million sums 2^24 / 9; normal rows scaled by their
+// largest stay 40 times away), and beyond that sums that each step of 16 cuts off to fp32.  So the operations cannot go
 // faster than the 16-bit rate, but the weights keep their single byte all the way from HBM to the SM:
 // they are widened on their way from shared to tensor memory, where tcgen05.mma takes its A operand from.
 //
