@@ -475,6 +475,10 @@ __global__ void __launch_bounds__(T8_THREADS, 1)
 //   one, rows anywhere    2/4/4 109, 4/4/2 122, 8/3/1 136, 4/3/2 149, 4/2/4 184
 //   four                  4/3/2 115, 4/2/4 129, 4/4/2 160, 8/3/1 190
 //   four, rows anywhere   4/2/4 164, 8/3/1 178, 4/4/2 194, 2/4/4 205, 4/3/2 240
+// Other heads, the choice and the best of the five: one token 4096 x 151936 109 / 104 (4/2/4), 1024 x 50257 12.1, 256 x 50257
+// 5.1, 2880 x 8192 12.0 / 8.6 (4/2/4), 1024 x 8192 5.7 / 4.7 (few rows a block leave fewer of the SMs' slots empty there);
+// rows anywhere 115, 13.9, 6.0 / 5.7, 10.1, 5.3; four 2880 x 8192 13.8 / 13.5, 1024 x 8192 6.7, 256 x 50257 6.9; four, rows
+// anywhere 4096 x 151936 166, 1024 x 50257 24, 2880 x 8192 14.8, 1024 x 8192 7.4 / 7.2.
 constexpr int F8_THREADS = 256;
 constexpr int F8_TOKENS = 4;
 constexpr int F8_MAX_SMEM = 64 * 1024;
@@ -882,8 +886,10 @@ constexpr int T8_SINGLE = 64;
 
 // Whether the tokens are few, and fit into a block's shared memory.  One always; up to F8_TOKENS where the tensor
 // cores' way would copy the weights to aligned rows first (four tokens, 2880 x 201088: 164 us against 287), or
-// where the weights are few, so that its longer start counts (four tokens, this / that: 2880 x 4096 9 / 13 us,
-// 2880 x 16000 17 / 13, 2880 x 201088 115 / 97).
+// where the weights are few, so that its longer start counts (two tokens, four, that way; us, weights not in the L2:
+// 256 x 50257 6.2, 7.2, 9.4; 1024 x 8192 5.4, 6.4, 8.9; 2880 x 4096 11.3, 12.2, 14.0; 4096 x 5000 13.3, 15.6, 17.1; 2880 x 8192,
+// 24 million, 12.2, 13.8, 14.4; 2880 x 16000 20.0, 20.3, 15.7; 4096 x 32000 35.6, 38.1, 31.6; 2880 x 201088 118, 117, 102.
+// K = 1024 turns later: 1024 x 50257 14.2, 15.1, 16.5).
 constexpr int64_t F8_WEIGHTS = 24000000;
 
 bool int8_few(int64_t M, int64_t N, int64_t K, bool aligned_rows) {
