@@ -750,6 +750,8 @@ class _FusedCrossEntropy(torch.autograd.Function):
         if not wanted:
             return _ce_forward(H, W, labels, mask, chunk, options, None, ctx.control)[0][0]
         if N <= chunk:
+            if chunk % 128:  # refused as by the calls that take it
+                _abi.check(_abi.KD_ERR_INVALID_ARG, "kd_fused_cross_entropy_keep")
             kept = (_scratch(_abi.kd_fused_cross_entropy_kept(N, d, V), dev),)
             loss = torch.empty((1,), dtype=torch.float32, device=dev)
             lse = torch.empty((N,), dtype=torch.float32, device=dev)

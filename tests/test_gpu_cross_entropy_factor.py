@@ -111,6 +111,14 @@ def test_positions_without_a_loss(kd, cuda_device):
         assert float(loss.detach()) == 0 and not gH.any() and not gW.any()
 
 
+@pytest.mark.parametrize("chunk", [0, 100, 129, -128])
+def test_chunks_are_refused_with_and_without_gradients(kd, cuda_device, chunk):
+    H, W, labels = case(64, 64, 500)
+    for h in (H, H.clone().requires_grad_()):
+        with pytest.raises(kd.KDError):
+            kd.fused_cross_entropy(h, W, labels, chunk=chunk)
+
+
 def test_changed_inputs_are_refused(kd, cuda_device):
     H, W, labels = case(100, 64, 500)
     h, w = H.clone().requires_grad_(), W.clone().requires_grad_()
