@@ -604,7 +604,9 @@ int ce_run(CeCall a, CeWhat what) {
     alignas(64) CUtensorMap th, tw, tq;
     GemmProblem p{};
     p.M = n; p.N = int(a.V); p.K = int(a.d);
-    p.epi = EPI_CE;
+    // (the loss alone has no codes: caps that need no series take the kernel with the fewer registers, 509 x 1000 x
+    // 50257 with c = 30 91 us a call, 100 with the other)
+    p.epi = EPI_CE + (what == CE_LOSS && a.softcap > 0.f && a.softcap <= CE_CAP_NEAR ? CE_CODE_EDGE : ce_code(a.softcap));
     p.m_tiles = (n + BM - 1) / BM;
     p.n_tiles = int((a.V + BN - 1) / BN);
     p.n_group = 1;

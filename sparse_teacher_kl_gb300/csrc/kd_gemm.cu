@@ -112,7 +112,7 @@ __device__ __forceinline__ void unit_coords(const GemmProblem& p, const Extent& 
   const int k_blocks = ((e.K + BK - 1) / BK + kkb - 1) / kkb;
   const int m_groups = (e.m_tiles + p.cluster - 1) / p.cluster;
   if (p.epi == EPI_LSE || p.epi == EPI_DZ || p.epi == EPI_LSE_Z || p.epi == EPI_LSE_H || p.epi == EPI_DZ_LP ||
-      p.epi == EPI_CE) {
+      is_ce(p.epi)) {
     const int g = u / m_groups;
     m_blk = (u - g * m_groups) * p.cluster + int(crank);
     n_first = g * p.n_group;
@@ -149,14 +149,14 @@ __device__ __forceinline__ void unit_coords(const GemmProblem& p, const Extent& 
 // special-function results for each logit: two warps on each of the SM's four schedulers, each with half of
 // the columns, hide their latency (509 x 50257, d = 1000, capped: 62 us, with four warps 78).
 template <int EPI>
-constexpr int kEpiWarps = EPI == EPI_CE ? 8 : 4;
+constexpr int kEpiWarps = is_ce(EPI) ? 8 : 4;
 template <int EPI>
 constexpr int kThreads = 64 + 32 * kEpiWarps<EPI>;
 static_assert(kThreads<EPI_STORE> == GEMM_THREADS, "TMA warp, MMA warp, 4 epilogue warps");
 
 // 32 logits' 16-bit codes (CeCode) into half of a row of a box: its 16-byte chunks j0 .. j0 + 3, swizzled.  2^23 added
 // to a number of steps leaves it, rounded, in the low bits of the sum.  CE_CODE_SPLIT without FAR: none of them is
-// CE_SPLIT or more below ref.
+// CE_SPLIT or more below ref.  CE_CODE_DIST takes the distances themselves for z.
 template <CeCode CODE, bool FAR = true>
 __device__ __forceinline__ void ce_codes(const float* z, float ref, float cap, float cap_inv, uint8_t* box, uint32_t lane,
                                          uint32_t j0) {
@@ -165,7 +165,7 @@ __device__ __forceinline__ void ce_codes(const float* z, float ref, float cap, f
     if (CODE == CE_CODE_EDGE)
       return __float_as_uint(fmaf(sqrt_approx(fmaxf(cap - fabsf(v), 0.f) * cap_inv), CE_EDGE_STEPS, kMagic));
     constexpr float most = kMagic + (CODE == CE_CODE_DIST ? 65535.f : float(CE_SPLIT_CODE - 1));
-    const float dist = ref - v;
+    const float dist = CODE == CE_CODE_DIST ? v : ref - v;
     float code = fminf(fmaxf(fmaf(dist, CE_STEPS, kMagic), kMagic), most);
     if (CODE == CE_CODE_SPLIT && FAR) {
       const float w = fminf(sqrt_approx(fmaxf(v + cap, 0.f) * (0.5f * cap_inv)), 1.f);
@@ -195,17 +195,20 @@ __device__ __forceinline__ void ce_codes(const float* z, float ref, float cap, f
 // EPI_CE therefore takes the reduction CE_CHUNK_K deep at a time and adds the parts in registers, in the time of
 // the next part's MMAs.  512 deep: the losses of 3 positions that lean towards their labels, d = 2328, are within
 // 5.3e-7 of float64 (1024 deep 1.4e-6), for 6 % of the projection (4096 x 2880 x 201088 2.73 ms; 1024 deep 2.69).
+// A kernel for each code: the three together spill more (8192 x 2048 x 32000 with smoothing, without a cap 680 us, and
+// 627 alone).  Even so 128 logits a thread at 168 registers (of ten warps, counted as twelve) leave 40 to 120 bytes of
+// spills.
+template <CeCode CODE>
 __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap& tmap_c, float (&z)[CE_COLS], int first,
                                         int m_blk, int row, int rows, int nid, uint8_t* box, uint32_t lane,
                                         uint32_t quarter) {
   constexpr float kL2E = 1.4426950408889634f;
   const bool last = first + CE_COLS > p.N;  // columns past the vocabulary: weight 0
-  const float cap = p.ce_cap, cap_inv = cap > 0.f ? 1.f / cap : 0.f, cap_k = cap > 0.f ? 2.f * kL2E / cap : 0.f;
-  const CeCode code = ce_code(cap);
-  if (cap > CE_CAP_NEAR) {
+  const float cap = p.ce_cap, cap_inv = 1.f / cap, cap_k = 2.f * kL2E * cap_inv;  // not looked at without a cap
+  if (CODE == CE_CODE_SPLIT && cap > CE_CAP_NEAR) {
 #pragma unroll
     for (int i = 0; i < CE_COLS; ++i) z[i] = ce_capped_far(z[i], cap, cap_k);
-  } else if (cap > 0.f) {
+  } else if (CODE != CE_CODE_DIST) {
 #pragma unroll
     for (int i = 0; i < CE_COLS; ++i) z[i] = ce_capped(z[i], cap, cap_k);
   }
@@ -241,38 +244,39 @@ __device__ __forceinline__ void ce_half(const GemmProblem& p, const CUtensorMap&
 #pragma unroll
   for (int c = 0; c < CE_COLS / 32; ++c) {
     float* x = z + c * 32;
-    if (p.ce_q) {
-      if ((c & 1) == 0) {
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-      }
-      const uint32_t j0 = uint32_t(c & 1) * 4;
-      if (code == CE_CODE_DIST) ce_codes<CE_CODE_DIST>(x, ref, cap, cap_inv, box, lane, j0);
-      else if (code == CE_CODE_EDGE) ce_codes<CE_CODE_EDGE>(x, ref, cap, cap_inv, box, lane, j0);
-      else {
-        // far logits are rare, and their codes twice the work (a step of 4096 x 2048 x 128000, c = 30: 4.24 ms,
-        // 4.33 with all logits coded so)
+    const uint32_t j0 = uint32_t(c & 1) * 4;
+    if (p.ce_q && (c & 1) == 0) {
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+    }
+    if (CODE != CE_CODE_DIST && p.ce_q) {
+      // far logits are rare, and their codes twice the work (a step of 4096 x 2048 x 128000, c = 30: 4.24 ms,
+      // 4.33 with all logits coded so)
+      bool far = true;
+      if (CODE == CE_CODE_SPLIT) {
         float least = x[0];
 #pragma unroll
         for (int i = 1; i < 32; ++i) least = fminf(least, x[i]);
-        if (__any_sync(0xffffffffu, ref - least >= CE_SPLIT))
-          ce_codes<CE_CODE_SPLIT>(x, ref, cap, cap_inv, box, lane, j0);
-        else
-          ce_codes<CE_CODE_SPLIT, false>(x, ref, cap, cap_inv, box, lane, j0);
+        far = __any_sync(0xffffffffu, ref - least >= CE_SPLIT);
       }
-      if (c & 1) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tmap_c, box, 0, m_blk * BM + int(quarter) * 32, (first + c * 32 - 32) / 64);
-          bulk_commit();
-        }
-      }
+      if (far) ce_codes<CODE>(x, ref, cap, cap_inv, box, lane, j0);
+      else ce_codes<CODE, false>(x, ref, cap, cap_inv, box, lane, j0);
     }
 #pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = ref - x[i];
+#pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      s0 += ex2_approx((ref - x[i]) * -kL2E);
-      s1 += ex2_approx((ref - x[i + 1]) * -kL2E);
+      s0 += ex2_approx(x[i] * -kL2E);
+      s1 += ex2_approx(x[i + 1] * -kL2E);
+    }
+    if (CODE == CE_CODE_DIST && p.ce_q) ce_codes<CODE>(x, ref, cap, cap_inv, box, lane, j0);
+    if (p.ce_q && (c & 1) != 0) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&tmap_c, box, 0, m_blk * BM + int(quarter) * 32, (first + c * 32 - 32) / 64);
+        bulk_commit();
+      }
     }
   }
   if (row < rows && first < p.N)
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tmap_a);
     tma_prefetch_map(&tmap_b);
-    if (EPI == EPI_DZ || EPI == EPI_LSE_Z || EPI == EPI_DZ_LP || EPI == EPI_CE) tma_prefetch_map(&tmap_c);
+    if (EPI == EPI_DZ || EPI == EPI_LSE_Z || EPI == EPI_DZ_LP || is_ce(EPI)) tma_prefetch_map(&tmap_c);
   }
   if (warp == 1) {
     if (CG == 2) tmem_alloc_pair(&tail->tmem_base, TMEM_COLS); else tmem_alloc(&tail->tmem_base, TMEM_COLS);
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
       for (int u = u_first; u < ext.n_units && ok; u += u_step) {
         int m_blk, n_first, n_count, kb_lo, kb_hi, split;
         unit_coords(p, ext, u, crank, G::kKB, m_blk, n_first, n_count, kb_lo, kb_hi, split);
-        const int k_step = EPI == EPI_CE ? CE_CHUNK_K / (BK * G::kKB) : kb_hi - kb_lo;
+        const int k_step = is_ce(EPI) ? CE_CHUNK_K / (BK * G::kKB) : kb_hi - kb_lo;
         for (int nb = n_first; nb < n_first + n_count && ok; ++nb) {
           // an accumulator for each k_step stages of the reduction: all of them but for EPI_CE
           for (int kc = kb_lo; kc < kb_hi && ok; kc += k_step, ++acc_it) {
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
         }
       }
 
-      if (EPI == EPI_CE && row < ext.rows) {
+      if (is_ce(EPI) && row < ext.rows) {
         nid = __ldg(p.tokens + row);
         if (nid < 0 || nid >= p.N) nid = 0x7fffffff;  // out of range: reported by the combine
       }
@@ -565,7 +569,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
         }
       }
 
-      if (EPI == EPI_CE) {
+      if constexpr (is_ce(EPI)) {
         const int half = int(warp - 2u) >> 2, k_step = CE_CHUNK_K / (BK * G::kKB);
         for (int nb = n_first; nb < n_first + n_count && ok; ++nb) {
           float x[CE_COLS];
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
             else mbar_arrive(&tail->tempty[a]);
           }
           if (ok)
-            ce_half(p, tmap_c, x, nb * BN + half * CE_COLS, m_blk, row, ext.rows, nid, staging + (warp - 2u) * 4096u,
+            ce_half<CeCode(EPI - EPI_CE)>(p, tmap_c, x, nb * BN + half * CE_COLS, m_blk, row, ext.rows, nid, staging + (warp - 2u) * 4096u,
                     lane, quarter);
         }
         continue;
@@ -952,7 +956,7 @@ __global__ void __launch_bounds__(kThreads<EPI>, 1)
         p.partials[size_t(n_first / p.n_group) * (p.m_tiles * BM) + row] =
             make_float4(run_m, run_s, run_g, run_u);
     }
-    if ((EPI == EPI_DZ || EPI == EPI_DZ_LP || EPI == EPI_LSE_Z || EPI == EPI_CE || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
+    if ((EPI == EPI_DZ || EPI == EPI_DZ_LP || EPI == EPI_LSE_Z || is_ce(EPI) || (EPI == EPI_STORE && p.c_tma) || (EPI == EPI_ACCUM && p.K <= ACCUM_STAGED_MAX_K)) && lane == 0)
       bulk_wait_all();  // output boxes done before exit
   }
 
@@ -1048,7 +1052,7 @@ static const char* gemm_name(int epi, int a_mn, int b_mn) {
     case EPI_DZ: return "kd_proj_dz_bwd";
     case EPI_LSE_H: return "kd_proj_logprob_fwd";
     case EPI_DZ_LP: return "kd_proj_logprob_bwd";
-    case EPI_CE: return "kd_proj_ce";
+    case EPI_CE: case EPI_CE_EDGE: case EPI_CE_SPLIT: return "kd_proj_ce";
     case EPI_STORE: return (a_mn == 0 && b_mn == 1) ? "kd_gemm_dz_w" : "kd_gemm_store";
     default: return (a_mn == 1 && b_mn == 1) ? "kd_gemm_dzT_h" : "kd_gemm_accum";
   }
@@ -1071,6 +1075,8 @@ cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUten
       case EPI_LSE_H: e = two ? launch_one<EPI_LSE_H, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_DZ_LP: e = two ? launch_one<EPI_DZ_LP, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_CE: e = two ? launch_one<EPI_CE, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
+      case EPI_CE_EDGE: e = two ? launch_one<EPI_CE_EDGE, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
+      case EPI_CE_SPLIT: e = two ? launch_one<EPI_CE_SPLIT, 2, 2>(p, ta, tb, tc, grid, s) : cudaErrorInvalidValue; break;
       case EPI_STORE:
         e = two ? launch_one<EPI_STORE, 2, 2>(p, ta, tb, tc, grid, s) : launch_one<EPI_STORE, 2, 1>(p, ta, tb, tc, grid, s);
         break;
@@ -1086,6 +1092,8 @@ cudaError_t launch_gemm(const GemmProblem& p, const CUtensorMap& ta, const CUten
       case EPI_LSE_H: e = launch_one<EPI_LSE_H, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_DZ_LP: e = launch_one<EPI_DZ_LP, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_CE: e = launch_one<EPI_CE, 1>(p, ta, tb, tc, grid, s); break;
+      case EPI_CE_EDGE: e = launch_one<EPI_CE_EDGE, 1>(p, ta, tb, tc, grid, s); break;
+      case EPI_CE_SPLIT: e = launch_one<EPI_CE_SPLIT, 1>(p, ta, tb, tc, grid, s); break;
       case EPI_STORE: e = launch_one<EPI_STORE, 1>(p, ta, tb, tc, grid, s); break;
       default: e = launch_one<EPI_ACCUM, 1>(p, ta, tb, tc, grid, s); break;
     }

@@ -57,8 +57,11 @@ enum EpiKind : int {
   EPI_LSE_H = 5,  // log probabilities: online logsumexp and entropy sum, the token's logit -> partials
   EPI_DZ_LP = 6,  // their gradient: dZ = p (c0 + c1 log2 p) + [v = token] g / tau -> bf16, blocked
   EPI_CE = 7,     // cross entropy: a tile's (max, sum, label's logit, sum of logits) -> partials; with ce_q the
-                  // logits in 16 bits (CeCode), blocked as dZ
+                  // logits in 16 bits (CeCode), blocked as dZ.  EPI_CE + code: without a cap
+  EPI_CE_EDGE = 8,   // caps up to CE_CAP_EDGE
+  EPI_CE_SPLIT = 9,  // wider ones
 };
+__host__ __device__ constexpr bool is_ce(int epi) { return epi >= EPI_CE && epi <= EPI_CE_SPLIT; }
 
 // 64-deep k-blocks per ring stage of a CTA-pair launch: two when both operands are
 // K-major (the loss sweeps and the teacher projection: each stage one depth-2 box per
