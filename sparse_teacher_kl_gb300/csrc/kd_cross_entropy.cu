@@ -19,9 +19,11 @@
 // front, in order, and the products stop after the last of them (GemmProblem::rows_dev).  Their hidden states
 // are never read, so they may hold anything.
 //
-// Measured (one pass of a step, H and W bf16): 4096 x 2880 x 201088 9.4 ms, of it the projection 2.7, dZ 0.55 (6.0 TB/s),
+// Measured (one pass of a step, H and W bf16): 4096 x 2880 x 201088 9.3 ms, of it the projection 2.6, dZ 0.53 (6.2 TB/s),
 // the products 2.7 each (1.75 PFLOP/s); 8192 x 2048 x 32000 with 5 % of the labels ignored 2.1 ms (fused_logprobs with
-// its gradient, which projects twice: 2.7); 4096 x 4096 x 151936 with 65 % ignored 3.7 ms, none ignored 9.0.
+// its gradient, which projects twice: 2.7); 4096 x 4096 x 151936 with 65 % ignored 3.65 ms, none ignored 9.0.  A softcap
+// adds 2 to 3 % to a step: 4096 x 2048 x 128000 4.05 ms, with c = 8 4.15, with 30 4.2.  kd_ce_combine_kernel's
+// loops over the phases are unrolled whole and spill 600 bytes a thread (8 to 45 us of a step).
 #include <math.h>
 
 #include <type_traits>

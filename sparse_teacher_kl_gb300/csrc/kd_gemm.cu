@@ -194,7 +194,8 @@ __device__ __forceinline__ void ce_codes(const float* z, float ref, float cap, f
 // steps of 16 is about n 2^-26 of itself too near to 0: 2e-6 of a label's logit at d = 2048, and of the losses.
 // EPI_CE therefore takes the reduction CE_CHUNK_K deep at a time and adds the parts in registers, in the time of
 // the next part's MMAs.  512 deep: the losses of 3 positions that lean towards their labels, d = 2328, are within
-// 5.3e-7 of float64 (1024 deep 1.4e-6), for 6 % of the projection (4096 x 2880 x 201088 2.73 ms; 1024 deep 2.69).
+// 5.3e-7 of float64 (1024 deep 1.4e-6), for 6 % of the projection (4096 x 2880 x 201088, before each
+// code had its kernel, 2.73 ms; 1024 deep 2.69; now 2.62).
 // A kernel for each code: the three together spill more (8192 x 2048 x 32000 with smoothing, without a cap 680 us, and
 // 627 alone).  Even so 128 logits a thread at 168 registers (of ten warps, counted as twelve) leave 40 to 120 bytes of
 // spills.
