@@ -478,7 +478,8 @@ KD_API int kd_fused_logprobs_bwd_ctl(const void* H_bf16, const void* W_bf16, con
  * kd_fused_cross_entropy_keep and _bwd are the step in two calls, for a grad_loss that is known only after the
  * loss (autograd's), all positions in one chunk: the first is the forward pass and leaves in `kept`
  * (kd_fused_cross_entropy_kept bytes, of any content before) what the second, given the same W, sizes and
- * options, makes the gradients of, once: it writes dZ where the logits lay.
+ * options, makes the gradients of, once: it writes dZ where the logits lay.  A `kept` that holds nothing for these
+ * sizes and options (never filled, spent) is recorded in the error word; the gradients are then zero.
  * Workspace, in bytes, for chunk positions or N where that is less, to whole tiles: 0 for `step` asks for the forward
  * pass's, chunk * (V / 8 + 2 d + 20) + 8 N; anything else for the step's, chunk * (2 V + 32 d) more, for the 16-bit
  * logits and for up to eight fp32 parts of grad_H.  `ws` may be memory of any content; the error word is in `control`

@@ -25,7 +25,9 @@
 // adds 2 to 3 % to a step: 4096 x 2048 x 128000 4.05 ms, with c = 8 4.15, with 30 4.2.  kd_ce_combine_kernel's
 // loops over the phases are unrolled whole and spill 600 bytes a thread (8 to 45 us of a step).
 #include <math.h>
+#include <string.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "kd_device.cuh"
@@ -50,7 +52,7 @@ constexpr int LIST_THREADS = 1024, LIST_EACH = 8;
 __global__ void __launch_bounds__(LIST_THREADS)
     kd_ce_list_kernel(const int32_t* __restrict__ labels, const uint8_t* __restrict__ mask, int64_t N, int ignore,
                       int32_t* __restrict__ list, int32_t* __restrict__ n_valid, float* __restrict__ lse,
-                      float* __restrict__ losses) {
+                      float* __restrict__ losses, uint32_t* __restrict__ kept, uint32_t tag) {
   __shared__ int warp_sum[LIST_THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int base = 0;
@@ -90,7 +92,25 @@ __global__ void __launch_bounds__(LIST_THREADS)
     base += total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) *n_valid = base;
+  if (threadIdx.x == 0) {
+    *n_valid = base;
+    *kept = tag;
+  }
+}
+
+// The start of a backward pass from a kept forward pass: what is not there (another call's, or already spent) leaves
+// no valid position, so that nothing of it is used as an index; grad_H zero, for the positions without a loss.
+__global__ void __launch_bounds__(256)
+    kd_ce_begin_kernel(Ctrl* __restrict__ ctrl, uint32_t tag, uint4* __restrict__ grad_H, int64_t vecs, uint32_t* err) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (ctrl->kept != tag) {
+      raise_error(err, KD_DEVERR_NOT_KEPT, 0);
+      ctrl->n_valid = 0;
+    }
+    ctrl->kept = 0;
+  }
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < vecs; i += int64_t(gridDim.x) * blockDim.x)
+    grad_H[i] = make_uint4(0, 0, 0, 0);
 }
 
 __device__ __forceinline__ int chunk_rows(const int32_t* n_valid, int64_t c0, int cap) {
@@ -560,6 +580,16 @@ kd_status ce_check_gradients(const CeCall& a) {
 // A single chunk for all N positions.
 int64_t one_chunk(int64_t N) { return N <= KD_MAX_EXTENT ? (N + BM - 1) / BM * BM : BM; }
 
+// Tells what was kept for these sizes and options from anything else; not 0.
+uint32_t ce_tag(const CeCall& a) {
+  uint32_t smooth, cap, h = 2166136261u;
+  memcpy(&smooth, &a.smooth, 4);
+  memcpy(&cap, &a.softcap, 4);
+  for (uint32_t x : {uint32_t(a.N), uint32_t(a.d), uint32_t(a.V), smooth, cap})
+    for (int b = 0; b < 32; b += 8) h = (h ^ (x >> b & 255u)) * 16777619u;
+  return h | 1u;
+}
+
 int ce_run(CeCall a, CeWhat what) {
   kd_status st = check_proj_args(a.H, a.W, a.N, a.d, a.V, a.chunk, 1.f);
   if (st == KD_OK) st = ce_check_options(a);
@@ -587,7 +617,8 @@ int ce_run(CeCall a, CeWhat what) {
   const int grid = gemm_max_grid();
 
   prof_before("kd_ce_list", s);
-  kd_ce_list_kernel<<<1, LIST_THREADS, 0, s>>>(a.labels, a.mask, a.N, a.ignore, list, &ctrl->n_valid, a.lse, losses);
+  kd_ce_list_kernel<<<1, LIST_THREADS, 0, s>>>(a.labels, a.mask, a.N, a.ignore, list, &ctrl->n_valid, a.lse, losses,
+                                             &ctrl->kept, what == CE_KEEP ? ce_tag(a) : 0u);
   prof_after(s);
   KD_TRY(cudaGetLastError());
 
@@ -662,8 +693,12 @@ int ce_from_kept(CeCall a) {
     return KD_ERR_WORKSPACE;
   if ((st = check_device()) != KD_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(a.stream);
-  // the rows of positions without a loss stay zero
-  KD_TRY(cudaMemsetAsync(a.grad_H, 0, size_t(a.N) * size_t(a.d) * (a.grad_H_f32 ? 4 : 2), s));
+  const int64_t vecs = a.N * a.d * (a.grad_H_f32 ? 4 : 2) / 16, blocks = (vecs + 255) / 256, most = 8 * gemm_max_grid();
+  prof_before("kd_ce_begin", s);
+  kd_ce_begin_kernel<<<unsigned(blocks < most ? blocks : most), 256, 0, s>>>(
+      static_cast<Ctrl*>(a.ws), ce_tag(a), static_cast<uint4*>(a.grad_H), vecs, &static_cast<Ctrl*>(a.control)->err);
+  prof_after(s);
+  KD_TRY(cudaGetLastError());
   return ce_gradients(a, L, static_cast<uint8_t*>(a.ws), 0, int(a.N), s);
 }
 

@@ -18,6 +18,7 @@ constexpr uint32_t KD_DEVERR_NONE = 0;
 constexpr uint32_t KD_DEVERR_TIMEOUT = 1;
 constexpr uint32_t KD_DEVERR_BAD_ID = 2;
 constexpr uint32_t KD_DEVERR_BOUNDS = 3;  // KD_DEBUG builds: a computed index out of range (skipped)
+constexpr uint32_t KD_DEVERR_NOT_KEPT = 4;  // a backward pass from what no forward pass has kept for it
 
 // Upper bound on any single wait inside a kernel.  A healthy wait lasts
 // microseconds; this only stops a kernel that would otherwise hang.
@@ -30,7 +31,8 @@ struct Ctrl {
   uint32_t topk_reselected;  // top-K: rows selected a second time after a speculative start
   uint32_t pad0;
   int32_t n_valid;     // number of valid positions of the current call
-  uint32_t pad1[59];
+  uint32_t kept;       // cross entropy: what a forward pass has kept here (ce_tag), 0 once it is spent
+  uint32_t pad1[58];
 };
 static_assert(sizeof(Ctrl) == 256, "control block is 256 bytes");
 

@@ -155,6 +155,51 @@ def test_backward_on_its_own_in_a_graph(kd, cuda_device):
         assert torch.equal(got[0], gH) and torch.equal(got[1], gW)
 
 
+def test_nothing_kept(kd, cuda_device):
+    """What no forward pass has kept, or another one's, or what is spent: an error, zero gradients, nothing out of place."""
+    N, d, V = 200, 64, 700
+    H, W, labels = case(N, d, V, 0.9)
+    abi, stream = kd._abi, torch.cuda.current_stream().cuda_stream
+    control = kd.workspace(256, "cuda")
+    kept = torch.full((abi.kd_fused_cross_entropy_kept(N, d, V),), 0x7F, dtype=torch.uint8, device="cuda")
+    ws = torch.empty((abi.kd_fused_cross_entropy_bwd_workspace(N, d, V),), dtype=torch.uint8, device="cuda")
+    f32 = lambda *s: torch.full(s, 7.0, device="cuda")
+    loss, lse = f32(1), f32(N)
+
+    def backward(cap=0.0, smooth=0.0):
+        gH, gW, base = f32(N, d), f32(V, d), f32(V, d)
+        for g, kind in ((gW, abi.KD_GRAD_STORE_F32), (base, abi.KD_GRAD_ADD_F32)):
+            st = abi.kd_fused_cross_entropy_bwd(W.data_ptr(), N, d, V, smooth, cap, None, gH.data_ptr(), 1, g.data_ptr(), kind,
+                                                kept.data_ptr(), kept.numel(), ws.data_ptr(), ws.numel(),
+                                                control.data_ptr(), stream)
+            assert st == 0
+            if kind == abi.KD_GRAD_STORE_F32:
+                found = kd.device_error(control)[0], gH.clone(), gW
+        # the second of the two finds it spent in any case
+        assert kd.device_error(control)[0] == abi.KD_ERR_DEVICE and not gH.any() and (base == 7).all()
+        return found
+
+    def forward():
+        st = abi.kd_fused_cross_entropy_keep(H.data_ptr(), W.data_ptr(), labels.data_ptr(), None, N, d, V, 0.0, 0.0, 0.0,
+                                             -100, loss.data_ptr(), lse.data_ptr(), None, kept.data_ptr(), kept.numel(),
+                                             control.data_ptr(), stream)
+        assert st == 0
+
+    st, gH, gW = backward()
+    assert st == abi.KD_ERR_DEVICE and not gH.any() and not gW.any()
+    forward()
+    st, gH, gW = backward()
+    _, wH, wW = kd.fused_cross_entropy_step(H, W, labels, chunk=256, grad_H_fp32=True)
+    assert st == 0 and torch.equal(gH, wH) and torch.equal(gW, wW)
+    forward()
+    st, gH, gW = backward(cap=5.0)
+    assert st == abi.KD_ERR_DEVICE and not gH.any() and not gW.any()
+    forward()
+    kd.fused_cross_entropy_forward(H, W, labels, ws=kept, chunk=256)   # another call's workspace since
+    st, gH, gW = backward()
+    assert st == abi.KD_ERR_DEVICE and not gH.any() and not gW.any()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_scale_gradient(kd, cuda_device, dtype):
     x = torch.randn((8 * 1003,), device="cuda").to(dtype)
