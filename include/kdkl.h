@@ -527,7 +527,8 @@ KD_API int kd_scale_gradient(void* x, int64_t n, int is_fp32, const float* facto
  * scale NaN and integers 0.  q_out: [N, d] with row stride ld_q >= d; d at most 2^31 - 1024.
  *
  * kd_gemm_int8: C_mn = (sum_k A_mk B_nk) a_scale_m b_scale_n, A [M, K] the tokens and B [N, K] the channels,
- * 1 <= K <= KD_MAX_INT8_K, M and N at most 2^31 - 1024, any row strides lda, ldb >= K, ldc >= N; C bf16, fp16 or fp32 (kd_dtype).  The
+ * 1 <= K <= KD_MAX_INT8_K, M and N at most 2^31 - 1024, any row strides lda, ldb >= K, ldc >= N; C bf16, fp16 or
+ * fp32 (kd_dtype).  The
  * integer sum is exact while it stays below 2^24 (always for K <= 1024); from there on the tensor cores add in
  * fp32 and cut off, up to a step of the sum for each 16 products.  Each of the two products with a scale rounds
  * once to fp32, and the result once to C's type.  Weights whose rows start on

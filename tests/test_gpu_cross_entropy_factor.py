@@ -155,6 +155,24 @@ def test_backward_on_its_own_in_a_graph(kd, cuda_device):
         assert torch.equal(got[0], gH) and torch.equal(got[1], gW)
 
 
+@pytest.mark.parametrize("chunk", [512, 128])
+def test_forward_and_backward_in_graphs_of_their_own(kd, cuda_device, chunk):
+    """What the forward graph keeps, the backward graph spends, replay after replay."""
+    H, W, labels = case(300, 64, 1000, 0.8)
+    h, w = H.clone().requires_grad_(), W.clone().requires_grad_()
+    step = torch.cuda.make_graphed_callables(lambda a, b: kd.fused_cross_entropy(a, b, labels, chunk=chunk), (h, w))
+    for seed, factor in ((1, 1 / 3), (2, 1.0), (3, -5.0)):
+        H2, W2, l2 = case(300, 64, 1000, 0.3 * seed, seed)
+        labels.copy_(l2)
+        a, b = H2.clone().requires_grad_(), W2.clone().requires_grad_()
+        loss = step(a, b)
+        (loss * factor).backward()
+        h2, w2 = H2.clone().requires_grad_(), W2.clone().requires_grad_()
+        want = kd.fused_cross_entropy(h2, w2, l2, chunk=chunk)
+        (want * factor).backward()
+        assert torch.equal(loss, want) and torch.equal(a.grad, h2.grad) and torch.equal(b.grad, w2.grad)
+
+
 def test_nothing_kept(kd, cuda_device):
     """What no forward pass has kept, or another one's, or what is spent: an error, zero gradients, nothing out of place."""
     N, d, V = 200, 64, 700
